@@ -1,0 +1,109 @@
+// Attention of new tokens over the paged cache, one warp a (token, query head) row: the running
+// maximum m and sum l of the softmax and the output row are carried over the visible slots, all
+// in fp32; with m' = max(m, s), l' = l exp(m - m') + exp(s - m') and the output likewise.
+// The mass pass takes one warp a (sequence, key head, slot) and adds exp(s - lse) over the rows
+// that see the slot, so each mass element has one writer and one order.
+#include "kv.cuh"
+
+namespace ftmoe {
+namespace kv {
+namespace {
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+template <bool BF, int D>
+__global__ void __launch_bounds__(128) attend_rows(const AttendParams p, float *lse) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5), b = blockIdx.z, i = blockIdx.x;
+    const Seq s = seq_info(p.bt, b, p.c.status);
+    if (h >= p.q_heads || i >= s.q_len) return;
+    const int t = s.q0 + i, at = s.kv_len - s.q_len + i, hk = h / p.group;
+    const int end = at < 0 ? 0 : (p.causal ? at + 1 : s.kv_len);
+    const int begin = p.window && at - p.window + 1 > 0 ? at - p.window + 1 : 0;
+    float q[E], o[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e++) q[e] = to_f<BF>(p.q.d[t * p.q.token + h * p.q.head + lane * E + e]), o[e] = 0.f;
+    for (int j = begin; j < end; j++) {
+        const int page = page_of(p.c, p.bt, b, j), row = j & ((1 << p.c.page_shift) - 1);
+        if (page < 0) continue;
+        float d = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e++) d += q[e] * to_f<BF>(p.c.k[k_at(p.c, page, row, hk) + lane * E + e]);
+        const float x = warp_sum(d) * p.scale, n = fmaxf(m, x);
+        if (n == -INFINITY) continue;
+        const float a = expf(m - n), w = expf(x - n);
+        m = n;
+        l = l * a + w;
+#pragma unroll
+        for (int e = 0; e < E; e++) o[e] = o[e] * a + w * to_f<BF>(p.c.v[v_at(p.c, page, row, hk) + lane * E + e]);
+    }
+    if (p.sinks) {
+        const float x = p.sinks[h], n = fmaxf(m, x);
+        if (n != -INFINITY) {
+            const float a = expf(m - n);
+            l = l * a + expf(x - n);
+            m = n;
+#pragma unroll
+            for (int e = 0; e < E; e++) o[e] *= a;
+        }
+    }
+    const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < E; e++) p.out.d[t * p.out.token + h * p.out.head + lane * E + e] = from_f<BF>(o[e] * r);
+    if (lane == 0 && lse) lse[(int64_t)t * p.q_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+template <bool BF, int D>
+__global__ void __launch_bounds__(128) mass_slots(const AttendParams p, const float *lse) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, j = blockIdx.x * 4 + (threadIdx.x >> 5), hk = blockIdx.y, b = blockIdx.z;
+    const Seq s = seq_info(p.bt, b, p.c.status);
+    if (j >= s.kv_len) return;
+    const int first = s.kv_len - s.q_len;
+    int lo = p.causal ? j - first : 0, hi = s.q_len;  // rows that see slot j
+    if (p.window && j + p.window - first < hi) hi = j + p.window - first;
+    if (lo < 0) lo = 0;
+    if (first < 0 && lo < -first) lo = -first;
+    if (lo >= hi) return;
+    const int page = page_of(p.c, p.bt, b, j), row = j & ((1 << p.c.page_shift) - 1);
+    if (page < 0) return;
+    float k[E], sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; e++) k[e] = to_f<BF>(p.c.k[k_at(p.c, page, row, hk) + lane * E + e]);
+    for (int i = lo; i < hi; i++)
+        for (int h = hk * p.group; h < (hk + 1) * p.group; h++) {
+            const int64_t t = s.q0 + i;
+            float d = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; e++) d += k[e] * to_f<BF>(p.q.d[t * p.q.token + h * p.q.head + lane * E + e]);
+            const float z = lse[t * p.q_heads + h];
+            if (z != -INFINITY) sum += expf(warp_sum(d) * p.scale - z);
+        }
+    if (lane == 0) p.mass[b * p.mass_seq + hk * p.mass_head + j] += sum;
+}
+
+template <bool BF, int D>
+cudaError_t launch(const AttendParams &p, cudaStream_t st) {
+    float *lse = p.lse ? p.lse : (p.mass ? reinterpret_cast<float *>(p.ws) : nullptr);
+    attend_rows<BF, D><<<dim3(p.bt.max_q, (p.q_heads + 3) / 4, p.bt.batch), 128, 0, st>>>(p, lse);
+    if (p.mass) mass_slots<BF, D><<<dim3((p.bt.max_kv + 3) / 4, p.c.kv_heads, p.bt.batch), 128, 0, st>>>(p, lse);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attend_workspace(const AttendParams &p, int) {
+    return p.mass ? (size_t)p.bt.tokens * p.q_heads * 4 : 0;
+}
+
+cudaError_t launch_attend(const AttendParams &p, bool bf16, int, cudaStream_t st) {
+    if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, st) : launch<false, 64>(p, st);
+    return bf16 ? launch<true, 128>(p, st) : launch<false, 128>(p, st);
+}
+
+}  // namespace kv
+}  // namespace ftmoe

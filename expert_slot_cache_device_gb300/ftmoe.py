@@ -37,6 +37,8 @@ EXPORTS = [
     "ftmoe_expert_ffn_hybrid", "ftmoe_cpu_expert_ffn", "ftmoe_prefetch_layer", "ftmoe_prefill_layers",
     "ftmoe_measure_link", "ftmoe_measure_cpu_moe", "ftmoe_moe_backend_decision", "ftmoe_get_counters",
     "ftmoe_set_ffn_kernels", "ftmoe_ffn_kernels_for", "ftmoe_measure_cpu_read", "ftmoe_set_debug",
+    "ftmoe_rope_append", "ftmoe_paged_attention_workspace_bytes", "ftmoe_paged_attention", "ftmoe_kv_evict",
+    "ftmoe_w4_packed_bytes", "ftmoe_w4_pack", "ftmoe_w4_matvec",
 ]
 BACKEND_OFFLOAD, BACKEND_HYBRID = 0, 1
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -59,6 +61,34 @@ class BankSpec(ctypes.Structure):
     ]
 
 
+class KVCacheView(ctypes.Structure):
+    """ftmoe_kv_cache: pages, strides in elements, geometry, device status word."""
+    _fields_ = [("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p),
+                ("k_page", ctypes.c_int64), ("k_slot", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_page", ctypes.c_int64), ("v_slot", ctypes.c_int64), ("v_head", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("d_status", ctypes.c_void_p)]
+
+
+class KVBatchView(ctypes.Structure):
+    """ftmoe_kv_batch: the sequences of one call."""
+    _fields_ = [("d_block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("d_kv_lens", ctypes.c_void_p), ("d_cu_q", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("tokens", ctypes.c_int32), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class RowsView(ctypes.Structure):
+    """ftmoe_rows: device address and strides (elements) of rows [tokens, heads, head_dim]."""
+    _fields_ = [("d", ctypes.c_void_p), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class RotaryView(ctypes.Structure):
+    """ftmoe_rotary: frequency table and the rotated part of a head."""
+    _fields_ = [("d_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -71,6 +101,7 @@ def lib() -> ctypes.CDLL:
         raise ImportError(f"{LIB_PATH} is missing: build it first (python -m expert_slot_cache_device_gb300.build)")
     L = ctypes.CDLL(LIB_PATH)
     i32, u32, P, sz = ctypes.c_int32, ctypes.c_uint32, ctypes.c_void_p, ctypes.c_size_t
+    i64 = ctypes.c_int64
     sig = {
         "ftmoe_cache_workspace_bytes": [i32, i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)],
         "ftmoe_cache_create": [ctypes.POINTER(BankSpec), i32, i32, i32, i32, i32, i32, i32, i32, P, sz, P,
@@ -100,6 +131,13 @@ def lib() -> ctypes.CDLL:
         "ftmoe_measure_cpu_read": [P, sz, i32, i32, P],
         "ftmoe_moe_backend_decision": [i32, ctypes.c_double, ctypes.c_double, ctypes.c_double, P, P],
         "ftmoe_get_counters": [P, P, i32, P],
+        "ftmoe_rope_append": [P, P, P, P, P, i32, P, P, P, P],
+        "ftmoe_paged_attention_workspace_bytes": [P, P, i32, i32, i32, i32, ctypes.POINTER(sz)],
+        "ftmoe_paged_attention": [P, P, P, i32, ctypes.c_float, i32, i32, P, P, P, P, i64, i64, P, sz, P],
+        "ftmoe_kv_evict": [P, P, P, i64, i64, i32, i32, P, i64, P, P, P, P],
+        "ftmoe_w4_packed_bytes": [i32, i32, i32, i32, ctypes.POINTER(sz)],
+        "ftmoe_w4_pack": [P, P, P, i32, i32, i32, P, sz, P],
+        "ftmoe_w4_matvec": [P, i32, i32, i32, i32, i32, P, i64, i32, P, i64, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -294,3 +332,45 @@ def ftmoe_get_counters(cache: int, reset: bool, stream: int):
     out = (ctypes.c_uint64 * 3)()
     _check(lib().ftmoe_get_counters(cache, out, 1 if reset else 0, stream))
     return int(out[0]), int(out[1]), int(out[2])
+
+
+# ---------------------------------------------------------------- attention half of a layer
+def ftmoe_rope_append(kv, batch, rotary, q, q_out, q_heads: int, k, v, d_positions: int, stream: int) -> None:
+    """kv, batch, rotary, q, q_out, k, v: ctypes references (byref) to their views; q and q_out
+    None with q_heads = 0."""
+    _check(lib().ftmoe_rope_append(kv, batch, rotary, q, q_out, q_heads, k, v, d_positions, stream))
+
+
+def ftmoe_paged_attention_workspace_bytes(kv, batch, q_heads: int, window: int, causal: bool, want_mass: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ftmoe_paged_attention_workspace_bytes(kv, batch, q_heads, window, causal, want_mass, ctypes.byref(out)))
+    return out.value
+
+
+def ftmoe_paged_attention(kv, batch, q, q_heads: int, scale: float, window: int, causal: bool, d_sinks: int, out,
+                          d_lse: int, d_mass: int, mass_seq: int, mass_head: int, d_workspace: int,
+                          workspace_bytes: int, stream: int) -> None:
+    _check(lib().ftmoe_paged_attention(kv, batch, q, q_heads, scale, window, causal, d_sinks, out, d_lse, d_mass,
+                                       mass_seq, mass_head, d_workspace, workspace_bytes, stream))
+
+
+def ftmoe_kv_evict(kv, batch, d_mass: int, mass_seq: int, mass_head: int, budget: int, recent: int, d_new_table: int,
+                   new_stride: int, d_kept: int, d_new_mass: int, d_new_lens: int, stream: int) -> None:
+    _check(lib().ftmoe_kv_evict(kv, batch, d_mass, mass_seq, mass_head, budget, recent, d_new_table, new_stride,
+                                d_kept, d_new_mass, d_new_lens, stream))
+
+
+def ftmoe_w4_packed_bytes(N: int, K: int, group: int, has_zeros: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ftmoe_w4_packed_bytes(N, K, group, has_zeros, ctypes.byref(out)))
+    return out.value
+
+
+def ftmoe_w4_pack(d_codes: int, d_scales: int, d_zeros: int, N: int, K: int, group: int, d_packed: int,
+                  packed_bytes: int, stream: int) -> None:
+    _check(lib().ftmoe_w4_pack(d_codes, d_scales, d_zeros, N, K, group, d_packed, packed_bytes, stream))
+
+
+def ftmoe_w4_matvec(d_packed: int, N: int, K: int, group: int, has_zeros: bool, dtype: int, d_x: int, x_stride: int,
+                    tokens: int, d_y: int, y_stride: int, stream: int) -> None:
+    _check(lib().ftmoe_w4_matvec(d_packed, N, K, group, has_zeros, dtype, d_x, x_stride, tokens, d_y, y_stride, stream))

@@ -1,0 +1,318 @@
+"""Paged key/value cache of a decoder layer's attention half, next to the expert slot cache.
+
+``PagedKVCache`` owns (or wraps) the pages of one layer; ``KVBatch`` names the sequences of one
+call and serves every layer of a step; ``Rotary`` holds the rotary frequencies. A step of a layer:
+
+    q = cache.append(batch, rotary, q, k, v, positions)    # rotate, write K and V to their slots
+    y = cache.attend(batch, q, mass=mass)                   # attention of the new tokens
+    cache.evict(batch, mass, new_table, budget, recent)     # now and then: keep the heavy slots
+
+Everything is computed by libftmoe through the C-ABI binding (``ftmoe``); PyTorch provides device
+memory. Arguments are checked here and in the library before anything is enqueued; what only the
+device can see (a page outside the cache, lengths out of range) is recorded in the cache's status
+word (``status()``). Calls go to ``stream`` (the current stream by default) and do not wait.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import ftmoe as F
+from .cache import _stream
+
+_DTYPES = {torch.bfloat16: F.DT_BF16, torch.float16: F.DT_F16}
+
+
+def _new(shape, dtype, device, stream):
+    """Device memory that the allocator does not hand out again while `stream` still uses it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+        if s != torch.cuda.current_stream(device):
+            s.wait_stream(torch.cuda.current_stream(device))  # memory freed there may still be in use
+            t.record_stream(s)
+    return t
+
+
+def _ints(t: torch.Tensor, name: str, dims: int) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims:
+        raise ValueError(f"{name}: needs an int32 device tensor of {dims} dimension(s)")
+    if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: needs consecutive elements")
+    return t
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: Optional[dict] = None):
+    """(frequencies in radians a position, fp64 [rot_dim / 2]; factor on the rotated part).
+
+    f_i = base^(-2i / rot_dim); ``scaling`` stretches them for contexts beyond the trained length:
+
+    None                                   f_i
+    dict(kind="linear", factor=s)          f_i / s
+    dict(kind="base", factor=s)            base * s^(rot_dim / (rot_dim - 2)) in place of base
+    dict(kind="yarn", factor=s, original=n, beta_fast=32, beta_slow=1, attention_factor=None)
+        pairs that turn more than beta_fast times in n positions keep f_i, those that turn less
+        than beta_slow times get f_i / s, a linear ramp over the pair index blends between; the
+        factor is attention_factor or 0.1 ln s + 1 (1 for s <= 1)
+    dict(kind="banded", factor=s, original=n, low=1, high=4)
+        with r = n f_i / 2 pi turns in n positions: f_i for r > high, f_i / s for r < low, and
+        between, (1 - a) f_i / s + a f_i with a = (r - low) / (high - low)
+    """
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError(f"rot_dim={rot_dim}: a positive even number")
+    if not base > 1.0 or not math.isfinite(base):
+        raise ValueError(f"base={base}: above 1")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    freq = lambda b: torch.exp(i * (-2.0 / rot_dim * math.log(b)))  # noqa: E731
+    if scaling is None:
+        return freq(base), 1.0
+    known = {"linear": {"factor"}, "base": {"factor"},
+             "yarn": {"factor", "original", "beta_fast", "beta_slow", "attention_factor"},
+             "banded": {"factor", "original", "low", "high"}}
+    a = dict(scaling)
+    kind = a.pop("kind", None)
+    if kind not in known:
+        raise ValueError(f"unknown rotary scaling {kind!r}")
+    if set(a) - known[kind] or "factor" not in a or ("original" in known[kind] and "original" not in a):
+        raise ValueError(f"rotary scaling {kind!r} takes {sorted(known[kind])}, got {sorted(a)}")
+    s = float(a["factor"])
+    if not s > 0 or not math.isfinite(s):
+        raise ValueError(f"rotary scaling factor {s}")
+    if kind == "linear":
+        return freq(base) / s, 1.0
+    if kind == "base":
+        if rot_dim == 2:
+            raise ValueError("base scaling needs rot_dim above 2")
+        return freq(base * s ** (rot_dim / (rot_dim - 2))), 1.0
+    f, n = freq(base), float(a["original"])
+    if not n > 0:
+        raise ValueError(f"original={n}")
+    if kind == "banded":
+        low, high = float(a.get("low", 1.0)), float(a.get("high", 4.0))
+        if not high > low:
+            raise ValueError("banded scaling needs high above low")
+        t = ((n * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        return (1 - t) * f / s + t * f, 1.0
+    fast, slow = float(a.get("beta_fast", 32.0)), float(a.get("beta_slow", 1.0))
+    if not fast > slow > 0:
+        raise ValueError("yarn scaling needs beta_fast above beta_slow above 0")
+    pair = lambda turns: rot_dim * math.log(n / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+    lo, hi = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot_dim - 1)
+    ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+    att = a.get("attention_factor")
+    att = float(att) if att is not None else (0.1 * math.log(s) + 1.0 if s > 1 else 1.0)
+    return f * (1 - ramp) + f / s * ramp, att
+
+
+class Rotary:
+    """Rotary plan of a model: ``layout`` "half" (pairs (i, i + rot_dim / 2)) or "interleaved"
+    (pairs (2i, 2i + 1)), on the first ``rot_dim`` elements of a head (all by default; a multiple
+    of 16), ``scaling`` as in ``rotary_frequencies``."""
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, base: float = 10000.0, layout: str = "half",
+                 scaling: Optional[dict] = None, device="cuda"):
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"layout {layout!r}: half or interleaved")
+        if rot_dim % 16 or not 0 < rot_dim <= head_dim:
+            raise ValueError(f"rot_dim={rot_dim}: a multiple of 16, at most head_dim={head_dim}")
+        self.head_dim, self.rot_dim, self.layout = head_dim, rot_dim, layout
+        freq, self.factor = rotary_frequencies(rot_dim, base, scaling)
+        turns = freq / (2 * math.pi)
+        hi = turns.to(torch.float32)
+        self.freq = torch.stack([hi, (turns - hi.double()).to(torch.float32)], -1).contiguous().to(device)
+        self._view = F.RotaryView(self.freq.data_ptr(), rot_dim, layout == "interleaved", self.factor)
+        self.ref = ctypes.byref(self._view)
+
+
+class KVBatch:
+    """The sequences of one call.
+
+    block_table  int32 [batch, pages]: page of each block of page_size slots
+    kv_lens      int32 [batch]: cached tokens, this call's new ones included (the last of them)
+    cu_q         int32 [batch + 1]: first row of each sequence's new tokens in the token arrays
+    max_q        upper bound of the new tokens of one sequence
+    max_kv       upper bound of kv_lens
+    The tensors are read when the kernels run, so one object can serve a captured step whose
+    lengths change within the bounds."""
+
+    def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor, max_q: int, max_kv: int):
+        self.block_table = _ints(block_table, "block_table", 2)
+        self.kv_lens, self.cu_q = _ints(kv_lens, "kv_lens", 1), _ints(cu_q, "cu_q", 1)
+        self.batch = block_table.shape[0]
+        if kv_lens.numel() != self.batch or cu_q.numel() != self.batch + 1:
+            raise ValueError(f"{self.batch} sequences: kv_lens has {kv_lens.numel()}, cu_q {cu_q.numel()} entries")
+        if max_q < 0 or max_kv < 0:
+            raise ValueError("max_q and max_kv must not be negative")
+        self.max_q, self.max_kv = int(max_q), int(max_kv)
+        self.device = block_table.device
+        stride = block_table.stride(0) if self.batch > 1 else block_table.shape[1]
+        self._args = (block_table.data_ptr(), stride, kv_lens.data_ptr(), cu_q.data_ptr(), self.batch)
+        self._views, self._bytes = {}, {}
+
+    def _ref(self, tokens: int):
+        """Reference to the C view for token arrays of `tokens` rows."""
+        v = self._views.get(tokens)
+        if v is None:
+            v = F.KVBatchView(*self._args, tokens, self.max_q, self.max_kv, self.block_table.shape[1])
+            v = self._views[tokens] = (ctypes.byref(v), v)
+        return v[0]
+
+
+class PagedKVCache:
+    """Keys and values of one layer in pages.
+
+    num_pages, page_size (a power of two, 16..256), kv_heads, head_dim (attention: 64 or 128)
+    k_pages, v_pages  optional device tensors [num_pages, page_size, kv_heads, head_dim] of
+                      ``dtype`` (bfloat16 or float16) in any stride order with the last axis
+                      contiguous; allocated here when omitted"""
+
+    def __init__(self, num_pages: int, page_size: int, kv_heads: int, head_dim: int, dtype=torch.bfloat16,
+                 k_pages: Optional[torch.Tensor] = None, v_pages: Optional[torch.Tensor] = None, device="cuda"):
+        F.lib()
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype {dtype}: bfloat16 or float16")
+        shape = (num_pages, page_size, kv_heads, head_dim)
+        pages = []
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=device)
+            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or t.stride(3) != 1:
+                raise ValueError(f"{name}: needs a {dtype} device tensor {list(shape)} with a contiguous last axis")
+            pages.append(t)
+        self.k_pages, self.v_pages = pages
+        self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.dtype = *shape, dtype
+        self.device = self.k_pages.device
+        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self._view = F.KVCacheView(self.k_pages.data_ptr(), self.v_pages.data_ptr(), *self.k_pages.stride()[:3],
+                                   *self.v_pages.stride()[:3], _DTYPES[dtype], num_pages, page_size, kv_heads, head_dim,
+                                   self._status.data_ptr())
+        self._ref = ctypes.byref(self._view)
+
+    def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, tokens: Optional[int] = None):
+        if not isinstance(t, torch.Tensor) or t.dtype != self.dtype or not t.is_cuda or t.dim() != 3:
+            raise ValueError(f"{name}: needs a {self.dtype} device tensor [tokens, heads, head_dim]")
+        n, h, d = t.shape
+        if d != self.head_dim or (heads is not None and h != heads) or (tokens is not None and n != tokens):
+            raise ValueError(f"{name}: shape {list(t.shape)} does not match the call")
+        st, sh, sd = t.stride()
+        if sd != 1:
+            raise ValueError(f"{name}: rows of head_dim must be contiguous")
+        # a stride over one element is never taken
+        return ctypes.byref(F.RowsView(t.data_ptr(), st if n > 1 else 8, sh if h > 1 else 8))
+
+    def append(self, batch: KVBatch, rotary: Rotary, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+               positions: torch.Tensor, q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+        """Rotate q and k [tokens, heads, head_dim] by ``positions`` (int32 [tokens]) and write k
+        and v to their slots. Returns the rotated queries (``q_out``, which may be q itself)."""
+        if rotary.head_dim != self.head_dim:
+            raise ValueError(f"rotary plan of head_dim {rotary.head_dim}, cache of {self.head_dim}")
+        n = k.shape[0]
+        kr, vr = self._rows(k, "k", self.kv_heads), self._rows(v, "v", self.kv_heads, n)
+        if _ints(positions, "positions", 1).numel() != n:
+            raise ValueError(f"positions has {positions.numel()} entries for {n} tokens")
+        if n == 0:
+            return q
+        qr = qo = None
+        heads = 0
+        if q is not None:
+            heads = q.shape[1]
+            qr = self._rows(q, "q", None, n)
+            if q_out is None:
+                q_out = _new(q.shape, q.dtype, q.device, stream)
+            qo = self._rows(q_out, "q_out", heads, n)
+        F.ftmoe_rope_append(self._ref, batch._ref(n), rotary.ref, qr, qo, heads, kr, vr, positions.data_ptr(),
+                            _stream(stream))
+        return q_out
+
+    def attend(self, batch: KVBatch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
+               sinks: Optional[torch.Tensor] = None, causal: bool = True, out: Optional[torch.Tensor] = None,
+               lse: Optional[torch.Tensor] = None, mass: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Attention of the new tokens' queries [tokens, heads, head_dim] over their sequences'
+        cached slots (``ftmoe_paged_attention``). ``scale`` defaults to head_dim ** -0.5,
+        ``sinks`` is fp32 [heads], ``lse`` fp32 [tokens, heads] receives the log-sum-exp, ``mass``
+        fp32 [batch, kv_heads, >= max_kv] gets each slot's attention weight added. Returns out."""
+        n, heads = q.shape[0], q.shape[1]
+        qr = self._rows(q, "q")
+        if heads % self.kv_heads:
+            raise ValueError(f"{heads} query heads over {self.kv_heads} key heads")
+        if out is None:
+            out = _new(q.shape, q.dtype, q.device, stream)
+        outr = self._rows(out, "out", heads, n)
+        for name, t, shape in (("sinks", sinks, (heads,)), ("lse", lse, (n, heads))):
+            if t is not None and (t.dtype != torch.float32 or not t.is_cuda or t.shape != shape or not t.is_contiguous()):
+                raise ValueError(f"{name}: needs a contiguous fp32 device tensor {list(shape)}")
+        ms = mh = 0
+        if mass is not None:
+            ms, mh = self._mass(batch, mass)
+        if n == 0:
+            return out
+        ref = batch._ref(n)
+        key = (n, heads, self.kv_heads, self.head_dim, self.page_size, window, causal, mass is not None)
+        need = batch._bytes.get(key)
+        if need is None:
+            need = batch._bytes[key] = F.ftmoe_paged_attention_workspace_bytes(self._ref, ref, heads, window, causal,
+                                                                               mass is not None)
+        ws = _new(need, torch.uint8, self.device, stream) if need else None
+        F.ftmoe_paged_attention(self._ref, ref, qr, heads, self.head_dim ** -0.5 if scale is None else scale, window,
+                                causal, sinks.data_ptr() if sinks is not None else None, outr,
+                                lse.data_ptr() if lse is not None else None,
+                                mass.data_ptr() if mass is not None else None, ms, mh,
+                                ws.data_ptr() if need else None, need, _stream(stream))
+        return out
+
+    def _mass(self, batch: KVBatch, mass: torch.Tensor):
+        if mass.dtype != torch.float32 or not mass.is_cuda or mass.dim() != 3 or mass.shape[:2] != (batch.batch, self.kv_heads):
+            raise ValueError(f"mass: needs an fp32 device tensor [{batch.batch}, {self.kv_heads}, slots]")
+        if mass.shape[2] < batch.max_kv or (mass.shape[2] > 1 and mass.stride(2) != 1):
+            raise ValueError(f"mass: rows of at least max_kv={batch.max_kv} consecutive elements")
+        ms, mh = mass.stride(0), mass.stride(1)
+        if self.kv_heads == 1:
+            mh = mass.shape[2]
+        if mh < mass.shape[2] or (batch.batch > 1 and ms < mass.shape[2]):
+            raise ValueError("mass: rows overlap")
+        return ms, mh
+
+    def evict(self, batch: KVBatch, mass: torch.Tensor, new_table: torch.Tensor, budget: int, recent: int,
+              kept: Optional[torch.Tensor] = None, new_mass: Optional[torch.Tensor] = None,
+              new_lens: Optional[torch.Tensor] = None, stream=None):
+        """Keep at most ``budget`` slots of each (sequence, key head): the last ``recent`` and
+        those of largest mass (``ftmoe_kv_evict``), moved in order to the pages of ``new_table``
+        (int32 [batch, pages], pages that ``block_table`` does not name). Returns (kept int32
+        [batch, kv_heads, budget], new_mass fp32 likewise, new_lens int32 [batch]); the old
+        pages can be reused by later work on the same stream."""
+        ms, mh = self._mass(batch, mass)
+        if _ints(new_table, "new_table", 2).shape[0] != batch.batch:
+            raise ValueError(f"new_table has {new_table.shape[0]} rows for {batch.batch} sequences")
+        shape = (batch.batch, self.kv_heads, budget)
+        if budget < 1:
+            raise ValueError(f"budget={budget}")
+        if kept is None:
+            kept = _new(shape, torch.int32, self.device, stream)
+        if new_mass is None:
+            new_mass = _new(shape, torch.float32, self.device, stream)
+        if new_lens is None:
+            new_lens = _new(batch.batch, torch.int32, self.device, stream)
+        for name, t, sh, dt in (("kept", kept, shape, torch.int32), ("new_mass", new_mass, shape, torch.float32),
+                                ("new_lens", new_lens, shape[:1], torch.int32)):
+            if t.dtype != dt or not t.is_cuda or t.shape != sh or not t.is_contiguous():
+                raise ValueError(f"{name}: needs a contiguous {dt} device tensor {list(sh)}")
+        # the C call takes one row length for every row
+        if new_table.shape[1] * self.page_size < min(budget, batch.max_kv):
+            raise ValueError(f"new_table: {new_table.shape[1]} pages a row for {min(budget, batch.max_kv)} slots")
+        stride = new_table.stride(0) if batch.batch > 1 else new_table.shape[1]
+        F.ftmoe_kv_evict(self._ref, batch._ref(0), mass.data_ptr(), ms, mh, budget, recent, new_table.data_ptr(), stride,
+                         kept.data_ptr(), new_mass.data_ptr(), new_lens.data_ptr(), _stream(stream))
+        return kept, new_mass, new_lens
+
+    def status(self, stream=None) -> int:
+        """Sticky device status of this cache's calls (synchronises the stream)."""
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=self.device)):
+            return int(self._status.item())
+
+    def reset_status(self, stream=None) -> None:
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=self.device)):
+            self._status.zero_()

@@ -423,6 +423,147 @@ int ftmoe_expert_ffn_noalloc(int32_t format, const void *const *d_slot_banks, in
                              const int32_t *d_slots, const float *d_weights, int32_t topk,
                              void *d_y_bf16, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * Attention half of a decoder layer: a paged key/value cache (rotary positions and the
+ * write of the new tokens, attention of the new tokens, eviction by attention weight) and
+ * products with 4-bit weights. These calls own nothing: the caller keeps pages, tables,
+ * packed weights and workspaces. All of them only enqueue kernels and can be captured in a
+ * CUDA graph (the device arrays are read at replay time).
+ * ------------------------------------------------------------------------------------ */
+
+/* View of one layer's paged key/value cache. d_k and d_v hold num_pages pages of page_size
+ * slots of kv_heads rows of head_dim elements; element (page, slot, head, i) sits at
+ * page * k_page + slot * k_slot + head * k_head + i elements (v_* for d_v), so any order of
+ * the three outer axes works. Bases are 16-byte aligned and strides positive multiples of
+ * eight elements.
+ *   dtype     FTMOE_DT_BF16 or FTMOE_DT_F16 (queries, new rows and outputs have it too);
+ *   page_size a power of two in [16, 256]; head_dim a multiple of 16, at most 256
+ *             (ftmoe_paged_attention: 64 or 128);
+ *   d_status  int32 [1], or NULL: sticky device status of the calls on this view, zeroed by
+ *             the caller. A block-table entry outside [0, num_pages) that a call needs gives
+ *             FTMOE_ERR_ID_RANGE: nothing is read from or written to such a page, and what
+ *             the call computes for that sequence is unspecified. A cu_q entry below its
+ *             predecessor or outside [0, tokens], a sequence with more than max_q new tokens,
+ *             or a kv_len outside [0, max_kv] gives FTMOE_ERR_STATE, and the value is used
+ *             cut to its range. A bounded wait that ran out gives FTMOE_ERR_STATE too. */
+typedef struct {
+    void *d_k, *d_v;
+    int64_t k_page, k_slot, k_head;
+    int64_t v_page, v_slot, v_head;
+    int32_t dtype, num_pages, page_size, kv_heads, head_dim;
+    int32_t *d_status;
+} ftmoe_kv_cache;
+
+/* The sequences of one call. Sequence b has q_len = cu_q[b + 1] - cu_q[b] new tokens, rows
+ * cu_q[b] .. of the call's token arrays, and kv_lens[b] cached tokens, the new ones the last
+ * of them: new token i sits in slot kv_lens[b] - q_len + i, slot s in page
+ * block_table[b * table_stride + s / page_size], row s % page_size. Entries of pages that
+ * hold no slot a call needs are not read (they may be anything). Rows of the token arrays
+ * that no sequence covers are left alone.
+ *   max_pages  readable entries of a block_table row;
+ *   tokens     rows of the token arrays; max_q and max_kv: host-side upper bounds of q_len
+ *              and kv_lens (they size grids and workspaces; max_kv <= max_pages * page_size). */
+typedef struct {
+    const int32_t *d_block_table;
+    int64_t table_stride;
+    const int32_t *d_kv_lens; /* [batch] */
+    const int32_t *d_cu_q;    /* [batch + 1] */
+    int32_t batch, tokens, max_q, max_kv, max_pages;
+} ftmoe_kv_batch;
+
+/* Rows [tokens, heads, head_dim] of a call: row (t, h) at t * token + h * head elements, a row
+ * contiguous, base 16-byte aligned, strides multiples of eight elements. */
+typedef struct {
+    void *d;
+    int64_t token, head;
+} ftmoe_rows;
+
+/* Rotary plan: the first rot_dim elements of a head are rotated in pairs, (i, i + rot_dim / 2)
+ * or, with interleaved != 0, (2i, 2i + 1), by the angle of d_freq's pair i, and multiplied by
+ * factor; the others are copied.
+ *   d_freq  float [rot_dim / 2][2]: hi = fp32(f), lo = fp32(f - hi) of the frequency f in
+ *           turns a position (radians / 2 pi), so that angles keep 2^-24 turns at positions
+ *           up to 2^24;
+ *   rot_dim a multiple of 16, at most head_dim, head_dim - rot_dim a multiple of 16. */
+typedef struct {
+    const float *d_freq;
+    int32_t rot_dim, interleaved;
+    float factor;
+} ftmoe_rotary;
+
+/* Rotate the new tokens' queries and keys by their positions and write keys and values to
+ * their slots. d_positions int32 [tokens] (|position| < 2^24; a slot need not equal its
+ * position: evicted caches are shorter). q_out may equal q (the same rows and strides);
+ * otherwise no array may overlap another. q_heads = 0 leaves the queries out (q and q_out
+ * unread). Angles and products are formed in fp32; each result is rounded once. */
+int ftmoe_rope_append(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, const ftmoe_rotary *rotary,
+                      const ftmoe_rows *q, const ftmoe_rows *q_out, int32_t q_heads, const ftmoe_rows *k,
+                      const ftmoe_rows *v, const int32_t *d_positions, void *stream);
+
+/* Attention of the new tokens over the cached ones:
+ *   s_j = scale * q . k_j over the visible slots j, l = sum_j exp(s_j) + exp(sink),
+ *   out = sum_j exp(s_j) v_j / l, lse = log l, mass_j += sum over the sequence's rows of the
+ *   key head's query heads of exp(s_j - lse).
+ * New token i in slot p = kv_len - q_len + i sees slots j <= p (causal != 0) or all below
+ * kv_len (causal = 0), and with window > 0 (causal only) those with j > p - window. A row that
+ * sees nothing (p < 0, kv_len = 0) gives out = 0, lse = log of its sink term (-inf without).
+ *   q_heads     a multiple of kv_heads; query head h reads key head h / (q_heads / kv_heads);
+ *   scale       positive and finite;
+ *   d_sinks     fp32 [q_heads] or NULL (no sink term);
+ *   out         rows like q; d_lse fp32 [tokens, q_heads] or NULL;
+ *   d_mass      fp32, element (b, key head, slot) at b * mass_seq + head * mass_head + slot,
+ *               rows of at least max_kv, or NULL. Each element is added to once, in one fixed
+ *               order, so results repeat bit for bit;
+ *   d_workspace 256-byte aligned device memory of at least the bytes that
+ *               ftmoe_paged_attention_workspace_bytes gives for the same arguments; calls
+ *               that overlap on the GPU need one each.
+ * Slots outside every row's visible range may hold anything, NaN included. Scores, the running
+ * maximum, sums and outputs are kept in fp32; the probabilities are rounded to the cache's
+ * type for the product with V (not for l, lse or mass). K and V of one sequence that are visible to some of
+ * its rows and masked for others have to be finite. */
+int ftmoe_paged_attention_workspace_bytes(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, int32_t q_heads,
+                                          int32_t window, int32_t causal, int32_t want_mass, size_t *bytes);
+int ftmoe_paged_attention(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, const ftmoe_rows *q, int32_t q_heads,
+                          float scale, int32_t window, int32_t causal, const float *d_sinks, const ftmoe_rows *out,
+                          float *d_lse, float *d_mass, int64_t mass_seq, int64_t mass_head, void *d_workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Eviction by accumulated attention weight, for each sequence and key head on its own: with
+ * n = kv_len cached tokens, all are kept when n <= budget; otherwise the last `recent` and, of
+ * the n - recent before them, the budget - recent with the largest mass (ties: the lowest
+ * slot; a NaN ranks below every number, -0 equals 0). Kept tokens go in slot order to slots
+ * 0, 1, ... of the sequence's row of d_new_table, which has to name pages that no row of
+ * block_table names.
+ *   d_mass      as in ftmoe_paged_attention; read only;
+ *   d_new_table int32 [batch, new_stride], at least ceil(min(budget, max_kv) / page_size)
+ *               entries a row;
+ *   d_kept      int32 [batch, kv_heads, budget]: source slots in order, then -1;
+ *   d_new_mass  fp32 [batch, kv_heads, budget]: their mass, then 0;
+ *   d_new_lens  int32 [batch]: min(n, budget).
+ * cu_q and tokens of the batch are not used. 0 <= recent <= budget, budget >= 1. */
+int ftmoe_kv_evict(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, const float *d_mass, int64_t mass_seq,
+                   int64_t mass_head, int32_t budget, int32_t recent, const int32_t *d_new_table, int64_t new_stride,
+                   int32_t *d_kept, float *d_new_mass, int32_t *d_new_lens, void *stream);
+
+/* 4-bit weights W [N, K]: w = (code - zero) * scale with one scale (and zero) per `group`
+ * consecutive k of a row.
+ *   d_codes  u8 [N, K / 2], low nibble = even k; d_scales [N, K / group] of `dtype`
+ *            (FTMOE_DT_BF16 or FTMOE_DT_F16); d_zeros u8 [N, K / group] (values 0..15), or
+ *            NULL for zero = 8;
+ *   group    32, 64 or 128; K a positive multiple of group.
+ * ftmoe_w4_pack lays them out once for the product kernel (d_packed: 256-byte aligned,
+ * ftmoe_w4_packed_bytes bytes); the plain arrays are not needed afterwards. */
+int ftmoe_w4_packed_bytes(int32_t N, int32_t K, int32_t group, int32_t has_zeros, size_t *bytes);
+int ftmoe_w4_pack(const void *d_codes, const void *d_scales, const void *d_zeros, int32_t N, int32_t K, int32_t group,
+                  void *d_packed, size_t packed_bytes, void *stream);
+
+/* y[t, n] = sum_k x[t, k] w[n, k] over packed weights. x [tokens, K] and y [tokens, N] of the
+ * scales' dtype, rows x_stride and y_stride elements apart (x 16-byte aligned, x_stride a
+ * multiple of eight). Codes less zeros are exact in dtype, products are summed in fp32 within
+ * a group, the scale is applied in fp32, and y is rounded once. tokens = 0 does nothing. */
+int ftmoe_w4_matvec(const void *d_packed, int32_t N, int32_t K, int32_t group, int32_t has_zeros, int32_t dtype,
+                    const void *d_x, int64_t x_stride, int32_t tokens, void *d_y, int64_t y_stride, void *stream);
+
 /* Message of the last failing call on this thread. */
 const char *ftmoe_last_error(void);
 
