@@ -156,7 +156,7 @@ int ftmoe_paged_attention_workspace_bytes(const ftmoe_kv_cache *kvc, const ftmoe
     if ((rc = num_sms(sms))) return rc;
     float want = 0.f;
     p.mass = want_mass ? &want : nullptr;
-    *bytes = kv::attend_workspace(p, sms);
+    *bytes = kv::attend_workspace(p, sms, nullptr);
     return FTMOE_OK;
 }
 
@@ -176,10 +176,9 @@ int ftmoe_paged_attention(const ftmoe_kv_cache *kvc, const ftmoe_kv_batch *batch
     if (p.bt.tokens == 0 || p.bt.batch == 0 || p.bt.max_q == 0) return FTMOE_OK;
     if ((rc = num_sms(sms))) return rc;
     p.scale = scale, p.sinks = d_sinks, p.lse = d_lse, p.mass = d_mass, p.mass_seq = mass_seq, p.mass_head = mass_head;
-    const size_t need = kv::attend_workspace(p, sms);
+    const size_t need = kv::attend_workspace(p, sms, static_cast<unsigned char *>(d_workspace));
     if (need && (!d_workspace || ((uintptr_t)d_workspace & 255) || workspace_bytes < need))
         return fail(FTMOE_ERR_INVALID_ARG, "workspace: %zu bytes at a 256-byte boundary needed, %zu given", need, workspace_bytes);
-    p.ws = static_cast<unsigned char *>(d_workspace);
     return cuda_rc(kv::launch_attend(p, kvc->dtype == FTMOE_DT_BF16, sms, static_cast<cudaStream_t>(stream)),
                    "attention kernels");
 }

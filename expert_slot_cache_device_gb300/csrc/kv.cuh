@@ -125,9 +125,17 @@ struct AttendParams {
     float *lse;   // [tokens, q_heads] (nullable)
     float *mass;  // (nullable)
     int64_t mass_seq, mass_head;
-    unsigned char *ws;
+    // workspace (attend_workspace): parts of split items, log-sum-exps in powers of two for the
+    // mass pass, the scores that it reads
+    float *part_o;
+    float2 *part_ml;
+    float *lse2;
+    float *logits;  // [batch, kv_heads, logit_rows][logit_stride]
+    int32_t logit_rows;
+    int64_t logit_stride;
 };
-size_t attend_workspace(const AttendParams &p, int num_sms);
+// Bytes of workspace; with `base` the pointers of p are set into it.
+size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base);
 cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 
 struct EvictParams {

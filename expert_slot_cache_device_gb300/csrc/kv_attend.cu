@@ -3,7 +3,7 @@
 // in fp32; with m' = max(m, s), l' = l exp(m - m') + exp(s - m') and the output likewise.
 // The mass pass takes one warp a (sequence, key head, slot) and adds exp(s - lse) over the rows
 // that see the slot, so each mass element has one writer and one order.
-#include "kv.cuh"
+#include "kv_attend.cuh"
 
 namespace ftmoe {
 namespace kv {
@@ -88,19 +88,43 @@ __global__ void __launch_bounds__(128) mass_slots(const AttendParams p, const fl
 
 template <bool BF, int D>
 cudaError_t launch(const AttendParams &p, cudaStream_t st) {
-    float *lse = p.lse ? p.lse : (p.mass ? reinterpret_cast<float *>(p.ws) : nullptr);
+    float *lse = p.lse ? p.lse : p.lse2;
     attend_rows<BF, D><<<dim3(p.bt.max_q, (p.q_heads + 3) / 4, p.bt.batch), 128, 0, st>>>(p, lse);
     if (p.mass) mass_slots<BF, D><<<dim3((p.bt.max_kv + 3) / 4, p.c.kv_heads, p.bt.batch), 128, 0, st>>>(p, lse);
     return cudaGetLastError();
 }
 
+// The single-token kernel takes calls whose rows a (sequence, key head) fit its 16.
+bool is_step(const AttendParams &p) { return (int64_t)p.bt.max_q * p.group <= kStepRows; }
+
 }  // namespace
 
-size_t attend_workspace(const AttendParams &p, int) {
-    return p.mass ? (size_t)p.bt.tokens * p.q_heads * 4 : 0;
+size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char *at = base ? base + off : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    p.part_o = nullptr, p.part_ml = nullptr, p.lse2 = nullptr, p.logits = nullptr;
+    if (is_step(p)) {
+        const size_t slots = 2 * (size_t)step_ctas(p, num_sms);
+        p.part_o = reinterpret_cast<float *>(take(slots * kStepRows * p.c.dim * 4));
+        p.part_ml = reinterpret_cast<float2 *>(take(slots * kStepRows * 8));
+    }
+    if (p.mass) {
+        p.lse2 = reinterpret_cast<float *>(take((size_t)p.bt.tokens * p.q_heads * 4));
+        if (is_step(p)) {
+            p.logit_rows = p.bt.max_q * p.group;
+            p.logit_stride = ((int64_t)p.bt.max_kv + 127) & ~(int64_t)127;
+            p.logits = reinterpret_cast<float *>(take((size_t)p.bt.batch * p.c.kv_heads * p.logit_rows * p.logit_stride * 4));
+        }
+    }
+    return off;
 }
 
-cudaError_t launch_attend(const AttendParams &p, bool bf16, int, cudaStream_t st) {
+cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
+    if (is_step(p)) return launch_step(p, bf16, num_sms, st);
     if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, st) : launch<false, 64>(p, st);
     return bf16 ? launch<true, 128>(p, st) : launch<false, 128>(p, st);
 }

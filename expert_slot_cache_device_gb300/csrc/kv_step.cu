@@ -1,0 +1,464 @@
+// Attention of at most 16 rows a (sequence, key head): the decode step, where the query heads of a
+// key head (and the few new tokens) are the M = 16 rows of mma.sync m16n8k16. Bound by reading
+// K and V once, 4 dim bytes a slot and key head.
+//
+// A CTA is four warps that share nothing while they read: warp w takes tiles w, w + 4, ... of kTile
+// slots (16 of 128 elements or 32 of 64: 4 KiB of K, 4 KiB of V) through its own ring of kStages
+// tiles filled by 16-byte cp.async, two CTAs an SM, so about 128 KiB are in flight on an SM. Rows
+// past the visible range are zero-filled by the copy itself, so what such slots hold never
+// reaches a product. Rows are stored with 16-byte chunk c of row r at c ^ (r % 8), which makes the
+// eight rows of an ldmatrix distinct banks. Scores S = Q K^T and O += P V per tile; the softmax keeps
+// a running maximum that O is rescaled to only when it grew by more than 2^8 (the sum and P use
+// the same stale maximum, so the result is the same).
+//
+// Work is cut by kv_split.cuh: one line of units of 4 kTile slots over all (sequence, key head)s, an
+// equal part for each CTA. With mass, the scaled scores are kept (fp32, powers of two) and the
+// mass kernel adds 2^(x - lse) once the log-sum-exp is known, reading 4 bytes a (row, slot)
+// instead of K again.
+#include "kv_split.cuh"
+#include "kv_attend.cuh"
+#include "pipeline.cuh"
+
+namespace ftmoe {
+namespace kv {
+namespace {
+
+constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 3, kRows = kStepRows;
+constexpr int kTileBytes = 4096;  // K or V of one tile
+template <int D>
+constexpr int kTile = kTileBytes / (2 * D);
+constexpr int kStageBytes = 2 * kTileBytes, kRingBytes = kStages * kStageBytes;
+constexpr int kSmem = kWarps * kRingBytes;
+constexpr float kSlack = 8.f;  // the maximum may lag by 2^8
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+template <bool BF>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF)
+        pipe::mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    else
+        pipe::mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+// Units of one (sequence, key head); a sequence with rows has at least one, which writes the
+// result of rows that see nothing.
+template <int D>
+__device__ __forceinline__ int units_of(const Seq &s, const AttendParams &p, Range &r) {
+    r = visible(s, 0, s.q_len, p.window, p.causal);
+    r.lo &= ~(kTile<D> - 1);
+    const int u = (r.hi - r.lo + kWarps * kTile<D> - 1) / (kWarps * kTile<D>);
+    return s.q_len == 0 ? 0 : (u > 0 ? u : 1);
+}
+
+// Total units, and the sequence that unit line position `at` (of one key head's share) falls in.
+template <int D>
+__device__ __forceinline__ long long total_units(const AttendParams &p, long long *s_warp, int32_t *status) {
+    long long mine = 0, total;
+    for (int b = threadIdx.x; b < p.bt.batch; b += kThreads) {
+        Range r;
+        mine += units_of<D>(seq_info(p.bt, b, status), p, r);
+    }
+    block_scan<kThreads>(mine, total, s_warp);
+    return total * p.c.kv_heads;
+}
+
+struct Spot {
+    int b;
+    long long before;  // units of the sequences before b, all heads
+};
+
+template <int D>
+__device__ __forceinline__ Spot find_unit(const AttendParams &p, long long u, long long *s_warp, Spot *s_spot) {
+    long long base = 0;
+    for (int b0 = 0; b0 < p.bt.batch; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        Range r;
+        const long long n = b < p.bt.batch ? (long long)units_of<D>(seq_info(p.bt, b, nullptr), p, r) * p.c.kv_heads : 0;
+        long long total;
+        const long long at = base + block_scan<kThreads>(n, total, s_warp);
+        if (u >= at && u < at + n) s_spot->b = b, s_spot->before = at;
+        base += total;
+        if (base > u) break;
+    }
+    __syncthreads();
+    return *s_spot;
+}
+
+template <bool BF, int D, bool LOGITS>
+__global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p) {
+    constexpr int T = kTile<D>, NT = T / 8, KT = T / 16, KS = D / 16, CH = D / 8, RPI = 32 / CH;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    __shared__ long long s_warp[kWarps];
+    __shared__ Spot s_spot;
+    __shared__ float s_ml[kWarps][kRows][2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = pipe::su32(sm) + warp * kRingBytes;
+
+    const long long W = total_units<D>(p, s_warp, blockIdx.x == 0 ? p.c.status : nullptr);
+    const int C = used_ctas(gridDim.x, W);
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    if (blockIdx.x >= C) return;
+    long long u = unit_start(blockIdx.x, C, W);
+    const long long u1 = unit_start(blockIdx.x + 1, C, W);
+    const Spot spot = find_unit<D>(p, u, s_warp, &s_spot);
+    int b = spot.b;
+    Range vis;
+    Seq sq = seq_info(p.bt, b, nullptr);
+    int n_units = units_of<D>(sq, p, vis);
+    int hk = (int)((u - spot.before) / n_units), first = (int)((u - spot.before) % n_units);
+
+    const float c2 = p.scale * kLog2e;
+    // this lane's chunk of a copied row, and its swizzled place in the RPI rows of one copy
+    const int crow = lane / CH, cch = lane % CH;
+
+    while (u < u1) {
+        const int last = (int)(u1 - u < n_units - first ? first + (u1 - u) : n_units);  // units [first, last)
+        const int rows = sq.q_len * p.group;
+        const int lo_q = visible(sq, 0, sq.q_len, p.window, p.causal).lo;
+        const int t0 = vis.lo / T + first * kWarps + warp;             // this warp's tiles: t0, t0 + 4, ...
+        const int tiles = last - first;
+        const uint16_t *kb = p.c.k + hk * p.c.k_head + 8 * cch, *vb = p.c.v + hk * p.c.v_head + 8 * cch;
+        const int32_t *tab = p.bt.table + (int64_t)b * p.bt.table_stride;
+        const int pmask = (1 << p.c.page_shift) - 1;
+
+        // page of each 16 slots of tile i, one tile ahead of its copy; -1: nothing there to read
+        auto pages = [&](int i, int (&pg)[KT]) {
+#pragma unroll
+            for (int k = 0; k < KT; k++) {
+                const int slot = (t0 + i * kWarps) * T + 16 * k;
+                pg[k] = -1;
+                if (i < tiles && slot < vis.hi && slot + 16 > lo_q) {
+                    pg[k] = tab[slot >> p.c.page_shift];
+                    if ((uint32_t)pg[k] >= (uint32_t)p.c.num_pages) {
+                        flag(p.c.status, FTMOE_ERR_ID_RANGE);
+                        pg[k] = -1;
+                    }
+                }
+            }
+        };
+        auto copy = [&](int i, const int (&pg)[KT]) {
+            if (i < tiles) {
+                const int slot0 = (t0 + i * kWarps) * T;
+                const uint32_t st = ring + (i % kStages) * kStageBytes;
+#pragma unroll
+                for (int n = 0; n < T / RPI; n++) {
+                    const int r = n * RPI + crow, slot = slot0 + r, page = pg[n * RPI / 16];
+                    const bool ok = page >= 0 && slot >= lo_q && slot < vis.hi;
+                    const uint32_t at = st + r * (2 * D) + (((cch & ~7) | ((cch ^ r) & 7)) << 4);
+                    const int64_t pr = ok ? page : 0, row = ok ? slot & pmask : 0;
+                    cp16(at, kb + pr * p.c.k_page + row * p.c.k_slot, ok ? 16 : 0);
+                    cp16(at + kTileBytes, vb + pr * p.c.v_page + row * p.c.v_slot, ok ? 16 : 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+
+        int pg[KT];
+#pragma unroll
+        for (int i = 0; i < kStages - 1; i++) {
+            pages(i, pg);
+            copy(i, pg);
+        }
+        pages(kStages - 1, pg);
+
+        // the rows' queries as A fragments: rows g and g + 8
+        uint32_t qf[KS][4];
+        int end[2], beg[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const int r = g + 8 * e, i = r / p.group, h = hk * p.group + r % p.group;
+            const bool live = r < rows;
+            const Range v = visible(sq, i, i + 1, p.window, p.causal);
+            beg[e] = live ? v.lo : 0, end[e] = live ? v.hi : 0;
+            const uint16_t *q = p.q.d + (int64_t)(sq.q0 + i) * p.q.token + h * p.q.head + 2 * t;
+#pragma unroll
+            for (int k = 0; k < KS; k++) {
+                qf[k][e] = live ? *reinterpret_cast<const uint32_t *>(q + 16 * k) : 0;
+                qf[k][2 + e] = live ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 8) : 0;
+            }
+        }
+        float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < D / 8; n++) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+        for (int i = 0; i < tiles; i++) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            copy(i + kStages - 1, pg);  // its stage was read in the last round
+            pages(i + kStages, pg);
+            const uint32_t st = ring + (i % kStages) * kStageBytes;
+            const int slot0 = (t0 + i * kWarps) * T;
+
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; n++) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            // matrices of an ldmatrix: (slots 0-7, d 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
+            const int kr = (lane & 7) + ((lane >> 4) << 3), kc = (lane >> 3) & 1;
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    const int r = kr + 8 * n, ch = 2 * k + kc;
+                    uint32_t f[4];
+                    ldsm4(f, st + r * (2 * D) + (((ch & ~7) | ((ch ^ r) & 7)) << 4));
+                    mma<BF>(s[n], qf[k], f[0], f[1]);
+                    mma<BF>(s[n + 1], qf[k], f[2], f[3]);
+                }
+            // visible slots, in powers of two
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < NT; n++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const int slot = slot0 + 8 * n + 2 * t + (e & 1), r = e >> 1;
+                    s[n][e] = slot >= beg[r] && slot < end[r] ? s[n][e] * c2 : -INFINITY;
+                    mx[r] = fmaxf(mx[r], s[n][e]);
+                }
+            if (LOGITS) {
+#pragma unroll
+                for (int r = 0; r < 2; r++)
+                    if (g + 8 * r < rows) {
+                        float *x = p.logits + ((int64_t)(b * p.c.kv_heads + hk) * p.logit_rows + g + 8 * r) * p.logit_stride;
+#pragma unroll
+                        for (int n = 0; n < NT; n++)
+                            if (slot0 + 8 * n < vis.hi)
+                                *reinterpret_cast<float2 *>(x + slot0 + 8 * n + 2 * t) = make_float2(s[n][2 * r], s[n][2 * r + 1]);
+                    }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
+                mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
+            }
+            if (__any_sync(~0u, mx[0] > m[0] + kSlack || mx[1] > m[1] + kSlack)) {
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const float n = fmaxf(m[r], mx[r]), a = m[r] == -INFINITY ? 0.f : ex2(m[r] - n);
+                    m[r] = n;
+                    l[r] *= a;
+#pragma unroll
+                    for (int k = 0; k < D / 8; k++) o[k][2 * r] *= a, o[k][2 * r + 1] *= a;
+                }
+            }
+            const float z[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+            uint32_t pf[KT][4];
+#pragma unroll
+            for (int n = 0; n < NT; n++) {
+                const float p0 = ex2(s[n][0] - z[0]), p1 = ex2(s[n][1] - z[0]);
+                const float p2 = ex2(s[n][2] - z[1]), p3 = ex2(s[n][3] - z[1]);
+                l[0] += p0 + p1;
+                l[1] += p2 + p3;
+                pf[n / 2][2 * (n & 1)] = from_f2<BF>(p0, p1);
+                pf[n / 2][2 * (n & 1) + 1] = from_f2<BF>(p2, p3);
+            }
+            // matrices: (slots 0-7, d 0-7), (slots 8-15, d 0-7), (0-7, 8-15), (8-15, 8-15)
+#pragma unroll
+            for (int k = 0; k < KT; k++)
+#pragma unroll
+                for (int n = 0; n < D / 8; n += 2) {
+                    const int r = 16 * k + (lane & 15), ch = n + (lane >> 4);
+                    uint32_t f[4];
+                    ldsm4t(f, st + kTileBytes + r * (2 * D) + (((ch & ~7) | ((ch ^ r) & 7)) << 4));
+                    mma<BF>(o[n], pf[k], f[0], f[1]);
+                    mma<BF>(o[n + 1], pf[k], f[2], f[3]);
+                }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        // ---- join the four warps: a common maximum, then the sums in warp order
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            l[r] += __shfl_xor_sync(~0u, l[r], 1);
+            l[r] += __shfl_xor_sync(~0u, l[r], 2);
+            if (t == 0) s_ml[warp][g + 8 * r][0] = m[r], s_ml[warp][g + 8 * r][1] = l[r];
+        }
+        __syncthreads();
+        constexpr int OS = D + 4;  // row stride of the exchanged rows (fp32), off the banks' period
+        float *mine = reinterpret_cast<float *>(sm + warp * kRingBytes);
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_ml[w][g + 8 * r][0]);
+            const float a = m[r] == -INFINITY ? 0.f : ex2(m[r] - M);
+#pragma unroll
+            for (int n = 0; n < D / 8; n++)
+                *reinterpret_cast<float2 *>(mine + (g + 8 * r) * OS + 8 * n + 2 * t) = make_float2(o[n][2 * r] * a, o[n][2 * r + 1] * a);
+        }
+        __syncthreads();
+        const bool whole = first == 0 && last == n_units;
+        constexpr int PER = kRows * D / kThreads;  // consecutive elements of one row a thread
+        const int row = tid / (D / PER), d0 = tid % (D / PER) * PER;
+        if (row < rows) {
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_ml[w][row][0]);
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) L += s_ml[w][row][0] == -INFINITY ? 0.f : s_ml[w][row][1] * ex2(s_ml[w][row][0] - M);
+            float x[PER];
+#pragma unroll
+            for (int e = 0; e < PER; e += 4) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) {
+                    const float4 y = *reinterpret_cast<const float4 *>(sm + w * kRingBytes + (row * OS + d0 + e) * 4);
+                    v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+                }
+                x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
+            }
+            if (whole) {
+                const int i = row / p.group, h = hk * p.group + row % p.group;
+                float lse2;
+                const float f = finish_row(M, L, p.sinks, h, lse2);
+                uint16_t *out = p.out.d + (int64_t)(sq.q0 + i) * p.out.token + h * p.out.head + d0;
+#pragma unroll
+                for (int e = 0; e < PER; e += 8)
+                    *reinterpret_cast<uint4 *>(out + e) =
+                        make_uint4(from_f2<BF>(x[e] * f, x[e + 1] * f), from_f2<BF>(x[e + 2] * f, x[e + 3] * f),
+                                   from_f2<BF>(x[e + 4] * f, x[e + 5] * f), from_f2<BF>(x[e + 6] * f, x[e + 7] * f));
+                if (d0 == 0) put_lse(p, sq.q0 + i, h, lse2);
+            } else {
+                const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+                float *po = p.part_o + ((int64_t)slot * kRows + row) * D + d0;
+#pragma unroll
+                for (int e = 0; e < PER; e += 4) *reinterpret_cast<float4 *>(po + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                if (d0 == 0) p.part_ml[slot * kRows + row] = make_float2(M, L);
+            }
+        }
+        __syncthreads();  // the rings are written again
+        // ---- the next item
+        u += last - first;
+        first = 0;
+        if (u < u1 && ++hk == p.c.kv_heads) {
+            hk = 0;
+            do {
+                sq = seq_info(p.bt, ++b, nullptr);
+                n_units = units_of<D>(sq, p, vis);
+            } while (n_units == 0);
+        }
+    }
+}
+
+// Joins the parts of an item that several CTAs covered, in unit order. One CTA an item.
+template <bool BF, int D>
+__global__ void __launch_bounds__(kThreads) step_combine(const AttendParams p, int grid) {
+    __shared__ long long s_warp[kWarps];
+    const int hk = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    long long before = 0, all = 0, total, less;
+    for (int i = tid; i < p.bt.batch; i += kThreads) {
+        Range r;
+        const int n = units_of<D>(seq_info(p.bt, i, nullptr), p, r);
+        all += n;
+        if (i < b) before += n;
+    }
+    block_scan<kThreads>(all, total, s_warp);
+    block_scan<kThreads>(before, less, s_warp);
+    const Seq sq = seq_info(p.bt, b, nullptr);
+    Range vis;
+    const int n_units = units_of<D>(sq, p, vis);
+    const long long W = total * p.c.kv_heads, s = less * p.c.kv_heads + (long long)hk * n_units;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: this grid ends after the one before it
+    if (n_units == 0) return;
+    const int C = used_ctas(grid, W), c0 = unit_owner(s, C, W), c1 = unit_owner(s + n_units - 1, C, W);
+    if (c0 == c1) return;
+    constexpr int PER = kRows * D / kThreads;
+    const int row = tid / (D / PER), d0 = tid % (D / PER) * PER;
+    if (row >= sq.q_len * p.group) return;
+    float M = -INFINITY, L = 0.f, x[PER];
+#pragma unroll
+    for (int e = 0; e < PER; e++) x[e] = 0.f;
+    for (int c = c0; c <= c1; c++) M = fmaxf(M, p.part_ml[(2 * c + (c == c0)) * kRows + row].x);
+    for (int c = c0; c <= c1; c++) {
+        const int slot = 2 * c + (c == c0);
+        const float2 ml = p.part_ml[slot * kRows + row];
+        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        L += ml.y * a;
+        const float *po = p.part_o + ((int64_t)slot * kRows + row) * D + d0;
+#pragma unroll
+        for (int e = 0; e < PER; e += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(po + e);
+            x[e] += v.x * a, x[e + 1] += v.y * a, x[e + 2] += v.z * a, x[e + 3] += v.w * a;
+        }
+    }
+    const int i = row / p.group, h = hk * p.group + row % p.group;
+    float lse2;
+    const float f = finish_row(M, L, p.sinks, h, lse2);
+    uint16_t *out = p.out.d + (int64_t)(sq.q0 + i) * p.out.token + h * p.out.head + d0;
+#pragma unroll
+    for (int e = 0; e < PER; e += 8)
+        *reinterpret_cast<uint4 *>(out + e) =
+            make_uint4(from_f2<BF>(x[e] * f, x[e + 1] * f), from_f2<BF>(x[e + 2] * f, x[e + 3] * f),
+                       from_f2<BF>(x[e + 4] * f, x[e + 5] * f), from_f2<BF>(x[e + 6] * f, x[e + 7] * f));
+    if (d0 == 0) put_lse(p, sq.q0 + i, h, lse2);
+}
+
+// mass += sum over rows of 2^(x - lse2), x the kept scores: one thread a slot, rows in order.
+__global__ void __launch_bounds__(256) step_mass(const AttendParams p) {
+    __shared__ float s_lse[kRows];
+    const int hk = blockIdx.y, b = blockIdx.z;
+    const Seq sq = seq_info(p.bt, b, nullptr);
+    const int rows = sq.q_len * p.group;
+    const Range vis = visible(sq, 0, sq.q_len, p.window, p.causal);
+    const int j0 = blockIdx.x * 1024;
+    if (rows == 0 || j0 >= vis.hi || j0 + 1024 <= vis.lo) return;
+    if (threadIdx.x < rows) {
+        const int i = threadIdx.x / p.group, h = hk * p.group + threadIdx.x % p.group;
+        s_lse[threadIdx.x] = p.lse2[(int64_t)(sq.q0 + i) * p.q_heads + h];
+    }
+    __syncthreads();
+    const int j = j0 + threadIdx.x * 4;
+    if (j >= vis.hi || j + 4 <= vis.lo) return;
+    const float *x = p.logits + (int64_t)(b * p.c.kv_heads + hk) * p.logit_rows * p.logit_stride + j;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < rows; r++) {
+        const float4 v = *reinterpret_cast<const float4 *>(x + r * p.logit_stride);
+        const float z = s_lse[r];
+        if (z == -INFINITY) continue;
+        s[0] += ex2(v.x - z), s[1] += ex2(v.y - z), s[2] += ex2(v.z - z), s[3] += ex2(v.w - z);
+    }
+    float *m = p.mass + b * p.mass_seq + hk * p.mass_head + j;
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        if (j + e >= vis.lo && j + e < vis.hi) m[e] += s[e];
+}
+
+template <bool BF, int D>
+cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
+    auto kern = p.logits ? step_kernel<BF, D, true> : step_kernel<BF, D, false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<C, kThreads, kSmem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(step_combine<BF, D>, dim3(p.c.kv_heads, p.bt.batch), kThreads, 0, st, p, C)) != cudaSuccess) return e;
+    if (p.mass && p.logits)
+        e = launch_plain(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
+    return e;
+}
+
+}  // namespace
+
+int step_ctas(const AttendParams &p, int num_sms) {
+    const int unit = kWarps * (p.c.dim == 64 ? kTile<64> : kTile<128>);
+    const long long most = (long long)p.bt.batch * p.c.kv_heads * ((p.bt.max_kv + unit - 1) / unit + 1);
+    return (int)(most < 2 * num_sms ? (most > 0 ? most : 1) : 2 * num_sms);
+}
+
+cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
+    const int C = step_ctas(p, num_sms);
+    if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, C, st) : launch<false, 64>(p, C, st);
+    return bf16 ? launch<true, 128>(p, C, st) : launch<false, 128>(p, C, st);
+}
+
+}  // namespace kv
+}  // namespace ftmoe
