@@ -1,8 +1,6 @@
-// Attention of new tokens over the paged cache, one warp a (token, query head) row: the running
-// maximum m and sum l of the softmax and the output row are carried over the visible slots, all
-// in fp32; with m' = max(m, s), l' = l exp(m - m') + exp(s - m') and the output likewise.
-// The mass pass takes one warp a (sequence, key head, slot) and adds exp(s - lse) over the rows
-// that see the slot, so each mass element has one writer and one order.
+// Which attention kernel a call runs, its workspace, and the mass pass of chunks: one warp a
+// (sequence, key head, slot) adds 2^(s - lse) over the rows that see the slot, so each mass element
+// has one writer and one order.
 #include "kv_attend.cuh"
 
 namespace ftmoe {
@@ -13,48 +11,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
     return v;
-}
-
-template <bool BF, int D>
-__global__ void __launch_bounds__(128) attend_rows(const AttendParams p, float *lse) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, h = blockIdx.y * 4 + (threadIdx.x >> 5), b = blockIdx.z, i = blockIdx.x;
-    const Seq s = seq_info(p.bt, b, p.c.status);
-    if (h >= p.q_heads || i >= s.q_len) return;
-    const int t = s.q0 + i, at = s.kv_len - s.q_len + i, hk = h / p.group;
-    const int end = at < 0 ? 0 : (p.causal ? at + 1 : s.kv_len);
-    const int begin = p.window && at - p.window + 1 > 0 ? at - p.window + 1 : 0;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; e++) q[e] = to_f<BF>(p.q.d[t * p.q.token + h * p.q.head + lane * E + e]), o[e] = 0.f;
-    for (int j = begin; j < end; j++) {
-        const int page = page_of(p.c, p.bt, b, j), row = j & ((1 << p.c.page_shift) - 1);
-        if (page < 0) continue;
-        float d = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; e++) d += q[e] * to_f<BF>(p.c.k[k_at(p.c, page, row, hk) + lane * E + e]);
-        const float x = warp_sum(d) * p.scale, n = fmaxf(m, x);
-        if (n == -INFINITY) continue;
-        const float a = expf(m - n), w = expf(x - n);
-        m = n;
-        l = l * a + w;
-#pragma unroll
-        for (int e = 0; e < E; e++) o[e] = o[e] * a + w * to_f<BF>(p.c.v[v_at(p.c, page, row, hk) + lane * E + e]);
-    }
-    if (p.sinks) {
-        const float x = p.sinks[h], n = fmaxf(m, x);
-        if (n != -INFINITY) {
-            const float a = expf(m - n);
-            l = l * a + expf(x - n);
-            m = n;
-#pragma unroll
-            for (int e = 0; e < E; e++) o[e] *= a;
-        }
-    }
-    const float r = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; e++) p.out.d[t * p.out.token + h * p.out.head + lane * E + e] = from_f<BF>(o[e] * r);
-    if (lane == 0 && lse) lse[(int64_t)t * p.q_heads + h] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 template <bool BF, int D>
@@ -81,16 +37,14 @@ __global__ void __launch_bounds__(128) mass_slots(const AttendParams p, const fl
 #pragma unroll
             for (int e = 0; e < E; e++) d += k[e] * to_f<BF>(p.q.d[t * p.q.token + h * p.q.head + lane * E + e]);
             const float z = lse[t * p.q_heads + h];
-            if (z != -INFINITY) sum += expf(warp_sum(d) * p.scale - z);
+            if (z != -INFINITY) sum += ex2(warp_sum(d) * p.scale * kLog2e - z);
         }
     if (lane == 0) p.mass[b * p.mass_seq + hk * p.mass_head + j] += sum;
 }
 
 template <bool BF, int D>
-cudaError_t launch(const AttendParams &p, cudaStream_t st) {
-    float *lse = p.lse ? p.lse : p.lse2;
-    attend_rows<BF, D><<<dim3(p.bt.max_q, (p.q_heads + 3) / 4, p.bt.batch), 128, 0, st>>>(p, lse);
-    if (p.mass) mass_slots<BF, D><<<dim3((p.bt.max_kv + 3) / 4, p.c.kv_heads, p.bt.batch), 128, 0, st>>>(p, lse);
+cudaError_t launch_mass(const AttendParams &p, cudaStream_t st) {
+    mass_slots<BF, D><<<dim3((p.bt.max_kv + 3) / 4, p.c.kv_heads, p.bt.batch), 128, 0, st>>>(p, p.lse2);
     return cudaGetLastError();
 }
 
@@ -111,6 +65,10 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
         const size_t slots = 2 * (size_t)step_ctas(p, num_sms);
         p.part_o = reinterpret_cast<float *>(take(slots * kStepRows * p.c.dim * 4));
         p.part_ml = reinterpret_cast<float2 *>(take(slots * kStepRows * 8));
+    } else {
+        const size_t rows = chunk_part_rows(p, num_sms);
+        p.part_o = reinterpret_cast<float *>(take(rows * p.c.dim * 4));
+        p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
     }
     if (p.mass) {
         p.lse2 = reinterpret_cast<float *>(take((size_t)p.bt.tokens * p.q_heads * 4));
@@ -125,8 +83,10 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
 
 cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
     if (is_step(p)) return launch_step(p, bf16, num_sms, st);
-    if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, st) : launch<false, 64>(p, st);
-    return bf16 ? launch<true, 128>(p, st) : launch<false, 128>(p, st);
+    cudaError_t e = launch_chunk(p, bf16, num_sms, st);
+    if (e != cudaSuccess || !p.mass) return e;
+    if (p.c.dim == 64) return bf16 ? launch_mass<true, 64>(p, st) : launch_mass<false, 64>(p, st);
+    return bf16 ? launch_mass<true, 128>(p, st) : launch_mass<false, 128>(p, st);
 }
 
 }  // namespace kv
