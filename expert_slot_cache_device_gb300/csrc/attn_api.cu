@@ -104,7 +104,10 @@ int attend_params(const ftmoe_kv_cache *kvc, const ftmoe_kv_batch *batch, int q_
         return fail(FTMOE_ERR_INVALID_ARG, "q_heads=%d: a multiple of kv_heads=%d", q_heads, p.c.kv_heads);
     if (window < 0) return fail(FTMOE_ERR_INVALID_ARG, "window=%d", window);
     if (window && !causal) return fail(FTMOE_ERR_INVALID_ARG, "a window needs causal attention");
+    if (q_heads / p.c.kv_heads > 128)
+        return fail(FTMOE_ERR_FORMAT, "%d query heads a key head: at most 128", q_heads / p.c.kv_heads);
     p.q_heads = q_heads, p.group = q_heads / p.c.kv_heads, p.window = window, p.causal = causal != 0;
+    p.item_tokens = 2 * (128 / p.group);
     return FTMOE_OK;
 }
 

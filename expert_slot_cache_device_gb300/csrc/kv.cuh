@@ -120,6 +120,7 @@ struct AttendParams {
     Batch bt;
     Rows q, out;
     int32_t q_heads, group, window, causal;
+    int32_t item_tokens;  // tokens of an item of the tiled kernels: two tiles of 128 / group
     float scale;
     const float *sinks;
     float *lse;   // [tokens, q_heads] (nullable)

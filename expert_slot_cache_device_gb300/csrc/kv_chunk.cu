@@ -5,17 +5,23 @@
 //
 // Persistent, one CTA an SM, work cut by kv_split.cuh in steps of 128 slots. Roles:
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread holds one row. S comes from tensor
-//                   memory; the row's maximum, P = 2^(s scale log2 e - m) in fp32, the row's sum; P
-//                   goes back as 16-bit pairs. O is rescaled (in tensor memory) only when the
-//                   maximum grew by more than 2^8; P and the sum share the stale maximum.
-//   warp 8          tensor copies of K and V tiles (a box a page and 64 elements, 128-byte swizzle)
-//                   into a ring of stages; pages outside the visible range are not touched.
-//   warp 9          issues tcgen05.mma: S_t = Q_t K^T (both from shared memory) and O_t += P_t V (P
-//                   from tensor memory, V with its elements consecutive). While the softmax of one
-//                   tile runs, the other tile's products do.
-//   warps 10, 11    copy Q of the next item as soon as the last S product has read the present
-//                   one, and zero the V rows of slots that no row sees in the tiles at the ends
-//                   of the visible range (what such slots hold must not reach 0 * V).
+//                   memory; P = 2^(s scale log2 e - m) in fp32 with the maximum m of the steps
+//                   before, so that the row's own maximum is off the path from S to P; P goes back
+//                   as 16-bit pairs, the first 64 slots as soon as they are formed. The maximum is
+//                   taken after that; one more than 2^8 above m raises m for the next step, which
+//                   first rescales O (in tensor memory). A half whose sum is too large for P's type (and
+//                   a row's first step) raises m at once. P, the sum and O always share one m.
+//   warp 8          tensor copies: K and V tiles (a box a page and 64 elements, 128-byte swizzle)
+//                   into a ring of stages, pages outside the visible range untouched; the
+//                   queries of the next item once the last S product has read the present ones.
+//   warp 9          issues tcgen05.mma, tile 0's and tile 1's in turn: O_t += P_t V (P from tensor
+//                   memory, V with its elements consecutive), S_t = Q_t K^T of the next step
+//                   (both from shared memory). While the softmax of one tile runs, the products of
+//                   the other do. (A warp for each tile fell into step and left no overlap.)
+//   warp 11         walks the work and hands the parts out through a small ring (done by each
+//                   role, a walk step cost 3000 to 5000 cycles of cold code between items); and zeroes
+//                   the V rows of slots that no row sees in the tiles at the ends of the visible
+//                   range (what such slots hold must not reach 0 * V).
 // Tensor memory: S_0, S_1 (128 columns each), O_0, O_1 (dim each). P_t lies over S_t for 128
 // elements a head: S_t of the next step is issued after the product that reads P_t, and products
 // of one shape run in order. For 64 the shapes differ, and P_0, P_1 have columns of their own.
@@ -27,8 +33,12 @@ namespace kv {
 namespace {
 
 constexpr int kWarps = 12, kThreads = kWarps * 32;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kHelpWarp = 10;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kHelpWarp = 11;
+constexpr int kParts = 4;  // entries of the ring of parts
 constexpr float kSlack = 8.f;
+// The largest sum of 64 P that is let through: P below it is finite in its type, sums in fp32.
+template <bool BF>
+constexpr float kMost = BF ? 18446744073709551616.f : 16384.f;
 constexpr int kMaxStages = 8;
 
 template <int D>
@@ -37,48 +47,72 @@ struct Shape {
     static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kHalf = kTileSlots * 128;            // 64 elements of 128 rows
     static constexpr int kQ = kTileRows * D * 2;
-    static constexpr int kSmem = 1024 + kStages * kStage + kQ;
+    static constexpr int kOut = 8 * 32 * 128;                 // a warp's 32 output rows, 64 elements at a time
+    static constexpr int kSmem = 1024 + kStages * kStage + kQ + kOut;
     static constexpr uint32_t kO = 256, kP = D == 128 ? 0 : 384;  // columns of O_0 and P_0
     static constexpr uint32_t kPStep = D == 128 ? 128 : 64;       // from P_0 to P_1
 };
 
+// A part of an item that this CTA works on, as the roles take it from the ring.
+struct Part {
+    int b, hk;
+    int token, left;        // first token row of the item; new tokens from there to the sequence's end
+    int slot, kv_len;       // the first token's slot
+    int lo, hi, seen_lo;    // Item
+    int first, last, tiles; // steps [first, last) of the item's tiles; tiles = 0: no more parts
+};
+
 struct Bars {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t qfull, qempty, s[2], p[2], o[2], clean, done;
+    uint64_t clean[kMaxStages];  // the stage's unseen V rows are zero (every use of a stage, K or V)
+    uint64_t qfull, qempty, s[2], p[2][2], half[2], o[2], done;
+    uint64_t part_full[kParts], part_empty[kParts];
 };
 
-// A part of an item that this CTA works on, and the walk from part to part. Every role walks on
-// its own.
-struct Part {
-    int b, hk, qt, first, last;  // steps [first, last) of the item
-    Item it;
-    Seq sq;
-};
-
+// The walk along the line of work.
 struct Walk {
     long long left;
-    int b, hk, qt, n_qt, first;
+    int b, hk, qt, n_qt, at;  // at: units into the item (its kItemCost first)
     Seq sq;
     __device__ __forceinline__ bool next(const AttendParams &p, Part &w) {
-        if (left <= 0) return false;
-        w.it = item_of(p, sq, qt);
-        w.b = b, w.hk = hk, w.qt = qt, w.sq = sq, w.first = first;
-        w.last = left < w.it.tiles - first ? first + (int)left : w.it.tiles;
-        left -= w.last - first;
-        first = 0;
-        if (left > 0 && ++qt == n_qt) {
-            qt = 0;
-            if (++hk == p.c.kv_heads) {
-                hk = 0;
-                do {
-                    sq = seq_info(p.bt, ++b, nullptr);
-                    n_qt = row_tiles(sq, p.group);
-                } while (n_qt == 0);
+        while (left > 0) {
+            const Item it = item_of(p, sq, qt);
+            const int n = it.tiles + kItemCost, end = left < n - at ? at + (int)left : n;
+            w.b = b, w.hk = hk;
+            w.token = sq.q0 + qt * p.item_tokens, w.left = sq.q_len - qt * p.item_tokens;
+            w.slot = sq.kv_len - sq.q_len + qt * p.item_tokens, w.kv_len = sq.kv_len;
+            w.lo = it.lo, w.hi = it.hi, w.seen_lo = it.seen_lo, w.tiles = it.tiles;
+            w.first = at > kItemCost ? at - kItemCost : 0, w.last = end - kItemCost;
+            left -= end - at;
+            at = 0;
+            if (left > 0 && ++qt == n_qt) {
+                qt = 0;
+                if (++hk == p.c.kv_heads) {
+                    hk = 0;
+                    do {
+                        sq = seq_info(p.bt, ++b, nullptr);
+                        n_qt = row_tiles(p, sq);
+                    } while (n_qt == 0);
+                }
             }
+            if (w.last > w.first) return true;
         }
-        return true;
+        w.tiles = 0;
+        return false;
     }
 };
+
+// Takes the next part; the whole warp calls. False at the end (or when the wait ran out: ok).
+__device__ __forceinline__ bool take(Bars &bar, const Part *ring, uint32_t &n, Part &w, bool &ok) {
+    const uint32_t e = n % kParts;
+    ok = warp_wait(&bar.part_full[e], (n / kParts) & 1);
+    if (!ok) return false;
+    w = ring[e];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(&bar.part_empty[e]);
+    n++;
+    return w.tiles > 0;
+}
 
 // Total steps and this CTA's start. s_sum: kThreads entries.
 __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *s_warp, int *s_sum, Walk *s_walk) {
@@ -89,7 +123,7 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
             int n = 0;
             if (b0 + i < p.bt.batch) {
                 const Seq s = seq_info(p.bt, b0 + i, blockIdx.x == 0 && lane == 0 ? p.c.status : nullptr);
-                n = seq_tiles(p, s, row_tiles(s, p.group));
+                n = seq_units(p, s, row_tiles(p, s));
             }
             if (lane == 0) s_sum[i] = n;
             if (b0 + i >= p.bt.batch) break;
@@ -110,7 +144,7 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
             for (int i = warp; i < kThreads; i += kWarps) {
                 if (b0 + i >= p.bt.batch) break;
                 const Seq s = seq_info(p.bt, b0 + i, nullptr);
-                const int n = seq_tiles(p, s, row_tiles(s, p.group));
+                const int n = seq_units(p, s, row_tiles(p, s));
                 if (lane == 0) s_sum[i] = n;
             }
             __syncthreads();
@@ -128,12 +162,12 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
     if (warp == 0) {
         const int b = s_walk->b;
         const Seq s = seq_info(p.bt, b, nullptr);
-        const int n_qt = row_tiles(s, p.group), per = seq_tiles(p, s, n_qt);
+        const int n_qt = row_tiles(p, s), per = seq_units(p, s, n_qt);
         long long at = s_walk->left;
         const int hk = (int)(at / per);
         int rem = (int)(at % per), found = -1, first = 0, before = 0;
         for (int q0 = 0; q0 < n_qt && found < 0; q0 += 32) {
-            const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles : 0;
+            const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles + kItemCost : 0;
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -150,7 +184,7 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
         }
         __syncwarp();
         if (lane == 0) {
-            s_walk->hk = hk, s_walk->qt = found, s_walk->n_qt = n_qt, s_walk->first = first, s_walk->sq = s;
+            s_walk->hk = hk, s_walk->qt = found, s_walk->n_qt = n_qt, s_walk->at = first, s_walk->sq = s;
             s_walk->left = u1 - u0;
         }
     }
@@ -159,18 +193,34 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
     return true;
 }
 
+// O *= a, a row's D columns of tensor memory. The whole warp calls.
+template <int D>
+__device__ __forceinline__ void rescale_o(uint32_t tO, float a) {
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+        uint32_t y[32];
+        tm_ld32(tO + k, y);
+#pragma unroll
+        for (int e = 0; e < 32; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+        tm_st32(tO + k, y);
+    }
+    tm_st_wait();
+}
+
 template <bool BF, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    chunk_kernel(const AttendParams p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    chunk_kernel(const AttendParams p, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                 const __grid_constant__ CUtensorMap vmap) {
     using S = Shape<D>;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
     __shared__ uint32_t s_tmem;
     __shared__ long long s_warp[kWarps];
-    __shared__ int s_sum[kThreads];
+    int *s_sum = reinterpret_cast<int *>(sm_raw);  // the ring is not in use yet
     __shared__ Walk s_walk;
+    __shared__ Part s_part[kParts];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t ring = (su32(sm_raw) + 1023u) & ~1023u, qs = ring + S::kStages * S::kStage;
+    const uint32_t ring = (su32(sm_raw) + 1023u) & ~1023u, qs = ring + S::kStages * S::kStage, stage_out = qs + S::kQ;
 
     Walk walk;
     const bool any = plan(p, walk, s_warp, s_sum, &s_walk);
@@ -178,9 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!any) return;
 
     if (tid == 0) {
-        for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1);
-        bar_init(&bar.qfull, 64), bar_init(&bar.qempty, 1), bar_init(&bar.clean, 64), bar_init(&bar.done, 1);
-        for (int t = 0; t < 2; t++) bar_init(&bar.s[t], 1), bar_init(&bar.p[t], 4), bar_init(&bar.o[t], 1);
+        for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1), bar_init(&bar.clean[i], 1);
+        for (int i = 0; i < kParts; i++) bar_init(&bar.part_full[i], 1), bar_init(&bar.part_empty[i], 10);  // softmax, copies, products
+        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.done, 1);
+        for (int t = 0; t < 2; t++) {
+            bar_init(&bar.s[t], 1), bar_init(&bar.p[t][0], 4), bar_init(&bar.p[t][1], 4);
+            bar_init(&bar.o[t], 1), bar_init(&bar.half[t], 1);
+        }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -193,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(&s_tmem);
     bool ok = true;
     Part w;
+    uint32_t n_part = 0;
 
     // registers: 384 threads x 168 at launch = 256 x 208 + 128 x 88
     if (warp < 8) {  // ---------------------------------------------------- softmax
@@ -201,18 +256,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tS = tm + lanes + 128 * t, tO = tm + lanes + S::kO + D * t, tP = tm + lanes + S::kP + S::kPStep * t;
         const float c2 = p.scale * kLog2e;
+        // this thread's row of the tile: token and query head
+        const int row_l = (tid & 127) / (uint32_t)p.group, row_g = (tid & 127) - row_l * p.group;
+        const int row_i = t * (p.item_tokens >> 1) + row_l;
+        const bool row_used = row_l < (p.item_tokens >> 1);
         uint32_t ns = 0, no = 0;
-        while (ok && walk.next(p, w)) {
-            const int64_t rows = (int64_t)w.sq.q_len * p.group;
-            const int64_t r = (int64_t)w.qt * kTileRows + tid;  // tid: 128 t + row of the tile
-            if (rows - (int64_t)w.qt * kTileRows <= 128 * t) continue;  // the second tile has no rows
-            const bool live = r < rows;
-            const int i = live ? (int)(r / p.group) : 0, h = w.hk * p.group + (live ? (int)(r % p.group) : 0);
-            const Range v = visible(w.sq, i, i + 1, p.window, p.causal);
-            const int beg = live ? v.lo : 0, end = live ? v.hi : 0;
-            float m = -INFINITY, l = 0.f;
+        while (take(bar, s_part, n_part, w, ok)) {
+            if (w.left <= t * (p.item_tokens >> 1)) continue;  // the second tile has no rows
+            const bool live = row_used && row_i < w.left;
+            const int h = w.hk * p.group + row_g, at = w.slot + row_i;
+            const int end = !live || at < 0 ? 0 : (p.causal ? at + 1 : w.kv_len);
+            const int beg = live && p.window && at >= p.window ? at - p.window + 1 : 0;
+            float m = live ? -INFINITY : 0.f, l = 0.f, up = 1.f;  // rows that are none stay at P = 0
+            bool raise = false;  // O is to be multiplied by up
             for (int j = w.first; j < w.last && ok; j++, ns++) {
-                const int s0 = w.it.lo + j * kTileSlots;
+                const int s0 = w.lo + j * kTileSlots;
                 if (!warp_wait(&bar.s[t], ns & 1)) {
                     ok = false;
                     break;
@@ -220,54 +278,94 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_after();
                 uint32_t x[128];
                 tm_ld64(tS, x);
-                tm_ld64(tS + 64, x + 64);
-                if (__any_sync(~0u, beg > s0 || end < s0 + kTileSlots)) {
-                    const int a = beg - s0, e = end - s0;
-#pragma unroll
-                    for (int k = 0; k < 128; k++)
-                        if (k < a || k >= e) x[k] = 0xff800000u;
+                tm_ld_wait(x);
+                tm_ld64(tS + 64, x + 64);  // in flight while the first half of P is formed
+                if (raise) {               // O's last product ended before this step's S did
+                    rescale_o<D>(tO, up);
+                    raise = false;
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const bool cut = __any_sync(~0u, beg > s0 || end < s0 + kTileSlots);
+                // slots that the row does not see, in the groups of 32 that some row of the warp does not see whole
+                auto hide = [&](int q) {
 #pragma unroll
-                for (int k = 0; k < 128; k++) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(x[k]));
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-                if (__any_sync(~0u, top > m + kSlack)) {
+                    for (int g = 64 * q; g < 64 * q + 64; g += 32) {
+                        const int a = beg - s0 - g, e = end - s0 - g;
+                        if (__any_sync(~0u, a > 0 || e < 32)) {
+#pragma unroll
+                            for (int k = 0; k < 32; k++)
+                                if (k < a || k >= e) x[g + k] = 0xff800000u;
+                        }
+                    }
+                };
+                const uint64_t cc = pack2(c2, c2);
+                // P of 64 slots, and their sum
+                auto form = [&](int q) {
+                    const float z = m == -INFINITY ? 0.f : -m;
+                    const uint64_t zz = pack2(z, z);
+                    uint64_t sum[2] = {0, 0};
+#pragma unroll
+                    for (int c = 2 * q; c < 2 * q + 2; c++) {
+                        uint32_t y[16];
+#pragma unroll
+                        for (int k = 0; k < 16; k++) {
+                            const int e = 32 * c + 2 * k;
+                            const float2 f = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, zz));
+                            const float a = ex2(f.x), b = ex2(f.y);
+                            sum[k & 1] = add2(sum[k & 1], pack2(a, b));
+                            y[k] = from_f2<BF>(a, b);
+                        }
+                        tm_st16(tP + 16 * c, y);
+                    }
+                    const float2 f = unpack2(add2(sum[0], sum[1]));
+                    return f.x + f.y;
+                };
+                auto announce = [&](int q) {
+                    tm_st_wait();
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&bar.p[t][q]);
+                };
+                auto top_of = [&] {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 128; k += 2)
+                        mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+                };
+                // m to at least the row's maximum; returns the factor of what was summed before
+                auto raised = [&](float top) {
                     const float n = fmaxf(m, top), a = m == -INFINITY ? 0.f : ex2(m - n);
                     m = n;
                     l *= a;
-                    if (j > w.first) {  // O's last product ended before this step's S did
-#pragma unroll
-                        for (int k = 0; k < D; k += 32) {
-                            uint32_t y[32];
-                            tm_ld32(tO + k, y);
-#pragma unroll
-                            for (int e = 0; e < 32; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
-                            tm_st32(tO + k, y);
-                        }
-                    }
+                    return a;
+                };
+                if (cut) hide(0);
+                const bool fresh = __any_sync(~0u, m == -INFINITY);
+                float part;
+                if (!fresh) part = form(0);
+                tm_ld_wait(x + 64);
+                if (cut) hide(1);
+                if (fresh || __any_sync(~0u, part > kMost<BF>)) {
+                    const float a = raised(top_of());
+                    if (j > w.first) rescale_o<D>(tO, a);
+                    part = form(0);
                 }
-                const float z = m == -INFINITY ? 0.f : -m;
-                const uint64_t cc = pack2(c2, c2), zz = pack2(z, z);
-                uint64_t sum[2] = {0, 0};
-#pragma unroll
-                for (int q = 0; q < 2; q++) {
-                    uint32_t y[32];
-#pragma unroll
-                    for (int k = 0; k < 32; k++) {
-                        const int e = 64 * q + 2 * k;
-                        const float2 f = unpack2(fma2(pack2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), cc, zz));
-                        const float a = ex2(f.x), b = ex2(f.y);
-                        sum[k & 1] = add2(sum[k & 1], pack2(a, b));
-                        y[k] = from_f2<BF>(a, b);
-                    }
-                    tm_st32(tP + 32 * q, y);
+                announce(0);
+                l += part;
+                part = form(1);
+                if (__any_sync(~0u, part > kMost<BF>)) {  // the first half's product has m as it was
+                    if (!warp_wait(&bar.half[t], ns & 1)) ok = false;
+                    fence_after();
+                    rescale_o<D>(tO, raised(top_of()));
+                    part = form(1);
                 }
-                const float2 f = unpack2(add2(sum[0], sum[1]));
-                l += f.x + f.y;
-                tm_st_wait();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&bar.p[t]);
+                announce(1);
+                l += part;
+                const float top = top_of();
+                if (__any_sync(~0u, top > m + kSlack)) {
+                    up = raised(top);
+                    raise = true;
+                }
             }
             if (!ok) break;
             if (!warp_wait(&bar.o[t], no & 1)) {
@@ -276,39 +374,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             no++;
             fence_after();
-            const bool whole = w.first == 0 && w.last == w.it.tiles;
-            const int64_t token = w.sq.q0 + i;
+            const bool whole = w.first == 0 && w.last == w.tiles;
+            const int64_t token = w.token + row_i;
             const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
-            float f = 1.f, lse2 = 0.f;
-            if (whole && live) f = finish_row(m, l, p.sinks, h, lse2);
-            uint16_t *out = p.out.d + token * p.out.token + h * p.out.head;
-            float *po = p.part_o + ((int64_t)part * kTileRows + tid) * D;
+            float f = raise ? up : 1.f, lse2 = 0.f;
+            if (whole) {
+                f *= finish_row(m, l, p.sinks, h, lse2);
+                // 64 elements of the warp's rows at a time through shared memory, 16-byte chunk c of row r at
+                // c ^ (r % 8), so that eight lanes write a row's 128 bytes together
+                const uint32_t st = stage_out + warp * 4096;
 #pragma unroll
-            for (int k = 0; k < D; k += 32) {
-                uint32_t y[32];
-                tm_ld32(tO + k, y);
-                if (live) {
+                for (int k = 0; k < D; k += 64) {
+                    uint32_t y[64];
+                    tm_ld64(tO + k, y);
+                    tm_ld_wait(y);
+                    __syncwarp();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        float z[8];
+                    for (int c = 0; c < 8; c++) {
+                        uint32_t z[4];
 #pragma unroll
-                        for (int q = 0; q < 8; q++) z[q] = __uint_as_float(y[e + q]) * f;
-                        if (whole) {
-                            *reinterpret_cast<uint4 *>(out + k + e) = make_uint4(from_f2<BF>(z[0], z[1]), from_f2<BF>(z[2], z[3]),
-                                                                                 from_f2<BF>(z[4], z[5]), from_f2<BF>(z[6], z[7]));
-                        } else {
-                            *reinterpret_cast<float4 *>(po + k + e) = make_float4(z[0], z[1], z[2], z[3]);
-                            *reinterpret_cast<float4 *>(po + k + e + 4) = make_float4(z[4], z[5], z[6], z[7]);
-                        }
+                        for (int e = 0; e < 4; e++)
+                            z[e] = from_f2<BF>(__uint_as_float(y[8 * c + 2 * e]) * f, __uint_as_float(y[8 * c + 2 * e + 1]) * f);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(z[0]),
+                                     "r"(z[1]), "r"(z[2]), "r"(z[3])
+                                     : "memory");
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; c++) {
+                        const int r = 4 * c + (lane >> 3), row = 32 * (warp & 3) + r;
+                        const int i = row / (uint32_t)p.group, g = row - i * p.group, per = p.item_tokens >> 1;
+                        uint4 z;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
+                                     : "r"(st + r * 128 + (((lane ^ r) & 7) << 4))
+                                     : "memory");
+                        if (i < per && t * per + i < w.left)
+                            *reinterpret_cast<uint4 *>(p.out.d + (int64_t)(w.token + t * per + i) * p.out.token +
+                                                       (w.hk * p.group + g) * p.out.head + k + 8 * (lane & 7)) = z;
                     }
                 }
-                __syncwarp();
-            }
-            if (live) {
-                if (whole)
-                    put_lse(p, token, h, lse2);
-                else
-                    p.part_ml[part * kTileRows + tid] = make_float2(m, l);
+                if (live) put_lse(p, token, h, lse2);
+            } else {
+                // parts are kept element by element, rows consecutive: a warp's store is one line
+                float *po = p.part_o + (int64_t)part * kTileRows * D + tid;
+#pragma unroll
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t y[32];
+                    tm_ld32(tO + k, y);
+#pragma unroll
+                    for (int e = 0; e < 32; e++) po[(k + e) * kTileRows] = __uint_as_float(y[e]) * f;
+                }
+                p.part_ml[part * kTileRows + tid] = make_float2(m, l);
             }
             fence_before();  // O is read before the next item's first P is announced
         }
@@ -318,13 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kCopyWarp) {  // -------------------------------------------- K and V
         const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTileSlots / box, halves = D / 64;
         const int mine = lane % boxes, half = lane / boxes;  // one box a lane (8 pages x 2 halves at most)
-        uint32_t cnt = 0;
-        while (ok && walk.next(p, w)) {
+        uint32_t cnt = 0, nq = 0;
+        while (ok && take(bar, s_part, n_part, w, ok)) {
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
             for (int j = w.first; j < w.last && ok; j++) {
-                const int slot = w.it.lo + j * kTileSlots + mine * box;
+                const int slot = w.lo + j * kTileSlots + mine * box;
                 int page = -1;
-                if (half < halves && slot < w.it.hi && slot + box > w.it.seen_lo) {
+                if (half < halves && slot < w.hi && slot + box > w.seen_lo) {
                     page = tab[slot >> p.c.page_shift];
                     if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
                         flag(p.c.status, FTMOE_ERR_ID_RANGE);
@@ -334,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * box * 128;
                 const int row = slot & ((1 << p.c.page_shift) - 1);
 #pragma unroll
-                for (int kv = 0; kv < 2; kv++, cnt++) {
+                for (int kv = 0; kv < 2; kv++) {
                     const int st = cnt % S::kStages;
                     if (!warp_wait(&bar.empty[st], ((cnt / S::kStages) & 1) ^ 1)) {
                         ok = false;
@@ -345,115 +462,153 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (page >= 0)
                         tma4(ring + st * S::kStage + half * S::kHalf + mine * box * 128, kv ? &vmap : &kmap, 64 * half, row, w.hk, page,
                              &bar.full[st]);
-                }
-            }
-        }
-        if (!ok)  // wait (bounded) until the copies already issued have landed
-            for (uint32_t c = cnt < S::kStages ? 0 : cnt - S::kStages; c < cnt; c++) wait_bar(&bar.full[c % S::kStages], (c / S::kStages) & 1);
-    } else if (warp == kMmaWarp) {  // -------------------------------------- products
-        if (lane == 0) {
-            constexpr uint32_t IS = kInstr<BF, kTileSlots, false>, IO = kInstr<BF, D, true>;
-            uint32_t cnt = 0, np[2] = {0, 0}, ni = 0, nc = 0;
-            auto scores = [&](int t, uint32_t st) {
-#pragma unroll
-                for (int k = 0; k < D / 16; k++) {
-                    const uint32_t off = (k >> 2) * S::kHalf + (k & 3) * 32;
-                    mma_ss<IS>(tm + 128 * t, desc128(qs + t * (128 * D * 2) + off, 16), desc128(ring + st * S::kStage + off, 16), k > 0);
-                }
-                commit(&bar.s[t]);
-            };
-            while (ok && walk.next(p, w)) {
-                const int n = w.last - w.first;
-                const int tiles = (int64_t)w.sq.q_len * p.group - (int64_t)w.qt * kTileRows > 128 ? 2 : 1;
-                if (!wait_bar(&bar.qfull, ni & 1)) ok = false;
-                ni++;
-                if (ok && !wait_bar(&bar.full[cnt % S::kStages], (cnt / S::kStages) & 1)) ok = false;
-                if (!ok) break;
-                fence_after();
-                for (int t = 0; t < tiles; t++) scores(t, cnt % S::kStages);
-                commit(&bar.empty[cnt % S::kStages]);
-                if (n == 1) commit(&bar.qempty);
-                cnt++;
-                for (int j = 0; j < n && ok; j++) {
-                    const uint32_t sv = cnt % S::kStages, pv = (cnt / S::kStages) & 1;
-                    const uint32_t sk = (cnt + 1) % S::kStages, pk = ((cnt + 1) / S::kStages) & 1;
-                    const int s0 = w.it.lo + (w.first + j) * kTileSlots;
-                    ok = wait_bar(&bar.full[sv], pv);
-                    if (ok && (s0 < w.it.seen_lo || s0 + kTileSlots > w.it.hi)) ok = wait_bar(&bar.clean, nc++ & 1);
-                    for (int t = 0; t < tiles && ok; t++) {
-                        ok = wait_bar(&bar.p[t], np[t]++ & 1);
-                        if (!ok) break;
-                        fence_after();
-#pragma unroll
-                        for (int k = 0; k < kTileSlots / 16; k++)
-                            mma_ts<IO>(tm + S::kO + D * t, tm + S::kP + S::kPStep * t + 8 * k,
-                                       desc128(ring + sv * S::kStage + k * 2048, S::kHalf), j > 0 || k > 0);
-                        if (j + 1 < n) {
-                            if (t == 0) ok = wait_bar(&bar.full[sk], pk);
-                            if (!ok) break;
-                            fence_after();
-                            scores(t, sk);
-                        } else {
-                            commit(&bar.o[t]);
-                        }
-                    }
-                    if (!ok) break;
-                    commit(&bar.empty[sv]);
                     cnt++;
-                    if (j + 1 < n) {
-                        commit(&bar.empty[sk]);
-                        cnt++;
-                        if (j + 2 == n) commit(&bar.qempty);
+                    if (kv == 0 && j == w.first) {  // the item's queries, after its first K
+                        if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        nq++;
+                        if (lane == 0) {
+                            const int per = p.item_tokens >> 1, tiles = w.left > per ? 2 : 1;
+                            bar_expect(&bar.qfull, tiles * (D / 64) * per * p.group * 128);
+                            for (int t = 0; t < tiles; t++)
+                                for (int e = 0; e < D / 64; e++)
+                                    tma3(qs + t * (128 * D * 2) + e * S::kHalf, &qmap, 64 * e, w.hk * p.group, w.token + t * per, &bar.qfull);
+                        }
+                        __syncwarp();
                     }
                 }
             }
-            commit(&bar.done);  // every product is done when this arrives
-            wait_bar(&bar.done, 0);
         }
-        __syncwarp();
-    } else if (warp >= kHelpWarp) {  // ------------------------------------- queries, ends of V
-        const int half = warp - kHelpWarp;
-        constexpr int CH = D / 8, RPI = 32 / CH;
-        uint32_t cnt = 0, nq = 0;
-        while (ok && walk.next(p, w)) {
-            if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
-                ok = false;
-                break;
+        if (!ok) {  // wait (bounded) until the copies already issued have landed
+            for (uint32_t c = cnt < S::kStages ? 0 : cnt - S::kStages; c < cnt; c++) wait_bar(&bar.full[c % S::kStages], (c / S::kStages) & 1);
+            if (nq > 0) wait_bar(&bar.qfull, (nq - 1) & 1);
+        }
+    } else if (warp == kMmaWarp) {  // -------------------------------------- products
+        constexpr uint32_t IS = kInstr<BF, kTileSlots, false>, IO = kInstr<BF, D, true>;
+        const uint32_t one = elect_one();
+        const uint32_t qd = desc_lo(qs, 16), kd = desc_lo(ring, 16), vd = desc_lo(ring, S::kHalf);
+        uint32_t st = 0, ph = 0, np = 0, ni = 0;  // the stage in turn and its phase; bit t of np: the phase of tile t's P
+        auto next_stage = [&] {
+            if (++st == S::kStages) st = 0, ph ^= 1;
+        };
+        auto scores = [&](int t, uint32_t sk) {
+            const uint32_t a = qd + t * (128 * D * 2 / 16), b = kd + sk * (S::kStage / 16);
+#pragma unroll
+            for (int k = 0; k < D / 16; k++) {
+                const uint32_t off = ((k >> 2) * S::kHalf + (k & 3) * 32) / 16;
+                mma_ss<IS>(one, tm + 128 * t, a + off, b + off, k > 0);
             }
-            nq++;
-            const int64_t rows = (int64_t)w.sq.q_len * p.group, r0 = (int64_t)w.qt * kTileRows;
-            const int ch = lane % CH;
-            for (int n = 0; n < 128; n += RPI) {  // half h copies tile h
-                const int row = n + lane / CH;
-                const int64_t r = r0 + 128 * half + row;
-                const bool live = r < rows;
-                const int64_t i = live ? r / p.group : 0;
-                const int h = w.hk * p.group + (live ? (int)(r % p.group) : 0);
-                const uint16_t *src = p.q.d + (w.sq.q0 + i) * p.q.token + h * p.q.head + 8 * ch;
-                const uint32_t dst = qs + half * (128 * D * 2) + (ch >> 3) * S::kHalf + row * 128 + (((ch ^ row) & 7) << 4);
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+            commit(one, &bar.s[t]);
+        };
+        auto values = [&](int t, uint32_t sv, uint32_t acc) {
+            const uint32_t v = vd + sv * (S::kStage / 16);
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                ok = ok && warp_wait(&bar.p[t][q], (np >> t) & 1);
+                fence_after();
+                if (ok) {
+#pragma unroll
+                    for (int k = 4 * q; k < 4 * q + 4; k++)
+                        mma_ts<IO>(one, tm + S::kO + D * t, tm + S::kP + S::kPStep * t + 8 * k, v + k * (2048 / 16), k > 0 ? 1u : acc);
+                    if (q == 0) commit(one, &bar.half[t]);
+                }
             }
-            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-            fence_async();
-            bar_arrive(&bar.qfull);
-            for (int j = w.first; j < w.last && ok; j++, cnt += 2) {
-                const int s0 = w.it.lo + j * kTileSlots;
-                if (s0 >= w.it.seen_lo && s0 + kTileSlots <= w.it.hi) continue;
-                const uint32_t st = (cnt + 1) % S::kStages;
-                if (!warp_wait(&bar.full[st], ((cnt + 1) / S::kStages) & 1)) {
+            np ^= 1 << t;
+        };
+        while (ok && take(bar, s_part, n_part, w, ok)) {
+            // uniform values keep the loop's addresses in uniform registers
+            const int n = __shfl_sync(~0u, w.last - w.first, 0), two = __shfl_sync(~0u, w.left > (p.item_tokens >> 1) ? 1 : 0, 0);
+            const int s0 = __shfl_sync(~0u, w.lo + w.first * kTileSlots, 0), lo = __shfl_sync(~0u, w.seen_lo, 0), hi = __shfl_sync(~0u, w.hi, 0);
+            ok = warp_wait(&bar.qfull, ni++ & 1) && warp_wait(&bar.full[st], ph);
+            if (!ok) break;
+            fence_after();
+            scores(0, st);
+            if (two) scores(1, st);
+            commit(one, &bar.empty[st]);
+            if (n == 1) commit(one, &bar.qempty);
+            next_stage();
+#pragma unroll 1
+            for (int j = 0; j < n && ok; j++) {  // O_t += P_t V_j, S_t = Q_t K_{j+1}
+                const uint32_t sv = st, pv = ph;
+                ok = warp_wait(&bar.full[sv], pv);
+                if (s0 + j * kTileSlots < lo || s0 + (j + 1) * kTileSlots > hi) ok = ok && warp_wait(&bar.clean[sv], pv);
+                next_stage();
+                if (j + 1 < n) {
+                    ok = ok && warp_wait(&bar.full[st], ph);
+                    values(0, sv, j > 0);
+                    if (ok) scores(0, st);
+                    if (two) {
+                        values(1, sv, j > 0);
+                        commit(one, &bar.empty[sv]);
+                        if (ok) scores(1, st);
+                    } else {
+                        commit(one, &bar.empty[sv]);
+                    }
+                    commit(one, &bar.empty[st]);
+                    if (j + 2 == n) commit(one, &bar.qempty);
+                    next_stage();
+                } else {
+                    values(0, sv, j > 0);
+                    commit(one, &bar.o[0]);
+                    if (two) {
+                        values(1, sv, j > 0);
+                        commit(one, &bar.o[1]);
+                    }
+                    commit(one, &bar.empty[sv]);
+                }
+            }
+        }
+        commit(one, &bar.done);  // every product is done when this arrives
+        warp_wait(&bar.done, 0);
+    } else if (warp == kHelpWarp) {  // ------------------------------------------ parts, ends of V
+        constexpr int CH = D / 8;
+        uint32_t cnt = 0, put = 0;
+        bool more = true;
+        auto hand_out = [&] {
+            if (!more) return;
+            if (put >= kParts && !warp_wait(&bar.part_empty[put % kParts], (put / kParts - 1) & 1)) {
+                ok = more = false;
+                return;
+            }
+            Part n;
+            more = walk.next(p, n);
+            __syncwarp();
+            if (lane == 0) {
+                s_part[put % kParts] = n;
+                bar_arrive(&bar.part_full[put % kParts]);
+            }
+            __syncwarp();
+            put++;
+        };
+        for (int i = 0; i < kParts - 1; i++) hand_out();
+        for (uint32_t n = 0; ok; n++) {
+            w = s_part[n % kParts];  // handed out by this warp and not yet overwritten
+            if (w.tiles == 0) break;
+            for (int j = 2 * w.first; j < 2 * w.last; j++, cnt++) {  // K and V of each step
+                const uint32_t st = cnt % S::kStages;
+                if (!warp_wait(&bar.full[st], (cnt / S::kStages) & 1)) {
                     ok = false;
                     break;
                 }
-                for (int c = half * 32 + lane; c < kTileSlots * CH; c += 64) {
-                    const int row = c / CH, k = c % CH;
-                    if (s0 + row < w.it.seen_lo || s0 + row >= w.it.hi)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + st * S::kStage + (k >> 3) * S::kHalf + row * 128 + ((k & 7) << 4)),
+                const int s0 = w.lo + (j >> 1) * kTileSlots;
+                if ((j & 1) && (s0 < w.seen_lo || s0 + kTileSlots > w.hi)) {
+                    const int r0 = w.seen_lo - s0, r1 = w.hi - s0 > 0 ? w.hi - s0 : 0;
+                    const uint32_t at = ring + st * S::kStage;
+                    auto zero = [&](int c) {
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + ((c % CH) >> 3) * S::kHalf + (c / CH) * 128 + ((c & 7) << 4)),
                                      "r"(0)
                                      : "memory");
+                    };
+                    for (int c = lane; c < r0 * CH; c += 32) zero(c);
+                    for (int c = r1 * CH + lane; c < kTileSlots * CH; c += 32) zero(c);
+                    fence_async();
+                    __syncwarp();
                 }
-                fence_async();
-                bar_arrive(&bar.clean);
+                if (lane == 0) bar_arrive(&bar.clean[st]);
             }
+            hand_out();
         }
     }
     if (!ok && lane == 0) flag(p.c.status, FTMOE_ERR_STATE);
@@ -463,22 +618,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-// Joins the parts of an item that several CTAs covered, in order. One CTA takes 32 rows of an item, a
-// warp four of them.
+// Joins the parts of an item that several CTAs covered, in order. One CTA takes 32 rows of an item,
+// its eight warps an eighth of the elements each, a lane a row; rows go out through shared memory.
 constexpr int kJoinThreads = 256, kJoinRows = 32;
 
 template <bool BF, int D>
 __global__ void __launch_bounds__(kJoinThreads) chunk_combine(const AttendParams p, int grid) {
+    constexpr int E = D / 8;  // elements a thread
     __shared__ long long s_warp[kJoinThreads / 32];
+    __shared__ __align__(16) uint16_t s_out[kJoinRows][D + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int qt = blockIdx.x / (kTileRows / kJoinRows), sub = blockIdx.x % (kTileRows / kJoinRows);
     const int hk = blockIdx.y, b = blockIdx.z;
     const Seq sq = seq_info(p.bt, b, nullptr);
-    const int n_qt = row_tiles(sq, p.group);
+    const int n_qt = row_tiles(p, sq);
     long long all = 0, less = 0, total, before;
     for (int i = warp; i < p.bt.batch; i += kJoinThreads / 32) {
         const Seq s = seq_info(p.bt, i, nullptr);
-        const int n = seq_tiles(p, s, row_tiles(s, p.group));
+        const int n = seq_units(p, s, row_tiles(p, s));
         all += n;
         if (i < b) less += n;
     }
@@ -486,54 +643,56 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_combine(const AttendParams
     block_scan<kJoinThreads>(lane == 0 ? less : 0, before, s_warp);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: this grid ends after the one before it
     if (qt >= n_qt) return;
-    const int per = seq_tiles(p, sq, n_qt), ahead = seq_tiles(p, sq, qt), n = item_of(p, sq, qt).tiles;
+    const int per = seq_units(p, sq, n_qt), n = item_of(p, sq, qt).tiles;
+    const int ahead = seq_units(p, sq, qt) + kItemCost;
     const long long W = total * p.c.kv_heads, u = before * p.c.kv_heads + (long long)hk * per + ahead;
     const int C = used_ctas(grid, W), c0 = unit_owner(u, C, W), c1 = unit_owner(u + n - 1, C, W);
     if (c0 == c1) return;
-    constexpr int E = D / 32;
-    for (int k = 0; k < kJoinRows / 8; k++) {
-        const int row = sub * kJoinRows + 8 * k + warp;
-        const int64_t r = (int64_t)qt * kTileRows + row;
-        if (r >= (int64_t)sq.q_len * p.group) break;
-        float M = -INFINITY, L = 0.f, x[E];
+    const int row = sub * kJoinRows + lane, half = p.item_tokens >> 1;
+    const int li = (row & 127) / (uint32_t)p.group, g = (row & 127) - li * p.group;
+    const int i = qt * p.item_tokens + (row >> 7) * half + li, h = hk * p.group + g;
+    const bool live = li < half && i < sq.q_len;
+    if (!__any_sync(~0u, live)) return;  // the same rows in every warp
+    float M = -INFINITY, L = 0.f, x[E];
 #pragma unroll
-        for (int e = 0; e < E; e++) x[e] = 0.f;
-        for (int c = c0; c <= c1; c++) M = fmaxf(M, p.part_ml[(2 * c + (c == c0)) * kTileRows + row].x);
-        for (int c = c0; c <= c1; c++) {
-            const int64_t at = (int64_t)(2 * c + (c == c0)) * kTileRows + row;
-            const float2 ml = p.part_ml[at];
-            const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-            L += ml.y * a;
-            const float *po = p.part_o + at * D + lane * E;
+    for (int e = 0; e < E; e++) x[e] = 0.f;
+    for (int c = c0; c <= c1; c++) M = fmaxf(M, p.part_ml[(2 * c + (c == c0)) * kTileRows + row].x);
+    for (int c = c0; c <= c1; c++) {
+        const int slot = 2 * c + (c == c0);
+        const float2 ml = p.part_ml[slot * kTileRows + row];
+        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        L += ml.y * a;
+        const float *po = p.part_o + ((int64_t)slot * D + warp * E) * kTileRows + row;
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(po + e);
-                x[e] += v.x * a, x[e + 1] += v.y * a;
-            }
-        }
-        const int64_t token = sq.q0 + r / p.group;
-        const int h = hk * p.group + (int)(r % p.group);
-        float lse2;
-        const float f = finish_row(M, L, p.sinks, h, lse2);
-        uint32_t *out = reinterpret_cast<uint32_t *>(p.out.d + token * p.out.token + h * p.out.head + lane * E);
+        for (int e = 0; e < E; e++) x[e] += po[e * kTileRows] * a;
+    }
+    float lse2;
+    const float f = finish_row(M, L, p.sinks, live ? h : 0, lse2);
 #pragma unroll
-        for (int e = 0; e < E; e += 2) out[e / 2] = from_f2<BF>(x[e] * f, x[e + 1] * f);
-        if (lane == 0) put_lse(p, token, h, lse2);
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(&s_out[lane][warp * E + e]) = from_f2<BF>(x[e] * f, x[e + 1] * f);
+    if (warp == 0 && live) put_lse(p, sq.q0 + i, h, lse2);
+    __syncthreads();
+    for (int k = threadIdx.x; k < kJoinRows * D / 8; k += kJoinThreads) {
+        const int r = k / (D / 8), c = k % (D / 8), rr = sub * kJoinRows + r;
+        const int ri = (rr & 127) / (uint32_t)p.group, rg = (rr & 127) - ri * p.group, rt = qt * p.item_tokens + (rr >> 7) * half + ri;
+        if (ri < half && rt < sq.q_len)
+            *reinterpret_cast<uint4 *>(p.out.d + (int64_t)(sq.q0 + rt) * p.out.token + (hk * p.group + rg) * p.out.head + 8 * c) =
+                *reinterpret_cast<const uint4 *>(&s_out[r][8 * c]);
     }
 }
 
 template <bool BF, int D>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     using S = Shape<D>;
-    CUtensorMap km, vm;
+    CUtensorMap qm, km, vm;
     const int box = p.c.page_shift < 7 ? 1 << p.c.page_shift : 128;
-    if (!page_map(km, p.c, true, BF, box) || !page_map(vm, p.c, false, BF, box)) return cudaErrorInvalidValue;
+    if (!query_map(qm, p, BF) || !page_map(km, p.c, true, BF, box) || !page_map(vm, p.c, false, BF, box)) return cudaErrorInvalidValue;
     auto kern = chunk_kernel<BF, D>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<C, kThreads, S::kSmem, st>>>(p, km, vm);
+    kern<<<C, kThreads, S::kSmem, st>>>(p, qm, km, vm);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int n_qt = (int)(((int64_t)p.bt.max_q * p.group + kTileRows - 1) / kTileRows);
+    const int n_qt = (p.bt.max_q + p.item_tokens - 1) / p.item_tokens;
     return launch_after(chunk_combine<BF, D>, dim3(n_qt * (kTileRows / kJoinRows), p.c.kv_heads, p.bt.batch), kJoinThreads, 0, st, p, C);
 }
 
@@ -568,8 +727,19 @@ bool page_map(CUtensorMap &m, const View &c, bool keys, bool bf16, int box_slots
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool query_map(CUtensorMap &m, const AttendParams &p, bool bf16) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.c.dim, (cuuint64_t)p.q_heads, (cuuint64_t)p.bt.tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)p.q.head * 2, (cuuint64_t)p.q.token * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)p.group, (cuuint32_t)(p.item_tokens / 2)}, es[3] = {1, 1, 1};
+    return fn(&m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p.q.d, dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int chunk_ctas(const AttendParams &p, int num_sms) {
-    const int64_t n_qt = ((int64_t)p.bt.max_q * p.group + kTileRows - 1) / kTileRows;
+    const int64_t n_qt = (p.bt.max_q + p.item_tokens - 1) / p.item_tokens;
     const int64_t most = n_qt * p.bt.batch * p.c.kv_heads * (p.bt.max_kv / kTileSlots + 2);
     return (int)(most < num_sms ? (most > 0 ? most : 1) : num_sms);
 }

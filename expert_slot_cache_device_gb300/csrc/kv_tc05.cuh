@@ -16,24 +16,36 @@ using pipe::bar_expect;
 using pipe::bar_init;
 using pipe::su32;
 
-// Wait for the phase with the given parity, for at most two seconds (false then). The clock is
-// read only once the barrier has not come at the first tries.
-__device__ __forceinline__ bool try_bar(uint64_t *b, uint32_t parity) {
+// Wait for the phase with the given parity: one test, which is all that a phase that is there
+// costs, then at most 2^21 tries that suspend the thread for up to a microsecond each (false after
+// the last).
+__device__ __forceinline__ bool test_bar(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(su32(b)), "r"(parity)
+        : "r"(bar), "r"(parity)
         : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t *b, uint32_t parity) {
+    const uint32_t bar = su32(b);
+    if (test_bar(bar, parity)) return true;
 #pragma unroll 1
-    for (int i = 0; i < 16; i++)
-        if (try_bar(b, parity)) return true;
-    return pipe::bar_wait(b, parity);
+    for (uint32_t i = 0; i < (1u << 21); i++) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
 }
 // The same for a whole warp, which is converged afterwards.
 __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity) { return __all_sync(~0u, wait_bar(b, parity)); }
@@ -41,8 +53,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity) { return
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(su32(bar)),
+        "r"(elected)
+        : "memory");
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B of one 16-bit type, M = 128;
@@ -52,29 +68,40 @@ constexpr uint32_t kInstr = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) 
                             ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 
 // Operand of 128-byte rows with the 128-byte swizzle, groups of eight rows 1024 bytes apart
-// (stride offset). K-major: rows are M or N, a K = 16 step 32 bytes further in the row. MN-major:
-// rows are K, the next 64 elements of N `lead` bytes further (leading offset).
-__device__ __forceinline__ uint64_t desc128(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lead >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// (stride offset), as the low word of its descriptor; the high word is kDescHi. K-major: rows are M
+// or N, a K = 16 step 32 bytes further in the row. MN-major: rows are K, the next 64 elements of
+// N `lead` bytes further (leading offset). Shared addresses fit the field, so a step of n bytes
+// adds n / 16.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
+
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
 }
 
+// The products are issued by a whole warp with one lane elected inside the statement, so that
+// descriptors and addresses stay in uniform registers: issued under a lane's own branch, each
+// instruction took 100 to 140 cycles to set up, longer than the 64 that it runs.
 template <uint32_t I>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(I), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(I), "r"(acc), "r"(elected), "r"(kDescHi)
         : "memory");
 }
 template <uint32_t I>
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(I), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 y, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(I), "r"(acc), "r"(elected), "r"(kDescHi)
         : "memory");
 }
 
@@ -94,18 +121,31 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t *x) {
         : "r"(a)
         : "memory");
 }
-// 64 columns, one wait.
+// 64 columns without a wait: the registers are valid after tm_ld_wait of the same registers.
 __device__ __forceinline__ void tm_ld64(uint32_t a, uint32_t *x) {
-    uint32_t *y = x + 32;
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-        "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : FTMOE_R32(x), FTMOE_R32(y)
-        : "r"(a), "r"(a + 32)
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+        "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+        : FTMOE_R32(x), FTMOE_R32(x + 32)
+        : "r"(a)
         : "memory");
+}
+#define FTMOE_U4(x, i) "+r"((x)[i]), "+r"((x)[i + 1]), "+r"((x)[i + 2]), "+r"((x)[i + 3])
+#define FTMOE_U32(x) FTMOE_U4(x, 0), FTMOE_U4(x, 4), FTMOE_U4(x, 8), FTMOE_U4(x, 12), FTMOE_U4(x, 16), FTMOE_U4(x, 20), FTMOE_U4(x, 24), FTMOE_U4(x, 28)
+__device__ __forceinline__ void tm_ld_wait(uint32_t *x) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : FTMOE_U32(x), FTMOE_U32(x + 32)::"memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t *x) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        FTMOE_I4(x, 0), FTMOE_I4(x, 4), FTMOE_I4(x, 8), FTMOE_I4(x, 12)
+        : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t *x) {
     asm volatile(
@@ -150,37 +190,49 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *map, int x
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(su32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(su32(bar))
+        : "memory");
+}
 
-// Rows of an item of the tiled kernels: kTileRows consecutive (token, query head of the key
-// head) rows, row r token r / group; an item's visible slots, lo cut down to a multiple of 128.
+// An item of the tiled kernels: two row tiles of 128 / group whole tokens each, row r of a tile
+// (token r / group, query head r % group of the key head), so that a tile of queries is one box of
+// a tensor map; the rows past the last whole token are not used. A step is 128 slots; an
+// item's visible slots start at lo, cut down to a multiple of 128.
 constexpr int kTileRows = 256, kTileSlots = 128;
 
 struct Item {
     int lo, hi, seen_lo, tiles;
 };
 
-__device__ __forceinline__ int row_tiles(const Seq &s, int group) {
-    return (int)(((int64_t)s.q_len * group + kTileRows - 1) / kTileRows);
+__device__ __forceinline__ int row_tiles(const AttendParams &p, const Seq &s) {
+    return (int)((uint32_t)(s.q_len + p.item_tokens - 1) / (uint32_t)p.item_tokens);
 }
 __device__ __forceinline__ Item item_of(const AttendParams &p, const Seq &s, int qt) {
-    const int64_t rows = (int64_t)s.q_len * p.group, r0 = (int64_t)qt * kTileRows;
-    const int64_t r1 = r0 + kTileRows < rows ? r0 + kTileRows : rows;
-    const Range v = visible(s, (int)(r0 / p.group), (int)((r1 - 1) / p.group) + 1, p.window, p.causal);
+    const int i0 = qt * p.item_tokens, i1 = i0 + p.item_tokens < s.q_len ? i0 + p.item_tokens : s.q_len;
+    const Range v = visible(s, i0, i1, p.window, p.causal);
     Item it;
     it.seen_lo = v.lo, it.hi = v.hi, it.lo = v.lo & ~(kTileSlots - 1);
     it.tiles = (it.hi - it.lo + kTileSlots - 1) / kTileSlots;
     if (it.tiles < 1) it.tiles = 1;
     return it;
 }
-// Steps of one (sequence, key head) over all its row tiles; the whole warp calls.
-__device__ __forceinline__ int seq_tiles(const AttendParams &p, const Seq &s, int end_qt) {
+// What an item adds to the line of work besides its steps: its start and end take about as long.
+constexpr int kItemCost = 2;
+
+// Units of one (sequence, key head) over its first end_qt items; the whole warp calls.
+__device__ __forceinline__ int seq_units(const AttendParams &p, const Seq &s, int end_qt) {
     int n = 0;
-    for (int qt = threadIdx.x & 31; qt < end_qt; qt += 32) n += item_of(p, s, qt).tiles;
+    for (int qt = threadIdx.x & 31; qt < end_qt; qt += 32) n += item_of(p, s, qt).tiles + kItemCost;
     return __reduce_add_sync(~0u, n);
 }
 
 // Tensor map of pages: [page][head][slot][element], boxes of 64 elements x box_slots slots.
 bool page_map(CUtensorMap &m, const View &c, bool keys, bool bf16, int box_slots);
+// Tensor map of query rows: [token][head][element], boxes of 64 elements x group heads x 128 / group tokens.
+bool query_map(CUtensorMap &m, const AttendParams &p, bool bf16);
 
 }  // namespace kv
 }  // namespace ftmoe
