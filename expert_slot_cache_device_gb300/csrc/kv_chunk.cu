@@ -493,27 +493,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto next_stage = [&] {
             if (++st == S::kStages) st = 0, ph ^= 1;
         };
+        // Loops, not unrolled code: the warp runs this once a step between the softmax's long code, and
+        // fetching instructions took longer than the products.
         auto scores = [&](int t, uint32_t sk) {
-            const uint32_t a = qd + t * (128 * D * 2 / 16), b = kd + sk * (S::kStage / 16);
+            uint32_t a = qd + t * (128 * D * 2 / 16), b = kd + sk * (S::kStage / 16), acc = 0;
+#pragma unroll 1
+            for (int e = 0; e < D / 64; e++) {
 #pragma unroll
-            for (int k = 0; k < D / 16; k++) {
-                const uint32_t off = ((k >> 2) * S::kHalf + (k & 3) * 32) / 16;
-                mma_ss<IS>(one, tm + 128 * t, a + off, b + off, k > 0);
+                for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + 128 * t, a + 2 * k, b + 2 * k, acc);
+                a += S::kHalf / 16, b += S::kHalf / 16;
             }
             commit(one, &bar.s[t]);
         };
         auto values = [&](int t, uint32_t sv, uint32_t acc) {
-            const uint32_t v = vd + sv * (S::kStage / 16);
-#pragma unroll
+            uint32_t v = vd + sv * (S::kStage / 16), a = tm + S::kP + S::kPStep * t;
+#pragma unroll 1
             for (int q = 0; q < 2; q++) {
                 ok = ok && warp_wait(&bar.p[t][q], (np >> t) & 1);
+                if (!ok) return;
                 fence_after();
-                if (ok) {
 #pragma unroll
-                    for (int k = 4 * q; k < 4 * q + 4; k++)
-                        mma_ts<IO>(one, tm + S::kO + D * t, tm + S::kP + S::kPStep * t + 8 * k, v + k * (2048 / 16), k > 0 ? 1u : acc);
-                    if (q == 0) commit(one, &bar.half[t]);
-                }
+                for (int k = 0; k < 4; k++, acc = 1) mma_ts<IO>(one, tm + S::kO + D * t, a + 8 * k, v + k * (2048 / 16), acc);
+                if (q == 0) commit(one, &bar.half[t]);
+                a += 32, v += 4 * 2048 / 16;
             }
             np ^= 1 << t;
         };
@@ -524,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_wait(&bar.qfull, ni++ & 1) && warp_wait(&bar.full[st], ph);
             if (!ok) break;
             fence_after();
-            scores(0, st);
-            if (two) scores(1, st);
+#pragma unroll 1
+            for (int t = 0; t <= two; t++) scores(t, st);
             commit(one, &bar.empty[st]);
             if (n == 1) commit(one, &bar.qempty);
             next_stage();
@@ -535,28 +537,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_wait(&bar.full[sv], pv);
                 if (s0 + j * kTileSlots < lo || s0 + (j + 1) * kTileSlots > hi) ok = ok && warp_wait(&bar.clean[sv], pv);
                 next_stage();
-                if (j + 1 < n) {
-                    ok = ok && warp_wait(&bar.full[st], ph);
-                    values(0, sv, j > 0);
-                    if (ok) scores(0, st);
-                    if (two) {
-                        values(1, sv, j > 0);
-                        commit(one, &bar.empty[sv]);
-                        if (ok) scores(1, st);
-                    } else {
-                        commit(one, &bar.empty[sv]);
-                    }
+                const bool more = j + 1 < n;
+                if (more) ok = ok && warp_wait(&bar.full[st], ph);
+#pragma unroll 1
+                for (int t = 0; t <= two && ok; t++) {
+                    values(t, sv, j > 0);
+                    if (!ok) break;
+                    if (t == two) commit(one, &bar.empty[sv]);
+                    if (more)
+                        scores(t, st);
+                    else
+                        commit(one, &bar.o[t]);
+                }
+                if (more) {
                     commit(one, &bar.empty[st]);
                     if (j + 2 == n) commit(one, &bar.qempty);
                     next_stage();
-                } else {
-                    values(0, sv, j > 0);
-                    commit(one, &bar.o[0]);
-                    if (two) {
-                        values(1, sv, j > 0);
-                        commit(one, &bar.o[1]);
-                    }
-                    commit(one, &bar.empty[sv]);
                 }
             }
         }
