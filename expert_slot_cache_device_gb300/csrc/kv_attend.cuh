@@ -37,6 +37,7 @@ int step_ctas(const AttendParams &p, int num_sms);
 cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 size_t chunk_part_rows(const AttendParams &p, int num_sms);
 cudaError_t launch_chunk(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
+cudaError_t launch_mass(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 
 }  // namespace kv
 }  // namespace ftmoe

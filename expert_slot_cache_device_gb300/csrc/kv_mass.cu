@@ -1,0 +1,279 @@
+// The mass pass of chunks: mass[j] += sum over the rows that see slot j of 2^(s scale log2 e - lse), on
+// the 5th-generation tensor cores. An item is 128 slots of one (sequence, key head): K is the A
+// operand (M = 128 slots), the queries of 128 / group tokens at a time are B, so a thread of the
+// epilogue holds one slot and adds over the columns (rows) in order: one writer and one order for each
+// mass element. Bound by the exponentials and the products alike: 2 dim flops and one exponential a
+// (row, slot).
+//
+// Persistent, one CTA an SM, items dealt round-robin with the slots that most rows see first. Roles:
+//   warps 0-3, 4-7  sums, the even and the odd row tiles of an item; the two join at its end;
+//   warp 8          tensor copies of K (two buffers) and the query tiles (a ring);
+//   warp 9          issues S = K Q^T into four tensor-memory buffers of 128 columns;
+//   warp 10         the rows' negated log-sum-exps (powers of two) of each tile.
+// Slots outside the visible range may hold anything: they only meet their own lane, whose sum
+// is not written. Every wait is bounded.
+#include "kv_tc05.cuh"
+
+namespace ftmoe {
+namespace kv {
+namespace {
+
+constexpr int kWarps = 12, kThreads = kWarps * 32, kCopyWarp = 8, kMmaWarp = 9, kLseWarp = 10;
+constexpr int kBufs = 4;
+
+template <int D>
+struct Shape {
+    static constexpr int kTile = 128 * D * 2, kHalf = 128 * 128;
+    static constexpr int kStages = 4;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+};
+
+struct Bars {
+    uint64_t kfull[2], kempty[2], qfull[4], qempty[4], s[kBufs], free[kBufs], lse[kBufs], odd, even, done;
+};
+
+// Item `n` of the line: slot tile, sequence, key head; the row tiles [first, last) that see some of it.
+struct Slots {
+    int b, hk, s0, first, last;
+    Seq sq;
+    Range vis;  // slots that some row sees
+};
+
+__device__ __forceinline__ bool slots_of(const AttendParams &p, int n, Slots &w) {
+    const int per = p.bt.batch * p.c.kv_heads;
+    w.s0 = n / per * kTileSlots;
+    w.b = n % per / p.c.kv_heads, w.hk = n % p.c.kv_heads;
+    w.sq = seq_info(p.bt, w.b, nullptr);
+    w.vis = visible(w.sq, 0, w.sq.q_len, p.window, p.causal);
+    if (w.s0 >= w.vis.hi || w.s0 + kTileSlots <= w.vis.lo) return false;
+    const int before = w.sq.kv_len - w.sq.q_len, tok = p.item_tokens >> 1;
+    // tokens i in [i0, i1) see a slot of the tile: slot before + i >= s0, and before + i - window < s0 + 127
+    int i0 = p.causal ? w.s0 - before : -before, i1 = p.window ? w.s0 + kTileSlots - 1 + p.window - before : w.sq.q_len;
+    if (i0 < 0) i0 = 0;
+    if (i1 > w.sq.q_len) i1 = w.sq.q_len;
+    w.first = i0 / tok, w.last = (i1 + tok - 1) / tok;
+    return w.first < w.last;
+}
+
+template <bool BF, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    mass_kernel(const AttendParams p, const int items, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap) {
+    using S = Shape<D>;
+    extern __shared__ __align__(1024) unsigned char sm_raw[];
+    __shared__ Bars bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ __align__(16) float s_lse[kBufs][128];
+    __shared__ float s_odd[128];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t ks = (su32(sm_raw) + 1023u) & ~1023u, qs = ks + 2 * S::kTile;
+    const int tok = p.item_tokens >> 1;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; i++) bar_init(&bar.kfull[i], 1), bar_init(&bar.kempty[i], 1);
+        for (int i = 0; i < S::kStages; i++) bar_init(&bar.qfull[i], 1), bar_init(&bar.qempty[i], 1);
+        for (int i = 0; i < kBufs; i++) bar_init(&bar.s[i], 1), bar_init(&bar.free[i], 4), bar_init(&bar.lse[i], 1);
+        bar_init(&bar.done, 1), bar_init(&bar.odd, 4), bar_init(&bar.even, 4);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(&s_tmem);
+    bool ok = true;
+    Slots w;
+
+    if (warp < 8) {  // ---------------------------------------------------- sums
+        const int t = warp >> 2;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const float c2 = p.scale * kLog2e;
+        const uint64_t cc = pack2(c2, c2);
+        uint32_t cnt = 0, ni = 0;
+        for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
+            if (!slots_of(p, n, w)) continue;
+            const int j = w.s0 + (tid & 127), before = w.sq.kv_len - w.sq.q_len;
+            // rows [ra, rb) of the sequence see slot j
+            int ia = p.causal ? j - before : -before, ib = p.window ? j + p.window - before : w.sq.q_len;
+            if (ia < 0) ia = 0;
+            if (ib > w.sq.q_len) ib = w.sq.q_len;
+            float total = 0.f;
+            for (int rt = w.first; rt < w.last && ok; rt++, cnt++) {
+                if (((rt - w.first) & 1) != t) continue;
+                const uint32_t bf = cnt % kBufs, ph = (cnt / kBufs) & 1;
+                ok = warp_wait(&bar.lse[bf], ph) && warp_wait(&bar.s[bf], ph);
+                if (!ok) break;
+                fence_after();
+                // the tile's columns [a, e) see the slot; those past the last whole token are none
+                const int ta = ia - rt * tok, te = ib - rt * tok;
+                const int a = ta > 0 ? (ta < tok ? ta : tok) * p.group : 0, e = te > 0 ? (te < tok ? te : tok) * p.group : 0;
+                const bool cut = __any_sync(~0u, a > 0 || e < 128);
+                uint64_t sum[2] = {0, 0};
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    uint32_t x[64];
+                    tm_ld64(tm + lanes + 128 * bf + 64 * q, x);
+                    tm_ld_wait(x);
+                    if (cut) {
+#pragma unroll
+                        for (int k = 0; k < 64; k++)
+                            if (64 * q + k < a || 64 * q + k >= e) x[k] = 0xff800000u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 64; k += 4) {
+                        const float4 z = *reinterpret_cast<const float4 *>(&s_lse[bf][64 * q + k]);
+                        const float2 f0 = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, pack2(z.x, z.y)));
+                        const float2 f1 = unpack2(fma2(pack2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), cc, pack2(z.z, z.w)));
+                        sum[0] = add2(sum[0], pack2(ex2(f0.x), ex2(f0.y)));
+                        sum[1] = add2(sum[1], pack2(ex2(f1.x), ex2(f1.y)));
+                    }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.free[bf]);
+                const float2 f = unpack2(add2(sum[0], sum[1]));
+                total += f.x + f.y;
+            }
+            // the odd tiles' sums join the even ones'
+            if (!ok) break;
+            if (t == 1) {
+                ok = warp_wait(&bar.even, (ni & 1) ^ 1);  // the last item's have been read
+                s_odd[tid & 127] = total;
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.odd);
+            } else {
+                ok = warp_wait(&bar.odd, ni & 1);
+                if (ok && j >= w.vis.lo && j < w.vis.hi) p.mass[w.b * p.mass_seq + w.hk * p.mass_head + j] += total + s_odd[tid];
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.even);
+            }
+            ni++;
+        }
+    } else if (warp == kCopyWarp) {  // ------------------------------------- K, queries
+        const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTileSlots / box, halves = D / 64;
+        const int mine = lane % boxes, half = lane / boxes;
+        uint32_t nk = 0, nq = 0;
+        for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
+            if (!slots_of(p, n, w)) continue;
+            const int slot = w.s0 + mine * box;
+            int page = -1;
+            if (half < halves && slot < w.vis.hi && slot + box > w.vis.lo) {
+                page = p.bt.table[(int64_t)w.b * p.bt.table_stride + (slot >> p.c.page_shift)];
+                if ((uint32_t)page >= (uint32_t)p.c.num_pages) page = -1;  // recorded by the pass before
+            }
+            const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * box * 128;
+            if (!warp_wait(&bar.kempty[nk & 1], ((nk >> 1) & 1) ^ 1)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) bar_expect(&bar.kfull[nk & 1], bytes);
+            __syncwarp();
+            if (page >= 0)
+                tma4(ks + (nk & 1) * S::kTile + half * S::kHalf + mine * box * 128, &kmap, 64 * half, slot & ((1 << p.c.page_shift) - 1), w.hk, page,
+                     &bar.kfull[nk & 1]);
+            nk++;
+            for (int rt = w.first; rt < w.last; rt++, nq++) {
+                const uint32_t st = nq % S::kStages;
+                if (!warp_wait(&bar.qempty[st], ((nq / S::kStages) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) bar_expect(&bar.qfull[st], halves * tok * p.group * 128);
+                __syncwarp();
+                if (lane < halves)
+                    tma3(qs + st * S::kTile + lane * S::kHalf, &qmap, 64 * lane, w.hk * p.group, w.sq.q0 + rt * tok, &bar.qfull[st]);
+            }
+        }
+        if (!ok) {  // wait (bounded) until the copies already issued have landed
+            for (uint32_t c = nk < 2 ? 0 : nk - 2; c < nk; c++) wait_bar(&bar.kfull[c & 1], (c >> 1) & 1);
+            for (uint32_t c = nq < S::kStages ? 0 : nq - S::kStages; c < nq; c++) wait_bar(&bar.qfull[c % S::kStages], (c / S::kStages) & 1);
+        }
+    } else if (warp == kMmaWarp) {  // -------------------------------------- products
+        constexpr uint32_t IS = kInstr<BF, 128, false>;
+        const uint32_t one = elect_one();
+        const uint32_t kd = desc_lo(ks, 16), qd = desc_lo(qs, 16);
+        uint32_t nk = 0, cnt = 0;
+        for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
+            if (!slots_of(p, n, w)) continue;
+            const int tiles = __shfl_sync(~0u, w.last - w.first, 0);
+            ok = warp_wait(&bar.kfull[nk & 1], (nk >> 1) & 1);
+            for (int i = 0; i < tiles && ok; i++, cnt++) {
+                const uint32_t st = cnt % S::kStages, bf = cnt % kBufs;
+                ok = warp_wait(&bar.qfull[st], (cnt / S::kStages) & 1) && warp_wait(&bar.free[bf], ((cnt / kBufs) & 1) ^ 1);
+                if (!ok) break;
+                fence_after();
+                uint32_t a = kd + (nk & 1) * (S::kTile / 16), b = qd + st * (S::kTile / 16), acc = 0;
+#pragma unroll 1
+                for (int e = 0; e < D / 64; e++) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + 128 * bf, a + 2 * k, b + 2 * k, acc);
+                    a += S::kHalf / 16, b += S::kHalf / 16;
+                }
+                commit(one, &bar.s[bf]);
+                commit(one, &bar.qempty[st]);
+            }
+            commit(one, &bar.kempty[nk & 1]);
+            nk++;
+        }
+        commit(one, &bar.done);
+        warp_wait(&bar.done, 0);
+    } else if (warp == kLseWarp) {  // -------------------------------------- log-sum-exps
+        uint32_t cnt = 0;
+        for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
+            if (!slots_of(p, n, w)) continue;
+            for (int rt = w.first; rt < w.last; rt++, cnt++) {
+                const uint32_t bf = cnt % kBufs;
+                float z[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int r = lane + 32 * k, i = r / (uint32_t)p.group, token = rt * tok + i;
+                    z[k] = -INFINITY;
+                    if (i < tok && token < w.sq.q_len) {
+                        const float v = p.lse2[(int64_t)(w.sq.q0 + token) * p.q_heads + w.hk * p.group + r - i * p.group];
+                        if (v != -INFINITY) z[k] = -v;  // a row that sees nothing adds nothing
+                    }
+                }
+                if (!warp_wait(&bar.free[bf], ((cnt / kBufs) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; k++) s_lse[bf][lane + 32 * k] = z[k];
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.lse[bf]);
+            }
+        }
+    }
+    if (!ok && lane == 0) flag(p.c.status, FTMOE_ERR_STATE);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+}
+
+template <bool BF, int D>
+cudaError_t launch(const AttendParams &p, int num_sms, cudaStream_t st) {
+    using S = Shape<D>;
+    CUtensorMap qm, km;
+    if (!query_map(qm, p, BF) || !page_map(km, p.c, true, BF, p.c.page_shift < 7 ? 1 << p.c.page_shift : 128)) return cudaErrorInvalidValue;
+    const int64_t items = ((int64_t)p.bt.max_kv + kTileSlots - 1) / kTileSlots * p.bt.batch * p.c.kv_heads;
+    if (items >= (int64_t)1 << 31) return cudaErrorInvalidValue;
+    if (items == 0) return cudaSuccess;
+    auto kern = mass_kernel<BF, D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(items < num_sms ? items : num_sms), kThreads, S::kSmem, st>>>(p, (int)items, qm, km);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mass(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
+    if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, num_sms, st) : launch<false, 64>(p, num_sms, st);
+    return bf16 ? launch<true, 128>(p, num_sms, st) : launch<false, 128>(p, num_sms, st);
+}
+
+}  // namespace kv
+}  // namespace ftmoe
