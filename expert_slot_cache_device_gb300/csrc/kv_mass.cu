@@ -219,32 +219,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(one, &bar.done);
         warp_wait(&bar.done, 0);
-    } else if (warp == kLseWarp) {  // -------------------------------------- log-sum-exps
-        uint32_t cnt = 0;
+    } else {  // -------------------------------------------------------------- log-sum-exps
+        // warp 10 the even, warp 11 the odd tiles of the whole line; a lane's four rows sit at the same
+        // places of every tile, and the next tile's values are under way while this one's wait
+        int at[4], i4[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int r = lane + 32 * k;
+            i4[k] = r / (uint32_t)p.group;
+            at[k] = i4[k] * p.q_heads + r - i4[k] * p.group;
+            if (i4[k] >= tok) i4[k] = 1 << 30;
+        }
+        uint32_t cnt = warp - kLseWarp, base = 0;
+        float z[4];
+        bool have = false;
+        auto put = [&] {  // the values of tile cnt
+            const uint32_t bf = cnt % kBufs;
+            if (!warp_wait(&bar.free[bf], ((cnt / kBufs) & 1) ^ 1)) return false;
+#pragma unroll
+            for (int k = 0; k < 4; k++) s_lse[bf][lane + 32 * k] = z[k];
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bar.lse[bf]);
+            cnt += 2;
+            return true;
+        };
         for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
             if (!slots_of(p, n, w)) continue;
-            for (int rt = w.first; rt < w.last; rt++, cnt++) {
-                const uint32_t bf = cnt % kBufs;
-                float z[4];
+            const uint32_t tiles = w.last - w.first;
+            const float *src = p.lse2 + (int64_t)w.sq.q0 * p.q_heads + w.hk * p.group;
+            for (uint32_t c = cnt + (have ? 2 : 0); c < base + tiles && ok; c += 2) {
+                const int t0 = (w.first + (int)(c - base)) * tok;
+                float y[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const int r = lane + 32 * k, i = r / (uint32_t)p.group, token = rt * tok + i;
-                    z[k] = -INFINITY;
-                    if (i < tok && token < w.sq.q_len) {
-                        const float v = p.lse2[(int64_t)(w.sq.q0 + token) * p.q_heads + w.hk * p.group + r - i * p.group];
-                        if (v != -INFINITY) z[k] = -v;  // a row that sees nothing adds nothing
-                    }
+                    y[k] = -INFINITY;
+                    if (i4[k] < w.sq.q_len - t0) y[k] = src[(int64_t)t0 * p.q_heads + at[k]];
                 }
-                if (!warp_wait(&bar.free[bf], ((cnt / kBufs) & 1) ^ 1)) {
-                    ok = false;
-                    break;
-                }
+                if (have) ok = put();
 #pragma unroll
-                for (int k = 0; k < 4; k++) s_lse[bf][lane + 32 * k] = z[k];
-                __syncwarp();
-                if (lane == 0) bar_arrive(&bar.lse[bf]);
+                for (int k = 0; k < 4; k++) z[k] = y[k] == -INFINITY ? y[k] : -y[k];  // a row that sees nothing adds nothing
+                have = true;
             }
+            base += tiles;
         }
+        if (have && ok) ok = put();
     }
     if (!ok && lane == 0) flag(p.c.status, FTMOE_ERR_STATE);
     fence_before();
