@@ -2,14 +2,24 @@
 //
 // The codes are laid out once, in the order in which mma.sync m16n8k16 takes its A operand, so
 // a warp's load of a tile of 16 rows x 64 k is 512 consecutive bytes: lane (g, t) = (lane / 4,
-// lane % 4) holds four words, word s the eight codes of k step s (16 k): nibble i of the low half is
-// the first and nibble i of the high half the second element of fragment register a_i (a0: row
-// g, k 2t; a1: row g + 8; a2, a3: the same at k 2t + 8). (w >> 4i) & 0x000f000f OR'ed into the
-// bits of (128, 128) in bf16, or (1024, 1024) in f16, makes 128 + q (1024 + q) exactly, and
-// subtracting 128 + z leaves the exact integer q - z. A group's products are summed by the
-// tensor cores in fp32 from zero; its scale multiplies that sum in fp32, so no weight is rounded.
+// lane % 4) holds four words, word s the eight codes of step s: nibble i of the low half is the
+// first and nibble i of the high half the second element of fragment register a_i (a0: row g, a1:
+// row g + 8 at the first two of the step's k; a2, a3 the same at its last two). Which k a lane's
+// fragment stands for is free as long as x agrees: step s of lane t takes k = 32 (s / 2) + 8 t +
+// 4 (s % 2) + 0..3 of the block, so that a lane's x for a block are two 16-byte reads of a plain row
+// and a step stays inside one group of 32. (w >> 4i) & 0x000f000f OR'ed into the bits of
+// (128, 128) in bf16, or (1024, 1024) in f16, makes 128 + q (1024 + q) exactly, and subtracting
+// 128 + z leaves the exact integer q - z. A group's products are summed by the tensor cores in
+// fp32 from zero; its scale multiplies that sum in fp32, so no weight is rounded.
 //   packed: codes [row tile][64-k block][lane][16 B], then scales [row tile][group][8] pairs (rows g,
 //   g + 8), then zeros [row tile][group][8] pairs of bytes. Rows past N and k past K hold zeros.
+//
+// Bound by reading the codes once. A CTA is eight warps: kWR row tiles (pairs of tiles for more than 16
+// tokens) times kWK slices of k, so that several warps share the x that a chunk of k stages in shared
+// memory. Codes and scales go to shared memory too (each lane copies the 16 bytes of codes that it
+// reads itself), kStages chunks deep: held in registers instead, two chunks of them spilled. Where row
+// tiles alone do not fill the SMs, up to eight CTAs of a cluster split k and join their sums
+// through distributed shared memory in rank order, so results repeat bit for bit.
 #include "kv.cuh"
 #include "pipeline.cuh"
 
@@ -36,7 +46,7 @@ __global__ void pack_kernel(const Geometry g, const uint8_t *codes, const uint16
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const int n = rt * 16 + (lane >> 2) + 8 * (r & 1);
-                    const int k = kb * 64 + s * 16 + 2 * (lane & 3) + 8 * (r >> 1) + e;
+                    const int k = kb * 64 + 32 * (s >> 1) + 8 * (lane & 3) + 4 * (s & 1) + 2 * (r >> 1) + e;
                     uint32_t q = 0;
                     if (n < g.N && k < g.K) q = codes[(int64_t)n * (g.K / 2) + (k >> 1)] >> (4 * (k & 1)) & 15;
                     w |= q << (4 * r + 16 * e);
@@ -76,80 +86,275 @@ __device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t off) {
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kThreads = kWarps * 32, kStages = 3;
+constexpr int kLoads = 4;  // 512-byte loads of codes a warp and chunk
 
-template <bool BF, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32) matvec_kernel(const MatvecParams p) {
-    constexpr int KB = GROUP > 64 ? GROUP / 64 : 1;      // 64-k blocks of one step
-    constexpr int GPB = GROUP < 64 ? 64 / GROUP : 1;     // groups of one 64-k block
-    __shared__ float s_acc[kWarps][32][4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rt = blockIdx.x, tok = blockIdx.y * 8 + g;
-    const uint4 *codes = reinterpret_cast<const uint4 *>(p.packed) + (int64_t)rt * p.g.k_blocks * 32 + lane;
-    const uint32_t *scales = reinterpret_cast<const uint32_t *>(p.packed + p.g.code_bytes) + (int64_t)rt * p.g.groups * 8 + g;
-    const uint16_t *zeros = reinterpret_cast<const uint16_t *>(p.packed + p.g.code_bytes + (int64_t)p.g.row_tiles * p.g.groups * 32) +
-                            (int64_t)rt * p.g.groups * 8 + g;
-    const uint16_t *x = p.x + (int64_t)tok * p.x_stride + 2 * t;
-    const bool live = tok < p.tokens;
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int kb = warp * KB; kb < p.g.k_blocks; kb += kWarps * KB) {
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
+// TN tiles of eight tokens.
+template <int GROUP, int TN>
+struct Shape {
+    static constexpr int RW = TN > 2 ? 2 : 1;                // row tiles of a warp, which share its x
+    static constexpr int WK = TN == 1 ? 4 : 2, WR = kWarps / WK;
+    static constexpr int KPW = kLoads / RW;                  // 64-k blocks of a warp and chunk
+    static constexpr int CB = KPW * WK;                      // blocks of a chunk
+    static constexpr int RS = CB * 128 + 64;                 // bytes of an x row: two rows cover the banks
+    static constexpr int NG = GROUP < 64 ? KPW * 2 : KPW * 64 / GROUP;  // groups of a warp's blocks
+    static constexpr int META = RW * NG * 48;                // scales [r][group][8 pairs], zeros likewise
+    static constexpr int WARP = kLoads * 512 + META;
+    static constexpr int STAGE = 8 * TN * RS + kWarps * WARP;
+    static constexpr int ROWS = WR * RW * 16;
+    static constexpr int TILE = 8 * TN * ROWS;               // sums of a CTA; one copy a k slice, over the stages
+    static constexpr int SMEM = kStages * STAGE;
+    static_assert(WK * TILE * 4 <= SMEM, "the sums fit the stages");
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_rank(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// `split` CTAs of a cluster share k; grid (row groups * split, token tiles of 8 TN).
+template <bool BF, int GROUP, bool ZEROS, int TN>
+__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const MatvecParams p, const int split) {
+    using S = Shape<GROUP, TN>;
+    constexpr int GK = GROUP > 64 ? 2 : 1;  // blocks that share a scale
+    extern __shared__ __align__(128) unsigned char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int rank = split > 1 ? (int)cluster_rank() : 0, wr = warp / S::WK, wk = warp % S::WK;
+    const int rt0 = (blockIdx.x / split * S::WR + wr) * S::RW, tok0 = blockIdx.y * 8 * TN;
+    const int live_x = p.tokens - tok0 < 8 * TN ? p.tokens - tok0 : 8 * TN;
+    // this CTA's blocks of k, whole groups
+    const int pairs = (p.g.k_blocks + GK - 1) / GK;
+    const int kb0 = (int)((int64_t)rank * pairs / split) * GK, kb1_ = (int)((int64_t)(rank + 1) * pairs / split) * GK;
+    const int kb1 = kb1_ < p.g.k_blocks ? kb1_ : p.g.k_blocks;
+    const int chunks = (kb1 - kb0 + S::CB - 1) / S::CB;
+
+    const unsigned char *scales = p.packed + p.g.code_bytes;
+    const unsigned char *zeros = scales + (int64_t)p.g.row_tiles * p.g.groups * 32;
+    const uint32_t base = pipe::su32(sm), mine = 8 * TN * S::RS + warp * S::WARP;  // a stage: x, then the warps' parts
+
+    auto copy = [&](int c) {
+        if (c < chunks) {
+            const uint32_t st = base + (c % kStages) * S::STAGE;
+            const int kc = kb0 + c * S::CB, kb = kc + wk * S::KPW;
 #pragma unroll
-        for (int u = 0; u < KB; u++) {
-            const uint4 c = codes[(int64_t)(kb + u) * 32];
-            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            for (int r = 0; r < S::RW; r++) {
+                const int rt = rt0 + r;
+                const bool live = rt < p.g.row_tiles;
 #pragma unroll
-            for (int s = 0; s < 4; s++) {
-                const int gi = GROUP > 64 ? kb / KB : kb * GPB + s * GPB / 4;
-                const uint32_t z = p.g.zeros ? zeros[(int64_t)gi * 8] : 0x0808u;
-                const uint32_t o0 = offset2<BF>(z & 255u), o1 = offset2<BF>(z >> 8);
-                const int k = (kb + u) * 64 + s * 16;
-                uint32_t b0 = 0, b1 = 0;
-                if (live && k < p.g.K) {
-                    b0 = *reinterpret_cast<const uint32_t *>(x + k);
-                    b1 = *reinterpret_cast<const uint32_t *>(x + k + 8);
+                for (int i = 0; i < S::KPW; i++) {
+                    const bool ok = live && kb + i < kb1;
+                    cp16(st + mine + (r * S::KPW + i) * 512 + lane * 16,
+                         p.packed + (ok ? (((int64_t)rt * p.g.k_blocks + kb + i) * 32 + lane) * 16 : 0), ok);
                 }
-                const uint32_t a0 = decode2<BF>(w[s], o0), a1 = decode2<BF>(w[s] >> 4, o1);
-                const uint32_t a2 = decode2<BF>(w[s] >> 8, o0), a3 = decode2<BF>(w[s] >> 12, o1);
-                if (BF)
-                    pipe::mma_bf16_16816(part, a0, a1, a2, a3, b0, b1);
-                else
-                    pipe::mma_f16_16816(part, a0, a1, a2, a3, b0, b1);
-                const bool last = GROUP > 64 ? (u == KB - 1 && s == 3) : (s + 1) % (4 / GPB) == 0;
-                if (last) {
-                    const uint32_t sc = scales[(int64_t)gi * 8];
-                    const float s0 = to_f<BF>((uint16_t)sc), s1 = to_f<BF>((uint16_t)(sc >> 16));
-                    acc[0] += s0 * part[0], acc[1] += s0 * part[1], acc[2] += s1 * part[2], acc[3] += s1 * part[3];
-                    part[0] = part[1] = part[2] = part[3] = 0.f;
+            }
+            // 16-byte pieces: two of scales, one of zeros a group
+            constexpr int PC = S::RW * S::NG;
+            for (int i = lane; i < PC * (ZEROS ? 3 : 2); i += 32) {
+                const bool z = ZEROS && i >= 2 * PC;
+                const int j = z ? i - 2 * PC : i >> 1, r = j / S::NG, rt = rt0 + r;
+                const int gi = (GROUP > 64 ? kb / 2 : (GROUP < 64 ? kb * 2 : kb)) + j % S::NG;
+                const bool ok = rt < p.g.row_tiles && gi < p.g.groups;
+                const int64_t at = (int64_t)rt * p.g.groups + gi;
+                cp16(st + mine + kLoads * 512 + i * 16, z ? zeros + (ok ? at * 16 : 0) : scales + (ok ? at * 32 + (i & 1) * 16 : 0), ok);
+            }
+            const int k0 = kc * 64, k1 = kb1 * 64 < p.g.K ? kb1 * 64 : p.g.K;
+            for (int i = tid; i < live_x * S::CB * 8; i += kThreads) {
+                const int r = i / (S::CB * 8), ch = i % (S::CB * 8), k = k0 + 8 * ch;
+                const bool ok = k < k1;
+                cp16(st + r * S::RS + 16 * ch, p.x + (ok ? (int64_t)(tok0 + r) * p.x_stride + k : 0), ok);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    float acc[S::RW][TN][4];
+#pragma unroll
+    for (int r = 0; r < S::RW; r++)
+#pragma unroll
+        for (int n = 0; n < TN; n++) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
+    // rows of x past the last token stay zero
+    for (int i = tid; i < (8 * TN - live_x) * (S::RS / 16); i += kThreads)
+#pragma unroll
+        for (int st = 0; st < kStages; st++) *reinterpret_cast<uint4 *>(sm + st * S::STAGE + live_x * S::RS + i * 16) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int c = 0; c < kStages - 1; c++) copy(c);
+    for (int c = 0; c < chunks; c++) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();  // this chunk is there, and the stage of the one before is read
+        copy(c + kStages - 1);
+        const unsigned char *st = sm + (c % kStages) * S::STAGE, *xs = st + g * S::RS + wk * S::KPW * 128 + 16 * t;
+        const unsigned char *wm = st + mine;
+        const uint32_t *sc = reinterpret_cast<const uint32_t *>(wm + kLoads * 512) + g;
+        const uint16_t *zc = reinterpret_cast<const uint16_t *>(wm + kLoads * 512 + S::RW * S::NG * 32) + g;
+        float part[S::RW][TN][4];
+#pragma unroll
+        for (int i = 0; i < S::KPW; i++) {
+            uint4 w[S::RW];
+#pragma unroll
+            for (int r = 0; r < S::RW; r++) w[r] = *reinterpret_cast<const uint4 *>(wm + (r * S::KPW + i) * 512 + lane * 16);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {  // 32 k: two steps
+                const int gi = GROUP > 64 ? i / 2 : (GROUP < 64 ? 2 * i + h : i);
+                const bool begin = GROUP < 64 || (h == 0 && i % GK == 0), end = GROUP < 64 || (h == 1 && i % GK == GK - 1);
+                uint32_t a[S::RW][2][4];
+#pragma unroll
+                for (int r = 0; r < S::RW; r++) {
+                    const uint32_t z = ZEROS ? zc[(r * S::NG + gi) * 8] : 0x0808u;
+                    const uint32_t o0 = offset2<BF>(z & 255u), o1 = offset2<BF>(z >> 8);
+                    const uint32_t v[2] = {h ? w[r].z : w[r].x, h ? w[r].w : w[r].y};
+#pragma unroll
+                    for (int s = 0; s < 2; s++) {
+                        a[r][s][0] = decode2<BF>(v[s], o0), a[r][s][1] = decode2<BF>(v[s] >> 4, o1);
+                        a[r][s][2] = decode2<BF>(v[s] >> 8, o0), a[r][s][3] = decode2<BF>(v[s] >> 12, o1);
+                    }
+                    if (begin) {
+#pragma unroll
+                        for (int n = 0; n < TN; n++) part[r][n][0] = part[r][n][1] = part[r][n][2] = part[r][n][3] = 0.f;
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < TN; n++) {
+                    const uint4 b = *reinterpret_cast<const uint4 *>(xs + n * 8 * S::RS + i * 128 + h * 64);
+#pragma unroll
+                    for (int r = 0; r < S::RW; r++) {
+                        if (BF) {
+                            pipe::mma_bf16_16816(part[r][n], a[r][0][0], a[r][0][1], a[r][0][2], a[r][0][3], b.x, b.y);
+                            pipe::mma_bf16_16816(part[r][n], a[r][1][0], a[r][1][1], a[r][1][2], a[r][1][3], b.z, b.w);
+                        } else {
+                            pipe::mma_f16_16816(part[r][n], a[r][0][0], a[r][0][1], a[r][0][2], a[r][0][3], b.x, b.y);
+                            pipe::mma_f16_16816(part[r][n], a[r][1][0], a[r][1][1], a[r][1][2], a[r][1][3], b.z, b.w);
+                        }
+                    }
+                }
+                if (end) {
+#pragma unroll
+                    for (int r = 0; r < S::RW; r++) {
+                        const uint32_t s2 = sc[(r * S::NG + gi) * 8];
+                        const float s0 = to_f<BF>((uint16_t)s2), s1 = to_f<BF>((uint16_t)(s2 >> 16));
+#pragma unroll
+                        for (int n = 0; n < TN; n++) {
+                            acc[r][n][0] += s0 * part[r][n][0], acc[r][n][1] += s0 * part[r][n][1];
+                            acc[r][n][2] += s1 * part[r][n][2], acc[r][n][3] += s1 * part[r][n][3];
+                        }
+                    }
                 }
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 4; i++) s_acc[warp][lane][i] = acc[i];
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // ---- join the k slices: [wk][token][row] over the stages, then the ranks
     __syncthreads();
-    if (warp == 0) {
+    float *so = reinterpret_cast<float *>(sm);
+    constexpr int TILE = S::TILE;
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            float v = 0.f;
+    for (int r = 0; r < S::RW; r++)
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) v += s_acc[w][lane][i];
-            const int n = rt * 16 + g + 8 * (i >> 1), to = blockIdx.y * 8 + 2 * t + (i & 1);
-            if (n < p.g.N && to < p.tokens) p.y[to * p.y_stride + n] = from_f<BF>(v);
+        for (int n = 0; n < TN; n++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                so[wk * TILE + (8 * n + 2 * t + (i & 1)) * S::ROWS + (wr * S::RW + r) * 16 + g + 8 * (i >> 1)] = acc[r][n][i];
+    __syncthreads();
+    if (split > 1) {
+        for (int i = tid * 4; i < TILE; i += kThreads * 4) {
+            float4 v = *reinterpret_cast<const float4 *>(so + i);
+#pragma unroll
+            for (int k = 1; k < S::WK; k++) {
+                const float4 u = *reinterpret_cast<const float4 *>(so + k * TILE + i);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+            *reinterpret_cast<float4 *>(so + i) = v;
+        }
+        cluster_sync();
+    }
+    const int row0 = blockIdx.x / split * S::ROWS;
+    for (int i = (tid + rank * kThreads) * 4; i < TILE; i += kThreads * split * 4) {
+        float4 v;
+        if (split > 1) {
+            v = ld_rank(pipe::su32(so + i), 0);
+            for (int k = 1; k < split; k++) {
+                const float4 u = ld_rank(pipe::su32(so + i), k);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+        } else {
+            v = *reinterpret_cast<const float4 *>(so + i);
+#pragma unroll
+            for (int k = 1; k < S::WK; k++) {
+                const float4 u = *reinterpret_cast<const float4 *>(so + k * TILE + i);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
+        }
+        const int tok = tok0 + i / S::ROWS, n = row0 + i % S::ROWS;
+        if (tok < p.tokens) {
+            uint16_t *y = p.y + (int64_t)tok * p.y_stride + n;
+            const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (n + k < p.g.N) y[k] = from_f<BF>(e[k]);
         }
     }
+    if (split > 1) cluster_sync();  // no rank leaves while its sums are read
+}
+
+template <bool BF, int GROUP, bool ZEROS, int TN>
+cudaError_t launch_tn(const MatvecParams &p, int num_sms, cudaStream_t st) {
+    using S = Shape<GROUP, TN>;
+    const int groups = (p.g.row_tiles + S::WR * S::RW - 1) / (S::WR * S::RW), tiles = (p.tokens + 8 * TN - 1) / (8 * TN);
+    // k is split where that shortens the longest SM's work: waves of two CTAs an SM, each as long as
+    // its chunks and about two more for its start and end
+    const int64_t ctas = (int64_t)groups * tiles, slots = 2 * num_sms;
+    int split = 1;
+    int64_t best = INT64_MAX;
+    for (int s = 1; s <= 8; s++) {
+        const int per = (p.g.k_blocks + s - 1) / s, chunks = (per + S::CB - 1) / S::CB;
+        const int64_t cost = (ctas * s + slots - 1) / slots * (chunks + 2);
+        if (cost < best) best = cost, split = s;
+        if (per <= S::CB) break;
+    }
+    auto kern = matvec_kernel<BF, GROUP, ZEROS, TN>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(groups * split, tiles), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = S::SMEM, cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, split);
+}
+
+template <bool BF, int GROUP, bool ZEROS>
+cudaError_t launch_group(const MatvecParams &p, int num_sms, cudaStream_t st) {
+    if (p.tokens <= 8) return launch_tn<BF, GROUP, ZEROS, 1>(p, num_sms, st);
+    if (p.tokens <= 16) return launch_tn<BF, GROUP, ZEROS, 2>(p, num_sms, st);
+    if (p.tokens <= 24) return launch_tn<BF, GROUP, ZEROS, 3>(p, num_sms, st);
+    return launch_tn<BF, GROUP, ZEROS, 4>(p, num_sms, st);
 }
 
 template <bool BF>
-cudaError_t launch(const MatvecParams &p, cudaStream_t st) {
-    const dim3 grid(p.g.row_tiles, (p.tokens + 7) / 8);
-    if (p.g.group == 32)
-        matvec_kernel<BF, 32><<<grid, kWarps * 32, 0, st>>>(p);
-    else if (p.g.group == 64)
-        matvec_kernel<BF, 64><<<grid, kWarps * 32, 0, st>>>(p);
-    else
-        matvec_kernel<BF, 128><<<grid, kWarps * 32, 0, st>>>(p);
-    return cudaGetLastError();
+cudaError_t launch(const MatvecParams &p, int num_sms, cudaStream_t st) {
+    if (p.g.zeros) {
+        if (p.g.group == 32) return launch_group<BF, 32, true>(p, num_sms, st);
+        return p.g.group == 64 ? launch_group<BF, 64, true>(p, num_sms, st) : launch_group<BF, 128, true>(p, num_sms, st);
+    }
+    if (p.g.group == 32) return launch_group<BF, 32, false>(p, num_sms, st);
+    return p.g.group == 64 ? launch_group<BF, 64, false>(p, num_sms, st) : launch_group<BF, 128, false>(p, num_sms, st);
 }
 
 }  // namespace
@@ -173,8 +378,8 @@ cudaError_t launch_pack(const Geometry &g, const uint8_t *codes, const uint16_t 
     return cudaGetLastError();
 }
 
-cudaError_t launch_matvec(const MatvecParams &p, bool bf16, int, cudaStream_t st) {
-    return bf16 ? launch<true>(p, st) : launch<false>(p, st);
+cudaError_t launch_matvec(const MatvecParams &p, bool bf16, int num_sms, cudaStream_t st) {
+    return bf16 ? launch<true>(p, num_sms, st) : launch<false>(p, num_sms, st);
 }
 
 }  // namespace w4
