@@ -130,6 +130,7 @@ struct AttendParams {
     // mass pass, the scores that it reads
     float *part_o;
     float2 *part_ml;
+    int4 *join;  // per CTA of the split kernels (Join)
     float *lse2;
     float *logits;  // [batch, kv_heads, logit_rows][logit_stride]
     int32_t logit_rows;

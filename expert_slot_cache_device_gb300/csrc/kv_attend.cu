@@ -18,15 +18,12 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
         return at;
     };
     p.part_o = nullptr, p.part_ml = nullptr, p.lse2 = nullptr, p.logits = nullptr;
-    if (is_step(p)) {
-        const size_t slots = 2 * (size_t)step_ctas(p, num_sms);
-        p.part_o = reinterpret_cast<float *>(take(slots * kStepRows * p.c.dim * 4));
-        p.part_ml = reinterpret_cast<float2 *>(take(slots * kStepRows * 8));
-    } else {
-        const size_t rows = chunk_part_rows(p, num_sms);
-        p.part_o = reinterpret_cast<float *>(take(rows * p.c.dim * 4));
-        p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
-    }
+    // a part that starts an item and one that goes on with one for each CTA
+    const size_t ctas = is_step(p) ? step_ctas(p, num_sms) : chunk_ctas(p, num_sms);
+    const size_t rows = 2 * ctas * (is_step(p) ? kStepRows : chunk_rows());
+    p.part_o = reinterpret_cast<float *>(take(rows * p.c.dim * 4));
+    p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
+    p.join = reinterpret_cast<int4 *>(take(ctas * 16));
     if (p.mass) {
         p.lse2 = reinterpret_cast<float *>(take((size_t)p.bt.tokens * p.q_heads * 4));
         if (is_step(p)) {

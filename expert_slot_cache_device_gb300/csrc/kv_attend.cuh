@@ -35,7 +35,8 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem
 
 int step_ctas(const AttendParams &p, int num_sms);
 cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
-size_t chunk_part_rows(const AttendParams &p, int num_sms);
+int chunk_ctas(const AttendParams &p, int num_sms);
+size_t chunk_rows();  // rows of an item of the chunk kernel
 cudaError_t launch_chunk(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 cudaError_t launch_mass(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 

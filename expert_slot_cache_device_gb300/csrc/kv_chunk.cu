@@ -225,7 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Walk walk;
     const bool any = plan(p, walk, s_warp, s_sum, &s_walk);
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    if (!any) return;
+    if (!any) {
+        if (tid == 0) p.join[blockIdx.x] = make_int4(0, 0, 0, kJoinNone);
+        return;
+    }
 
     if (tid == 0) {
         for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1), bar_init(&bar.clean[i], 1);
@@ -562,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int CH = D / 8;
         uint32_t cnt = 0, put = 0;
         bool more = true;
+        int4 join = make_int4(0, 0, 0, kJoinNone);
         auto hand_out = [&] {
             if (!more) return;
             if (put >= kParts && !warp_wait(&bar.part_empty[put % kParts], (put / kParts - 1) & 1)) {
@@ -570,6 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             Part n;
             more = walk.next(p, n);
+            if (more && (n.first > 0 || n.last < n.tiles)) {
+                if (n.first == 0)
+                    join.x = n.left, join.y = n.hk, join.z = n.token;
+                else
+                    join.w = n.last == n.tiles ? kJoinEnd : kJoinOn;
+            }
             __syncwarp();
             if (lane == 0) {
                 s_part[put % kParts] = n;
@@ -606,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             hand_out();
         }
+        if (lane == 0) p.join[blockIdx.x] = join;
     }
     if (!ok && lane == 0) flag(p.c.status, FTMOE_ERR_STATE);
     fence_before();
@@ -614,47 +625,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-// Joins the parts of an item that several CTAs covered, in order. One CTA takes 32 rows of an item,
-// its eight warps an eighth of the elements each, a lane a row; rows go out through shared memory.
+// Joins the parts of the item that CTA c of the chunk kernel started. A CTA takes 32 rows, a lane a row
+// and a warp an eighth of the elements; rows go out through shared memory.
 constexpr int kJoinThreads = 256, kJoinRows = 32;
 
 template <bool BF, int D>
-__global__ void __launch_bounds__(kJoinThreads) chunk_combine(const AttendParams p, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) chunk_combine(const AttendParams p) {
     constexpr int E = D / 8;  // elements a thread
-    __shared__ long long s_warp[kJoinThreads / 32];
     __shared__ __align__(16) uint16_t s_out[kJoinRows][D + 8];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int qt = blockIdx.x / (kTileRows / kJoinRows), sub = blockIdx.x % (kTileRows / kJoinRows);
-    const int hk = blockIdx.y, b = blockIdx.z;
-    const Seq sq = seq_info(p.bt, b, nullptr);
-    const int n_qt = row_tiles(p, sq);
-    long long all = 0, less = 0, total, before;
-    for (int i = warp; i < p.bt.batch; i += kJoinThreads / 32) {
-        const Seq s = seq_info(p.bt, i, nullptr);
-        const int n = seq_units(p, s, row_tiles(p, s));
-        all += n;
-        if (i < b) less += n;
-    }
-    block_scan<kJoinThreads>(lane == 0 ? all : 0, total, s_warp);
-    block_scan<kJoinThreads>(lane == 0 ? less : 0, before, s_warp);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: this grid ends after the one before it
-    if (qt >= n_qt) return;
-    const int per = seq_units(p, sq, n_qt), n = item_of(p, sq, qt).tiles;
-    const int ahead = seq_units(p, sq, qt) + kItemCost;
-    const long long W = total * p.c.kv_heads, u = before * p.c.kv_heads + (long long)hk * per + ahead;
-    const int C = used_ctas(grid, W), c0 = unit_owner(u, C, W), c1 = unit_owner(u + n - 1, C, W);
-    if (c0 == c1) return;
-    const int row = sub * kJoinRows + lane, half = p.item_tokens >> 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 join = p.join[c];
+    const int row = blockIdx.y * kJoinRows + lane, half = p.item_tokens >> 1;
     const int li = (row & 127) / (uint32_t)p.group, g = (row & 127) - li * p.group;
-    const int i = qt * p.item_tokens + (row >> 7) * half + li, h = hk * p.group + g;
-    const bool live = li < half && i < sq.q_len;
+    const int i = (row >> 7) * half + li, h = join.y * p.group + g;
+    const bool live = li < half && i < join.x;
     if (!__any_sync(~0u, live)) return;  // the same rows in every warp
+    const int n = count_parts(p.join, c, gridDim.x);
     float M = -INFINITY, L = 0.f, x[E];
 #pragma unroll
     for (int e = 0; e < E; e++) x[e] = 0.f;
-    for (int c = c0; c <= c1; c++) M = fmaxf(M, p.part_ml[(2 * c + (c == c0)) * kTileRows + row].x);
-    for (int c = c0; c <= c1; c++) {
-        const int slot = 2 * c + (c == c0);
+#pragma unroll 4
+    for (int k = 0; k < n; k++) M = fmaxf(M, p.part_ml[(2 * (c + k) + (k == 0)) * kTileRows + row].x);
+#pragma unroll 2
+    for (int k = 0; k < n; k++) {
+        const int slot = 2 * (c + k) + (k == 0);
         const float2 ml = p.part_ml[slot * kTileRows + row];
         const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
         L += ml.y * a;
@@ -666,14 +661,14 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_combine(const AttendParams
     const float f = finish_row(M, L, p.sinks, live ? h : 0, lse2);
 #pragma unroll
     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(&s_out[lane][warp * E + e]) = from_f2<BF>(x[e] * f, x[e + 1] * f);
-    if (warp == 0 && live) put_lse(p, sq.q0 + i, h, lse2);
+    if (warp == 0 && live) put_lse(p, join.z + i, h, lse2);
     __syncthreads();
     for (int k = threadIdx.x; k < kJoinRows * D / 8; k += kJoinThreads) {
-        const int r = k / (D / 8), c = k % (D / 8), rr = sub * kJoinRows + r;
-        const int ri = (rr & 127) / (uint32_t)p.group, rg = (rr & 127) - ri * p.group, rt = qt * p.item_tokens + (rr >> 7) * half + ri;
-        if (ri < half && rt < sq.q_len)
-            *reinterpret_cast<uint4 *>(p.out.d + (int64_t)(sq.q0 + rt) * p.out.token + (hk * p.group + rg) * p.out.head + 8 * c) =
-                *reinterpret_cast<const uint4 *>(&s_out[r][8 * c]);
+        const int r = k / (D / 8), ch = k % (D / 8), rr = blockIdx.y * kJoinRows + r;
+        const int ri = (rr & 127) / (uint32_t)p.group, rg = (rr & 127) - ri * p.group, rt = (rr >> 7) * half + ri;
+        if (ri < half && rt < join.x)
+            *reinterpret_cast<uint4 *>(p.out.d + (int64_t)(join.z + rt) * p.out.token + (join.y * p.group + rg) * p.out.head + 8 * ch) =
+                *reinterpret_cast<const uint4 *>(&s_out[r][8 * ch]);
     }
 }
 
@@ -688,8 +683,7 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     kern<<<C, kThreads, S::kSmem, st>>>(p, qm, km, vm);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int n_qt = (p.bt.max_q + p.item_tokens - 1) / p.item_tokens;
-    return launch_after(chunk_combine<BF, D>, dim3(n_qt * (kTileRows / kJoinRows), p.c.kv_heads, p.bt.batch), kJoinThreads, 0, st, p, C);
+    return launch_after(chunk_combine<BF, D>, dim3(C, kTileRows / kJoinRows), kJoinThreads, 0, st, p);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -740,7 +734,7 @@ int chunk_ctas(const AttendParams &p, int num_sms) {
     return (int)(most < num_sms ? (most > 0 ? most : 1) : num_sms);
 }
 
-size_t chunk_part_rows(const AttendParams &p, int num_sms) { return 2 * (size_t)chunk_ctas(p, num_sms) * kTileRows; }
+size_t chunk_rows() { return kTileRows; }
 
 cudaError_t launch_chunk(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
     const int C = chunk_ctas(p, num_sms);

@@ -2,19 +2,21 @@
 // move of their rows to new pages.
 //
 // Select (one CTA a (sequence, key head)): masses become 32-bit keys in the floats' order (NaN
-// lowest, -0 as 0). Four passes of eight bits from the top find the key T that the
-// (budget - recent)-th largest has: a pass counts, among the keys that agree with T's known
-// bits, each value of the next eight. Then one pass in slot order keeps keys above T and, of those
-// equal to T, the first ones that fill the budget; positions come from block-wide prefix counts.
+// lowest, -0 as 0) in registers, warp w's keys consecutive in slots. The key T of the
+// (budget - recent)-th largest is found two bits at a time from the top: the CTA counts the keys at or
+// above three candidates, sixteen times. (Counting digits in shared memory took four times as
+// long: most masses share their top bits, and atomics on one address wait for each other.)
+// Keys above T stay and, of those equal to T, the first ones that fill the budget; their places
+// come from ballots within a warp and one prefix over the warps.
 //
 // Move: a kept row of K and of V is read and written once, 16 bytes a thread.
-#include "kv.cuh"
+#include "kv_attend.cuh"
 
 namespace ftmoe {
 namespace kv {
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kMoveThreads = 256;
 
 __device__ __forceinline__ uint32_t mass_key(float m) {
@@ -23,90 +25,115 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sums of two 16-bit counts packed in v over the threads before this one, and over all.
-__device__ __forceinline__ uint32_t block_prefix(uint32_t v, uint32_t &total, uint32_t *s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(~0u, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t w = s_warp[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t y = __shfl_up_sync(~0u, w, o);
-            if (lane >= o) w += y;
-        }
-        s_warp[lane] = w;
-    }
-    __syncthreads();
-    total = s_warp[31];
-    const uint32_t r = x - v + (warp ? s_warp[warp - 1] : 0u);
-    __syncthreads();
-    return r;
-}
-
+// KPT: keys a thread holds at once; longer rows take several rounds, read again each time.
+template <int KPT>
 __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p) {
-    __shared__ uint32_t s_hist[256], s_warp[32];
-    __shared__ uint32_t s_pick[2];
-    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
+    __shared__ int s_count[16][3];
+    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
+    constexpr int ROUND = kSelThreads * KPT;
+    const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" :::);
     const int n = seq_kv_len(p.bt, b, p.c.status);
     const int m = n < p.budget ? n : p.budget;
-    const int old = n <= p.budget ? n : n - p.recent;        // candidates: slots [0, old)
-    const int need = m - (n - old);                          // of which this many stay
+    const int old = n <= p.budget ? n : n - p.recent;  // candidates: slots [0, old)
+    const int need = m - (n - old);                    // of which this many stay
     const float *mass = p.mass + b * p.mass_seq + h * p.mass_head;
     int32_t *kept = p.kept + ((int64_t)b * p.c.kv_heads + h) * p.budget;
     float *out = p.new_mass + ((int64_t)b * p.c.kv_heads + h) * p.budget;
     if (h == 0 && tid == 0) p.new_lens[b] = m;
+    if (tid < 48) reinterpret_cast<int *>(s_count)[tid] = 0;
 
-    uint32_t top = 0, mask = 0, left = need;  // T's known bits; how many of the keys that have them stay
-    if (need < old && need > 0)
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) s_hist[tid] = 0;
-            __syncthreads();
-            for (int j = tid; j < old; j += kSelThreads) {
-                const uint32_t k = mass_key(mass[j]);
-                if ((k & mask) == top) atomicAdd(&s_hist[(k >> shift) & 255], 1u);
-            }
-            __syncthreads();
-            if (tid == 0) {
-                uint32_t c = 0;
-                int d = 255;
-                while (c + s_hist[d] < left) c += s_hist[d--];
-                s_pick[0] = d;
-                s_pick[1] = left - c;
-            }
-            __syncthreads();
-            top |= s_pick[0] << shift;
-            mask |= 255u << shift;
-            left = s_pick[1];
-            __syncthreads();
+    const int rounds = (old + ROUND - 1) / ROUND;
+    uint32_t key[KPT];
+    float val[KPT];
+    auto slot = [&](int r, int k) { return r * ROUND + (warp * KPT + k) * 32 + lane; };
+    auto load = [&](int r) {
+#pragma unroll
+        for (int k = 0; k < KPT; k++) {
+            const int j = slot(r, k);
+            val[k] = j < old ? mass[j] : 0.f;
+            key[k] = mass_key(val[k]);
         }
-    // slot order: above T, and the first `left` of those equal to it
-    const bool all = need >= old;
-    int base = 0, eq_before = 0;
-    if (need > 0)
-        for (int j0 = 0; j0 < old; j0 += kSelThreads) {
-            const int j = j0 + tid;
-            const float v = j < old ? mass[j] : 0.f;
-            const uint32_t k = mass_key(v);
-            const bool gt = j < old && (all || k > top), eq = j < old && !all && k == top;
-            uint32_t total;
-            const uint32_t pre = block_prefix((gt ? 1u : 0u) | (eq ? 1u << 16 : 0u), total, s_warp);
-            const int e = eq_before + (int)(pre >> 16), used = e < (int)left ? e : (int)left;
-            const int used0 = eq_before < (int)left ? eq_before : (int)left;
-            const int at = base + (int)(pre & 0xffffu) + used - used0;
-            if (gt || (eq && e < (int)left)) {
-                kept[at] = j;
-                out[at] = v;
+    };
+    if (rounds > 0) load(0);
+    __syncthreads();
+    uint32_t T = 0;  // at least `need` keys are at or above it
+    if (need < old && need > 0) {
+        for (int it = 0; it < 16; it++) {
+            const int shift = 30 - 2 * it;
+            int c[3] = {0, 0, 0};
+            for (int r = 0; r < rounds; r++) {
+                if (rounds > 1) load(r);
+#pragma unroll
+                for (int k = 0; k < KPT; k++)
+                    if (slot(r, k) < old) {
+#pragma unroll
+                        for (int q = 0; q < 3; q++) c[q] += key[k] >= (T | (uint32_t)(q + 1) << shift);
+                    }
             }
-            eq_before += total >> 16;
-            const int used1 = eq_before < (int)left ? eq_before : (int)left;
-            base += (int)(total & 0xffffu) + used1 - used0;
+#pragma unroll
+            for (int q = 0; q < 3; q++) {
+                c[q] = __reduce_add_sync(~0u, c[q]);
+                if (lane == 0 && c[q]) atomicAdd(&s_count[it][q], c[q]);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int q = 2; q >= 0; q--)
+                if (s_count[it][q] >= need) {
+                    T |= (uint32_t)(q + 1) << shift;
+                    break;
+                }
+        }
+    }
+    const bool all = need >= old;
+    int gt_before = 0, eq_before = 0, above = 0;
+    if (!all && need > 0) {  // keys above T: the rest of `need` are equal to it
+        int c = 0;
+        for (int r = 0; r < rounds; r++) {
+            if (rounds > 1) load(r);
+#pragma unroll
+            for (int k = 0; k < KPT; k++) c += slot(r, k) < old && key[k] > T;
+        }
+        if (tid < kSelWarps) s_gt[tid] = 0;
+        c = __reduce_add_sync(~0u, c);
+        __syncthreads();
+        if (lane == 0) s_gt[warp] = c;
+        __syncthreads();
+        above = __reduce_add_sync(~0u, s_gt[lane]);
+        __syncthreads();
+    }
+    const int quota = all ? 0 : need - above;  // keys equal to T that stay
+    if (need > 0)
+        for (int r = 0; r < rounds; r++) {
+            if (rounds > 1) load(r);
+            int gt = 0, eq = 0;
+#pragma unroll
+            for (int k = 0; k < KPT; k++) {
+                const bool in = slot(r, k) < old;
+                gt += __popc(__ballot_sync(~0u, in && (all || key[k] > T)));
+                eq += __popc(__ballot_sync(~0u, in && !all && key[k] == T));
+            }
+            if (lane == 0) s_gt[warp] = gt, s_eq[warp] = eq;
+            __syncthreads();
+            int g0 = gt_before + __reduce_add_sync(~0u, lane < warp ? s_gt[lane] : 0);
+            int e0 = eq_before + __reduce_add_sync(~0u, lane < warp ? s_eq[lane] : 0);
+            gt_before += __reduce_add_sync(~0u, s_gt[lane]);
+            eq_before += __reduce_add_sync(~0u, s_eq[lane]);
+            const uint32_t lt = (1u << lane) - 1;
+#pragma unroll
+            for (int k = 0; k < KPT; k++) {
+                const int j = slot(r, k);
+                const bool isgt = j < old && (all || key[k] > T), iseq = j < old && !all && key[k] == T;
+                const uint32_t bg = __ballot_sync(~0u, isgt), be = __ballot_sync(~0u, iseq);
+                const int g = g0 + __popc(bg & lt), e = e0 + __popc(be & lt);
+                if (isgt || (iseq && e < quota)) {
+                    const int at = g + (e < quota ? e : quota);
+                    kept[at] = j;
+                    out[at] = val[k];
+                }
+                g0 += __popc(bg), e0 += __popc(be);
+            }
+            __syncthreads();
         }
     for (int i = need + tid; i < p.budget; i += kSelThreads) {
         const int j = old + (i - need);
@@ -117,6 +144,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictParams p) {
     const int chunks = p.c.dim >> 3, heads = p.c.kv_heads, b = blockIdx.y;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = seq_kv_len(p.bt, b, p.c.status);
     const int m = n < p.budget ? n : p.budget;
     const int64_t items = (int64_t)m * heads * chunks;
@@ -141,13 +169,22 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictParams p) 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t st) {
-    evict_select<<<dim3(p.c.kv_heads, p.bt.batch), kSelThreads, 0, st>>>(p);
+    const dim3 grid(p.c.kv_heads, p.bt.batch);
+    // keys a thread: the fewest that hold the longest row at once
+    if (p.bt.max_kv <= 2 * kSelThreads)
+        evict_select<2><<<grid, kSelThreads, 0, st>>>(p);
+    else if (p.bt.max_kv <= 8 * kSelThreads)
+        evict_select<8><<<grid, kSelThreads, 0, st>>>(p);
+    else
+        evict_select<16><<<grid, kSelThreads, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     const int most = p.budget < p.bt.max_kv ? p.budget : p.bt.max_kv;
     int64_t blocks = ((int64_t)most * p.c.kv_heads * (p.c.dim >> 3) + kMoveThreads - 1) / kMoveThreads;
     const int64_t cap = ((int64_t)num_sms * 8 + p.bt.batch - 1) / p.bt.batch;
     if (blocks > cap) blocks = cap;
-    if (blocks > 0) evict_move<<<dim3((unsigned)blocks, p.bt.batch), kMoveThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    if (blocks == 0) return cudaSuccess;
+    return launch_after(evict_move, dim3((unsigned)blocks, p.bt.batch), kMoveThreads, 0, st, p);
 }
 
 }  // namespace kv

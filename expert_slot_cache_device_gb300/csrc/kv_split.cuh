@@ -5,13 +5,19 @@
 // that one CTA covers is finished there. Of an item that several cover, each leaves the running
 // maximum, sum and output rows of its part: in slot 2c + 1 if the part starts the item, else in
 // slot 2c (a CTA has at most one part of each kind), and the combine kernel joins them in
-// order. Nothing depends on which CTA runs first.
+// order: one CTA for each item that CTA c starts and does not end. Nothing depends on which
+// runs first.
 #pragma once
 
 #include "kv.cuh"
 
 namespace ftmoe {
 namespace kv {
+
+// What CTA c tells the joining kernel: x rows (or tokens) left of the item that its last part starts
+// without ending (0: none), y key head, z first token row; w: its first part goes on with an item
+// that an earlier CTA started (1), and ends it (2), or neither (0).
+enum { kJoinNone = 0, kJoinOn = 1, kJoinEnd = 2 };
 
 struct Range {
     int lo, hi;  // slots [lo, hi) that at least one row of the item sees; lo is cut down to a multiple of kAlign
@@ -33,7 +39,16 @@ __device__ __forceinline__ Range visible(const Seq &s, int i0, int i1, int windo
 // No CTA is left without a unit: of a grid wider than the line the first W take one each.
 __device__ __forceinline__ int used_ctas(int grid, long long W) { return W < grid ? (int)W : grid; }
 __device__ __forceinline__ long long unit_start(int c, int C, long long W) { return (long long)c * W / C; }
-__device__ __forceinline__ int unit_owner(long long u, int C, long long W) { return (int)(((u + 1) * C - 1) / W); }
+
+// Parts of the item that CTA c starts: its own and those of the CTAs after it, up to the one that ends it.
+__device__ __forceinline__ int count_parts(const int4 *join, int c, int grid) {
+    const int lane = threadIdx.x & 31;
+    for (int n = 1;; n += 32) {
+        const int at = c + n + lane;
+        const unsigned end = __ballot_sync(~0u, at >= grid || join[at].w == kJoinEnd);
+        if (end) return n + __ffs(end);
+    }
+}
 
 // Sum of v over the CTA's NT threads, and over the threads before this one.
 template <int NT>

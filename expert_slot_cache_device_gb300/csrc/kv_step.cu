@@ -109,7 +109,11 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
     const long long W = total_units<D>(p, s_warp, blockIdx.x == 0 ? p.c.status : nullptr);
     const int C = used_ctas(gridDim.x, W);
     asm volatile("griddepcontrol.launch_dependents;" :::);
-    if (blockIdx.x >= C) return;
+    int4 join = make_int4(0, 0, 0, kJoinNone);
+    if (blockIdx.x >= C) {
+        if (tid == 0) p.join[blockIdx.x] = join;
+        return;
+    }
     long long u = unit_start(blockIdx.x, C, W);
     const long long u1 = unit_start(blockIdx.x + 1, C, W);
     const Spot spot = find_unit<D>(p, u, s_warp, &s_spot);
@@ -336,6 +340,12 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
                 if (d0 == 0) p.part_ml[slot * kRows + row] = make_float2(M, L);
             }
         }
+        if (!whole) {
+            if (first == 0)
+                join.x = rows, join.y = hk, join.z = sq.q0;
+            else
+                join.w = last == n_units ? kJoinEnd : kJoinOn;
+        }
         __syncthreads();  // the rings are written again
         // ---- the next item
         u += last - first;
@@ -348,59 +358,56 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
             } while (n_units == 0);
         }
     }
+    if (tid == 0) p.join[blockIdx.x] = join;
 }
 
-// Joins the parts of an item that several CTAs covered, in unit order. One CTA an item.
+// Joins the parts of the item that CTA c of the step kernel started: one warp a row, lanes over the
+// elements, the parts' weights first.
 template <bool BF, int D>
-__global__ void __launch_bounds__(kThreads) step_combine(const AttendParams p, int grid) {
-    __shared__ long long s_warp[kWarps];
-    const int hk = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
-    long long before = 0, all = 0, total, less;
-    for (int i = tid; i < p.bt.batch; i += kThreads) {
-        Range r;
-        const int n = units_of<D>(seq_info(p.bt, i, nullptr), p, r);
-        all += n;
-        if (i < b) before += n;
-    }
-    block_scan<kThreads>(all, total, s_warp);
-    block_scan<kThreads>(before, less, s_warp);
-    const Seq sq = seq_info(p.bt, b, nullptr);
-    Range vis;
-    const int n_units = units_of<D>(sq, p, vis);
-    const long long W = total * p.c.kv_heads, s = less * p.c.kv_heads + (long long)hk * n_units;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // on every path: this grid ends after the one before it
-    if (n_units == 0) return;
-    const int C = used_ctas(grid, W), c0 = unit_owner(s, C, W), c1 = unit_owner(s + n_units - 1, C, W);
-    if (c0 == c1) return;
-    constexpr int PER = kRows * D / kThreads;
-    const int row = tid / (D / PER), d0 = tid % (D / PER) * PER;
-    if (row >= sq.q_len * p.group) return;
-    float M = -INFINITY, L = 0.f, x[PER];
+__global__ void __launch_bounds__(32 * kRows) step_combine(const AttendParams p) {
+    constexpr int E = D / 32;
+    const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 join = p.join[c];
+    if (row >= join.x) return;
+    const int n = count_parts(p.join, c, gridDim.x);
+    auto slot = [&](int i) { return (2 * (c + i) + (i == 0)) * kRows + row; };
+    float M = -INFINITY, L = 0.f, x[E];
 #pragma unroll
-    for (int e = 0; e < PER; e++) x[e] = 0.f;
-    for (int c = c0; c <= c1; c++) M = fmaxf(M, p.part_ml[(2 * c + (c == c0)) * kRows + row].x);
-    for (int c = c0; c <= c1; c++) {
-        const int slot = 2 * c + (c == c0);
-        const float2 ml = p.part_ml[slot * kRows + row];
-        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        L += ml.y * a;
-        const float *po = p.part_o + ((int64_t)slot * kRows + row) * D + d0;
+    for (int e = 0; e < E; e++) x[e] = 0.f;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
 #pragma unroll
-        for (int e = 0; e < PER; e += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(po + e);
-            x[e] += v.x * a, x[e + 1] += v.y * a, x[e + 2] += v.z * a, x[e + 3] += v.w * a;
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float a = 0.f;
+        if (i0 + lane < n) {
+            const float2 ml = p.part_ml[slot(i0 + lane)];
+            a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            L += ml.y * a;
+        }
+        const int m = n - i0 < 32 ? n - i0 : 32;
+#pragma unroll 8
+        for (int i = 0; i < m; i++) {
+            const float w = __shfl_sync(~0u, a, i);
+            const float *po = p.part_o + (int64_t)slot(i0 + i) * D + lane * E;
+            float v[E];
+            if (E == 4)
+                *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(po);
+            else
+                *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(po);
+#pragma unroll
+            for (int e = 0; e < E; e++) x[e] += v[e] * w;
         }
     }
-    const int i = row / p.group, h = hk * p.group + row % p.group;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(~0u, L, o);
+    const int i = row / (uint32_t)p.group, h = join.y * p.group + row - i * p.group;
     float lse2;
     const float f = finish_row(M, L, p.sinks, h, lse2);
-    uint16_t *out = p.out.d + (int64_t)(sq.q0 + i) * p.out.token + h * p.out.head + d0;
+    uint32_t *out = reinterpret_cast<uint32_t *>(p.out.d + (int64_t)(join.z + i) * p.out.token + h * p.out.head + lane * E);
 #pragma unroll
-    for (int e = 0; e < PER; e += 8)
-        *reinterpret_cast<uint4 *>(out + e) =
-            make_uint4(from_f2<BF>(x[e] * f, x[e + 1] * f), from_f2<BF>(x[e + 2] * f, x[e + 3] * f),
-                       from_f2<BF>(x[e + 4] * f, x[e + 5] * f), from_f2<BF>(x[e + 6] * f, x[e + 7] * f));
-    if (d0 == 0) put_lse(p, sq.q0 + i, h, lse2);
+    for (int e = 0; e < E; e += 2) out[e / 2] = from_f2<BF>(x[e] * f, x[e + 1] * f);
+    if (lane == 0) put_lse(p, join.z + i, h, lse2);
 }
 
 // mass += sum over rows of 2^(x - lse2), x the kept scores: one thread a slot, rows in order.
@@ -440,7 +447,7 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     kern<<<C, kThreads, kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(step_combine<BF, D>, dim3(p.c.kv_heads, p.bt.batch), kThreads, 0, st, p, C)) != cudaSuccess) return e;
+    if ((e = launch_after(step_combine<BF, D>, dim3(C), 32 * kRows, 0, st, p)) != cudaSuccess) return e;
     if (p.mass && p.logits)
         e = launch_plain(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
     return e;
