@@ -1,5 +1,6 @@
 // Host side of the attention entry points: argument checks and launches. See include/ftmoe.h
 // for the contract of every entry point.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -34,10 +35,14 @@ int cuda_rc(cudaError_t e, const char *what) {
     return fail(FTMOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// SMs of the current device, asked for once a device.
 int num_sms(int &n) {
+    static std::atomic<int> known[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return FTMOE_OK;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return cuda_rc(e, "device query");
 }
 

@@ -2,6 +2,8 @@
 // points for the dispatch in kv_attend.cu.
 #pragma once
 
+#include <atomic>
+
 #include "kv_split.cuh"
 
 namespace ftmoe {
@@ -12,6 +14,21 @@ constexpr int kStepRows = 16;  // rows a (sequence, key head) of the single-toke
 __device__ __forceinline__ void put_lse(const AttendParams &p, int64_t token, int h, float lse2) {
     if (p.lse) p.lse[token * p.q_heads + h] = lse2 * 0.6931471805599453f;
     if (p.lse2) p.lse2[token * p.q_heads + h] = lse2;
+}
+
+// Dynamic shared memory of a kernel, allowed once a device (the call costs as much as a launch's
+// other host work).
+template <auto Kern>
+cudaError_t allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 template <typename... P, typename... A>

@@ -678,10 +678,9 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     CUtensorMap qm, km, vm;
     const int box = p.c.page_shift < 7 ? 1 << p.c.page_shift : 128;
     if (!query_map(qm, p, BF) || !page_map(km, p.c, true, BF, box) || !page_map(vm, p.c, false, BF, box)) return cudaErrorInvalidValue;
-    auto kern = chunk_kernel<BF, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    cudaError_t e = allow_smem<chunk_kernel<BF, D>>(S::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<C, kThreads, S::kSmem, st>>>(p, qm, km, vm);
+    chunk_kernel<BF, D><<<C, kThreads, S::kSmem, st>>>(p, qm, km, vm);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_after(chunk_combine<BF, D>, dim3(C, kTileRows / kJoinRows), kJoinThreads, 0, st, p);
 }

@@ -5,7 +5,8 @@
 // lowest, -0 as 0) in registers, warp w's keys consecutive in slots. The key T of the
 // (budget - recent)-th largest is found two bits at a time from the top: the CTA counts the keys at or
 // above three candidates, sixteen times. (Counting digits in shared memory took four times as
-// long: most masses share their top bits, and atomics on one address wait for each other.)
+// long: most masses share their top bits, and atomics on one address wait for each other.) The search
+// ends as soon as a candidate has exactly as many keys as are wanted.
 // Keys above T stay and, of those equal to T, the first ones that fill the budget; their places
 // come from ballots within a warp and one prefix over the warps.
 //
@@ -52,7 +53,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
         for (int k = 0; k < KPT; k++) {
             const int j = slot(r, k);
             val[k] = j < old ? mass[j] : 0.f;
-            key[k] = mass_key(val[k]);
+            key[k] = j < old ? mass_key(val[k]) : 0u;  // below every candidate threshold
         }
     };
     if (rounds > 0) load(0);
@@ -66,10 +67,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
                 if (rounds > 1) load(r);
 #pragma unroll
                 for (int k = 0; k < KPT; k++)
-                    if (slot(r, k) < old) {
 #pragma unroll
-                        for (int q = 0; q < 3; q++) c[q] += key[k] >= (T | (uint32_t)(q + 1) << shift);
-                    }
+                    for (int q = 0; q < 3; q++) c[q] += key[k] >= (T | (uint32_t)(q + 1) << shift);
             }
 #pragma unroll
             for (int q = 0; q < 3; q++) {
@@ -77,12 +76,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
                 if (lane == 0 && c[q]) atomicAdd(&s_count[it][q], c[q]);
             }
             __syncthreads();
+            int at = 0;
 #pragma unroll
             for (int q = 2; q >= 0; q--)
-                if (s_count[it][q] >= need) {
-                    T |= (uint32_t)(q + 1) << shift;
-                    break;
-                }
+                if (at == 0 && s_count[it][q] >= need) at = q + 1;
+            T |= (uint32_t)at << shift;
+            if (at && s_count[it][at - 1] == need) {  // exactly the keys at or above T stay
+                T--;
+                break;
+            }
         }
     }
     const bool all = need >= old;
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
         for (int r = 0; r < rounds; r++) {
             if (rounds > 1) load(r);
 #pragma unroll
-            for (int k = 0; k < KPT; k++) c += slot(r, k) < old && key[k] > T;
+            for (int k = 0; k < KPT; k++) c += key[k] > T;
         }
         if (tid < kSelWarps) s_gt[tid] = 0;
         c = __reduce_add_sync(~0u, c);

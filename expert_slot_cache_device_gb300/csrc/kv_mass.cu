@@ -279,10 +279,9 @@ cudaError_t launch(const AttendParams &p, int num_sms, cudaStream_t st) {
     const int64_t items = ((int64_t)p.bt.max_kv + kTileSlots - 1) / kTileSlots * p.bt.batch * p.c.kv_heads;
     if (items >= (int64_t)1 << 31) return cudaErrorInvalidValue;
     if (items == 0) return cudaSuccess;
-    auto kern = mass_kernel<BF, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    cudaError_t e = allow_smem<mass_kernel<BF, D>>(S::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(items < num_sms ? items : num_sms), kThreads, S::kSmem, st>>>(p, (int)items, qm, km);
+    mass_kernel<BF, D><<<(unsigned)(items < num_sms ? items : num_sms), kThreads, S::kSmem, st>>>(p, (int)items, qm, km);
     return cudaGetLastError();
 }
 

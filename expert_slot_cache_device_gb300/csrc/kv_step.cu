@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(256) step_mass(const AttendParams p) {
 template <bool BF, int D>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     auto kern = p.logits ? step_kernel<BF, D, true> : step_kernel<BF, D, false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = p.logits ? allow_smem<step_kernel<BF, D, true>>(kSmem) : allow_smem<step_kernel<BF, D, false>>(kSmem);
     if (e != cudaSuccess) return e;
     kern<<<C, kThreads, kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

@@ -20,7 +20,7 @@
 // reads itself), kStages chunks deep: held in registers instead, two chunks of them spilled. Where row
 // tiles alone do not fill the SMs, up to eight CTAs of a cluster split k and join their sums
 // through distributed shared memory in rank order, so results repeat bit for bit.
-#include "kv.cuh"
+#include "kv_attend.cuh"
 #include "pipeline.cuh"
 
 namespace ftmoe {
@@ -327,8 +327,7 @@ cudaError_t launch_tn(const MatvecParams &p, int num_sms, cudaStream_t st) {
         if (cost < best) best = cost, split = s;
         if (per <= S::CB) break;
     }
-    auto kern = matvec_kernel<BF, GROUP, ZEROS, TN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+    cudaError_t e = kv::allow_smem<matvec_kernel<BF, GROUP, ZEROS, TN>>(S::SMEM);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(groups * split, tiles), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = S::SMEM, cfg.stream = st;
@@ -336,7 +335,7 @@ cudaError_t launch_tn(const MatvecParams &p, int num_sms, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = split, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr, cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p, split);
+    return cudaLaunchKernelEx(&cfg, matvec_kernel<BF, GROUP, ZEROS, TN>, p, split);
 }
 
 template <bool BF, int GROUP, bool ZEROS>

@@ -24,6 +24,15 @@ from . import ftmoe as F
 from .cache import _stream
 
 _DTYPES = {torch.bfloat16: F.DT_BF16, torch.float16: F.DT_F16}
+_F32 = torch.float32
+# The current stream's handle without a Stream object around it (3 us of a call's 13 on the host)
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, device: torch.device) -> int:
+    if stream is None and _current is not None:
+        return _current(device.index)
+    return _stream(stream)
 
 
 def _new(shape, dtype, device, stream):
@@ -186,6 +195,7 @@ class PagedKVCache:
         self.k_pages, self.v_pages = pages
         self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.dtype = *shape, dtype
         self.device = self.k_pages.device
+        self._scale = head_dim ** -0.5
         self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._view = F.KVCacheView(self.k_pages.data_ptr(), self.v_pages.data_ptr(), *self.k_pages.stride()[:3],
                                    *self.v_pages.stride()[:3], _DTYPES[dtype], num_pages, page_size, kv_heads, head_dim,
@@ -193,14 +203,12 @@ class PagedKVCache:
         self._ref = ctypes.byref(self._view)
 
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, tokens: Optional[int] = None):
-        if not isinstance(t, torch.Tensor) or t.dtype != self.dtype or not t.is_cuda or t.dim() != 3:
+        if not isinstance(t, torch.Tensor) or t.dtype is not self.dtype or not t.is_cuda or t.dim() != 3:
             raise ValueError(f"{name}: needs a {self.dtype} device tensor [tokens, heads, head_dim]")
         n, h, d = t.shape
-        if d != self.head_dim or (heads is not None and h != heads) or (tokens is not None and n != tokens):
-            raise ValueError(f"{name}: shape {list(t.shape)} does not match the call")
         st, sh, sd = t.stride()
-        if sd != 1:
-            raise ValueError(f"{name}: rows of head_dim must be contiguous")
+        if d != self.head_dim or sd != 1 or (heads is not None and h != heads) or (tokens is not None and n != tokens):
+            raise ValueError(f"{name}: shape {list(t.shape)} does not match the call, or rows of head_dim are not contiguous")
         # a stride over one element is never taken
         return ctypes.byref(F.RowsView(t.data_ptr(), st if n > 1 else 8, sh if h > 1 else 8))
 
@@ -225,7 +233,7 @@ class PagedKVCache:
                 q_out = _new(q.shape, q.dtype, q.device, stream)
             qo = self._rows(q_out, "q_out", heads, n)
         F.ftmoe_rope_append(self._ref, batch._ref(n), rotary.ref, qr, qo, heads, kr, vr, positions.data_ptr(),
-                            _stream(stream))
+                            _handle(stream, self.device))
         return q_out
 
     def attend(self, batch: KVBatch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
@@ -235,16 +243,17 @@ class PagedKVCache:
         cached slots (``ftmoe_paged_attention``). ``scale`` defaults to head_dim ** -0.5,
         ``sinks`` is fp32 [heads], ``lse`` fp32 [tokens, heads] receives the log-sum-exp, ``mass``
         fp32 [batch, kv_heads, >= max_kv] gets each slot's attention weight added. Returns out."""
-        n, heads = q.shape[0], q.shape[1]
         qr = self._rows(q, "q")
+        n, heads, _ = q.shape
         if heads % self.kv_heads:
             raise ValueError(f"{heads} query heads over {self.kv_heads} key heads")
         if out is None:
             out = _new(q.shape, q.dtype, q.device, stream)
         outr = self._rows(out, "out", heads, n)
-        for name, t, shape in (("sinks", sinks, (heads,)), ("lse", lse, (n, heads))):
-            if t is not None and (t.dtype != torch.float32 or not t.is_cuda or t.shape != shape or not t.is_contiguous()):
-                raise ValueError(f"{name}: needs a contiguous fp32 device tensor {list(shape)}")
+        if sinks is not None and (sinks.dtype is not _F32 or not sinks.is_cuda or sinks.shape != (heads,) or not sinks.is_contiguous()):
+            raise ValueError(f"sinks: needs a contiguous fp32 device tensor [{heads}]")
+        if lse is not None and (lse.dtype is not _F32 or not lse.is_cuda or lse.shape != (n, heads) or not lse.is_contiguous()):
+            raise ValueError(f"lse: needs a contiguous fp32 device tensor [{n}, {heads}]")
         ms = mh = 0
         if mass is not None:
             ms, mh = self._mass(batch, mass)
@@ -257,22 +266,23 @@ class PagedKVCache:
             need = batch._bytes[key] = F.ftmoe_paged_attention_workspace_bytes(self._ref, ref, heads, window, causal,
                                                                                mass is not None)
         ws = _new(need, torch.uint8, self.device, stream) if need else None
-        F.ftmoe_paged_attention(self._ref, ref, qr, heads, self.head_dim ** -0.5 if scale is None else scale, window,
-                                causal, sinks.data_ptr() if sinks is not None else None, outr,
+        F.ftmoe_paged_attention(self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal, sinks.data_ptr() if sinks is not None else None, outr,
                                 lse.data_ptr() if lse is not None else None,
                                 mass.data_ptr() if mass is not None else None, ms, mh,
-                                ws.data_ptr() if need else None, need, _stream(stream))
+                                ws.data_ptr() if need else None, need, _handle(stream, self.device))
         return out
 
     def _mass(self, batch: KVBatch, mass: torch.Tensor):
-        if mass.dtype != torch.float32 or not mass.is_cuda or mass.dim() != 3 or mass.shape[:2] != (batch.batch, self.kv_heads):
+        if mass.dtype is not _F32 or not mass.is_cuda or mass.dim() != 3:
             raise ValueError(f"mass: needs an fp32 device tensor [{batch.batch}, {self.kv_heads}, slots]")
-        if mass.shape[2] < batch.max_kv or (mass.shape[2] > 1 and mass.stride(2) != 1):
-            raise ValueError(f"mass: rows of at least max_kv={batch.max_kv} consecutive elements")
-        ms, mh = mass.stride(0), mass.stride(1)
-        if self.kv_heads == 1:
-            mh = mass.shape[2]
-        if mh < mass.shape[2] or (batch.batch > 1 and ms < mass.shape[2]):
+        b, h, n = mass.shape
+        ms, mh, m1 = mass.stride()
+        if b != batch.batch or h != self.kv_heads or n < batch.max_kv or (n > 1 and m1 != 1):
+            raise ValueError(f"mass: shape {list(mass.shape)}, needs [{batch.batch}, {self.kv_heads}, >= max_kv={batch.max_kv}] "
+                             "with consecutive slots")
+        if h == 1:
+            mh = n
+        if mh < n or (b > 1 and ms < n):
             raise ValueError("mass: rows overlap")
         return ms, mh
 
@@ -296,16 +306,16 @@ class PagedKVCache:
             new_mass = _new(shape, torch.float32, self.device, stream)
         if new_lens is None:
             new_lens = _new(batch.batch, torch.int32, self.device, stream)
-        for name, t, sh, dt in (("kept", kept, shape, torch.int32), ("new_mass", new_mass, shape, torch.float32),
+        for name, t, sh, dt in (("kept", kept, shape, torch.int32), ("new_mass", new_mass, shape, _F32),
                                 ("new_lens", new_lens, shape[:1], torch.int32)):
-            if t.dtype != dt or not t.is_cuda or t.shape != sh or not t.is_contiguous():
+            if t.dtype is not dt or not t.is_cuda or t.shape != sh or not t.is_contiguous():
                 raise ValueError(f"{name}: needs a contiguous {dt} device tensor {list(sh)}")
         # the C call takes one row length for every row
         if new_table.shape[1] * self.page_size < min(budget, batch.max_kv):
             raise ValueError(f"new_table: {new_table.shape[1]} pages a row for {min(budget, batch.max_kv)} slots")
         stride = new_table.stride(0) if batch.batch > 1 else new_table.shape[1]
         F.ftmoe_kv_evict(self._ref, batch._ref(0), mass.data_ptr(), ms, mh, budget, recent, new_table.data_ptr(), stride,
-                         kept.data_ptr(), new_mass.data_ptr(), new_lens.data_ptr(), _stream(stream))
+                         kept.data_ptr(), new_mass.data_ptr(), new_lens.data_ptr(), _handle(stream, self.device))
         return kept, new_mass, new_lens
 
     def status(self, stream=None) -> int:

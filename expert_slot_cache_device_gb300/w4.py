@@ -9,7 +9,7 @@ import torch
 
 from . import ftmoe as F
 from .cache import _stream
-from .kv_cache import _DTYPES, _new
+from .kv_cache import _DTYPES, _handle, _new
 
 
 class W4Weights:
@@ -38,17 +38,21 @@ class W4Weights:
         self.packed = _new(nbytes, torch.uint8, self.device, stream)
         F.ftmoe_w4_pack(codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if self.zeros else None, self.N, self.K,
                         group, self.packed.data_ptr(), nbytes, _stream(stream))
+        self._row = self.K + (-self.K) % 8  # a row stride that is never taken
         self._args = (self.packed.data_ptr(), self.N, self.K, group, self.zeros, _DTYPES[self.dtype])
 
     def matvec(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """y [tokens, N] = x [tokens, K] times the weights' transpose."""
-        if x.dtype != self.dtype or x.dim() != 2 or not x.is_cuda or x.shape[1] != self.K or x.stride(1) != 1:
+        if x.dtype is not self.dtype or x.dim() != 2 or not x.is_cuda:
             raise ValueError(f"x: needs a {self.dtype} device tensor [tokens, {self.K}] with contiguous rows")
-        n = x.shape[0]
+        n, k = x.shape
+        xs, x1 = x.stride()
+        if k != self.K or x1 != 1:
+            raise ValueError(f"x: needs a {self.dtype} device tensor [tokens, {self.K}] with contiguous rows")
         if out is None:
             out = _new((n, self.N), self.dtype, self.device, stream)
-        elif out.dtype != self.dtype or out.shape != (n, self.N) or not out.is_cuda or (self.N > 1 and out.stride(1) != 1):
+        elif out.dtype is not self.dtype or out.shape != (n, self.N) or not out.is_cuda or (self.N > 1 and out.stride(1) != 1):
             raise ValueError(f"out: needs a {self.dtype} device tensor [{n}, {self.N}] with contiguous rows")
-        F.ftmoe_w4_matvec(*self._args, x.data_ptr(), x.stride(0) if n > 1 else self.K + (-self.K) % 8, n,
-                          out.data_ptr(), out.stride(0) if n > 1 else self.N, _stream(stream))
+        F.ftmoe_w4_matvec(*self._args, x.data_ptr(), xs if n > 1 else self._row, n, out.data_ptr(),
+                          out.stride(0) if n > 1 else self.N, _handle(stream, self.device))
         return out
