@@ -93,18 +93,18 @@ constexpr int kLoads = 4;  // 512-byte loads of codes a warp and chunk
 template <int GROUP, int TN>
 struct Shape {
     static constexpr int RW = TN > 2 ? 2 : 1;                // row tiles of a warp, which share its x
-    static constexpr int WK = TN == 1 ? 4 : 2, WR = kWarps / WK;
+    static constexpr int WK = 2, WR = kWarps / WK;
+    static constexpr int CTAS = TN == 1 ? 3 : 2;             // CTAs an SM
     static constexpr int KPW = kLoads / RW;                  // 64-k blocks of a warp and chunk
     static constexpr int CB = KPW * WK;                      // blocks of a chunk
     static constexpr int RS = CB * 128 + 64;                 // bytes of an x row: two rows cover the banks
     static constexpr int NG = GROUP < 64 ? KPW * 2 : KPW * 64 / GROUP;  // groups of a warp's blocks
     static constexpr int META = RW * NG * 48;                // scales [r][group][8 pairs], zeros likewise
     static constexpr int WARP = kLoads * 512 + META;
-    static constexpr int STAGE = 8 * TN * RS + kWarps * WARP;
+    static constexpr int MOST = (8 * TN + 1) * RS + kWarps * WARP; // bytes of a stage with every row of x
     static constexpr int ROWS = WR * RW * 16;
     static constexpr int TILE = 8 * TN * ROWS;               // sums of a CTA; one copy a k slice, over the stages
-    static constexpr int SMEM = kStages * STAGE;
-    static_assert(WK * TILE * 4 <= SMEM, "the sums fit the stages");
+    static_assert(WK * TILE * 4 <= kStages * kWarps * WARP, "the sums fit the stages");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
@@ -129,9 +129,29 @@ __device__ __forceinline__ float4 ld_rank(uint32_t addr, uint32_t rank) {
     return v;
 }
 
-// `split` CTAs of a cluster share k; grid (row groups * split, token tiles of 8 TN).
+template <bool BF>
+__device__ __forceinline__ void mma_next(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF)
+        pipe::mma_bf16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+    else
+        pipe::mma_f16_16816(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+// The same from zero.
+template <bool BF>
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if (BF)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %10, %10, %10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    else
+        pipe::mma_f16_16816_z(d, a[0], a[1], a[2], a[3], b0, b1);
+}
+
+// `split` CTAs of a cluster share k; grid (row groups * split, token tiles of 8 TN); a stage holds `rows`
+// rows of x: those that the call has, and one of zeros where they do not fill the token tiles.
 template <bool BF, int GROUP, bool ZEROS, int TN>
-__global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const MatvecParams p, const int split) {
+__global__ void __launch_bounds__(kThreads, Shape<GROUP, TN>::CTAS) matvec_kernel(const MatvecParams p, const int split, const int rows) {
     using S = Shape<GROUP, TN>;
     constexpr int GK = GROUP > 64 ? 2 : 1;  // blocks that share a scale
     extern __shared__ __align__(128) unsigned char sm[];
@@ -145,41 +165,67 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const MatvecParams 
     const int kb1 = kb1_ < p.g.k_blocks ? kb1_ : p.g.k_blocks;
     const int chunks = (kb1 - kb0 + S::CB - 1) / S::CB;
 
-    const unsigned char *scales = p.packed + p.g.code_bytes;
-    const unsigned char *zeros = scales + (int64_t)p.g.row_tiles * p.g.groups * 32;
-    const uint32_t base = pipe::su32(sm), mine = 8 * TN * S::RS + warp * S::WARP;  // a stage: x, then the warps' parts
+    const uint32_t base = pipe::su32(sm), stage = rows * S::RS + kWarps * S::WARP, mine = rows * S::RS + warp * S::WARP;  // x, the warps' parts
+
+    // What this thread copies of each chunk stays at one place of it: pointers advance by the chunk.
+    // Codes: KPW blocks of each row tile.
+    const int kb_w = kb0 + wk * S::KPW;
+    const unsigned char *cp = p.packed + (((int64_t)rt0 * p.g.k_blocks + kb_w) * 32 + lane) * 16;
+    const int live_r = p.g.row_tiles - rt0;  // row tiles of this warp that there are
+    // Scales and zeros: 16-byte pieces, two of scales and one of zeros a group, PC groups.
+    constexpr int PC = S::RW * S::NG, PIECES = PC * (ZEROS ? 3 : 2), STEP = GROUP > 64 ? S::CB / 2 : (GROUP < 64 ? S::CB * 2 : S::CB);
+    static_assert(PIECES <= 64, "two pieces a lane at most");
+    const unsigned char *mp[PIECES > 32 ? 2 : 1];
+    int m_left[PIECES > 32 ? 2 : 1], m_step[PIECES > 32 ? 2 : 1];  // groups before the row's end; bytes a chunk
+#pragma unroll
+    for (int q = 0; q < (PIECES > 32 ? 2 : 1); q++) {
+        const int i = lane + 32 * q;
+        const bool z = ZEROS && i >= 2 * PC;
+        const int j = z ? i - 2 * PC : i >> 1, r = j / S::NG, rt = rt0 + r;
+        const int gi = (GROUP > 64 ? kb_w / 2 : (GROUP < 64 ? kb_w * 2 : kb_w)) + j % S::NG;
+        const unsigned char *sp = p.packed + p.g.code_bytes;
+        const int64_t at = (int64_t)rt * p.g.groups + gi;
+        mp[q] = z ? sp + (int64_t)p.g.row_tiles * p.g.groups * 32 + at * 16 : sp + at * 32 + (i & 1) * 16;
+        m_left[q] = i < PIECES && rt < p.g.row_tiles ? p.g.groups - gi : 0;
+        m_step[q] = STEP * (z ? 16 : 32);
+    }
+    // x: chunk tid % (8 CB) of rows tid / (8 CB), ...
+    constexpr int XC = S::CB * 8, XR = kThreads / XC;  // 16-byte chunks a row, rows a round
+    const int xr = tid / XC, k1 = kb1 * 64 < p.g.K ? kb1 * 64 : p.g.K;
+    int xk = kb0 * 64 + 8 * (tid % XC);
+    const uint16_t *xp = p.x + (int64_t)(tok0 + xr) * p.x_stride + xk;
+    const uint32_t xd = xr * S::RS + 16 * (tid % XC);
+    int kb_next = kb_w;
+
+    // this lane's x in a stage, a row for each token tile; tokens that are none read a row of zeros
+    uint32_t xo[TN];
+#pragma unroll
+    for (int n = 0; n < TN; n++) xo[n] = (8 * n + g < live_x ? 8 * n + g : rows - 1) * S::RS + wk * S::KPW * 128 + 16 * t;
+    if (live_x < 8 * TN)
+        for (int i = tid; i < kStages * (S::RS / 16); i += kThreads)
+            *reinterpret_cast<uint4 *>(sm + i / (S::RS / 16) * stage + (rows - 1) * S::RS + i % (S::RS / 16) * 16) = make_uint4(0, 0, 0, 0);
 
     auto copy = [&](int c) {
         if (c < chunks) {
-            const uint32_t st = base + (c % kStages) * S::STAGE;
-            const int kc = kb0 + c * S::CB, kb = kc + wk * S::KPW;
+            const uint32_t st = base + (c % kStages) * stage;
+            const int n = kb1 - kb_next;
 #pragma unroll
-            for (int r = 0; r < S::RW; r++) {
-                const int rt = rt0 + r;
-                const bool live = rt < p.g.row_tiles;
+            for (int r = 0; r < S::RW; r++)
 #pragma unroll
                 for (int i = 0; i < S::KPW; i++) {
-                    const bool ok = live && kb + i < kb1;
-                    cp16(st + mine + (r * S::KPW + i) * 512 + lane * 16,
-                         p.packed + (ok ? (((int64_t)rt * p.g.k_blocks + kb + i) * 32 + lane) * 16 : 0), ok);
+                    const bool ok = r < live_r && i < n;
+                    cp16(st + mine + (r * S::KPW + i) * 512 + lane * 16, ok ? cp + (int64_t)r * p.g.k_blocks * 512 + i * 512 : p.packed, ok);
                 }
+#pragma unroll
+            for (int q = 0; q < (PIECES > 32 ? 2 : 1); q++) {
+                if (lane + 32 * q < PIECES) cp16(st + mine + kLoads * 512 + (lane + 32 * q) * 16, m_left[q] > 0 ? mp[q] : p.packed, m_left[q] > 0);
+                mp[q] += m_step[q], m_left[q] -= STEP;
             }
-            // 16-byte pieces: two of scales, one of zeros a group
-            constexpr int PC = S::RW * S::NG;
-            for (int i = lane; i < PC * (ZEROS ? 3 : 2); i += 32) {
-                const bool z = ZEROS && i >= 2 * PC;
-                const int j = z ? i - 2 * PC : i >> 1, r = j / S::NG, rt = rt0 + r;
-                const int gi = (GROUP > 64 ? kb / 2 : (GROUP < 64 ? kb * 2 : kb)) + j % S::NG;
-                const bool ok = rt < p.g.row_tiles && gi < p.g.groups;
-                const int64_t at = (int64_t)rt * p.g.groups + gi;
-                cp16(st + mine + kLoads * 512 + i * 16, z ? zeros + (ok ? at * 16 : 0) : scales + (ok ? at * 32 + (i & 1) * 16 : 0), ok);
-            }
-            const int k0 = kc * 64, k1 = kb1 * 64 < p.g.K ? kb1 * 64 : p.g.K;
-            for (int i = tid; i < live_x * S::CB * 8; i += kThreads) {
-                const int r = i / (S::CB * 8), ch = i % (S::CB * 8), k = k0 + 8 * ch;
-                const bool ok = k < k1;
-                cp16(st + r * S::RS + 16 * ch, p.x + (ok ? (int64_t)(tok0 + r) * p.x_stride + k : 0), ok);
-            }
+            const bool in = xk < k1;
+#pragma unroll
+            for (int r = 0; r < 8 * TN; r += XR)
+                if (xr + r < live_x) cp16(st + xd + r * S::RS, in ? xp + (int64_t)r * p.x_stride : p.x, in);
+            cp += S::CB * 512, kb_next += S::CB, xk += S::CB * 64, xp += S::CB * 64;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -189,17 +235,13 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const MatvecParams 
     for (int r = 0; r < S::RW; r++)
 #pragma unroll
         for (int n = 0; n < TN; n++) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
-    // rows of x past the last token stay zero
-    for (int i = tid; i < (8 * TN - live_x) * (S::RS / 16); i += kThreads)
-#pragma unroll
-        for (int st = 0; st < kStages; st++) *reinterpret_cast<uint4 *>(sm + st * S::STAGE + live_x * S::RS + i * 16) = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int c = 0; c < kStages - 1; c++) copy(c);
     for (int c = 0; c < chunks; c++) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncthreads();  // this chunk is there, and the stage of the one before is read
         copy(c + kStages - 1);
-        const unsigned char *st = sm + (c % kStages) * S::STAGE, *xs = st + g * S::RS + wk * S::KPW * 128 + 16 * t;
+        const unsigned char *st = sm + (c % kStages) * stage;
         const unsigned char *wm = st + mine;
         const uint32_t *sc = reinterpret_cast<const uint32_t *>(wm + kLoads * 512) + g;
         const uint16_t *zc = reinterpret_cast<const uint16_t *>(wm + kLoads * 512 + S::RW * S::NG * 32) + g;
@@ -224,23 +266,17 @@ __global__ void __launch_bounds__(kThreads, 2) matvec_kernel(const MatvecParams 
                         a[r][s][0] = decode2<BF>(v[s], o0), a[r][s][1] = decode2<BF>(v[s] >> 4, o1);
                         a[r][s][2] = decode2<BF>(v[s] >> 8, o0), a[r][s][3] = decode2<BF>(v[s] >> 12, o1);
                     }
-                    if (begin) {
-#pragma unroll
-                        for (int n = 0; n < TN; n++) part[r][n][0] = part[r][n][1] = part[r][n][2] = part[r][n][3] = 0.f;
-                    }
                 }
 #pragma unroll
                 for (int n = 0; n < TN; n++) {
-                    const uint4 b = *reinterpret_cast<const uint4 *>(xs + n * 8 * S::RS + i * 128 + h * 64);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(st + xo[n] + i * 128 + h * 64);
 #pragma unroll
                     for (int r = 0; r < S::RW; r++) {
-                        if (BF) {
-                            pipe::mma_bf16_16816(part[r][n], a[r][0][0], a[r][0][1], a[r][0][2], a[r][0][3], b.x, b.y);
-                            pipe::mma_bf16_16816(part[r][n], a[r][1][0], a[r][1][1], a[r][1][2], a[r][1][3], b.z, b.w);
-                        } else {
-                            pipe::mma_f16_16816(part[r][n], a[r][0][0], a[r][0][1], a[r][0][2], a[r][0][3], b.x, b.y);
-                            pipe::mma_f16_16816(part[r][n], a[r][1][0], a[r][1][1], a[r][1][2], a[r][1][3], b.z, b.w);
-                        }
+                        if (begin)
+                            mma_first<BF>(part[r][n], a[r][0], b.x, b.y);
+                        else
+                            mma_next<BF>(part[r][n], a[r][0], b.x, b.y);
+                        mma_next<BF>(part[r][n], a[r][1], b.z, b.w);
                     }
                 }
                 if (end) {
@@ -316,26 +352,27 @@ template <bool BF, int GROUP, bool ZEROS, int TN>
 cudaError_t launch_tn(const MatvecParams &p, int num_sms, cudaStream_t st) {
     using S = Shape<GROUP, TN>;
     const int groups = (p.g.row_tiles + S::WR * S::RW - 1) / (S::WR * S::RW), tiles = (p.tokens + 8 * TN - 1) / (8 * TN);
-    // k is split where that shortens the longest SM's work: waves of two CTAs an SM, each as long as
-    // its chunks and about two more for its start and end
-    const int64_t ctas = (int64_t)groups * tiles, slots = 2 * num_sms;
+    // k is split where that shortens the busiest SM's work: its CTAs (S::CTAS at once), each as long as its
+    // chunks and about two more for its start and end
+    const int64_t ctas = (int64_t)groups * tiles;
     int split = 1;
     int64_t best = INT64_MAX;
     for (int s = 1; s <= 8; s++) {
         const int per = (p.g.k_blocks + s - 1) / s, chunks = (per + S::CB - 1) / S::CB;
-        const int64_t cost = (ctas * s + slots - 1) / slots * (chunks + 2);
+        const int64_t an_sm = (ctas * s + num_sms - 1) / num_sms, cost = an_sm * chunks + (an_sm + S::CTAS - 1) / S::CTAS * 4;
         if (cost < best) best = cost, split = s;
         if (per <= S::CB) break;
     }
-    cudaError_t e = kv::allow_smem<matvec_kernel<BF, GROUP, ZEROS, TN>>(S::SMEM);
+    cudaError_t e = kv::allow_smem<matvec_kernel<BF, GROUP, ZEROS, TN>>(kStages * S::MOST);
+    const int rows = p.tokens % (8 * TN) == 0 ? 8 * TN : (p.tokens < 8 * TN ? p.tokens : 8 * TN) + 1;
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(groups * split, tiles), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = S::SMEM, cfg.stream = st;
+    cfg.gridDim = dim3(groups * split, tiles), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = kStages * (rows * S::RS + kWarps * S::WARP), cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = split, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr, cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<BF, GROUP, ZEROS, TN>, p, split);
+    return cudaLaunchKernelEx(&cfg, matvec_kernel<BF, GROUP, ZEROS, TN>, p, split, rows);
 }
 
 template <bool BF, int GROUP, bool ZEROS>
