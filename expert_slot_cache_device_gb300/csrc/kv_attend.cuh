@@ -16,6 +16,37 @@ __device__ __forceinline__ void put_lse(const AttendParams &p, int64_t token, in
     if (p.lse2) p.lse2[token * p.q_heads + h] = lse2;
 }
 
+// Clusters: this CTA's rank, a barrier of all, a read of another rank's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();  // the barrier's instructions want converged warps
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_rank(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
+        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_rank1(uint32_t addr, uint32_t rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+        "ld.shared::cluster.f32 %0, [a];\n\t}"
+        : "=f"(v)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
+}
+
 // Dynamic shared memory of a kernel, allowed once a device (the call costs as much as a launch's
 // other host work).
 template <auto Kern>
@@ -31,10 +62,16 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
+// Launch in clusters of `size` CTAs along x.
 template <typename... P, typename... A>
-cudaError_t launch_plain(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args) {
-    kern<<<grid, threads, smem, st>>>(args...);
-    return cudaGetLastError();
+cudaError_t launch_clusters(void (*kern)(P...), dim3 grid, int size, int threads, size_t smem, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = size > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
 // Launch that may start while the kernel before it still runs; it waits (griddepcontrol.wait)

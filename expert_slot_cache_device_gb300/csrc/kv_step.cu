@@ -2,17 +2,20 @@
 // key head (and the few new tokens) are the M = 16 rows of mma.sync m16n8k16. Bound by reading
 // K and V once, 4 dim bytes a slot and key head.
 //
-// A CTA is four warps that share nothing while they read: warp w takes tiles w, w + 4, ... of kTile
-// slots (16 of 128 elements or 32 of 64: 4 KiB of K, 4 KiB of V) through its own ring of kStages
-// tiles filled by 16-byte cp.async, two CTAs an SM, so about 128 KiB are in flight on an SM. Rows
+// A CTA is four warps that share nothing while they read: warp w takes tiles w, w + 4, ... of 16
+// slots (4 KiB of K and of V of 128 elements a head, 2 KiB of 64) through its own ring of kStages
+// tiles filled by 16-byte cp.async, two CTAs an SM (four for 64), so about 128 KiB are in flight on an SM. Rows
 // past the visible range are zero-filled by the copy itself, so what such slots hold never
 // reaches a product. Rows are stored with 16-byte chunk c of row r at c ^ (r % 8), which makes the
 // eight rows of an ldmatrix distinct banks. Scores S = Q K^T and O += P V per tile; the softmax keeps
 // a running maximum that O is rescaled to only when it grew by more than 2^8 (the sum and P use
 // the same stale maximum, so the result is the same).
 //
-// Work is cut by kv_split.cuh: one line of units of 4 kTile slots over all (sequence, key head)s, an
-// equal part for each CTA. With mass, the scaled scores are kept (fp32, powers of two) and the
+// Work is cut by kv_split.cuh: one line of units of 64 slots over all (sequence, key head)s, an equal
+// part for each CTA; a cut inside an item of at most kSnap units moves to its start, since joining
+// parts costs more than the imbalance. Calls with few items and short caches, where latency is
+// all, give each item to the eight CTAs of a cluster instead, which join through distributed shared
+// memory: one launch, and no line of work to walk. With mass, the scaled scores are kept (fp32, powers of two) and the
 // mass kernel adds 2^(x - lse) once the log-sum-exp is known, reading 4 bytes a (row, slot)
 // instead of K again.
 #include "kv_split.cuh"
@@ -24,11 +27,13 @@ namespace kv {
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 3, kRows = kStepRows;
-constexpr int kTileBytes = 4096;  // K or V of one tile
+constexpr int kTile = 16, kUnit = kWarps * kTile, kSnap = 4, kCluster = 8;
 template <int D>
-constexpr int kTile = kTileBytes / (2 * D);
-constexpr int kStageBytes = 2 * kTileBytes, kRingBytes = kStages * kStageBytes;
-constexpr int kSmem = kWarps * kRingBytes;
+struct Shape {
+    static constexpr int kTileBytes = kTile * D * 2;  // K or V of one tile
+    static constexpr int kStageBytes = 2 * kTileBytes, kRingBytes = kStages * kStageBytes, kSmem = kWarps * kRingBytes;
+    static constexpr int kCtas = D == 64 ? 4 : 2;     // an SM
+};
 constexpr float kSlack = 8.f;  // the maximum may lag by 2^8
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -54,80 +59,107 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 
 // Units of one (sequence, key head); a sequence with rows has at least one, which writes the
 // result of rows that see nothing.
-template <int D>
 __device__ __forceinline__ int units_of(const Seq &s, const AttendParams &p, Range &r) {
     r = visible(s, 0, s.q_len, p.window, p.causal);
-    r.lo &= ~(kTile<D> - 1);
-    const int u = (r.hi - r.lo + kWarps * kTile<D> - 1) / (kWarps * kTile<D>);
+    r.lo &= ~(kTile - 1);
+    const int u = (r.hi - r.lo + kUnit - 1) / kUnit;
     return s.q_len == 0 ? 0 : (u > 0 ? u : 1);
 }
 
-// Total units, and the sequence that unit line position `at` (of one key head's share) falls in.
-template <int D>
-__device__ __forceinline__ long long total_units(const AttendParams &p, long long *s_warp, int32_t *status) {
-    long long mine = 0, total;
-    for (int b = threadIdx.x; b < p.bt.batch; b += kThreads) {
-        Range r;
-        mine += units_of<D>(seq_info(p.bt, b, status), p, r);
-    }
-    block_scan<kThreads>(mine, total, s_warp);
-    return total * p.c.kv_heads;
-}
-
+// A place on the line of units: sequence, key head, units into the item.
 struct Spot {
-    int b;
-    long long before;  // units of the sequences before b, all heads
+    int b, hk, first;
 };
 
-template <int D>
-__device__ __forceinline__ Spot find_unit(const AttendParams &p, long long u, long long *s_warp, Spot *s_spot) {
+// This CTA's units [u0, u1) and where u0 lies; false if there are none. s_cut: two entries.
+__device__ __forceinline__ bool plan(const AttendParams &p, long long &u0, long long &u1, Spot &spot, long long *s_warp, Spot *s_spot,
+                                     long long *s_cut) {
+    const int tid = threadIdx.x;
+    int32_t *status = blockIdx.x == 0 ? p.c.status : nullptr;
+    long long mine = 0, total, at = 0;
+    for (int b = tid; b < p.bt.batch; b += kThreads) {
+        Range r;
+        mine += units_of(seq_info(p.bt, b, status), p, r);
+    }
+    const bool once = p.bt.batch <= kThreads;  // then `mine` is sequence tid's, and one scan is all
+    at = block_scan<kThreads>(mine, total, s_warp);
+    const long long W = total * p.c.kv_heads;
+    const int C = used_ctas(gridDim.x, W);
+    if (blockIdx.x >= C) return false;
+    u0 = unit_start(blockIdx.x, C, W), u1 = unit_start(blockIdx.x + 1, C, W);
+    if (tid == 0) s_cut[0] = u0, s_cut[1] = u1;
+    __syncthreads();
     long long base = 0;
     for (int b0 = 0; b0 < p.bt.batch; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        Range r;
-        const long long n = b < p.bt.batch ? (long long)units_of<D>(seq_info(p.bt, b, nullptr), p, r) * p.c.kv_heads : 0;
-        long long total;
-        const long long at = base + block_scan<kThreads>(n, total, s_warp);
-        if (u >= at && u < at + n) s_spot->b = b, s_spot->before = at;
-        base += total;
-        if (base > u) break;
+        const int b = b0 + tid;
+        if (!once) {
+            Range r;
+            mine = b < p.bt.batch ? units_of(seq_info(p.bt, b, nullptr), p, r) : 0;
+            at = block_scan<kThreads>(mine, total, s_warp);
+        }
+        const long long from = base + at * p.c.kv_heads, to = from + mine * p.c.kv_heads;
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            const long long u = e ? u1 : u0;
+            if (u >= from && u < to) {
+                const int n = (int)mine;
+                int first = (int)((u - from) % n);
+                if (n <= kSnap) s_cut[e] = u - first, first = 0;
+                if (e == 0) s_spot->b = b, s_spot->hk = (int)((u - from) / n), s_spot->first = first;
+            }
+        }
+        base += total * p.c.kv_heads;
+        if (once || base > u1) break;
     }
     __syncthreads();
-    return *s_spot;
+    u0 = s_cut[0], u1 = s_cut[1], spot = *s_spot;
+    return u0 < u1;
 }
 
-template <bool BF, int D, bool LOGITS>
-__global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p) {
-    constexpr int T = kTile<D>, NT = T / 8, KT = T / 16, KS = D / 16, CH = D / 8, RPI = 32 / CH;
+template <bool BF, int D, bool LOGITS, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const AttendParams p) {
+    constexpr int kTileBytes = Shape<D>::kTileBytes, kStageBytes = Shape<D>::kStageBytes, kRingBytes = Shape<D>::kRingBytes;
+    constexpr int T = kTile, NT = T / 8, KT = T / 16, KS = D / 16, CH = D / 8, RPI = 32 / CH;
     extern __shared__ __align__(1024) unsigned char sm[];
-    __shared__ long long s_warp[kWarps];
+    __shared__ long long s_warp[kWarps], s_cut[2];
     __shared__ Spot s_spot;
     __shared__ float s_ml[kWarps][kRows][2];
+    __shared__ __align__(16) float s_out[CLUSTER ? kRows : 1][D + 4];  // joined across the cluster
+    __shared__ __align__(16) float s_sum[CLUSTER ? kRows : 1][4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = pipe::su32(sm) + warp * kRingBytes;
 
-    const long long W = total_units<D>(p, s_warp, blockIdx.x == 0 ? p.c.status : nullptr);
-    const int C = used_ctas(gridDim.x, W);
-    asm volatile("griddepcontrol.launch_dependents;" :::);
+    int b, hk, first, n_units;
+    long long u = 0, u1 = 0;
     int4 join = make_int4(0, 0, 0, kJoinNone);
-    if (blockIdx.x >= C) {
-        if (tid == 0) p.join[blockIdx.x] = join;
-        return;
-    }
-    long long u = unit_start(blockIdx.x, C, W);
-    const long long u1 = unit_start(blockIdx.x + 1, C, W);
-    const Spot spot = find_unit<D>(p, u, s_warp, &s_spot);
-    int b = spot.b;
+    Seq sq;
     Range vis;
-    Seq sq = seq_info(p.bt, b, nullptr);
-    int n_units = units_of<D>(sq, p, vis);
-    int hk = (int)((u - spot.before) / n_units), first = (int)((u - spot.before) % n_units);
+    if (CLUSTER) {
+        const int item = blockIdx.x / kCluster, rank = blockIdx.x % kCluster;
+        b = item / p.c.kv_heads, hk = item % p.c.kv_heads;
+        sq = seq_info(p.bt, b, p.c.status);
+        n_units = units_of(sq, p, vis);
+        asm volatile("griddepcontrol.launch_dependents;" :::);
+        if (n_units == 0) return;  // the whole cluster
+        first = rank * n_units / kCluster, u1 = (rank + 1) * n_units / kCluster - first;
+    } else {
+        Spot spot;
+        const bool any = plan(p, u, u1, spot, s_warp, &s_spot, s_cut);
+        asm volatile("griddepcontrol.launch_dependents;" :::);
+        if (!any) {
+            if (tid == 0) p.join[blockIdx.x] = join;
+            return;
+        }
+        b = spot.b, hk = spot.hk, first = spot.first;
+        sq = seq_info(p.bt, b, nullptr);
+        n_units = units_of(sq, p, vis);
+    }
 
     const float c2 = p.scale * kLog2e;
     // this lane's chunk of a copied row, and its swizzled place in the RPI rows of one copy
     const int crow = lane / CH, cch = lane % CH;
 
-    while (u < u1) {
+    do {
         const int last = (int)(u1 - u < n_units - first ? first + (u1 - u) : n_units);  // units [first, last)
         const int rows = sq.q_len * p.group;
         const int lo_q = visible(sq, 0, sq.q_len, p.window, p.causal).lo;
@@ -301,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
                 *reinterpret_cast<float2 *>(mine + (g + 8 * r) * OS + 8 * n + 2 * t) = make_float2(o[n][2 * r] * a, o[n][2 * r + 1] * a);
         }
         __syncthreads();
-        const bool whole = first == 0 && last == n_units;
+        const bool whole = !CLUSTER && first == 0 && last == n_units;
         constexpr int PER = kRows * D / kThreads;  // consecutive elements of one row a thread
         const int row = tid / (D / PER), d0 = tid % (D / PER) * PER;
         if (row < rows) {
@@ -321,7 +353,11 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
                 }
                 x[e] = v.x, x[e + 1] = v.y, x[e + 2] = v.z, x[e + 3] = v.w;
             }
-            if (whole) {
+            if (CLUSTER) {
+#pragma unroll
+                for (int e = 0; e < PER; e += 4) *reinterpret_cast<float4 *>(&s_out[row][d0 + e]) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                if (d0 == 0) *reinterpret_cast<float4 *>(s_sum[row]) = make_float4(M, L, 0.f, 0.f);
+            } else if (whole) {
                 const int i = row / p.group, h = hk * p.group + row % p.group;
                 float lse2;
                 const float f = finish_row(M, L, p.sinks, h, lse2);
@@ -340,6 +376,38 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
                 if (d0 == 0) p.part_ml[slot * kRows + row] = make_float2(M, L);
             }
         }
+        if (CLUSTER) {
+            cluster_sync();
+            // rank r joins rows 2r and 2r + 1: half the threads a row
+            constexpr int EP = kRows * D / kCluster / kThreads;
+            const int jr = (blockIdx.x % kCluster) * (kRows / kCluster) + tid / (D / EP), d = tid % (D / EP) * EP;
+            float M = -INFINITY, L = 0.f, x[2] = {0.f, 0.f};
+            if (jr < rows) {
+                float4 ml[kCluster];
+#pragma unroll
+                for (int k = 0; k < kCluster; k++) ml[k] = ld_rank(pipe::su32(s_sum[jr]), k);
+#pragma unroll
+                for (int k = 0; k < kCluster; k++) M = fmaxf(M, ml[k].x);
+#pragma unroll
+                for (int k = 0; k < kCluster; k++) {
+                    const float a = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+                    L += ml[k].y * a;
+#pragma unroll
+                    for (int e = 0; e < EP; e++) x[e] += ld_rank1(pipe::su32(&s_out[jr][d + e]), k) * a;
+                }
+                const int i = jr / (uint32_t)p.group, h = hk * p.group + jr - i * p.group;
+                float lse2;
+                const float f = finish_row(M, L, p.sinks, h, lse2);
+                uint16_t *out = p.out.d + (int64_t)(sq.q0 + i) * p.out.token + h * p.out.head + d;
+                if (EP == 2)
+                    *reinterpret_cast<uint32_t *>(out) = from_f2<BF>(x[0] * f, x[1] * f);
+                else
+                    *out = from_f<BF>(x[0] * f);
+                if (d == 0) put_lse(p, sq.q0 + i, h, lse2);
+            }
+            cluster_sync();  // no rank leaves while its rows are read
+            return;
+        }
         if (!whole) {
             if (first == 0)
                 join.x = rows, join.y = hk, join.z = sq.q0;
@@ -354,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 2) step_kernel(const AttendParams p)
             hk = 0;
             do {
                 sq = seq_info(p.bt, ++b, nullptr);
-                n_units = units_of<D>(sq, p, vis);
+                n_units = units_of(sq, p, vis);
             } while (n_units == 0);
         }
-    }
+    } while (u < u1);
     if (tid == 0) p.join[blockIdx.x] = join;
 }
 
@@ -368,25 +436,32 @@ __global__ void __launch_bounds__(32 * kRows) step_combine(const AttendParams p)
     constexpr int E = D / 32;
     const int c = blockIdx.x, row = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 join = p.join[c];
-    if (row >= join.x) return;
-    const int n = count_parts(p.join, c, gridDim.x);
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    // the first 32 CTAs' entries and this row's sums of their parts come together
     auto slot = [&](int i) { return (2 * (c + i) + (i == 0)) * kRows + row; };
+    const bool in = c + lane < gridDim.x;
+    const int4 mine = in ? p.join[c + lane] : make_int4(0, 0, 0, kJoinEnd);
+    float2 ml = in ? p.part_ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+    const int4 join = make_int4(__shfl_sync(~0u, mine.x, 0), __shfl_sync(~0u, mine.y, 0), __shfl_sync(~0u, mine.z, 0), 0);
+    if (row >= join.x) return;
+    const unsigned end = __ballot_sync(~0u, lane > 0 && mine.w == kJoinEnd);
+    const int n = end ? __ffs(end) : count_parts(p.join, c, gridDim.x);
     float M = -INFINITY, L = 0.f, x[E];
 #pragma unroll
     for (int e = 0; e < E; e++) x[e] = 0.f;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+    if (lane < n) M = ml.x;
+    for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
     for (int i0 = 0; i0 < n; i0 += 32) {
         float a = 0.f;
         if (i0 + lane < n) {
-            const float2 ml = p.part_ml[slot(i0 + lane)];
+            if (i0) ml = p.part_ml[slot(i0 + lane)];
             a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
             L += ml.y * a;
         }
         const int m = n - i0 < 32 ? n - i0 : 32;
-#pragma unroll 8
+#pragma unroll 16
         for (int i = 0; i < m; i++) {
             const float w = __shfl_sync(~0u, a, i);
             const float *po = p.part_o + (int64_t)slot(i0 + i) * D + lane * E;
@@ -413,6 +488,7 @@ __global__ void __launch_bounds__(32 * kRows) step_combine(const AttendParams p)
 // mass += sum over rows of 2^(x - lse2), x the kept scores: one thread a slot, rows in order.
 __global__ void __launch_bounds__(256) step_mass(const AttendParams p) {
     __shared__ float s_lse[kRows];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int hk = blockIdx.y, b = blockIdx.z;
     const Seq sq = seq_info(p.bt, b, nullptr);
     const int rows = sq.q_len * p.group;
@@ -428,6 +504,7 @@ __global__ void __launch_bounds__(256) step_mass(const AttendParams p) {
     if (j >= vis.hi || j + 4 <= vis.lo) return;
     const float *x = p.logits + (int64_t)(b * p.c.kv_heads + hk) * p.logit_rows * p.logit_stride + j;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int r = 0; r < rows; r++) {
         const float4 v = *reinterpret_cast<const float4 *>(x + r * p.logit_stride);
         const float z = s_lse[r];
@@ -440,31 +517,51 @@ __global__ void __launch_bounds__(256) step_mass(const AttendParams p) {
         if (j + e >= vis.lo && j + e < vis.hi) m[e] += s[e];
 }
 
-template <bool BF, int D>
-cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
-    auto kern = p.logits ? step_kernel<BF, D, true> : step_kernel<BF, D, false>;
-    cudaError_t e = p.logits ? allow_smem<step_kernel<BF, D, true>>(kSmem) : allow_smem<step_kernel<BF, D, false>>(kSmem);
-    if (e != cudaSuccess) return e;
-    kern<<<C, kThreads, kSmem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(step_combine<BF, D>, dim3(C), 32 * kRows, 0, st, p)) != cudaSuccess) return e;
-    if (p.mass && p.logits)
-        e = launch_plain(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
+// The most units that an item of this call can have.
+int most_units(const AttendParams &p) {
+    int64_t slots = p.bt.max_kv;
+    if (p.window && (int64_t)p.window + p.bt.max_q + kTile < slots) slots = p.window + p.bt.max_q + kTile;
+    return (int)((slots + kUnit - 1) / kUnit);
+}
+
+template <bool BF, int D, bool LOGITS>
+cudaError_t launch_kernels(const AttendParams &p, int num_sms, cudaStream_t st) {
+    constexpr int smem = Shape<D>::kSmem;
+    const int C = step_ctas(p, num_sms), most = most_units(p);
+    const int64_t items = (int64_t)p.bt.batch * p.c.kv_heads;
+    cudaError_t e;
+    // Clusters while all of them fit at once and a rank has at most eight units (one sequence of 777
+    // tokens, four key heads: 6 us against 12 with a second kernel; beyond, the line of work
+    // uses every SM); no joining kernel where no item is long enough to be cut.
+    if (items * kCluster <= (int64_t)num_sms * Shape<D>::kCtas && most <= 8 * kCluster) {
+        if ((e = allow_smem<step_kernel<BF, D, LOGITS, true>>(smem)) != cudaSuccess) return e;
+        e = launch_clusters(step_kernel<BF, D, LOGITS, true>, dim3((unsigned)items * kCluster), kCluster, kThreads, smem, st, p);
+    } else {
+        if ((e = allow_smem<step_kernel<BF, D, LOGITS, false>>(smem)) != cudaSuccess) return e;
+        step_kernel<BF, D, LOGITS, false><<<C, kThreads, smem, st>>>(p);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && most > kSnap) e = launch_after(step_combine<BF, D>, dim3(C), 32 * kRows, 0, st, p);
+    }
+    if (e == cudaSuccess && LOGITS) e = launch_after(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
     return e;
+}
+
+template <bool BF, int D>
+cudaError_t launch(const AttendParams &p, int num_sms, cudaStream_t st) {
+    return p.logits ? launch_kernels<BF, D, true>(p, num_sms, st) : launch_kernels<BF, D, false>(p, num_sms, st);
 }
 
 }  // namespace
 
 int step_ctas(const AttendParams &p, int num_sms) {
-    const int unit = kWarps * (p.c.dim == 64 ? kTile<64> : kTile<128>);
-    const long long most = (long long)p.bt.batch * p.c.kv_heads * ((p.bt.max_kv + unit - 1) / unit + 1);
-    return (int)(most < 2 * num_sms ? (most > 0 ? most : 1) : 2 * num_sms);
+    const long long most = (long long)p.bt.batch * p.c.kv_heads * ((p.bt.max_kv + kUnit - 1) / kUnit + 1);
+    const int fit = num_sms * (p.c.dim == 64 ? Shape<64>::kCtas : Shape<128>::kCtas);
+    return (int)(most < fit ? (most > 0 ? most : 1) : fit);
 }
 
 cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
-    const int C = step_ctas(p, num_sms);
-    if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, C, st) : launch<false, 64>(p, C, st);
-    return bf16 ? launch<true, 128>(p, C, st) : launch<false, 128>(p, C, st);
+    if (p.c.dim == 64) return bf16 ? launch<true, 64>(p, num_sms, st) : launch<false, 64>(p, num_sms, st);
+    return bf16 ? launch<true, 128>(p, num_sms, st) : launch<false, 128>(p, num_sms, st);
 }
 
 }  // namespace kv

@@ -110,25 +110,6 @@ struct Shape {
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float4 ld_rank(uint32_t addr, uint32_t rank) {
-    float4 v;
-    asm volatile(
-        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-        "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "r"(addr), "r"(rank)
-        : "memory");
-    return v;
-}
-
 template <bool BF>
 __device__ __forceinline__ void mma_next(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (BF)
@@ -156,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN>::CTAS) matvec_kerne
     constexpr int GK = GROUP > 64 ? 2 : 1;  // blocks that share a scale
     extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rank = split > 1 ? (int)cluster_rank() : 0, wr = warp / S::WK, wk = warp % S::WK;
+    const int rank = split > 1 ? (int)kv::cluster_rank() : 0, wr = warp / S::WK, wk = warp % S::WK;
     const int rt0 = (blockIdx.x / split * S::WR + wr) * S::RW, tok0 = blockIdx.y * 8 * TN;
     const int live_x = p.tokens - tok0 < 8 * TN ? p.tokens - tok0 : 8 * TN;
     // this CTA's blocks of k, whole groups
@@ -317,15 +298,15 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN>::CTAS) matvec_kerne
             }
             *reinterpret_cast<float4 *>(so + i) = v;
         }
-        cluster_sync();
+        kv::cluster_sync();
     }
     const int row0 = blockIdx.x / split * S::ROWS;
     for (int i = (tid + rank * kThreads) * 4; i < TILE; i += kThreads * split * 4) {
         float4 v;
         if (split > 1) {
-            v = ld_rank(pipe::su32(so + i), 0);
+            v = kv::ld_rank(pipe::su32(so + i), 0);
             for (int k = 1; k < split; k++) {
-                const float4 u = ld_rank(pipe::su32(so + i), k);
+                const float4 u = kv::ld_rank(pipe::su32(so + i), k);
                 v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
             }
         } else {
@@ -345,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN>::CTAS) matvec_kerne
                 if (n + k < p.g.N) y[k] = from_f<BF>(e[k]);
         }
     }
-    if (split > 1) cluster_sync();  // no rank leaves while its sums are read
+    if (split > 1) kv::cluster_sync();  // no rank leaves while its sums are read
 }
 
 template <bool BF, int GROUP, bool ZEROS, int TN>
@@ -366,13 +347,8 @@ cudaError_t launch_tn(const MatvecParams &p, int num_sms, cudaStream_t st) {
     cudaError_t e = kv::allow_smem<matvec_kernel<BF, GROUP, ZEROS, TN>>(kStages * S::MOST);
     const int rows = p.tokens % (8 * TN) == 0 ? 8 * TN : (p.tokens < 8 * TN ? p.tokens : 8 * TN) + 1;
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(groups * split, tiles), cfg.blockDim = dim3(kThreads), cfg.dynamicSmemBytes = kStages * (rows * S::RS + kWarps * S::WARP), cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr, cfg.numAttrs = split > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, matvec_kernel<BF, GROUP, ZEROS, TN>, p, split, rows);
+    return kv::launch_clusters(matvec_kernel<BF, GROUP, ZEROS, TN>, dim3(groups * split, tiles), split, kThreads,
+                               kStages * (rows * S::RS + kWarps * S::WARP), st, p, split, rows);
 }
 
 template <bool BF, int GROUP, bool ZEROS>
