@@ -11,9 +11,9 @@
 //                   taken after that; one more than 2^8 above m raises m for the next step, which
 //                   first rescales O (in tensor memory). A half whose sum is too large for P's type (and
 //                   a row's first step) raises m at once. P, the sum and O always share one m.
-//   warp 8          tensor copies: K and V tiles (a box a page and 64 elements, 128-byte swizzle)
-//                   into a ring of stages, pages outside the visible range untouched; the
-//                   queries of the next item once the last S product has read the present ones.
+//   warps 8, 10     tensor copies: K and V tiles (a box a page and 64 elements, 128-byte swizzle)
+//                   into a ring of stages, pages outside the visible range untouched; warp 8 also
+//                   the queries of the next item once the last S product has read the present ones.
 //   warp 9          issues tcgen05.mma, tile 0's and tile 1's in turn: O_t += P_t V (P from tensor
 //                   memory, V with its elements consecutive), S_t = Q_t K^T of the next step
 //                   (both from shared memory). While the softmax of one tile runs, the products of
@@ -33,7 +33,7 @@ namespace kv {
 namespace {
 
 constexpr int kWarps = 12, kThreads = kWarps * 32;
-constexpr int kCopyWarp = 8, kMmaWarp = 9, kHelpWarp = 11;
+constexpr int kCopyWarp = 8, kMmaWarp = 9, kCopyWarp2 = 10, kHelpWarp = 11;
 constexpr int kParts = 4;  // entries of the ring of parts
 constexpr float kSlack = 8.f;
 // The largest sum of 64 P that is let through: P below it is finite in its type, sums in fp32.
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1), bar_init(&bar.clean[i], 1);
-        for (int i = 0; i < kParts; i++) bar_init(&bar.part_full[i], 1), bar_init(&bar.part_empty[i], 10);  // softmax, copies, products
+        for (int i = 0; i < kParts; i++) bar_init(&bar.part_full[i], 1), bar_init(&bar.part_empty[i], 11);  // softmax, copies, products
         bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.done, 1);
         for (int t = 0; t < 2; t++) {
             bar_init(&bar.s[t], 1), bar_init(&bar.p[t][0], 4), bar_init(&bar.p[t][1], 4);
@@ -435,57 +435,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     }
-    if (warp == kCopyWarp) {  // -------------------------------------------- K and V
+    if (warp == kCopyWarp || warp == kCopyWarp2) {  // ------------------------- K and the queries; V
+        const int kv = warp == kCopyWarp2;
         const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTileSlots / box, halves = D / 64;
         const int mine = lane % boxes, half = lane / boxes;  // one box a lane (8 pages x 2 halves at most)
-        uint32_t cnt = 0, nq = 0;
+        uint32_t cnt = kv, nq = 0;                           // stages alternate: K, V
         while (ok && take(bar, s_part, n_part, w, ok)) {
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
-            for (int j = w.first; j < w.last && ok; j++) {
+            auto page_at = [&](int j) {  // this lane's page of step j, -1: nothing to read
                 const int slot = w.lo + j * kTileSlots + mine * box;
-                int page = -1;
-                if (half < halves && slot < w.hi && slot + box > w.seen_lo) {
-                    page = tab[slot >> p.c.page_shift];
-                    if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
-                        flag(p.c.status, FTMOE_ERR_ID_RANGE);
-                        page = -1;
-                    }
+                if (half >= halves || j >= w.last || slot >= w.hi || slot + box <= w.seen_lo) return -1;
+                return (int)tab[slot >> p.c.page_shift];
+            };
+            int next = page_at(w.first);
+            for (int j = w.first; j < w.last && ok; j++, cnt += 2) {
+                int page = next;
+                next = page_at(j + 1);  // on its way while this step waits for its stage
+                if (page != -1 && (uint32_t)page >= (uint32_t)p.c.num_pages) {
+                    flag(p.c.status, FTMOE_ERR_ID_RANGE);
+                    page = -1;
                 }
                 const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * box * 128;
-                const int row = slot & ((1 << p.c.page_shift) - 1);
-#pragma unroll
-                for (int kv = 0; kv < 2; kv++) {
-                    const int st = cnt % S::kStages;
-                    if (!warp_wait(&bar.empty[st], ((cnt / S::kStages) & 1) ^ 1)) {
+                const int slot = w.lo + j * kTileSlots + mine * box, row = slot & ((1 << p.c.page_shift) - 1);
+                const int st = cnt % S::kStages;
+                if (!warp_wait(&bar.empty[st], ((cnt / S::kStages) & 1) ^ 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) bar_expect(&bar.full[st], bytes);
+                __syncwarp();
+                if (page >= 0)
+                    tma4(ring + st * S::kStage + half * S::kHalf + mine * box * 128, kv ? &vmap : &kmap, 64 * half, row, w.hk, page, &bar.full[st]);
+                if (kv == 0 && j == w.first) {  // the item's queries, after its first K
+                    if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) bar_expect(&bar.full[st], bytes);
-                    __syncwarp();
-                    if (page >= 0)
-                        tma4(ring + st * S::kStage + half * S::kHalf + mine * box * 128, kv ? &vmap : &kmap, 64 * half, row, w.hk, page,
-                             &bar.full[st]);
-                    cnt++;
-                    if (kv == 0 && j == w.first) {  // the item's queries, after its first K
-                        if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        nq++;
-                        if (lane == 0) {
-                            const int per = p.item_tokens >> 1, tiles = w.left > per ? 2 : 1;
-                            bar_expect(&bar.qfull, tiles * (D / 64) * per * p.group * 128);
-                            for (int t = 0; t < tiles; t++)
-                                for (int e = 0; e < D / 64; e++)
-                                    tma3(qs + t * (128 * D * 2) + e * S::kHalf, &qmap, 64 * e, w.hk * p.group, w.token + t * per, &bar.qfull);
-                        }
-                        __syncwarp();
+                    nq++;
+                    if (lane == 0) {
+                        const int per = p.item_tokens >> 1, tiles = w.left > per ? 2 : 1;
+                        bar_expect(&bar.qfull, tiles * (D / 64) * per * p.group * 128);
+                        for (int t = 0; t < tiles; t++)
+                            for (int e = 0; e < D / 64; e++)
+                                tma3(qs + t * (128 * D * 2) + e * S::kHalf, &qmap, 64 * e, w.hk * p.group, w.token + t * per, &bar.qfull);
                     }
+                    __syncwarp();
                 }
             }
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed
-            for (uint32_t c = cnt < S::kStages ? 0 : cnt - S::kStages; c < cnt; c++) wait_bar(&bar.full[c % S::kStages], (c / S::kStages) & 1);
+            for (uint32_t c = cnt < S::kStages ? kv : cnt - S::kStages; c < cnt; c += 2) wait_bar(&bar.full[c % S::kStages], (c / S::kStages) & 1);
             if (nq > 0) wait_bar(&bar.qfull, (nq - 1) & 1);
         }
     } else if (warp == kMmaWarp) {  // -------------------------------------- products

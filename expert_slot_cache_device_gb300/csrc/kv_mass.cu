@@ -6,9 +6,12 @@
 // (row, slot).
 //
 // Persistent, one CTA an SM, items dealt round-robin with the slots that most rows see first. Roles:
-//   warps 0-3, 4-7  sums, the even and the odd row tiles of an item; the two join at its end;
-//   warp 8          tensor copies of K (two buffers) and the query tiles (a ring);
-//   warp 9          issues S = K Q^T into four tensor-memory buffers of 128 columns;
+//   warps 0-3, 4-7  sums, the even and the odd row tiles of an item; the two join at its end. The
+//                   first four move the next item's K from shared to tensor memory: read from
+//                   there, a product needs only its queries from shared memory and runs at 64
+//                   cycles instead of 98;
+//   warp 8          tensor copies of K and the query tiles (a ring);
+//   warp 9          issues S = K Q^T into three tensor-memory buffers of 128 columns;
 //   warp 10         the rows' negated log-sum-exps (powers of two) of each tile.
 // Slots outside the visible range may hold anything: they only meet their own lane, whose sum
 // is not written. Every wait is bounded.
@@ -19,17 +22,19 @@ namespace kv {
 namespace {
 
 constexpr int kWarps = 12, kThreads = kWarps * 32, kCopyWarp = 8, kMmaWarp = 9, kLseWarp = 10;
-constexpr int kBufs = 4;
+constexpr int kBufs = 3;
+constexpr int kLse = 4;  // buffers of log-sum-exps, two a loading warp
+constexpr uint32_t kKCol = 384;  // two buffers of K in tensor memory, 64 columns each
 
 template <int D>
 struct Shape {
     static constexpr int kTile = 128 * D * 2, kHalf = 128 * 128;
     static constexpr int kStages = 4;
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTile;
+    static constexpr int kSmem = 1024 + (1 + kStages) * kTile;
 };
 
 struct Bars {
-    uint64_t kfull[2], kempty[2], qfull[4], qempty[4], s[kBufs], free[kBufs], lse[kBufs], odd, even, done;
+    uint64_t kfull, kread, ktm[2], kempty[2], qfull[4], qempty[4], s[kBufs], free[kBufs], lse[kLse], lfree[kLse], odd, even, done;
 };
 
 // Item `n` of the line: slot tile, sequence, key head; the row tiles [first, last) that see some of it.
@@ -55,6 +60,12 @@ __device__ __forceinline__ bool slots_of(const AttendParams &p, int n, Slots &w)
     return w.first < w.last;
 }
 
+// The first of items n, n + gridDim.x, ... that has rows.
+__device__ __forceinline__ int next_item(const AttendParams &p, int items, int n, Slots &w) {
+    while (n < items && !slots_of(p, n, w)) n += gridDim.x;
+    return n;
+}
+
 template <bool BF, int D>
 __global__ void __launch_bounds__(kThreads, 1)
     mass_kernel(const AttendParams p, const int items, const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap) {
@@ -62,16 +73,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
     __shared__ uint32_t s_tmem;
-    __shared__ __align__(16) float s_lse[kBufs][128];
+    __shared__ __align__(16) float s_lse[kLse][128];
     __shared__ float s_odd[128];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t ks = (su32(sm_raw) + 1023u) & ~1023u, qs = ks + 2 * S::kTile;
+    const uint32_t ks = (su32(sm_raw) + 1023u) & ~1023u, qs = ks + S::kTile;
     const int tok = p.item_tokens >> 1;
 
     if (tid == 0) {
-        for (int i = 0; i < 2; i++) bar_init(&bar.kfull[i], 1), bar_init(&bar.kempty[i], 1);
+        bar_init(&bar.kfull, 1), bar_init(&bar.kread, 4);
+        for (int i = 0; i < 2; i++) bar_init(&bar.ktm[i], 4), bar_init(&bar.kempty[i], 1);
         for (int i = 0; i < S::kStages; i++) bar_init(&bar.qfull[i], 1), bar_init(&bar.qempty[i], 1);
-        for (int i = 0; i < kBufs; i++) bar_init(&bar.s[i], 1), bar_init(&bar.free[i], 4), bar_init(&bar.lse[i], 1);
+        for (int i = 0; i < kBufs; i++) bar_init(&bar.s[i], 1), bar_init(&bar.free[i], 4);
+        for (int i = 0; i < kLse; i++) bar_init(&bar.lse[i], 1), bar_init(&bar.lfree[i], 4);
         bar_init(&bar.done, 1), bar_init(&bar.odd, 4), bar_init(&bar.even, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -92,8 +105,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c2 = p.scale * kLog2e;
         const uint64_t cc = pack2(c2, c2);
         uint32_t cnt = 0, ni = 0;
-        for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
-            if (!slots_of(p, n, w)) continue;
+        // K of the item that is `m`-th here, from shared memory to its tensor-memory buffer
+        auto move_k = [&](uint32_t m) {
+            const uint32_t to = tm + lanes + kKCol + 64 * (m & 1), row = tid & 127;
+            if (!warp_wait(&bar.kfull, m & 1) || !warp_wait(&bar.kempty[m & 1], ((m >> 1) & 1) ^ 1)) return false;
+#pragma unroll
+            for (int e = 0; e < D / 64; e++) {
+                uint32_t x[32];
+#pragma unroll
+                for (int c = 0; c < 8; c++)
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(x[4 * c]), "=r"(x[4 * c + 1]), "=r"(x[4 * c + 2]), "=r"(x[4 * c + 3])
+                                 : "r"(ks + e * S::kHalf + row * 128 + ((c ^ (row & 7)) << 4))
+                                 : "memory");
+                tm_st32(to + 32 * e, x);
+            }
+            tm_st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bar.ktm[m & 1]), bar_arrive(&bar.kread);
+            return true;
+        };
+        Slots v;
+        int n = next_item(p, items, blockIdx.x, w);
+        if (t == 0 && n < items) ok = move_k(0);
+        while (n < items && ok) {
+            const int nn = next_item(p, items, n + gridDim.x, v);
+            if (t == 0 && nn < items) ok = move_k(ni + 1);
+            if (!ok) break;
             const int j = w.s0 + (tid & 127), before = w.sq.kv_len - w.sq.q_len;
             // rows [ra, rb) of the sequence see slot j
             int ia = p.causal ? j - before : -before, ib = p.window ? j + p.window - before : w.sq.q_len;
@@ -102,8 +141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float total = 0.f;
             for (int rt = w.first; rt < w.last && ok; rt++, cnt++) {
                 if (((rt - w.first) & 1) != t) continue;
-                const uint32_t bf = cnt % kBufs, ph = (cnt / kBufs) & 1;
-                ok = warp_wait(&bar.lse[bf], ph) && warp_wait(&bar.s[bf], ph);
+                const uint32_t bf = cnt % kBufs, lb = cnt % kLse;
+                ok = warp_wait(&bar.lse[lb], (cnt / kLse) & 1) && warp_wait(&bar.s[bf], (cnt / kBufs) & 1);
                 if (!ok) break;
                 fence_after();
                 // the tile's columns [a, e) see the slot; those past the last whole token are none
@@ -123,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
 #pragma unroll
                     for (int k = 0; k < 64; k += 4) {
-                        const float4 z = *reinterpret_cast<const float4 *>(&s_lse[bf][64 * q + k]);
+                        const float4 z = *reinterpret_cast<const float4 *>(&s_lse[lb][64 * q + k]);
                         const float2 f0 = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, pack2(z.x, z.y)));
                         const float2 f1 = unpack2(fma2(pack2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), cc, pack2(z.z, z.w)));
                         sum[0] = add2(sum[0], pack2(ex2(f0.x), ex2(f0.y)));
@@ -132,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bar.free[bf]);
+                if (lane == 0) bar_arrive(&bar.free[bf]), bar_arrive(&bar.lfree[lb]);
                 const float2 f = unpack2(add2(sum[0], sum[1]));
                 total += f.x + f.y;
             }
@@ -150,30 +189,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) bar_arrive(&bar.even);
             }
             ni++;
+            n = nn, w = v;
         }
     } else if (warp == kCopyWarp) {  // ------------------------------------- K, queries
         const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTileSlots / box, halves = D / 64;
         const int mine = lane % boxes, half = lane / boxes;
         uint32_t nk = 0, nq = 0;
-        for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
-            if (!slots_of(p, n, w)) continue;
-            const int slot = w.s0 + mine * box;
+        auto copy_k = [&](const Slots &v) {
+            const int slot = v.s0 + mine * box;
             int page = -1;
-            if (half < halves && slot < w.vis.hi && slot + box > w.vis.lo) {
-                page = p.bt.table[(int64_t)w.b * p.bt.table_stride + (slot >> p.c.page_shift)];
+            if (half < halves && slot < v.vis.hi && slot + box > v.vis.lo) {
+                page = p.bt.table[(int64_t)v.b * p.bt.table_stride + (slot >> p.c.page_shift)];
                 if ((uint32_t)page >= (uint32_t)p.c.num_pages) page = -1;  // recorded by the pass before
             }
             const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * box * 128;
-            if (!warp_wait(&bar.kempty[nk & 1], ((nk >> 1) & 1) ^ 1)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) bar_expect(&bar.kfull[nk & 1], bytes);
+            if (nk > 0 && !warp_wait(&bar.kread, (nk - 1) & 1)) return false;
+            if (lane == 0) bar_expect(&bar.kfull, bytes);
             __syncwarp();
             if (page >= 0)
-                tma4(ks + (nk & 1) * S::kTile + half * S::kHalf + mine * box * 128, &kmap, 64 * half, slot & ((1 << p.c.page_shift) - 1), w.hk, page,
-                     &bar.kfull[nk & 1]);
+                tma4(ks + half * S::kHalf + mine * box * 128, &kmap, 64 * half, slot & ((1 << p.c.page_shift) - 1), v.hk, page, &bar.kfull);
             nk++;
+            return true;
+        };
+        Slots v;
+        int n = next_item(p, items, blockIdx.x, w);
+        if (n < items) ok = copy_k(w);
+        while (n < items && ok) {
+            // the next item's K goes before this one's queries: it is moved before this item is summed
+            const int nn = next_item(p, items, n + gridDim.x, v);
+            if (nn < items) ok = copy_k(v);
+            if (!ok) break;
             for (int rt = w.first; rt < w.last; rt++, nq++) {
                 const uint32_t st = nq % S::kStages;
                 if (!warp_wait(&bar.qempty[st], ((nq / S::kStages) & 1) ^ 1)) {
@@ -185,31 +230,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < halves)
                     tma3(qs + st * S::kTile + lane * S::kHalf, &qmap, 64 * lane, w.hk * p.group, w.sq.q0 + rt * tok, &bar.qfull[st]);
             }
+            n = nn, w = v;
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed
-            for (uint32_t c = nk < 2 ? 0 : nk - 2; c < nk; c++) wait_bar(&bar.kfull[c & 1], (c >> 1) & 1);
+            if (nk > 0) wait_bar(&bar.kfull, (nk - 1) & 1);
             for (uint32_t c = nq < S::kStages ? 0 : nq - S::kStages; c < nq; c++) wait_bar(&bar.qfull[c % S::kStages], (c / S::kStages) & 1);
         }
     } else if (warp == kMmaWarp) {  // -------------------------------------- products
         constexpr uint32_t IS = kInstr<BF, 128, false>;
         const uint32_t one = elect_one();
-        const uint32_t kd = desc_lo(ks, 16), qd = desc_lo(qs, 16);
+        const uint32_t qd = desc_lo(qs, 16);
         uint32_t nk = 0, cnt = 0;
         for (int n = blockIdx.x; n < items && ok; n += gridDim.x) {
             if (!slots_of(p, n, w)) continue;
             const int tiles = __shfl_sync(~0u, w.last - w.first, 0);
-            ok = warp_wait(&bar.kfull[nk & 1], (nk >> 1) & 1);
+            ok = warp_wait(&bar.ktm[nk & 1], (nk >> 1) & 1);
             for (int i = 0; i < tiles && ok; i++, cnt++) {
                 const uint32_t st = cnt % S::kStages, bf = cnt % kBufs;
                 ok = warp_wait(&bar.qfull[st], (cnt / S::kStages) & 1) && warp_wait(&bar.free[bf], ((cnt / kBufs) & 1) ^ 1);
                 if (!ok) break;
                 fence_after();
-                uint32_t a = kd + (nk & 1) * (S::kTile / 16), b = qd + st * (S::kTile / 16), acc = 0;
+                uint32_t a = tm + kKCol + 64 * (nk & 1), b = qd + st * (S::kTile / 16), acc = 0;
 #pragma unroll 1
                 for (int e = 0; e < D / 64; e++) {
 #pragma unroll
-                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + 128 * bf, a + 2 * k, b + 2 * k, acc);
-                    a += S::kHalf / 16, b += S::kHalf / 16;
+                    for (int k = 0; k < 4; k++, acc = 1) mma_ts<IS>(one, tm + 128 * bf, a + 8 * k, b + 2 * k, acc);
+                    a += 32, b += S::kHalf / 16;
                 }
                 commit(one, &bar.s[bf]);
                 commit(one, &bar.qempty[st]);
@@ -234,12 +280,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         float z[4];
         bool have = false;
         auto put = [&] {  // the values of tile cnt
-            const uint32_t bf = cnt % kBufs;
-            if (!warp_wait(&bar.free[bf], ((cnt / kBufs) & 1) ^ 1)) return false;
+            const uint32_t lb = cnt % kLse;
+            if (!warp_wait(&bar.lfree[lb], ((cnt / kLse) & 1) ^ 1)) return false;
 #pragma unroll
-            for (int k = 0; k < 4; k++) s_lse[bf][lane + 32 * k] = z[k];
+            for (int k = 0; k < 4; k++) s_lse[lb][lane + 32 * k] = z[k];
             __syncwarp();
-            if (lane == 0) bar_arrive(&bar.lse[bf]);
+            if (lane == 0) bar_arrive(&bar.lse[lb]);
             cnt += 2;
             return true;
         };

@@ -90,6 +90,8 @@ ATTEND = [
     ([300, 3], [170, 0], 4, 2, 128, 16, 0, HF),
     ([40, 4], [9000, 6100], 4, 1, 128, 16, 0, BF),
     ([2, 2], [3000, 12000], 8, 8, 64, 16, 0, HF),
+    ([20, 9], [20000, 700], 8, 8, 64, 16, 0, BF),   # more pieces of work than SMs, in both passes of a chunk
+    ([33, 40], [9000, 4100], 24, 8, 128, 32, 0, HF),
 ]
 
 
