@@ -6,13 +6,13 @@
 // (row, slot).
 //
 // Persistent, one CTA an SM, items dealt round-robin with the slots that most rows see first. Roles:
-//   warps 0-3, 4-7  sums, the even and the odd row tiles of an item; the two join at its end. The
+//   warps 0-11      sums: three groups of four warps take an item's row tiles in turn and join at its end. The
 //                   first four move the next item's K from shared to tensor memory: read from
 //                   there, a product needs only its queries from shared memory and runs at 64
 //                   cycles instead of 98;
-//   warp 8          tensor copies of K and the query tiles (a ring);
-//   warp 9          issues S = K Q^T into three tensor-memory buffers of 128 columns;
-//   warp 10         the rows' negated log-sum-exps (powers of two) of each tile.
+//   warp 12         tensor copies of K and the query tiles (a ring);
+//   warp 13         issues S = K Q^T into three tensor-memory buffers of 128 columns;
+//   warps 14, 15    the rows' negated log-sum-exps (powers of two) of each tile.
 // Slots outside the visible range may hold anything: they only meet their own lane, whose sum
 // is not written. Every wait is bounded.
 #include "kv_tc05.cuh"
@@ -21,7 +21,10 @@ namespace ftmoe {
 namespace kv {
 namespace {
 
-constexpr int kWarps = 12, kThreads = kWarps * 32, kCopyWarp = 8, kMmaWarp = 9, kLseWarp = 10;
+// Three groups of four warps sum: with two, every pipe was below half (exponentials 49 %, products 48 %)
+// for want of warps to cover the loads of the others.
+constexpr int kGroups = 3, kSums = 4 * kGroups, kWarps = kSums + 4, kThreads = kWarps * 32;
+constexpr int kCopyWarp = kSums, kMmaWarp = kSums + 1, kLseWarp = kSums + 2;
 constexpr int kBufs = 3;
 constexpr int kLse = 4;  // buffers of log-sum-exps, two a loading warp
 constexpr uint32_t kKCol = 384;  // two buffers of K in tensor memory, 64 columns each
@@ -34,7 +37,7 @@ struct Shape {
 };
 
 struct Bars {
-    uint64_t kfull, kread, ktm[2], kempty[2], qfull[4], qempty[4], s[kBufs], free[kBufs], lse[kLse], lfree[kLse], odd, even, done;
+    uint64_t kfull, kread, ktm[2], kempty[2], qfull[4], qempty[4], s[kBufs], free[kBufs], lse[kLse], lfree[kLse], joined, read, done;
 };
 
 // Item `n` of the line: slot tile, sequence, key head; the row tiles [first, last) that see some of it.
@@ -74,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Bars bar;
     __shared__ uint32_t s_tmem;
     __shared__ __align__(16) float s_lse[kLse][128];
-    __shared__ float s_odd[128];
+    __shared__ float s_part[kGroups - 1][128];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ks = (su32(sm_raw) + 1023u) & ~1023u, qs = ks + S::kTile;
     const int tok = p.item_tokens >> 1;
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < S::kStages; i++) bar_init(&bar.qfull[i], 1), bar_init(&bar.qempty[i], 1);
         for (int i = 0; i < kBufs; i++) bar_init(&bar.s[i], 1), bar_init(&bar.free[i], 4);
         for (int i = 0; i < kLse; i++) bar_init(&bar.lse[i], 1), bar_init(&bar.lfree[i], 4);
-        bar_init(&bar.done, 1), bar_init(&bar.odd, 4), bar_init(&bar.even, 4);
+        bar_init(&bar.done, 1), bar_init(&bar.joined, 4 * (kGroups - 1)), bar_init(&bar.read, 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -99,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     Slots w;
 
-    if (warp < 8) {  // ---------------------------------------------------- sums
+    if (warp < kSums) {  // ---------------------------------------------------- sums
         const int t = warp >> 2;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const float c2 = p.scale * kLog2e;
@@ -140,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ib > w.sq.q_len) ib = w.sq.q_len;
             float total = 0.f;
             for (int rt = w.first; rt < w.last && ok; rt++, cnt++) {
-                if (((rt - w.first) & 1) != t) continue;
+                if ((rt - w.first) % kGroups != t) continue;
                 const uint32_t bf = cnt % kBufs, lb = cnt % kLse;
                 ok = warp_wait(&bar.lse[lb], (cnt / kLse) & 1) && warp_wait(&bar.s[bf], (cnt / kBufs) & 1);
                 if (!ok) break;
@@ -175,18 +178,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 f = unpack2(add2(sum[0], sum[1]));
                 total += f.x + f.y;
             }
-            // the odd tiles' sums join the even ones'
+            // the other groups' sums join the first's, in order
             if (!ok) break;
-            if (t == 1) {
-                ok = warp_wait(&bar.even, (ni & 1) ^ 1);  // the last item's have been read
-                s_odd[tid & 127] = total;
+            if (t > 0) {
+                ok = warp_wait(&bar.read, (ni & 1) ^ 1);  // the last item's have been read
+                s_part[t - 1][tid & 127] = total;
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bar.odd);
+                if (lane == 0) bar_arrive(&bar.joined);
             } else {
-                ok = warp_wait(&bar.odd, ni & 1);
-                if (ok && j >= w.vis.lo && j < w.vis.hi) p.mass[w.b * p.mass_seq + w.hk * p.mass_head + j] += total + s_odd[tid];
+                ok = warp_wait(&bar.joined, ni & 1);
+#pragma unroll
+                for (int k = 0; k < kGroups - 1; k++) total += s_part[k][tid];
+                if (ok && j >= w.vis.lo && j < w.vis.hi) p.mass[w.b * p.mass_seq + w.hk * p.mass_head + j] += total;
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bar.even);
+                if (lane == 0) bar_arrive(&bar.read);
             }
             ni++;
             n = nn, w = v;
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(one, &bar.done);
         warp_wait(&bar.done, 0);
     } else {  // -------------------------------------------------------------- log-sum-exps
-        // warp 10 the even, warp 11 the odd tiles of the whole line; a lane's four rows sit at the same
+        // one the even, one the odd tiles of the whole line; a lane's four rows sit at the same
         // places of every tile, and the next tile's values are under way while this one's wait
         int at[4], i4[4];
 #pragma unroll
