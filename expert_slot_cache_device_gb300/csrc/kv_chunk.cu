@@ -47,7 +47,7 @@ struct Shape {
     static constexpr int kStages = D == 128 ? 4 : 8;
     static constexpr int kHalf = kTileSlots * 128;            // 64 elements of 128 rows
     static constexpr int kQ = kTileRows * D * 2;
-    static constexpr int kOut = 8 * 32 * 128;                 // a warp's 32 output rows, 64 elements at a time
+    static constexpr int kOut = 8 * 32 * 64;                  // a warp's 32 output rows, 32 elements at a time
     static constexpr int kSmem = 1024 + kStages * kStage + kQ + kOut;
     static constexpr uint32_t kO = 256, kP = D == 128 ? 0 : 384;  // columns of O_0 and P_0
     static constexpr uint32_t kPStep = D == 128 ? 128 : 64;       // from P_0 to P_1
@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int *s_sum = reinterpret_cast<int *>(sm_raw);  // the ring is not in use yet
     __shared__ Walk s_walk;
     __shared__ Part s_part[kParts];
+    __shared__ int64_t s_row[128];  // offset of a tile's row from its first token and head, -1 past the last
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = (su32(sm_raw) + 1023u) & ~1023u, qs = ring + S::kStages * S::kStage, stage_out = qs + S::kQ;
 
@@ -230,6 +231,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
+    if (tid < 128) {
+        const int i = tid / (uint32_t)p.group, g = tid - i * p.group;
+        s_row[tid] = i < p.item_tokens >> 1 ? i * p.out.token + g * p.out.head : -1;
+    }
     if (tid == 0) {
         for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1), bar_init(&bar.clean[i], 1);
         for (int i = 0; i < kParts; i++) bar_init(&bar.part_full[i], 1), bar_init(&bar.part_empty[i], 11);  // softmax, copies, products
@@ -381,55 +386,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t token = w.token + row_i;
             const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
             float f = raise ? up : 1.f, lse2 = 0.f;
-            if (whole) {
-                f *= finish_row(m, l, p.sinks, h, lse2);
-                // 64 elements of the warp's rows at a time through shared memory, 16-byte chunk c of row r at
-                // c ^ (r % 8), so that eight lanes write a row's 128 bytes together
-                const uint32_t st = stage_out + warp * 4096;
+            if (whole) f *= finish_row(m, l, p.sinks, h, lse2);
+            // 32 elements of the warp's rows at a time, in a loop: run once an item, unrolled code took most of its
+            // time to be fetched
+            const uint32_t st = stage_out + warp * 2048;
+            uint16_t *out = p.out.d + (int64_t)(w.token + t * (p.item_tokens >> 1)) * p.out.token + w.hk * p.group * p.out.head;
+            const int here = w.left < p.item_tokens ? w.left : p.item_tokens;
+            const int rows = (here - t * (p.item_tokens >> 1)) * p.group - 32 * (warp & 3);  // of this warp's 32
+            float *po = p.part_o + (int64_t)part * kTileRows * D + tid;
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+                uint32_t y[32];
+                tm_ld32(tO + k, y);
+                if (whole) {
+                    // through shared memory, 16-byte chunk c of row r at c ^ (r / 2 % 4), so that four lanes write a
+                    // row's 64 bytes together
 #pragma unroll
-                for (int k = 0; k < D; k += 64) {
-                    uint32_t y[64];
-                    tm_ld64(tO + k, y);
-                    tm_ld_wait(y);
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < 8; c++) {
+                    for (int c = 0; c < 4; c++) {
                         uint32_t z[4];
 #pragma unroll
                         for (int e = 0; e < 4; e++)
                             z[e] = from_f2<BF>(__uint_as_float(y[8 * c + 2 * e]) * f, __uint_as_float(y[8 * c + 2 * e + 1]) * f);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st + lane * 128 + ((c ^ (lane & 7)) << 4)), "r"(z[0]),
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(st + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)), "r"(z[0]),
                                      "r"(z[1]), "r"(z[2]), "r"(z[3])
                                      : "memory");
                     }
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 8; c++) {
-                        const int r = 4 * c + (lane >> 3), row = 32 * (warp & 3) + r;
-                        const int i = row / (uint32_t)p.group, g = row - i * p.group, per = p.item_tokens >> 1;
+                    for (int c = 0; c < 4; c++) {
+                        const int r = 8 * c + (lane >> 2);
+                        const int64_t off = s_row[32 * (warp & 3) + r];
                         uint4 z;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(z.x), "=r"(z.y), "=r"(z.z), "=r"(z.w)
-                                     : "r"(st + r * 128 + (((lane ^ r) & 7) << 4))
+                                     : "r"(st + r * 64 + (((lane ^ (r >> 1)) & 3) << 4))
                                      : "memory");
-                        if (i < per && t * per + i < w.left)
-                            *reinterpret_cast<uint4 *>(p.out.d + (int64_t)(w.token + t * per + i) * p.out.token +
-                                                       (w.hk * p.group + g) * p.out.head + k + 8 * (lane & 7)) = z;
+                        if (off >= 0 && r < rows) *reinterpret_cast<uint4 *>(out + off + k + 8 * (lane & 3)) = z;
                     }
-                }
-                if (live) put_lse(p, token, h, lse2);
-            } else {
-                // parts are kept element by element, rows consecutive: a warp's store is one line
-                float *po = p.part_o + (int64_t)part * kTileRows * D + tid;
-#pragma unroll
-                for (int k = 0; k < D; k += 32) {
-                    uint32_t y[32];
-                    tm_ld32(tO + k, y);
+                    __syncwarp();
+                } else {  // parts are kept element by element, rows consecutive: a warp's store is one line
 #pragma unroll
                     for (int e = 0; e < 32; e++) po[(k + e) * kTileRows] = __uint_as_float(y[e]) * f;
                 }
-                p.part_ml[part * kTileRows + tid] = make_float2(m, l);
             }
+            if (!whole)
+                p.part_ml[part * kTileRows + tid] = make_float2(m, l);
+            else if (live)
+                put_lse(p, token, h, lse2);
             fence_before();  // O is read before the next item's first P is announced
         }
     } else {
