@@ -445,17 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t cnt = kv, nq = 0;                           // stages alternate: K, V
         while (ok && take(bar, s_part, n_part, w, ok)) {
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
-            auto page_at = [&](int j) {  // this lane's page of step j, -1: nothing to read
+            auto wanted = [&](int j) {  // whether this lane has a box of step j to read
                 const int slot = w.lo + j * kTileSlots + mine * box;
-                if (half >= halves || j >= w.last || slot >= w.hi || slot + box <= w.seen_lo) return -1;
-                return (int)tab[slot >> p.c.page_shift];
+                return half < halves && j < w.last && slot < w.hi && slot + box > w.seen_lo;
             };
+            auto page_at = [&](int j) { return wanted(j) ? tab[(w.lo + j * kTileSlots + mine * box) >> p.c.page_shift] : -1; };
             int next = page_at(w.first);
             for (int j = w.first; j < w.last && ok; j++, cnt += 2) {
                 int page = next;
                 next = page_at(j + 1);  // on its way while this step waits for its stage
-                if (page != -1 && (uint32_t)page >= (uint32_t)p.c.num_pages) {
-                    flag(p.c.status, FTMOE_ERR_ID_RANGE);
+                if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
+                    if (wanted(j)) flag(p.c.status, FTMOE_ERR_ID_RANGE);
                     page = -1;
                 }
                 const uint32_t bytes = __popc(__ballot_sync(~0u, page >= 0)) * box * 128;
