@@ -163,9 +163,9 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
         const int b = s_walk->b;
         const Seq s = seq_info(p.bt, b, nullptr);
         const int n_qt = row_tiles(p, s), per = seq_units(p, s, n_qt);
-        long long at = s_walk->left;
-        const int hk = (int)(at / per);
-        int rem = (int)(at % per), found = -1, first = 0, before = 0;
+        const uint32_t at = (uint32_t)s_walk->left;  // within one sequence: below 2^32
+        const int hk = at / (uint32_t)per;
+        int rem = at - hk * per, found = -1, first = 0, before = 0;
         for (int q0 = 0; q0 < n_qt && found < 0; q0 += 32) {
             const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles + kItemCost : 0;
             int x = n;
@@ -223,18 +223,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = (su32(sm_raw) + 1023u) & ~1023u, qs = ring + S::kStages * S::kStage, stage_out = qs + S::kQ;
 
-    Walk walk;
-    const bool any = plan(p, walk, s_warp, s_sum, &s_walk);
-    asm volatile("griddepcontrol.launch_dependents;" :::);
-    if (!any) {
-        if (tid == 0) p.join[blockIdx.x] = make_int4(0, 0, 0, kJoinNone);
-        return;
-    }
-
-    if (tid < 128) {
-        const int i = tid / (uint32_t)p.group, g = tid - i * p.group;
-        s_row[tid] = i < p.item_tokens >> 1 ? i * p.out.token + g * p.out.head : -1;
-    }
     if (tid == 0) {
         for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1), bar_init(&bar.clean[i], 1);
         for (int i = 0; i < kParts; i++) bar_init(&bar.part_full[i], 1), bar_init(&bar.part_empty[i], 11);  // softmax, copies, products
@@ -249,9 +237,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    if (tid < 128) {
+        const int i = tid / (uint32_t)p.group, g = tid - i * p.group;
+        s_row[tid] = i < p.item_tokens >> 1 ? i * p.out.token + g * p.out.head : -1;
+    }
+    Walk walk;
+    const bool any = plan(p, walk, s_warp, s_sum, &s_walk);
+    asm volatile("griddepcontrol.launch_dependents;" :::);
     fence_before();
     __syncthreads();
     fence_after();
+    if (!any) {  // the whole CTA
+        if (tid == 0) p.join[blockIdx.x] = make_int4(0, 0, 0, kJoinNone);
+        if (warp == kMmaWarp)
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*reinterpret_cast<volatile uint32_t *>(&s_tmem)) : "memory");
+        return;
+    }
     const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(&s_tmem);
     bool ok = true;
     Part w;
@@ -637,27 +638,46 @@ __global__ void __launch_bounds__(kJoinThreads) chunk_combine(const AttendParams
     __shared__ __align__(16) uint16_t s_out[kJoinRows][D + 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 join = p.join[c];
+    // the first 32 CTAs' entries come together
+    const int4 mine = c + lane < gridDim.x ? p.join[c + lane] : make_int4(0, 0, 0, kJoinEnd);
+    const int4 join = make_int4(__shfl_sync(~0u, mine.x, 0), __shfl_sync(~0u, mine.y, 0), __shfl_sync(~0u, mine.z, 0), 0);
     const int row = blockIdx.y * kJoinRows + lane, half = p.item_tokens >> 1;
     const int li = (row & 127) / (uint32_t)p.group, g = (row & 127) - li * p.group;
     const int i = (row >> 7) * half + li, h = join.y * p.group + g;
     const bool live = li < half && i < join.x;
     if (!__any_sync(~0u, live)) return;  // the same rows in every warp
-    const int n = count_parts(p.join, c, gridDim.x);
-    float M = -INFINITY, L = 0.f, x[E];
+    const unsigned end = __ballot_sync(~0u, lane > 0 && mine.w == kJoinEnd);
+    const int n = end ? __ffs(end) : count_parts(p.join, c, gridDim.x);
+    // the first four parts, which are mostly all, load at once
+    constexpr int K = 4;
+    auto slot = [&](int k) { return 2 * (c + k) + (k == 0); };
+    auto part = [&](int k) { return p.part_o + ((int64_t)slot(k) * D + warp * E) * kTileRows + row; };
+    float2 ml[K];
+    float v[K][E], M = -INFINITY, L = 0.f, x[E];
+#pragma unroll
+    for (int k = 0; k < K; k++) {
+        ml[k] = k < n ? p.part_ml[slot(k) * kTileRows + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; e++) v[k][e] = k < n ? part(k)[e * kTileRows] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < K; k++) M = fmaxf(M, ml[k].x);
+    for (int k = K; k < n; k++) M = fmaxf(M, p.part_ml[slot(k) * kTileRows + row].x);
 #pragma unroll
     for (int e = 0; e < E; e++) x[e] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < n; k++) M = fmaxf(M, p.part_ml[(2 * (c + k) + (k == 0)) * kTileRows + row].x);
-#pragma unroll 2
-    for (int k = 0; k < n; k++) {
-        const int slot = 2 * (c + k) + (k == 0);
-        const float2 ml = p.part_ml[slot * kTileRows + row];
-        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        L += ml.y * a;
-        const float *po = p.part_o + ((int64_t)slot * D + warp * E) * kTileRows + row;
 #pragma unroll
-        for (int e = 0; e < E; e++) x[e] += po[e * kTileRows] * a;
+    for (int k = 0; k < K; k++) {
+        const float a = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - M);
+        L += ml[k].y * a;
+#pragma unroll
+        for (int e = 0; e < E; e++) x[e] += v[k][e] * a;
+    }
+    for (int k = K; k < n; k++) {
+        const float2 y = p.part_ml[slot(k) * kTileRows + row];
+        const float a = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+        L += y.y * a;
+#pragma unroll
+        for (int e = 0; e < E; e++) x[e] += part(k)[e * kTileRows] * a;
     }
     float lse2;
     const float f = finish_row(M, L, p.sinks, live ? h : 0, lse2);

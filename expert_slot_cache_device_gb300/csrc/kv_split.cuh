@@ -38,7 +38,10 @@ __device__ __forceinline__ Range visible(const Seq &s, int i0, int i1, int windo
 
 // No CTA is left without a unit: of a grid wider than the line the first W take one each.
 __device__ __forceinline__ int used_ctas(int grid, long long W) { return W < grid ? (int)W : grid; }
-__device__ __forceinline__ long long unit_start(int c, int C, long long W) { return (long long)c * W / C; }
+__device__ __forceinline__ long long unit_start(int c, int C, long long W) {
+    if ((uint64_t)c * (uint64_t)W < (1ull << 32)) return (uint32_t)(c * (uint32_t)W) / (uint32_t)C;  // (a 64-bit division takes longer than the rest)
+    return (long long)c * W / C;
+}
 
 // Parts of the item that CTA c starts: its own and those of the CTAs after it, up to the one that ends it.
 __device__ __forceinline__ int count_parts(const int4 *join, int c, int grid) {
