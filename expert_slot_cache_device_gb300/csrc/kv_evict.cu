@@ -17,7 +17,6 @@ namespace ftmoe {
 namespace kv {
 namespace {
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kMoveThreads = 256;
 
 __device__ __forceinline__ uint32_t mass_key(float m) {
@@ -26,12 +25,12 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// KPT: keys a thread holds at once; longer rows take several rounds, read again each time.
-template <int KPT>
-__global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p) {
-    __shared__ int s_count[16][3];
-    __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
-    constexpr int ROUND = kSelThreads * KPT;
+// NT threads hold KPT keys each at once; longer rows take several rounds, read again each time.
+template <int NT, int KPT>
+__global__ void __launch_bounds__(NT) evict_select(const EvictParams p) {
+    constexpr int ROUND = NT * KPT;
+    __shared__ int s_count[2][3][32];  // per warp, two iterations' in turn
+    __shared__ int s_gt[32], s_eq[32];
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" :::);
     const int n = seq_kv_len(p.bt, b, p.c.status);
@@ -42,7 +41,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
     int32_t *kept = p.kept + ((int64_t)b * p.c.kv_heads + h) * p.budget;
     float *out = p.new_mass + ((int64_t)b * p.c.kv_heads + h) * p.budget;
     if (h == 0 && tid == 0) p.new_lens[b] = m;
-    if (tid < 48) reinterpret_cast<int *>(s_count)[tid] = 0;
+    if (tid < 32) {
+        s_gt[tid] = s_eq[tid] = 0;
+#pragma unroll
+        for (int q = 0; q < 3; q++) s_count[0][q][tid] = s_count[1][q][tid] = 0;
+    }
 
     const int rounds = (old + ROUND - 1) / ROUND;
     uint32_t key[KPT];
@@ -73,15 +76,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
 #pragma unroll
             for (int q = 0; q < 3; q++) {
                 c[q] = __reduce_add_sync(~0u, c[q]);
-                if (lane == 0 && c[q]) atomicAdd(&s_count[it][q], c[q]);
+                if (lane == 0) s_count[it & 1][q][warp] = c[q];
             }
             __syncthreads();
-            int at = 0;
+            int at = 0, has = 0;
 #pragma unroll
-            for (int q = 2; q >= 0; q--)
-                if (at == 0 && s_count[it][q] >= need) at = q + 1;
+            for (int q = 2; q >= 0; q--) {
+                const int sum = __reduce_add_sync(~0u, s_count[it & 1][q][lane]);
+                if (at == 0 && sum >= need) at = q + 1, has = sum;
+            }
             T |= (uint32_t)at << shift;
-            if (at && s_count[it][at - 1] == need) {  // exactly the keys at or above T stay
+            if (has == need) {  // exactly the keys at or above T stay
                 T--;
                 break;
             }
@@ -96,9 +101,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
 #pragma unroll
             for (int k = 0; k < KPT; k++) c += key[k] > T;
         }
-        if (tid < kSelWarps) s_gt[tid] = 0;
         c = __reduce_add_sync(~0u, c);
-        __syncthreads();
         if (lane == 0) s_gt[warp] = c;
         __syncthreads();
         above = __reduce_add_sync(~0u, s_gt[lane]);
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select(const EvictParams p)
             }
             __syncthreads();
         }
-    for (int i = need + tid; i < p.budget; i += kSelThreads) {
+    for (int i = need + tid; i < p.budget; i += NT) {
         const int j = old + (i - need);
         kept[i] = i < m ? j : -1;
         out[i] = i < m ? mass[j] : 0.f;
@@ -172,13 +175,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictParams p) 
 
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t st) {
     const dim3 grid(p.c.kv_heads, p.bt.batch);
-    // keys a thread: the fewest that hold the longest row at once
-    if (p.bt.max_kv <= 2 * kSelThreads)
-        evict_select<2><<<grid, kSelThreads, 0, st>>>(p);
-    else if (p.bt.max_kv <= 8 * kSelThreads)
-        evict_select<8><<<grid, kSelThreads, 0, st>>>(p);
+    // the fewest threads that hold the longest row at once: every count waits for all of them (1013 slots:
+    // 256 threads 7.7 us, 1024 threads 12.2)
+    if (p.bt.max_kv <= 256 * 8)
+        evict_select<256, 8><<<grid, 256, 0, st>>>(p);
+    else if (p.bt.max_kv <= 512 * 16)
+        evict_select<512, 16><<<grid, 512, 0, st>>>(p);
     else
-        evict_select<16><<<grid, kSelThreads, 0, st>>>(p);
+        evict_select<1024, 16><<<grid, 1024, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int most = p.budget < p.bt.max_kv ? p.budget : p.bt.max_kv;
