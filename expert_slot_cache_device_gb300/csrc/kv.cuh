@@ -133,6 +133,8 @@ struct AttendParams {
     int4 *join;  // per CTA of the split kernels (Join)
     float *lse2;
     float *logits;  // [batch, kv_heads, logit_rows][logit_stride]
+    float *mass_parts;  // [mass_split][batch, kv_heads][logit_stride], the mass pass of chunks cut by rows
+    int32_t mass_split;
     int32_t logit_rows;
     int64_t logit_stride;
 };

@@ -17,7 +17,7 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
         off += (bytes + 255) & ~(size_t)255;
         return at;
     };
-    p.part_o = nullptr, p.part_ml = nullptr, p.lse2 = nullptr, p.logits = nullptr;
+    p.part_o = nullptr, p.part_ml = nullptr, p.lse2 = nullptr, p.logits = nullptr, p.mass_parts = nullptr, p.mass_split = 1;
     // a part that starts an item and one that goes on with one for each CTA
     const size_t ctas = is_step(p) ? step_ctas(p, num_sms) : chunk_ctas(p, num_sms);
     const size_t rows = 2 * ctas * (is_step(p) ? kStepRows : chunk_rows());
@@ -30,6 +30,9 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
             p.logit_rows = p.bt.max_q * p.group;
             p.logit_stride = ((int64_t)p.bt.max_kv + 127) & ~(int64_t)127;
             p.logits = reinterpret_cast<float *>(take((size_t)p.bt.batch * p.c.kv_heads * p.logit_rows * p.logit_stride * 4));
+        } else if ((p.mass_split = mass_split(p, num_sms)) > 1) {
+            p.logit_stride = ((int64_t)p.bt.max_kv + 127) & ~(int64_t)127;
+            p.mass_parts = reinterpret_cast<float *>(take((size_t)p.mass_split * p.bt.batch * p.c.kv_heads * p.logit_stride * 4));
         }
     }
     return off;

@@ -92,6 +92,7 @@ cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStrea
 int chunk_ctas(const AttendParams &p, int num_sms);
 size_t chunk_rows();  // rows of an item of the chunk kernel
 cudaError_t launch_chunk(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
+int mass_split(const AttendParams &p, int num_sms);
 cudaError_t launch_mass(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 
 }  // namespace kv

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = (su32(sm_raw) + 1023u) & ~1023u, qs = ring + S::kStages * S::kStage, stage_out = qs + S::kQ;
 
     if (tid == 0) {
-        for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 1), bar_init(&bar.clean[i], 1);
+        for (int i = 0; i < S::kStages; i++) bar_init(&bar.full[i], 1), bar_init(&bar.empty[i], 2), bar_init(&bar.clean[i], 1);
         for (int i = 0; i < kParts; i++) bar_init(&bar.part_full[i], 1), bar_init(&bar.part_empty[i], 11);  // softmax, copies, products
         bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.done, 1);
         for (int t = 0; t < 2; t++) {
@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_async();
                     __syncwarp();
                 }
-                if (lane == 0) bar_arrive(&bar.clean[st]);
+                // the stage is not filled again before this warp has seen it, so that no wait meets a barrier two phases on
+                if (lane == 0) bar_arrive(&bar.clean[st]), bar_arrive(&bar.empty[st]);
             }
             hand_out();
         }

@@ -92,6 +92,8 @@ ATTEND = [
     ([2, 2], [3000, 12000], 8, 8, 64, 16, 0, HF),
     ([20, 9], [20000, 700], 8, 8, 64, 16, 0, BF),   # more pieces of work than SMs, in both passes of a chunk
     ([33, 40], [9000, 4100], 24, 8, 128, 32, 0, HF),
+    ([97, 40, 13, 88, 2, 61, 30], [1500, 900, 1100, 300, 640, 1290, 200], 40, 8, 64, 16, 0, HF),  # pieces of 1, 2, ... row tiles
+    ([300, 120, 7], [900, 2500, 3100], 32, 8, 64, 16, 200, BF),
 ]
 
 
