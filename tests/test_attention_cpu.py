@@ -68,6 +68,7 @@ def test_attention_refusals():
         refused(F.ERR_INVALID_ARG, attend, cache(), batch(**bad))
     refused(F.ERR_FORMAT, attend, cache(dtype=F.DT_F32), batch())
     refused(F.ERR_FORMAT, attend, cache(head_dim=96), batch())
+    refused(F.ERR_FORMAT, lambda: attend(cache(), batch(), heads=2 * 129))
     for kw in (dict(heads=3), dict(heads=0), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf),
                dict(window=-1), dict(window=4, causal=False), dict(q=rows(d=A + 8)), dict(q=rows(token=100)),
                dict(out=rows(head=8)), dict(out=rows(d=None)), dict(mass=A, mh=63)):

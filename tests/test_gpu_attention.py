@@ -136,6 +136,26 @@ def test_attention(case, mass):
     check_attend(w, window, None, True, mass=mass)
 
 
+@pytest.mark.parametrize("count,q,heads,kv,dim,page", [(400, 1, 17, 1, 64, 16), (300, 1, 2, 1, 128, 16), (390, 3, 8, 1, 64, 32),
+                                                       (150, 2, 6, 2, 128, 16)])
+def test_attention_many_sequences(count, q, heads, kv, dim, page):
+    """More sequences than a CTA has threads, some without new tokens, some empty."""
+    r = torch.Generator().manual_seed(count)
+    q_lens = [int(torch.randint(0, q + 1, (1,), generator=r)) for _ in range(count)]
+    kv_lens = [int(torch.randint(0, 70, (1,), generator=r)) + n for n in q_lens]
+    kv_lens[3], kv_lens[count - 1], q_lens[count - 1] = 0, 300, q
+    w = World(q_lens, kv_lens, heads, kv, dim, page, BF, seed=count)
+    check_attend(w, 0, None, True)
+
+
+@pytest.mark.parametrize("heads,kv,q_lens,kv_lens", [(128, 1, [3, 2], [200, 90]), (40, 1, [9, 1], [30, 400]), (33, 1, [1], [77]),
+                                                     (100, 2, [5], [300])])
+def test_attention_wide_groups(heads, kv, q_lens, kv_lens):
+    """Query heads a key head up to the most there can be, and ones that leave rows of a tile unused."""
+    for dim, dt in ((64, BF), (128, HF)):
+        check_attend(World(q_lens, kv_lens, heads, kv, dim, 16, dt, seed=heads), 0, None, True)
+
+
 @pytest.mark.parametrize("case", [ATTEND[i] for i in (1, 4, 6, 9, 13, 17, 19)], ids=str)
 def test_attention_sinks_and_head_order(case):
     """A sink logit per head (one of them -inf: none), and caches with heads outside slots."""
