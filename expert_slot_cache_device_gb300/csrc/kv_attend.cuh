@@ -62,6 +62,28 @@ cudaError_t allow_smem(int bytes) {
     return e;
 }
 
+// Clusters of `size` (at most 8) CTAs of a kernel that the device holds at once, asked once a device.
+template <auto Kern>
+int most_clusters(int size, int threads, int smem) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    int n = dev < 64 ? known[dev][size].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size), cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, Kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev < 64) known[dev][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Launch in clusters of `size` CTAs along x.
 template <typename... P, typename... A>
 cudaError_t launch_clusters(void (*kern)(P...), dim3 grid, int size, int threads, size_t smem, cudaStream_t st, A... args) {

@@ -233,6 +233,8 @@ __device__ __forceinline__ int seq_units(const AttendParams &p, const Seq &s, in
 bool page_map(CUtensorMap &m, const View &c, bool keys, bool bf16, int box_slots);
 // Tensor map of query rows: [token][head][element], boxes of 64 elements x group heads x 128 / group tokens.
 bool query_map(CUtensorMap &m, const AttendParams &p, bool bf16);
+// Tensor map of rows: [row][column], boxes of 64 columns x box_rows rows; zeros past the ends.
+bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, int box_rows, bool bf16);
 
 }  // namespace kv
 }  // namespace ftmoe

@@ -2,26 +2,25 @@
 //
 // The codes are laid out once, in the order in which mma.sync m16n8k16 takes its A operand, so
 // a warp's load of a tile of 16 rows x 64 k is 512 consecutive bytes: lane (g, t) = (lane / 4,
-// lane % 4) holds four words, word s the eight codes of step s: nibble i of the low half is the
+// lane % 4) holds four words, word s the eight codes of the 16 k of step s: nibble i of the low half is the
 // first and nibble i of the high half the second element of fragment register a_i (a0: row g, a1:
-// row g + 8 at the first two of the step's k; a2, a3 the same at its last two). Which k a lane's
-// fragment stands for is free as long as x agrees: step s of lane t takes k = 32 (s / 2) + 8 t +
-// 4 (s % 2) + 0..3 of the block, so that a lane's x for a block are two 16-byte reads of a plain row
-// and a step stays inside one group of 32. (w >> 4i) & 0x000f000f OR'ed into the bits of
+// row g + 8 at k = 2 t; a2, a3 the same at 2 t + 8). (w >> 4i) & 0x000f000f OR'ed into the bits of
 // (128, 128) in bf16, or (1024, 1024) in f16, makes 128 + q (1024 + q) exactly, and subtracting
 // 128 + z leaves the exact integer q - z. A group's products are summed by the tensor cores in
 // fp32 from zero; its scale multiplies that sum in fp32, so no weight is rounded.
 //   packed: codes [row tile][64-k block][lane][16 B], then scales [row tile][group][8] pairs (rows g,
 //   g + 8), then zeros [row tile][group][8] pairs of bytes. Rows past N and k past K hold zeros.
 //
-// Bound by reading the codes once. A CTA is eight warps: kWR row tiles (pairs of tiles for more than 16
-// tokens) times kWK slices of k, so that several warps share the x that a chunk of k stages in shared
-// memory. Codes and scales go to shared memory too (each lane copies the 16 bytes of codes that it
-// reads itself), kStages chunks deep: held in registers instead, two chunks of them spilled. Where row
-// tiles alone do not fill the SMs, up to eight CTAs of a cluster split k and join their sums
+// This kernel is for up to 16 tokens, w4_tc05.cu for more. Bound by the instructions that decode (about 100 a warp for 16 x 64 codes)
+// and by a call's start and end; the codes alone are 1.2 us of the 6.2 us of one token times 2048 x 7168, and 8.8 of the 18.5
+// (3.6 TB/s) of 16384 x 7168. A CTA is eight warps: WR row tiles times WK slices of k, so that several
+// warps share the x that a chunk of k stages in shared memory. Codes and scales go to shared memory too (each lane
+// copies the 16 bytes of codes that it reads itself), kStages chunks deep: held in registers instead, two
+// chunks of them spilled. Where row tiles alone do not fill the SMs, up to eight CTAs of a cluster split k and join their sums
 // through distributed shared memory in rank order, so results repeat bit for bit.
 #include "kv_attend.cuh"
 #include "pipeline.cuh"
+#include "w4.cuh"
 
 namespace ftmoe {
 namespace w4 {
@@ -46,7 +45,7 @@ __global__ void pack_kernel(const Geometry g, const uint8_t *codes, const uint16
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
                     const int n = rt * 16 + (lane >> 2) + 8 * (r & 1);
-                    const int k = kb * 64 + 32 * (s >> 1) + 8 * (lane & 3) + 4 * (s & 1) + 2 * (r >> 1) + e;
+                    const int k = kb * 64 + 16 * s + 8 * (r >> 1) + 2 * (lane & 3) + e;
                     uint32_t q = 0;
                     if (n < g.N && k < g.K) q = codes[(int64_t)n * (g.K / 2) + (k >> 1)] >> (4 * (k & 1)) & 15;
                     w |= q << (4 * r + 16 * e);
@@ -69,40 +68,21 @@ __global__ void pack_kernel(const Geometry g, const uint8_t *codes, const uint16
     }
 }
 
-// (128 + z, 128 + z) in bf16 or (1024 + z, 1024 + z) in f16.
-template <bool BF>
-__device__ __forceinline__ uint32_t offset2(uint32_t z) {
-    return (BF ? 0x43004300u : 0x64006400u) | z | z << 16;
-}
-template <bool BF>
-__device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t off) {
-    uint32_t v;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(w), "r"(0x000f000fu), "r"(BF ? 0x43004300u : 0x64006400u));
-    if (BF) {
-        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&off));
-        return *reinterpret_cast<const uint32_t *>(&d);
-    }
-    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&v), *reinterpret_cast<const __half2 *>(&off));
-    return *reinterpret_cast<const uint32_t *>(&d);
-}
-
 constexpr int kWarps = 8, kThreads = kWarps * 32, kStages = 3;
-constexpr int kLoads = 4;  // 512-byte loads of codes a warp and chunk
 
 // TN tiles of eight tokens; WK_ slices of k a CTA.
 template <int GROUP, int TN, int WK_>
 struct Shape {
-    static constexpr int RW = TN > 2 ? 2 : 1;                // row tiles of a warp, which share its x
     static constexpr int WK = WK_, WR = kWarps / WK;
     static constexpr int CTAS = TN == 1 ? 3 : 2;             // CTAs an SM
-    static constexpr int KPW = kLoads / RW;                  // 64-k blocks of a warp and chunk
+    static constexpr int KPW = 4;                            // 64-k blocks of a warp and chunk
     static constexpr int CB = KPW * WK;                      // blocks of a chunk
-    static constexpr int RS = CB * 128 + 64;                 // bytes of an x row: two rows cover the banks
+    static constexpr int RS = CB * 128 + 16;                 // bytes of an x row: eight rows' 16 bytes cover the banks
     static constexpr int NG = GROUP < 64 ? KPW * 2 : KPW * 64 / GROUP;  // groups of a warp's blocks
-    static constexpr int META = RW * NG * 48;                // scales [r][group][8 pairs], zeros likewise
-    static constexpr int WARP = kLoads * 512 + META;
+    static constexpr int META = NG * 48;                     // scales [group][8 pairs], zeros likewise
+    static constexpr int WARP = KPW * 512 + META;
     static constexpr int MOST = (8 * TN + 1) * RS + kWarps * WARP; // bytes of a stage with every row of x
-    static constexpr int ROWS = WR * RW * 16;
+    static constexpr int ROWS = WR * 16;
     static constexpr int TILE = 8 * TN * ROWS;               // sums of a CTA; one copy a k slice, over the stages
     static_assert(WK * TILE * 4 <= kStages * kWarps * WARP, "the sums fit the stages");
 };
@@ -138,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
     extern __shared__ __align__(128) unsigned char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int rank = split > 1 ? (int)kv::cluster_rank() : 0, wr = warp / S::WK, wk = warp % S::WK;
-    const int rt0 = (blockIdx.x / split * S::WR + wr) * S::RW, tok0 = blockIdx.y * 8 * TN;
+    const int rt0 = blockIdx.x / split * S::WR + wr, tok0 = blockIdx.y * 8 * TN;
     const int live_x = p.tokens - tok0 < 8 * TN ? p.tokens - tok0 : 8 * TN;
     // this CTA's blocks of k, whole groups
     const int pairs = (p.g.k_blocks + GK - 1) / GK;
@@ -152,9 +132,9 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
     // Codes: KPW blocks of each row tile.
     const int kb_w = kb0 + wk * S::KPW;
     const unsigned char *cp = p.packed + (((int64_t)rt0 * p.g.k_blocks + kb_w) * 32 + lane) * 16;
-    const int live_r = p.g.row_tiles - rt0;  // row tiles of this warp that there are
+    const bool live_r = rt0 < p.g.row_tiles;
     // Scales and zeros: 16-byte pieces, two of scales and one of zeros a group, PC groups.
-    constexpr int PC = S::RW * S::NG, PIECES = PC * (ZEROS ? 3 : 2), STEP = GROUP > 64 ? S::CB / 2 : (GROUP < 64 ? S::CB * 2 : S::CB);
+    constexpr int PC = S::NG, PIECES = PC * (ZEROS ? 3 : 2), STEP = GROUP > 64 ? S::CB / 2 : (GROUP < 64 ? S::CB * 2 : S::CB);
     static_assert(PIECES <= 64, "two pieces a lane at most");
     const unsigned char *mp[PIECES > 32 ? 2 : 1];
     int m_left[PIECES > 32 ? 2 : 1], m_step[PIECES > 32 ? 2 : 1];  // groups before the row's end; bytes a chunk
@@ -162,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
     for (int q = 0; q < (PIECES > 32 ? 2 : 1); q++) {
         const int i = lane + 32 * q;
         const bool z = ZEROS && i >= 2 * PC;
-        const int j = z ? i - 2 * PC : i >> 1, r = j / S::NG, rt = rt0 + r;
+        const int j = z ? i - 2 * PC : i >> 1, rt = rt0;
         const int gi = (GROUP > 64 ? kb_w / 2 : (GROUP < 64 ? kb_w * 2 : kb_w)) + j % S::NG;
         const unsigned char *sp = p.packed + p.g.code_bytes;
         const int64_t at = (int64_t)rt * p.g.groups + gi;
@@ -178,10 +158,11 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
     const uint32_t xd = xr * S::RS + 16 * (tid % XC);
     int kb_next = kb_w;
 
-    // this lane's x in a stage, a row for each token tile; tokens that are none read a row of zeros
+    // the row of x in a stage, one for each token tile, whose address this lane gives to ldmatrix; tokens that are none read a
+    // row of zeros
     uint32_t xo[TN];
 #pragma unroll
-    for (int n = 0; n < TN; n++) xo[n] = (8 * n + g < live_x ? 8 * n + g : rows - 1) * S::RS + wk * S::KPW * 128 + 16 * t;
+    for (int n = 0; n < TN; n++) xo[n] = (8 * n + (lane & 7) < live_x ? 8 * n + (lane & 7) : rows - 1) * S::RS + wk * S::KPW * 128 + 16 * (lane >> 3);
     if (live_x < 8 * TN)
         for (int i = tid; i < kStages * (S::RS / 16); i += kThreads)
             *reinterpret_cast<uint4 *>(sm + i / (S::RS / 16) * stage + (rows - 1) * S::RS + i % (S::RS / 16) * 16) = make_uint4(0, 0, 0, 0);
@@ -191,15 +172,13 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
             const uint32_t st = base + (c % kStages) * stage;
             const int n = kb1 - kb_next;
 #pragma unroll
-            for (int r = 0; r < S::RW; r++)
-#pragma unroll
-                for (int i = 0; i < S::KPW; i++) {
-                    const bool ok = r < live_r && i < n;
-                    cp16(st + mine + (r * S::KPW + i) * 512 + lane * 16, ok ? cp + (int64_t)r * p.g.k_blocks * 512 + i * 512 : p.packed, ok);
-                }
+            for (int i = 0; i < S::KPW; i++) {
+                const bool ok = live_r && i < n;
+                cp16(st + mine + i * 512 + lane * 16, ok ? cp + i * 512 : p.packed, ok);
+            }
 #pragma unroll
             for (int q = 0; q < (PIECES > 32 ? 2 : 1); q++) {
-                if (lane + 32 * q < PIECES) cp16(st + mine + kLoads * 512 + (lane + 32 * q) * 16, m_left[q] > 0 ? mp[q] : p.packed, m_left[q] > 0);
+                if (lane + 32 * q < PIECES) cp16(st + mine + S::KPW * 512 + (lane + 32 * q) * 16, m_left[q] > 0 ? mp[q] : p.packed, m_left[q] > 0);
                 mp[q] += m_step[q], m_left[q] -= STEP;
             }
             const bool in = xk < k1;
@@ -211,11 +190,9 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    float acc[S::RW][TN][4];
+    float acc[TN][4];
 #pragma unroll
-    for (int r = 0; r < S::RW; r++)
-#pragma unroll
-        for (int n = 0; n < TN; n++) acc[r][n][0] = acc[r][n][1] = acc[r][n][2] = acc[r][n][3] = 0.f;
+    for (int n = 0; n < TN; n++) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
     for (int c = 0; c < kStages - 1; c++) copy(c);
     for (int c = 0; c < chunks; c++) {
@@ -224,52 +201,42 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
         copy(c + kStages - 1);
         const unsigned char *st = sm + (c % kStages) * stage;
         const unsigned char *wm = st + mine;
-        const uint32_t *sc = reinterpret_cast<const uint32_t *>(wm + kLoads * 512) + g;
-        const uint16_t *zc = reinterpret_cast<const uint16_t *>(wm + kLoads * 512 + S::RW * S::NG * 32) + g;
-        float part[S::RW][TN][4];
+        const uint32_t *sc = reinterpret_cast<const uint32_t *>(wm + S::KPW * 512) + g;
+        const uint16_t *zc = reinterpret_cast<const uint16_t *>(wm + S::KPW * 512 + S::NG * 32) + g;
+        float part[TN][4];
 #pragma unroll
         for (int i = 0; i < S::KPW; i++) {
-            uint4 w[S::RW];
-#pragma unroll
-            for (int r = 0; r < S::RW; r++) w[r] = *reinterpret_cast<const uint4 *>(wm + (r * S::KPW + i) * 512 + lane * 16);
+            const uint4 w = *reinterpret_cast<const uint4 *>(wm + i * 512 + lane * 16);
 #pragma unroll
             for (int h = 0; h < 2; h++) {  // 32 k: two steps
                 const int gi = GROUP > 64 ? i / 2 : (GROUP < 64 ? 2 * i + h : i);
                 const bool begin = GROUP < 64 || (h == 0 && i % GK == 0), end = GROUP < 64 || (h == 1 && i % GK == GK - 1);
-                uint32_t a[S::RW][2][4];
+                const uint32_t z = ZEROS ? zc[gi * 8] : 0x0808u;
+                const uint32_t o0 = offset2<BF>(z & 255u), o1 = offset2<BF>(z >> 8);
+                const uint32_t v[2] = {h ? w.z : w.x, h ? w.w : w.y};
+                uint32_t a[2][4];
 #pragma unroll
-                for (int r = 0; r < S::RW; r++) {
-                    const uint32_t z = ZEROS ? zc[(r * S::NG + gi) * 8] : 0x0808u;
-                    const uint32_t o0 = offset2<BF>(z & 255u), o1 = offset2<BF>(z >> 8);
-                    const uint32_t v[2] = {h ? w[r].z : w[r].x, h ? w[r].w : w[r].y};
-#pragma unroll
-                    for (int s = 0; s < 2; s++) {
-                        a[r][s][0] = decode2<BF>(v[s], o0), a[r][s][1] = decode2<BF>(v[s] >> 4, o1);
-                        a[r][s][2] = decode2<BF>(v[s] >> 8, o0), a[r][s][3] = decode2<BF>(v[s] >> 12, o1);
-                    }
+                for (int s = 0; s < 2; s++) {
+                    a[s][0] = decode2<BF>(v[s], o0), a[s][1] = decode2<BF>(v[s] >> 4, o1);
+                    a[s][2] = decode2<BF>(v[s] >> 8, o0), a[s][3] = decode2<BF>(v[s] >> 12, o1);
                 }
 #pragma unroll
                 for (int n = 0; n < TN; n++) {
-                    const uint4 b = *reinterpret_cast<const uint4 *>(st + xo[n] + i * 128 + h * 64);
-#pragma unroll
-                    for (int r = 0; r < S::RW; r++) {
-                        if (begin)
-                            mma_first<BF>(part[r][n], a[r][0], b.x, b.y);
-                        else
-                            mma_next<BF>(part[r][n], a[r][0], b.x, b.y);
-                        mma_next<BF>(part[r][n], a[r][1], b.z, b.w);
-                    }
+                    uint32_t b[4];
+                    pipe::ldsm_x4(b, st + xo[n] + i * 128 + h * 64);
+                    if (begin)
+                        mma_first<BF>(part[n], a[0], b[0], b[1]);
+                    else
+                        mma_next<BF>(part[n], a[0], b[0], b[1]);
+                    mma_next<BF>(part[n], a[1], b[2], b[3]);
                 }
                 if (end) {
+                    const uint32_t s2 = sc[gi * 8];
+                    const float s0 = to_f<BF>((uint16_t)s2), s1 = to_f<BF>((uint16_t)(s2 >> 16));
 #pragma unroll
-                    for (int r = 0; r < S::RW; r++) {
-                        const uint32_t s2 = sc[(r * S::NG + gi) * 8];
-                        const float s0 = to_f<BF>((uint16_t)s2), s1 = to_f<BF>((uint16_t)(s2 >> 16));
-#pragma unroll
-                        for (int n = 0; n < TN; n++) {
-                            acc[r][n][0] += s0 * part[r][n][0], acc[r][n][1] += s0 * part[r][n][1];
-                            acc[r][n][2] += s1 * part[r][n][2], acc[r][n][3] += s1 * part[r][n][3];
-                        }
+                    for (int n = 0; n < TN; n++) {
+                        acc[n][0] += s0 * part[n][0], acc[n][1] += s0 * part[n][1];
+                        acc[n][2] += s1 * part[n][2], acc[n][3] += s1 * part[n][3];
                     }
                 }
             }
@@ -281,12 +248,9 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
     float *so = reinterpret_cast<float *>(sm);
     constexpr int TILE = S::TILE;
 #pragma unroll
-    for (int r = 0; r < S::RW; r++)
+    for (int n = 0; n < TN; n++)
 #pragma unroll
-        for (int n = 0; n < TN; n++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                so[wk * TILE + (8 * n + 2 * t + (i & 1)) * S::ROWS + (wr * S::RW + r) * 16 + g + 8 * (i >> 1)] = acc[r][n][i];
+        for (int i = 0; i < 4; i++) so[wk * TILE + (8 * n + 2 * t + (i & 1)) * S::ROWS + wr * 16 + g + 8 * (i >> 1)] = acc[n][i];
     __syncthreads();
     if (split > 1) {
         for (int i = tid * 4; i < TILE; i += kThreads * 4) {
@@ -332,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
 template <bool BF, int GROUP, bool ZEROS, int TN, int WK>
 cudaError_t launch_tn(const MatvecParams &p, int num_sms, cudaStream_t st) {
     using S = Shape<GROUP, TN, WK>;
-    const int groups = (p.g.row_tiles + S::WR * S::RW - 1) / (S::WR * S::RW), tiles = (p.tokens + 8 * TN - 1) / (8 * TN);
+    const int groups = (p.g.row_tiles + S::WR - 1) / S::WR, tiles = (p.tokens + 8 * TN - 1) / (8 * TN);
     // k is split where that shortens the busiest SM's work: its CTAs (S::CTAS at once), each as long as its
     // chunks and about two more for its start and end
     const int64_t ctas = (int64_t)groups * tiles;
@@ -357,9 +321,7 @@ cudaError_t launch_group(const MatvecParams &p, int num_sms, cudaStream_t st) {
     // over clusters (2048 rows of 7168, one token: 6.3 us against 8.3; 6000 rows, eight tokens: 14.5 against 10.4).
     if (p.tokens <= 8)
         return p.g.row_tiles <= num_sms ? launch_tn<BF, GROUP, ZEROS, 1, 8>(p, num_sms, st) : launch_tn<BF, GROUP, ZEROS, 1, 2>(p, num_sms, st);
-    if (p.tokens <= 16) return launch_tn<BF, GROUP, ZEROS, 2, 2>(p, num_sms, st);
-    if (p.tokens <= 24) return launch_tn<BF, GROUP, ZEROS, 3, 2>(p, num_sms, st);
-    return launch_tn<BF, GROUP, ZEROS, 4, 2>(p, num_sms, st);
+    return launch_tn<BF, GROUP, ZEROS, 2, 2>(p, num_sms, st);
 }
 
 template <bool BF>
@@ -394,6 +356,10 @@ cudaError_t launch_pack(const Geometry &g, const uint8_t *codes, const uint16_t 
 }
 
 cudaError_t launch_matvec(const MatvecParams &p, bool bf16, int num_sms, cudaStream_t st) {
+    // More than 16 tokens go to the tensor-memory kernel (16384 rows of 7168: with 24 tokens 26.7 us against 28.7 here, with 32
+    // 26.7 against 36.9; 2048 rows, 32 tokens: 12.4 against 15.5). At 16 tokens this one takes 24.7 as that one does, and 12.4
+    // against 14.6 for 6000 rows, 8.5 against 12.3 for 2048.
+    if (p.tokens > 16) return launch_tc05(p, bf16, st);
     return bf16 ? launch<true>(p, num_sms, st) : launch<false>(p, num_sms, st);
 }
 

@@ -507,7 +507,8 @@ int ftmoe_rope_append(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, con
  * New token i in slot p = kv_len - q_len + i sees slots j <= p (causal != 0) or all below
  * kv_len (causal = 0), and with window > 0 (causal only) those with j > p - window. A row that
  * sees nothing (p < 0, kv_len = 0) gives out = 0, lse = log of its sink term (-inf without).
- *   q_heads     a multiple of kv_heads; query head h reads key head h / (q_heads / kv_heads);
+ *   q_heads     a multiple of kv_heads, at most 128 times as many (FTMOE_ERR_FORMAT); query
+ *               head h reads key head h / (q_heads / kv_heads);
  *   scale       positive and finite;
  *   d_sinks     fp32 [q_heads] or NULL (no sink term);
  *   out         rows like q; d_lse fp32 [tokens, q_heads] or NULL;
@@ -560,7 +561,8 @@ int ftmoe_w4_pack(const void *d_codes, const void *d_scales, const void *d_zeros
 /* y[t, n] = sum_k x[t, k] w[n, k] over packed weights. x [tokens, K] and y [tokens, N] of the
  * scales' dtype, rows x_stride and y_stride elements apart (x 16-byte aligned, x_stride a
  * multiple of eight). Codes less zeros are exact in dtype, products are summed in fp32 within
- * a group, the scale is applied in fp32, and y is rounded once. tokens = 0 does nothing. */
+ * a group, the scale is applied in fp32, and y is rounded once. tokens = 0 does nothing. Should a
+ * bounded wait inside run out, the rows of y that it concerns are NaN. */
 int ftmoe_w4_matvec(const void *d_packed, int32_t N, int32_t K, int32_t group, int32_t has_zeros, int32_t dtype,
                     const void *d_x, int64_t x_stride, int32_t tokens, void *d_y, int64_t y_stride, void *stream);
 

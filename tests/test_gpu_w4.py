@@ -24,7 +24,7 @@ def _weights(n, k, group, zeros, dt, g):
 
 @pytest.mark.parametrize("n,k,group", [(1, 32, 32), (16, 64, 64), (17, 96, 32), (100, 128, 128), (33, 320, 64),
                                        (250, 2880, 32), (384, 7168, 128), (1000, 1344, 64), (4113, 640, 128)])
-@pytest.mark.parametrize("tokens", [1, 2, 7, 8, 9, 16, 24, 33, 70])
+@pytest.mark.parametrize("tokens", [1, 2, 7, 8, 9, 16, 17, 24, 32, 33, 65, 70, 131])
 @pytest.mark.parametrize("zeros", [False, True])
 def test_matvec(n, k, group, tokens, zeros):
     from expert_slot_cache_device_gb300.w4 import W4Weights
@@ -80,3 +80,37 @@ def test_matvec_repeats_bit_for_bit_and_keeps_values():
     y = w.matvec(x.cuda()).cpu()
     assert torch.isfinite(y[[0, 1, 3, 4]]).all() and y[2, 4] == float("inf")
     assert w.matvec(x.cuda()[:0]).shape == (0, n)
+
+
+@pytest.mark.parametrize("tokens,n,group", [(24, 300, 64), (70, 144, 128), (17, 2000, 32)])
+def test_matvec_many_tokens_repeats_and_keeps_values(tokens, n, group):
+    """The same for more tokens: bit for bit again, from a graph too; a token's infinity or NaN and a row's
+    infinite scale stay their own."""
+    from expert_slot_cache_device_gb300.w4 import W4Weights
+
+    k = 1024
+    g = torch.Generator().manual_seed(tokens)
+    codes, scales, z = _weights(n, k, group, True, BF, g)
+    w = W4Weights(codes.cuda(), scales.cuda(), z.cuda(), group)
+    x = torch.randn((tokens, k), generator=g).to(BF).cuda()
+    y = w.matvec(x)
+    out = torch.empty_like(y)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            w.matvec(x, out=out)
+    for _ in range(2):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
+    x[3, 5], x[tokens - 1, k - 1] = float("inf"), float("nan")
+    scales[n - 1, 0] = float("inf")
+    w = W4Weights(codes.cuda(), scales.cuda(), z.cuda(), group)
+    got = w.matvec(x)
+    keep = [t for t in range(tokens) if t not in (3, tokens - 1)]
+    assert torch.equal(got[keep, :n - 1], y[keep, :n - 1])
+    assert not torch.isfinite(got[3]).any() and torch.isnan(got[tokens - 1]).all() and not torch.isfinite(got[:, n - 1]).any()
