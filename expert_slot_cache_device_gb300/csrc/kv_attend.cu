@@ -17,13 +17,15 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
         off += (bytes + 255) & ~(size_t)255;
         return at;
     };
-    p.part_o = nullptr, p.part_ml = nullptr, p.lse2 = nullptr, p.logits = nullptr, p.mass_parts = nullptr, p.mass_split = 1;
+    p.part_o = nullptr, p.part_ml = nullptr, p.join = nullptr, p.lse2 = nullptr, p.logits = nullptr, p.mass_parts = nullptr, p.mass_split = 1;
     // a part that starts an item and one that goes on with one for each CTA
     const size_t ctas = is_step(p) ? step_ctas(p, num_sms) : chunk_ctas(p, num_sms);
     const size_t rows = 2 * ctas * (is_step(p) ? kStepRows : chunk_rows());
-    p.part_o = reinterpret_cast<float *>(take(rows * p.c.dim * 4));
-    p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
-    p.join = reinterpret_cast<int4 *>(take(ctas * 16));
+    if (!is_step(p) || step_parts(p, num_sms)) {
+        p.part_o = reinterpret_cast<float *>(take(rows * p.c.dim * 4));
+        p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
+        p.join = reinterpret_cast<int4 *>(take(ctas * 16));
+    }
     if (p.mass) {
         p.lse2 = reinterpret_cast<float *>(take((size_t)p.bt.tokens * p.q_heads * 4));
         if (is_step(p)) {

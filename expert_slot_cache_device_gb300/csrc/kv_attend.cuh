@@ -110,6 +110,7 @@ cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem
 }
 
 int step_ctas(const AttendParams &p, int num_sms);
+bool step_parts(const AttendParams &p, int num_sms);  // whether CTAs may leave parts to join
 cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 int chunk_ctas(const AttendParams &p, int num_sms);
 size_t chunk_rows();  // rows of an item of the chunk kernel

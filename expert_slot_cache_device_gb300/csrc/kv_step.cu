@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const A
         const bool any = plan(p, u, u1, spot, s_warp, &s_spot, s_cut);
         asm volatile("griddepcontrol.launch_dependents;" :::);
         if (!any) {
-            if (tid == 0) p.join[blockIdx.x] = join;
+            if (tid == 0 && p.join) p.join[blockIdx.x] = join;
             return;
         }
         b = spot.b, hk = spot.hk, first = spot.first;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const A
             } while (n_units == 0);
         }
     } while (u < u1);
-    if (tid == 0) p.join[blockIdx.x] = join;
+    if (tid == 0 && p.join) p.join[blockIdx.x] = join;  // (null where no item is cut)
 }
 
 // Joins the parts of the item that CTA c of the step kernel started: one warp a row, lanes over the
@@ -524,23 +524,28 @@ int most_units(const AttendParams &p) {
     return (int)((slots + kUnit - 1) / kUnit);
 }
 
+// Clusters while all of them fit at once and a rank has at most eight units (one sequence of 777
+// tokens, four key heads: 6 us against 12 with a second kernel; beyond, the line of work
+// uses every SM).
+bool in_clusters(const AttendParams &p, int num_sms) {
+    const int fit = num_sms * (p.c.dim == 64 ? Shape<64>::kCtas : Shape<128>::kCtas);
+    return (int64_t)p.bt.batch * p.c.kv_heads * kCluster <= fit && most_units(p) <= 8 * kCluster;
+}
+
 template <bool BF, int D, bool LOGITS>
 cudaError_t launch_kernels(const AttendParams &p, int num_sms, cudaStream_t st) {
     constexpr int smem = Shape<D>::kSmem;
-    const int C = step_ctas(p, num_sms), most = most_units(p);
+    const int C = step_ctas(p, num_sms);
     const int64_t items = (int64_t)p.bt.batch * p.c.kv_heads;
     cudaError_t e;
-    // Clusters while all of them fit at once and a rank has at most eight units (one sequence of 777
-    // tokens, four key heads: 6 us against 12 with a second kernel; beyond, the line of work
-    // uses every SM); no joining kernel where no item is long enough to be cut.
-    if (items * kCluster <= (int64_t)num_sms * Shape<D>::kCtas && most <= 8 * kCluster) {
+    if (in_clusters(p, num_sms)) {
         if ((e = allow_smem<step_kernel<BF, D, LOGITS, true>>(smem)) != cudaSuccess) return e;
         e = launch_clusters(step_kernel<BF, D, LOGITS, true>, dim3((unsigned)items * kCluster), kCluster, kThreads, smem, st, p);
     } else {
         if ((e = allow_smem<step_kernel<BF, D, LOGITS, false>>(smem)) != cudaSuccess) return e;
         step_kernel<BF, D, LOGITS, false><<<C, kThreads, smem, st>>>(p);
         e = cudaGetLastError();
-        if (e == cudaSuccess && most > kSnap) e = launch_after(step_combine<BF, D>, dim3(C), 32 * kRows, 0, st, p);
+        if (e == cudaSuccess && step_parts(p, num_sms)) e = launch_after(step_combine<BF, D>, dim3(C), 32 * kRows, 0, st, p);
     }
     if (e == cudaSuccess && LOGITS) e = launch_after(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
     return e;
@@ -552,6 +557,9 @@ cudaError_t launch(const AttendParams &p, int num_sms, cudaStream_t st) {
 }
 
 }  // namespace
+
+// No joining kernel where no item is long enough to be cut.
+bool step_parts(const AttendParams &p, int num_sms) { return !in_clusters(p, num_sms) && most_units(p) > kSnap; }
 
 int step_ctas(const AttendParams &p, int num_sms) {
     const long long most = (long long)p.bt.batch * p.c.kv_heads * ((p.bt.max_kv + kUnit - 1) / kUnit + 1);
