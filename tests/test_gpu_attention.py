@@ -195,6 +195,25 @@ def test_attention_repeats_bit_for_bit_and_on_another_stream():
         assert torch.equal(o, got[0][0]) and torch.equal(m, got[0][1])
 
 
+def test_attention_of_one_batch_on_two_streams_at_once():
+    """Calls of one batch that overlap on two streams, whose workspaces the batch keeps, growing in between."""
+    w = World([1, 90, 5], [4000, 800, 2600], 12, 2, 128, 16, BF, seed=5)
+    want = w.cache.attend(w.batch, w.q).clone()
+    mass = torch.zeros((3, 2, 4000), device="cuda")
+    w.cache.attend(w.batch, w.q, mass=mass)
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.empty_like(want) for _ in range(12)] for _ in sides]
+    sums = [torch.zeros_like(mass) for _ in sides]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for s, o, m in zip(sides, outs, sums):
+            with torch.cuda.stream(s):
+                w.cache.attend(w.batch, w.q, out=o[i], mass=m if i == 7 else None)
+    torch.cuda.synchronize()
+    for o, m in zip(outs, sums):
+        assert all(torch.equal(x, want) for x in o) and torch.equal(m, mass)
+
+
 def test_attention_in_a_graph_follows_its_device_arrays():
     """A captured step reads lengths and tables when it is replayed."""
     w = World([1, 1, 1], [900, 17, 450], 8, 2, 64, 16, BF, seed=4)
