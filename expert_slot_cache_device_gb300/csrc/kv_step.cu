@@ -208,11 +208,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const A
 
         int pg[KT];
 #pragma unroll
-        for (int i = 0; i < kStages - 1; i++) {
+        for (int i = 0; i < kStages; i++) {
             pages(i, pg);
             copy(i, pg);
         }
-        pages(kStages - 1, pg);
 
         // the rows' queries as A fragments: rows g and g + 8
         uint32_t qf[KS][4];
@@ -235,10 +234,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const A
         for (int n = 0; n < D / 8; n++) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
 
         for (int i = 0; i < tiles; i++) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            __syncwarp();
-            copy(i + kStages - 1, pg);  // its stage was read in the last round
             pages(i + kStages, pg);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();
             const uint32_t st = ring + (i % kStages) * kStageBytes;
             const int slot0 = (t0 + i * kWarps) * T;
 
@@ -315,6 +313,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const A
                     mma<BF>(o[n], pf[k], f[0], f[1]);
                     mma<BF>(o[n + 1], pf[k], f[2], f[3]);
                 }
+            __syncwarp();
+            copy(i + kStages, pg);  // into the stage just read, before the next wait: kStages tiles are in flight then
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         // ---- join the four warps: a common maximum, then the sums in warp order
