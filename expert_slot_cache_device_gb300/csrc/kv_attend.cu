@@ -21,7 +21,7 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
     // a part that starts an item and one that goes on with one for each CTA
     const size_t ctas = is_step(p) ? step_ctas(p, num_sms) : chunk_ctas(p, num_sms);
     const size_t rows = 2 * ctas * (is_step(p) ? kStepRows : chunk_rows());
-    if (!is_step(p) || step_parts(p, num_sms)) {
+    if (is_step(p) ? step_parts(p, num_sms) : chunk_parts(p, num_sms)) {
         p.part_o = reinterpret_cast<float *>(take(rows * p.c.dim * 4));
         p.part_ml = reinterpret_cast<float2 *>(take(rows * 8));
         p.join = reinterpret_cast<int4 *>(take(ctas * 16));

@@ -113,6 +113,7 @@ int step_ctas(const AttendParams &p, int num_sms);
 bool step_parts(const AttendParams &p, int num_sms);  // whether CTAs may leave parts to join
 cudaError_t launch_step(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 int chunk_ctas(const AttendParams &p, int num_sms);
+bool chunk_parts(const AttendParams &p, int num_sms);
 size_t chunk_rows();  // rows of an item of the chunk kernel
 cudaError_t launch_chunk(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
 int mass_split(const AttendParams &p, int num_sms);

@@ -82,12 +82,12 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttendParams &p, Part &w) {
         while (left > 0) {
             const Item it = item_of(p, sq, qt);
-            const int n = it.tiles + kItemCost, end = left < n - at ? at + (int)left : n;
+            const int n = item_units(p, it), end = left < n - at ? at + (int)left : n;
             w.b = b, w.hk = hk;
             w.token = sq.q0 + qt * p.item_tokens, w.left = sq.q_len - qt * p.item_tokens;
             w.slot = sq.kv_len - sq.q_len + qt * p.item_tokens, w.kv_len = sq.kv_len;
             w.lo = it.lo, w.hi = it.hi, w.seen_lo = it.seen_lo, w.tiles = it.tiles;
-            w.first = at > kItemCost ? at - kItemCost : 0, w.last = end - kItemCost;
+            w.first = at > kItemCost ? at - kItemCost : 0, w.last = p.join ? end - kItemCost : it.tiles;
             left -= end - at;
             at = 0;
             if (left > 0 && ++qt == n_qt) {
@@ -172,7 +172,7 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
         const int hk = at / (uint32_t)per;
         int rem = at - hk * per, found = -1, first = 0, before = 0;
         for (int q0 = 0; q0 < n_qt && found < 0; q0 += 32) {
-            const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles + kItemCost : 0;
+            const int n = q0 + lane < n_qt ? item_units(p, item_of(p, s, q0 + lane)) : 0;
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     fence_after();
     if (!any) {  // the whole CTA
-        if (tid == 0) p.join[blockIdx.x] = make_int4(0, 0, 0, kJoinNone);
+        if (tid == 0 && p.join) p.join[blockIdx.x] = make_int4(0, 0, 0, kJoinNone);
         if (warp == kMmaWarp)
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*reinterpret_cast<volatile uint32_t *>(&s_tmem)) : "memory");
         return;
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             hand_out();
         }
-        if (lane == 0) p.join[blockIdx.x] = join;
+        if (lane == 0 && p.join) p.join[blockIdx.x] = join;
     }
     if (!ok && lane == 0) flag(p.c.status, FTMOE_ERR_STATE);
     fence_before();
@@ -710,7 +710,7 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     chunk_kernel<BF, D><<<C, kThreads, S::kSmem, st>>>(p, qm, km, vm);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_after(chunk_combine<BF, D>, dim3(C, kTileRows / kJoinRows), kJoinThreads, 0, st, p);
+    return !p.join ? e : launch_after(chunk_combine<BF, D>, dim3(C, kTileRows / kJoinRows), kJoinThreads, 0, st, p);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -763,6 +763,18 @@ bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, 
     return fn(&m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(x), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether the call's items are cut. Not if there is an SM for each, and the longest has few steps and no more than an even
+// share of all steps (112 items, heads of 64, one step: 10.8 us whole, 12.6 cut and joined, which costs a second kernel;
+// three steps: 15.9 and 18.8; six: 21.9 and 21.5; eight: 26.0 and 21.9. 32 items of three steps, whose share is two: 16.0 and
+// 13.8. Heads of 128, 112 items of three steps: 17.9 and 22.9).
+bool chunk_parts(const AttendParams &p, int num_sms) {
+    const int64_t items = (int64_t)((p.bt.max_q + p.item_tokens - 1) / p.item_tokens) * p.bt.batch * p.c.kv_heads;
+    int64_t slots = p.bt.max_kv;
+    if (p.window && (int64_t)p.window + p.item_tokens + kTileSlots < slots) slots = p.window + p.item_tokens + kTileSlots;
+    const int64_t steps = (slots + kTileSlots - 1) / kTileSlots;
+    return items > num_sms || steps > 6 || steps > (items * (steps + kItemCost) + num_sms - 1) / num_sms;
 }
 
 int chunk_ctas(const AttendParams &p, int num_sms) {

@@ -516,8 +516,8 @@ int ftmoe_rope_append(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, con
  *               rows of at least max_kv, or NULL. Each element is added to once, in one fixed
  *               order, so results repeat bit for bit;
  *   d_workspace 256-byte aligned device memory of at least the bytes that
- *               ftmoe_paged_attention_workspace_bytes gives for the same arguments; calls
- *               that overlap on the GPU need one each.
+ *               ftmoe_paged_attention_workspace_bytes gives for the same arguments (0 for
+ *               some: NULL will do then); calls that overlap on the GPU need one each.
  * Slots outside every row's visible range may hold anything, NaN included. Scores, the running
  * maximum, sums and outputs are kept in fp32; the probabilities are rounded to the cache's
  * type for the product with V (not for l, lse or mass). K and V of one sequence that are visible to some of
