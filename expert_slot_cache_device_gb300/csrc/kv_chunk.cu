@@ -82,13 +82,13 @@ struct Walk {
     __device__ __forceinline__ bool next(const AttendParams &p, Part &w) {
         while (left > 0) {
             const Item it = item_of(p, sq, qt);
-            const int n = item_units(p, it), end = left < n - at ? at + (int)left : n;
+            const int n = it.tiles + kItemCost, end = left < n - at && p.join ? at + (int)left : n;
             w.b = b, w.hk = hk;
             w.token = sq.q0 + qt * p.item_tokens, w.left = sq.q_len - qt * p.item_tokens;
             w.slot = sq.kv_len - sq.q_len + qt * p.item_tokens, w.kv_len = sq.kv_len;
             w.lo = it.lo, w.hi = it.hi, w.seen_lo = it.seen_lo, w.tiles = it.tiles;
-            w.first = at > kItemCost ? at - kItemCost : 0, w.last = p.join ? end - kItemCost : it.tiles;
-            left -= end - at;
+            w.first = at > kItemCost ? at - kItemCost : 0, w.last = end - kItemCost;
+            left = p.join ? left - (end - at) : 0;  // (no join array: a CTA has one item, whole)
             at = 0;
             if (left > 0 && ++qt == n_qt) {
                 qt = 0;
@@ -122,6 +122,13 @@ __device__ __forceinline__ bool take(Bars &bar, const Part *ring, uint32_t &n, P
 // Total steps and this CTA's start. s_sum: kThreads entries.
 __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *s_warp, int *s_sum, Walk *s_walk) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (!p.join) {  // a CTA an item that there can be, and no line to walk
+        const int most = (p.bt.max_q + p.item_tokens - 1) / p.item_tokens, head = blockIdx.x / most;
+        w.qt = blockIdx.x - head * most, w.b = head / p.c.kv_heads, w.hk = head - w.b * p.c.kv_heads;
+        w.sq = seq_info(p.bt, w.b, w.qt == 0 && w.hk == 0 && tid == 0 ? p.c.status : nullptr);
+        w.n_qt = row_tiles(p, w.sq), w.at = 0, w.left = 1;
+        return w.qt < w.n_qt;
+    }
     long long sum = 0, total;
     for (int b0 = 0; b0 < p.bt.batch; b0 += kThreads) {
         for (int i = warp; i < kThreads; i += kWarps) {
@@ -172,7 +179,7 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
         const int hk = at / (uint32_t)per;
         int rem = at - hk * per, found = -1, first = 0, before = 0;
         for (int q0 = 0; q0 < n_qt && found < 0; q0 += 32) {
-            const int n = q0 + lane < n_qt ? item_units(p, item_of(p, s, q0 + lane)) : 0;
+            const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles + kItemCost : 0;
             int x = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -765,20 +772,21 @@ bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the call's items are cut. Not if there is an SM for each, and the longest has few steps and no more than an even
-// share of all steps (112 items, heads of 64, one step: 10.8 us whole, 12.6 cut and joined, which costs a second kernel;
-// three steps: 15.9 and 18.8; six: 21.9 and 21.5; eight: 26.0 and 21.9. 32 items of three steps, whose share is two: 16.0 and
-// 13.8. Heads of 128, 112 items of three steps: 17.9 and 22.9).
+// Whether the call's items are cut. Not if there is an SM for each, and the longest has few steps and hardly more than an
+// even share of all steps: that saves the walk along the line (2 us) and the joining kernel (112 items, heads of 64, one
+// step: 8.9 us whole, 12.6 cut; three steps: 13.9 and 18.8; six: 20.0 and 21.5; eight: 24 and 21.6. Heads of 128, three
+// steps: 16.1 and 22.9, eight: 27 and 26.7; 32 items of three steps, whose share is two: 16 and 17).
 bool chunk_parts(const AttendParams &p, int num_sms) {
     const int64_t items = (int64_t)((p.bt.max_q + p.item_tokens - 1) / p.item_tokens) * p.bt.batch * p.c.kv_heads;
     int64_t slots = p.bt.max_kv;
     if (p.window && (int64_t)p.window + p.item_tokens + kTileSlots < slots) slots = p.window + p.item_tokens + kTileSlots;
     const int64_t steps = (slots + kTileSlots - 1) / kTileSlots;
-    return items > num_sms || steps > 6 || steps > (items * (steps + kItemCost) + num_sms - 1) / num_sms;
+    return items > num_sms || steps > 6 || steps > (items * (steps + kItemCost) + num_sms - 1) / num_sms + 1;
 }
 
 int chunk_ctas(const AttendParams &p, int num_sms) {
     const int64_t n_qt = (p.bt.max_q + p.item_tokens - 1) / p.item_tokens;
+    if (!chunk_parts(p, num_sms)) return (int)(n_qt * p.bt.batch * p.c.kv_heads);
     const int64_t most = n_qt * p.bt.batch * p.c.kv_heads * (p.bt.max_kv / kTileSlots + 2);
     return (int)(most < num_sms ? (most > 0 ? most : 1) : num_sms);
 }

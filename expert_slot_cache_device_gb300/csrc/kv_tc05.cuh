@@ -221,13 +221,11 @@ __device__ __forceinline__ Item item_of(const AttendParams &p, const Seq &s, int
 }
 // What an item adds to the line of work besides its steps: its start and end take about as long.
 constexpr int kItemCost = 2;
-// Units of an item on the line; of a call that cuts no items (no join array), one: a CTA takes whole items.
-__device__ __forceinline__ int item_units(const AttendParams &p, const Item &it) { return p.join ? it.tiles + kItemCost : 1; }
 
 // Units of one (sequence, key head) over its first end_qt items; the whole warp calls.
 __device__ __forceinline__ int seq_units(const AttendParams &p, const Seq &s, int end_qt) {
     int n = 0;
-    for (int qt = threadIdx.x & 31; qt < end_qt; qt += 32) n += item_units(p, item_of(p, s, qt));
+    for (int qt = threadIdx.x & 31; qt < end_qt; qt += 32) n += item_of(p, s, qt).tiles + kItemCost;
     return __reduce_add_sync(~0u, n);
 }
 
