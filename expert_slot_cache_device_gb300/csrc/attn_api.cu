@@ -111,7 +111,8 @@ int attend_params(const ftmoe_kv_cache *kvc, const ftmoe_kv_batch *batch, int q_
     if (window && !causal) return fail(FTMOE_ERR_INVALID_ARG, "a window needs causal attention");
     if (q_heads / p.c.kv_heads > 128)
         return fail(FTMOE_ERR_FORMAT, "%d query heads a key head: at most 128", q_heads / p.c.kv_heads);
-    p.q_heads = q_heads, p.group = q_heads / p.c.kv_heads, p.window = window, p.causal = causal != 0;
+    p.q_heads = q_heads, p.group = q_heads / p.c.kv_heads, p.causal = causal != 0;
+    p.window = window < p.bt.max_kv ? window : 0;  // a wider one hides no slot, and sums with it could pass 32 bits
     p.item_tokens = 2 * (128 / p.group);
     return FTMOE_OK;
 }

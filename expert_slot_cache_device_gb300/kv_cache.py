@@ -25,6 +25,7 @@ from .cache import _stream
 
 _DTYPES = {torch.bfloat16: F.DT_BF16, torch.float16: F.DT_F16}
 _F32 = torch.float32
+_INT_MAX = 2 ** 31 - 1  # the C calls' integers
 # The current stream's handle without a Stream object around it (3 us of a call's 13 on the host)
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -253,7 +254,10 @@ class PagedKVCache:
         """Attention of the new tokens' queries [tokens, heads, head_dim] over their sequences'
         cached slots (``ftmoe_paged_attention``). ``scale`` defaults to head_dim ** -0.5,
         ``sinks`` is fp32 [heads], ``lse`` fp32 [tokens, heads] receives the log-sum-exp, ``mass``
-        fp32 [batch, kv_heads, >= max_kv] gets each slot's attention weight added. Returns out."""
+        fp32 [batch, kv_heads, >= max_kv] gets each slot's attention weight added. A ``window`` of any
+        size above the cached tokens is none. Returns out."""
+        if window > _INT_MAX:
+            window = _INT_MAX
         qr = self._rows(q, "q")
         n, heads, _ = q.shape
         if heads % self.kv_heads:

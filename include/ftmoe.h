@@ -505,7 +505,8 @@ int ftmoe_rope_append(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, con
  *   out = sum_j exp(s_j) v_j / l, lse = log l, mass_j += sum over the sequence's rows of the
  *   key head's query heads of exp(s_j - lse).
  * New token i in slot p = kv_len - q_len + i sees slots j <= p (causal != 0) or all below
- * kv_len (causal = 0), and with window > 0 (causal only) those with j > p - window. A row that
+ * kv_len (causal = 0), and with window > 0 (causal only) those with j > p - window (a window of
+ * max_kv or more, up to INT32_MAX, hides none). A row that
  * sees nothing (p < 0, kv_len = 0) gives out = 0, lse = log of its sink term (-inf without).
  *   q_heads     a multiple of kv_heads, at most 128 times as many (FTMOE_ERR_FORMAT); query
  *               head h reads key head h / (q_heads / kv_heads);

@@ -1,0 +1,49 @@
+"""The attention half at the ends of what its calls take, against its calls in plain use and plain
+implementations in 64 bits."""
+import pytest
+import torch
+
+from test_gpu_attention import BF, HF, World, check_attend
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from expert_slot_cache_device_gb300 import build
+
+    build.build()
+
+
+def run(w, window=0, sinks=None, mass=True, q=None, out=None):
+    """(out, lse, mass) of a call on the world's cache."""
+    q = w.q if q is None else q
+    out = torch.full((w.tokens, w.heads, w.dim), 7.0, dtype=w.dtype, device="cuda") if out is None else out
+    lse = torch.full((w.tokens, w.heads), 7.0, device="cuda")
+    m = torch.zeros((len(w.kv_lens), w.kv_heads, max(w.kv_lens + [1])), device="cuda") if mass else None
+    w.cache.attend(w.batch, q, window=window, sinks=sinks, out=out, lse=lse, mass=m)
+    torch.cuda.synchronize()
+    assert w.cache.status() == 0
+    return out, lse, m
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 60, 1 << 30, 2 ** 32 + 5, 2 ** 63 - 1])
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv,dim,dt", [
+    ([300, 70], [300, 200], 8, 2, 64, BF),     # chunks: a whole prompt, and one late in its context
+    ([90, 40], [70, 11], 4, 2, 128, HF),       # more new tokens than cached ones
+    ([1, 1], [500, 33], 8, 2, 64, BF),         # single tokens
+    ([4, 2], [1, 9], 4, 2, 128, BF),
+])
+def test_a_window_wider_than_any_cache_is_none(q_lens, kv_lens, heads, kv, dim, dt, window):
+    w = World(q_lens, kv_lens, heads, kv, dim, 16, dt, seed=21)
+    got, want = run(w, window), run(w, 0)
+    for g, x in zip(got, want):
+        assert torch.equal(g, x)
+    check_attend(w, 0, None, True)
+
+
+@pytest.mark.parametrize("q,kv_len", [(1, 130), (40, 130)])
+def test_windows_about_the_length_of_the_cache(q, kv_len):
+    for window in (kv_len - 1, kv_len, kv_len + 1):
+        w = World([q], [kv_len], 4, 2, 64, 16, BF, seed=window, window=window)
+        check_attend(w, window, None, True)
