@@ -551,7 +551,7 @@ cudaError_t launch_kernels(const AttendParams &p, int num_sms, cudaStream_t st) 
         e = cudaGetLastError();
         if (e == cudaSuccess && step_parts(p, num_sms)) e = launch_after(step_combine<BF, D>, dim3(C), 32 * kRows, 0, st, p);
     }
-    if (e == cudaSuccess && LOGITS) e = launch_after(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
+    if (e == cudaSuccess && LOGITS && p.bt.max_kv > 0) e = launch_after(step_mass, dim3((p.bt.max_kv + 1023) / 1024, p.c.kv_heads, p.bt.batch), 256, 0, st, p);
     return e;
 }
 

@@ -1,5 +1,7 @@
 """The attention half at the ends of what its calls take, against its calls in plain use and plain
 implementations in 64 bits."""
+import math
+
 import pytest
 import torch
 
@@ -47,3 +49,18 @@ def test_windows_about_the_length_of_the_cache(q, kv_len):
     for window in (kv_len - 1, kv_len, kv_len + 1):
         w = World([q], [kv_len], 4, 2, 64, 16, BF, seed=window, window=window)
         check_attend(w, window, None, True)
+
+
+@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("with_sinks", [False, True])
+def test_mass_of_caches_that_hold_nothing(q, with_sinks):
+    """No sequence has a cached token, and the bound says so: out = 0, lse is the sink, mass stays."""
+    w = World([q, q], [0, 0], 4, 2, 64, 16, BF, seed=3)
+    assert w.batch.max_kv == 0
+    sinks = torch.linspace(-1, 1, 4).cuda() if with_sinks else None
+    out, lse, mass = run(w, 0, sinks)
+    assert (out == 0).all() and (mass == 0).all()
+    if with_sinks:
+        assert torch.allclose(lse, sinks.expand_as(lse), rtol=1e-6, atol=1e-6)
+    else:
+        assert (lse == -math.inf).all()
