@@ -32,6 +32,7 @@ int fail(int code, const char *fmt, ...) {
 
 int cuda_rc(cudaError_t e, const char *what) {
     if (e == cudaSuccess) return FTMOE_OK;
+    cudaGetLastError();  // reported here: not again by the caller's next call
     return fail(FTMOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
