@@ -355,11 +355,21 @@ cudaError_t launch_pack(const Geometry &g, const uint8_t *codes, const uint16_t 
     return cudaGetLastError();
 }
 
+constexpr int32_t kMostTokens = 1 << 21;  // of one launch
+
 cudaError_t launch_matvec(const MatvecParams &p, bool bf16, int num_sms, cudaStream_t st) {
     // More than 16 tokens go to the tensor-memory kernel (16384 rows of 7168: with 24 tokens 26.7 us against 28.7 here, with 32
     // 26.7 against 36.9; 2048 rows, 32 tokens: 12.4 against 15.5). At 16 tokens this one takes 24.7 as that one does, and 12.4
     // against 14.6 for 6000 rows, 8.5 against 12.3 for 2048.
-    if (p.tokens > 16) return launch_tc05(p, bf16, st);
+    if (p.tokens > 16) {
+        MatvecParams q = p;  // a grid has 65535 tiles of 64 tokens at most
+        for (int64_t t = 0; t < p.tokens; t += kMostTokens) {
+            q.x = p.x + t * p.x_stride, q.y = p.y + t * p.y_stride;
+            q.tokens = p.tokens - t < kMostTokens ? (int32_t)(p.tokens - t) : kMostTokens;
+            if (const cudaError_t e = launch_tc05(q, bf16, st)) return e;
+        }
+        return cudaSuccess;
+    }
     return bf16 ? launch<true>(p, num_sms, st) : launch<false>(p, num_sms, st);
 }
 
