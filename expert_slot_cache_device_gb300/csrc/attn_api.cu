@@ -181,6 +181,8 @@ int ftmoe_paged_attention(const ftmoe_kv_cache *kvc, const ftmoe_kv_batch *batch
     if (!(scale > 0.f) || !std::isfinite(scale)) return fail(FTMOE_ERR_INVALID_ARG, "scale must be positive and finite");
     if ((rc = check_rows(q, "q", q_heads, p.c.dim, p.q))) return rc;
     if ((rc = check_rows(out, "out", q_heads, p.c.dim, p.out))) return rc;
+    if (p.out.d == p.q.d && ((p.bt.tokens > 1 && p.out.token != p.q.token) || (q_heads > 1 && p.out.head != p.q.head)))
+        return fail(FTMOE_ERR_INVALID_ARG, "out over q needs q's strides");
     if (d_mass && (mass_head < p.bt.max_kv || mass_seq < 0))
         return fail(FTMOE_ERR_INVALID_ARG, "mass rows of %lld elements for max_kv=%d", (long long)mass_head, p.bt.max_kv);
     if (p.bt.tokens == 0 || p.bt.batch == 0 || p.bt.max_q == 0) return FTMOE_OK;

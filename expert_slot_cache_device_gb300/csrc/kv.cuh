@@ -137,6 +137,7 @@ struct AttendParams {
     int32_t mass_split;
     int32_t logit_rows;
     int64_t logit_stride;
+    uint16_t *q_copy;  // [tokens, q_heads, dim]: the queries of a call whose output replaces them before the mass pass of chunks
 };
 // Bytes of workspace; with `base` the pointers of p are set into it.
 size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base);

@@ -255,7 +255,7 @@ class PagedKVCache:
         cached slots (``ftmoe_paged_attention``). ``scale`` defaults to head_dim ** -0.5,
         ``sinks`` is fp32 [heads], ``lse`` fp32 [tokens, heads] receives the log-sum-exp, ``mass``
         fp32 [batch, kv_heads, >= max_kv] gets each slot's attention weight added. A ``window`` of any
-        size above the cached tokens is none. Returns out."""
+        size above the cached tokens is none. ``out`` may be q itself. Returns out."""
         if window > _INT_MAX:
             window = _INT_MAX
         qr = self._rows(q, "q")

@@ -512,7 +512,8 @@ int ftmoe_rope_append(const ftmoe_kv_cache *kv, const ftmoe_kv_batch *batch, con
  *               head h reads key head h / (q_heads / kv_heads);
  *   scale       positive and finite;
  *   d_sinks     fp32 [q_heads] or NULL (no sink term);
- *   out         rows like q; d_lse fp32 [tokens, q_heads] or NULL;
+ *   out         rows like q, or q itself (the same rows and strides; no other overlap);
+ *   d_lse       fp32 [tokens, q_heads] or NULL;
  *   d_mass      fp32, element (b, key head, slot) at b * mass_seq + head * mass_head + slot,
  *               rows of at least max_kv, or NULL. Each element is added to once, in one fixed
  *               order, so results repeat bit for bit;

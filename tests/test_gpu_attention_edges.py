@@ -64,3 +64,23 @@ def test_mass_of_caches_that_hold_nothing(q, with_sinks):
         assert torch.allclose(lse, sinks.expand_as(lse), rtol=1e-6, atol=1e-6)
     else:
         assert (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,heads,kv,dim,page,dt", [
+    ([1, 1, 1], [700, 5, 64], 8, 2, 128, 16, BF),      # single tokens
+    ([1, 2], [9000, 4000], 8, 2, 64, 16, HF),
+    ([70, 3, 0, 20], [400, 500, 9, 20], 8, 2, 64, 16, HF),  # chunks: whole items
+    ([600, 90], [4000, 300], 12, 4, 128, 32, BF),      # joined parts
+    ([30], [33], 17, 1, 128, 16, BF),                  # rows of a tile unused
+])
+@pytest.mark.parametrize("mass", [False, True])
+def test_output_over_the_queries(q_lens, kv_lens, heads, kv, dim, page, dt, mass):
+    """`out` may be the queries themselves, as a view of a wider projection too."""
+    w = World(q_lens, kv_lens, heads, kv, dim, page, dt, seed=heads, slack=1)
+    want = run(w, mass=mass)
+    q = w.q._base.clone()[:, 1:heads + 1]  # w.q is a slice of a wider array
+    assert q.stride() == w.q.stride()
+    got = run(w, mass=mass, q=q, out=q)
+    assert torch.equal(got[0][:w.cu[-1]], want[0][:w.cu[-1]]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[0][w.cu[-1]:], w.q[w.cu[-1]:])  # a row of no sequence stays
+    assert not mass or torch.equal(got[2], want[2])
