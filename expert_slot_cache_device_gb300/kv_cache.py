@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import threading
 from typing import Optional
 
 import torch
@@ -162,6 +163,7 @@ class KVBatch:
         stride = block_table.stride(0) if self.batch > 1 else block_table.shape[1]
         self._args = (block_table.data_ptr(), stride, kv_lens.data_ptr(), cu_q.data_ptr(), self.batch)
         self._views, self._bytes, self._spaces = {}, {}, {}
+        self._lock = threading.Lock()
 
     def _ref(self, tokens: int):
         """Reference to the C view for token arrays of `tokens` rows."""
@@ -174,7 +176,8 @@ class KVBatch:
     def _workspace(self, need: int, handle: int, stream) -> torch.Tensor:
         """At least ``need`` bytes for a call on stream ``handle``, kept for the next one there: a step's layers
         run one after another (an allocation a call takes 4 us of its 12 on the host). A captured call gets
-        its own, which lives with the graph."""
+        its own, which lives with the graph. The caller holds ``_lock`` until the call's kernels are
+        enqueued: another thread's may not come between them, which share it."""
         if torch.cuda.is_current_stream_capturing():
             return _new(need, torch.uint8, self.device, stream)
         t = self._spaces.get(handle)
@@ -281,12 +284,15 @@ class PagedKVCache:
             need = batch._bytes[key] = F.ftmoe_paged_attention_workspace_bytes(self._ref, ref, heads, window, causal,
                                                                                mass is not None)
         handle = _handle(stream, self.device)
-        ws = batch._workspace(need, handle, stream) if need else None
-        F.ftmoe_paged_attention(self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal,
-                                sinks.data_ptr() if sinks is not None else None, outr,
-                                lse.data_ptr() if lse is not None else None,
-                                mass.data_ptr() if mass is not None else None, ms, mh,
-                                ws.data_ptr() if need else None, need, handle)
+        args = (self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal,
+                sinks.data_ptr() if sinks is not None else None, outr, lse.data_ptr() if lse is not None else None,
+                mass.data_ptr() if mass is not None else None, ms, mh)
+        if need:
+            with batch._lock:
+                ws = batch._workspace(need, handle, stream)
+                F.ftmoe_paged_attention(*args, ws.data_ptr(), need, handle)
+        else:
+            F.ftmoe_paged_attention(*args, None, 0, handle)
         return out
 
     def _mass(self, batch: KVBatch, mass: torch.Tensor):

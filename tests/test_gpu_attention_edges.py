@@ -84,3 +84,58 @@ def test_output_over_the_queries(q_lens, kv_lens, heads, kv, dim, page, dt, mass
     assert torch.equal(got[0][:w.cu[-1]], want[0][:w.cu[-1]]) and torch.equal(got[1], want[1])
     assert torch.equal(got[0][w.cu[-1]:], w.q[w.cu[-1]:])  # a row of no sequence stays
     assert not mass or torch.equal(got[2], want[2])
+
+
+def test_calls_of_one_batch_from_two_threads_do_not_share_a_workspace_at_once(monkeypatch):
+    """Two host threads that use one batch on one stream: the launches of a call, which share its workspace, may not come between
+    another's. The library's call is a stand-in that waits; nothing is launched."""
+    import threading
+    import time
+
+    from expert_slot_cache_device_gb300 import ftmoe as F
+
+    w = World([1, 90], [4000, 800], 12, 2, 128, 16, BF, seed=3)
+    inside, clashes = {}, []
+
+    def call(*args):
+        ws = args[-3]
+        assert ws
+        if inside.get(ws):
+            clashes.append(ws)
+        inside[ws] = inside.get(ws, 0) + 1
+        time.sleep(0.02)
+        inside[ws] -= 1
+
+    monkeypatch.setattr(F, "ftmoe_paged_attention", call)
+    threads = [threading.Thread(target=lambda: [w.cache.attend(w.batch, w.q) for _ in range(5)]) for _ in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not clashes
+
+
+def test_attention_of_one_batch_from_two_threads():
+    """Calls of one batch from several threads on the default stream, with and without mass, give what each gives alone."""
+    import threading
+
+    w = World([1, 90, 5], [4000, 800, 2600], 12, 2, 128, 16, BF, seed=5)
+    want, _, mass = run(w)
+    outs = [[torch.empty_like(want) for _ in range(20)] for _ in range(4)]
+    sums = [[torch.zeros_like(mass) for _ in range(20)] for _ in range(4)]
+    torch.cuda.synchronize()
+
+    def work(k):
+        for i in range(20):
+            w.cache.attend(w.batch, w.q, out=outs[k][i], mass=sums[k][i] if (i + k) % 2 else None)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in range(4):
+        for i in range(20):
+            assert torch.equal(outs[k][i], want), (k, i)
+            assert not (i + k) % 2 or torch.equal(sums[k][i], mass), (k, i)
