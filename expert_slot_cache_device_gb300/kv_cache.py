@@ -27,6 +27,7 @@ from .cache import _stream
 _DTYPES = {torch.bfloat16: F.DT_BF16, torch.float16: F.DT_F16}
 _F32 = torch.float32
 _INT_MAX = 2 ** 31 - 1  # the C calls' integers
+_KEPT = 256 << 20       # the largest workspace that a batch keeps, in bytes
 # The current stream's handle without a Stream object around it (3 us of a call's 13 on the host)
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -175,10 +176,11 @@ class KVBatch:
 
     def _workspace(self, need: int, handle: int, stream) -> torch.Tensor:
         """At least ``need`` bytes for a call on stream ``handle``, kept for the next one there: a step's layers
-        run one after another (an allocation a call takes 4 us of its 12 on the host). A captured call gets
-        its own, which lives with the graph. The caller holds ``_lock`` until the call's kernels are
+        run one after another (an allocation a call takes 4 us of its 12 on the host). A large one is not
+        kept: 64 sequences of 128k tokens with mass need 4 GB, and their call takes longer on the GPU than
+        the allocation on the host. A captured call gets its own, which lives with the graph. The caller holds ``_lock`` until the call's kernels are
         enqueued: another thread's may not come between them, which share it."""
-        if torch.cuda.is_current_stream_capturing():
+        if need > _KEPT or torch.cuda.is_current_stream_capturing():
             return _new(need, torch.uint8, self.device, stream)
         t = self._spaces.get(handle)
         if t is None or t.numel() < need:

@@ -139,3 +139,20 @@ def test_attention_of_one_batch_from_two_threads():
         for i in range(20):
             assert torch.equal(outs[k][i], want), (k, i)
             assert not (i + k) % 2 or torch.equal(sums[k][i], mass), (k, i)
+
+
+def test_a_batch_keeps_no_large_workspace():
+    """Kept scores of long caches go back to the allocator after the call (their call takes far longer than the allocation)."""
+    n = 70000
+    w = World([1] * 16, [n] + [40] * 14 + [3000], 64, 4, 64, 16, BF, seed=6)
+    w.cache.attend(w.batch, w.q)
+    small = sum(t.numel() for t in w.batch._spaces.values())
+    before = torch.cuda.memory_allocated()
+    mass = torch.zeros((16, 4, n), device="cuda")
+    for _ in range(2):
+        out, _, mass = run(w)
+        torch.cuda.synchronize()
+    assert sum(t.numel() for t in w.batch._spaces.values()) == small <= 256 << 20
+    del out
+    assert torch.cuda.memory_allocated() - before <= 4 * mass.numel() + (1 << 20)
+    check_attend(w, 0, None, True)
