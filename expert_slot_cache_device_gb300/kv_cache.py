@@ -30,11 +30,18 @@ _INT_MAX = 2 ** 31 - 1  # the C calls' integers
 _KEPT = 256 << 20       # the largest workspace that a batch keeps, in bytes
 # The current stream's handle without a Stream object around it (3 us of a call's 13 on the host)
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _handle(stream, device: torch.device) -> int:
+def _handle(stream, dev: int) -> int:
+    """Handle of the stream of a call on memory of device `dev`. The library's kernels go to the current
+    device, so that has to be it."""
+    if _current_device() != dev:
+        raise ValueError(f"memory of device {dev}: make it the current device first")
     if stream is None and _current is not None:
-        return _current(device.index)
+        return _current(dev)
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"memory of device {dev}, a stream of device {stream.device_index}")
     return _stream(stream)
 
 
@@ -49,9 +56,11 @@ def _new(shape, dtype, device, stream):
     return t
 
 
-def _ints(t: torch.Tensor, name: str, dims: int) -> torch.Tensor:
+def _ints(t: torch.Tensor, name: str, dims: int, dev: Optional[int] = None) -> torch.Tensor:
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or t.dim() != dims:
         raise ValueError(f"{name}: needs an int32 device tensor of {dims} dimension(s)")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name}: on device {t.get_device()}, the call's is {dev}")
     if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name}: needs consecutive elements")
     return t
@@ -136,6 +145,7 @@ class Rotary:
         turns = freq / (2 * math.pi)
         hi = turns.to(torch.float32)
         self.freq = torch.stack([hi, (turns - hi.double()).to(torch.float32)], -1).contiguous().to(device)
+        self._dev = self.freq.get_device()
         self._view = F.RotaryView(self.freq.data_ptr(), rot_dim, layout == "interleaved", self.factor)
         self.ref = ctypes.byref(self._view)
 
@@ -153,7 +163,8 @@ class KVBatch:
 
     def __init__(self, block_table: torch.Tensor, kv_lens: torch.Tensor, cu_q: torch.Tensor, max_q: int, max_kv: int):
         self.block_table = _ints(block_table, "block_table", 2)
-        self.kv_lens, self.cu_q = _ints(kv_lens, "kv_lens", 1), _ints(cu_q, "cu_q", 1)
+        self._dev = block_table.get_device()
+        self.kv_lens, self.cu_q = _ints(kv_lens, "kv_lens", 1, self._dev), _ints(cu_q, "cu_q", 1, self._dev)
         self.batch = block_table.shape[0]
         if kv_lens.numel() != self.batch or cu_q.numel() != self.batch + 1:
             raise ValueError(f"{self.batch} sequences: kv_lens has {kv_lens.numel()}, cu_q {cu_q.numel()} entries")
@@ -210,6 +221,9 @@ class PagedKVCache:
                 raise ValueError(f"{name}: needs a {dtype} device tensor {list(shape)} with a contiguous last axis")
             pages.append(t)
         self.k_pages, self.v_pages = pages
+        self._dev = self.k_pages.get_device()
+        if self.v_pages.get_device() != self._dev:
+            raise ValueError("k_pages and v_pages are on different devices")
         self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.dtype = *shape, dtype
         self.device = self.k_pages.device
         self._scale = head_dim ** -0.5
@@ -220,37 +234,39 @@ class PagedKVCache:
         self._ref = ctypes.byref(self._view)
 
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int] = None, tokens: Optional[int] = None):
-        if not isinstance(t, torch.Tensor) or t.dtype is not self.dtype or not t.is_cuda or t.dim() != 3:
-            raise ValueError(f"{name}: needs a {self.dtype} device tensor [tokens, heads, head_dim]")
-        n, h, d = t.shape
+        """(reference to the C view of t [tokens, heads, head_dim], tokens, heads)."""
+        if not isinstance(t, torch.Tensor) or t.dtype is not self.dtype or t.get_device() != self._dev or len(shape := t.shape) != 3:
+            raise ValueError(f"{name}: needs a {self.dtype} tensor [tokens, heads, head_dim] on device {self._dev}")
+        n, h, d = shape
         st, sh, sd = t.stride()
         if d != self.head_dim or sd != 1 or (heads is not None and h != heads) or (tokens is not None and n != tokens):
             raise ValueError(f"{name}: shape {list(t.shape)} does not match the call, or rows of head_dim are not contiguous")
         # a stride over one element is never taken
-        return ctypes.byref(F.RowsView(t.data_ptr(), st if n > 1 else 8, sh if h > 1 else 8))
+        return ctypes.byref(F.RowsView(t.data_ptr(), st if n > 1 else 8, sh if h > 1 else 8)), n, h
 
     def append(self, batch: KVBatch, rotary: Rotary, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
                positions: torch.Tensor, q_out: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
         """Rotate q and k [tokens, heads, head_dim] by ``positions`` (int32 [tokens]) and write k
         and v to their slots. Returns the rotated queries (``q_out``, which may be q itself)."""
+        if batch._dev != self._dev or rotary._dev != self._dev:
+            raise ValueError(f"batch on device {batch._dev}, rotary plan on {rotary._dev}, cache on {self._dev}")
         if rotary.head_dim != self.head_dim:
             raise ValueError(f"rotary plan of head_dim {rotary.head_dim}, cache of {self.head_dim}")
-        n = k.shape[0]
-        kr, vr = self._rows(k, "k", self.kv_heads), self._rows(v, "v", self.kv_heads, n)
-        if _ints(positions, "positions", 1).numel() != n:
+        kr, n, _ = self._rows(k, "k", self.kv_heads)
+        vr, _, _ = self._rows(v, "v", self.kv_heads, n)
+        if _ints(positions, "positions", 1, self._dev).numel() != n:
             raise ValueError(f"positions has {positions.numel()} entries for {n} tokens")
         if n == 0:
             return q
         qr = qo = None
         heads = 0
         if q is not None:
-            heads = q.shape[1]
-            qr = self._rows(q, "q", None, n)
+            qr, _, heads = self._rows(q, "q", None, n)
             if q_out is None:
                 q_out = _new(q.shape, q.dtype, q.device, stream)
-            qo = self._rows(q_out, "q_out", heads, n)
+            qo, _, _ = self._rows(q_out, "q_out", heads, n)
         F.ftmoe_rope_append(self._ref, batch._ref(n), rotary.ref, qr, qo, heads, kr, vr, positions.data_ptr(),
-                            _handle(stream, self.device))
+                            _handle(stream, self._dev))
         return q_out
 
     def attend(self, batch: KVBatch, q: torch.Tensor, scale: Optional[float] = None, window: int = 0,
@@ -263,17 +279,18 @@ class PagedKVCache:
         size above the cached tokens is none. ``out`` may be q itself. Returns out."""
         if window > _INT_MAX:
             window = _INT_MAX
-        qr = self._rows(q, "q")
-        n, heads, _ = q.shape
+        if batch._dev != self._dev:
+            raise ValueError(f"batch on device {batch._dev}, cache on {self._dev}")
+        qr, n, heads = self._rows(q, "q")
         if heads % self.kv_heads:
             raise ValueError(f"{heads} query heads over {self.kv_heads} key heads")
         if out is None:
             out = _new(q.shape, q.dtype, q.device, stream)
-        outr = self._rows(out, "out", heads, n)
-        if sinks is not None and (sinks.dtype is not _F32 or not sinks.is_cuda or sinks.shape != (heads,) or not sinks.is_contiguous()):
-            raise ValueError(f"sinks: needs a contiguous fp32 device tensor [{heads}]")
-        if lse is not None and (lse.dtype is not _F32 or not lse.is_cuda or lse.shape != (n, heads) or not lse.is_contiguous()):
-            raise ValueError(f"lse: needs a contiguous fp32 device tensor [{n}, {heads}]")
+        outr, _, _ = self._rows(out, "out", heads, n)
+        if sinks is not None and (sinks.dtype is not _F32 or sinks.get_device() != self._dev or sinks.shape != (heads,) or not sinks.is_contiguous()):
+            raise ValueError(f"sinks: needs a contiguous fp32 tensor [{heads}] on device {self._dev}")
+        if lse is not None and (lse.dtype is not _F32 or lse.get_device() != self._dev or lse.shape != (n, heads) or not lse.is_contiguous()):
+            raise ValueError(f"lse: needs a contiguous fp32 tensor [{n}, {heads}] on device {self._dev}")
         ms = mh = 0
         if mass is not None:
             ms, mh = self._mass(batch, mass)
@@ -285,21 +302,19 @@ class PagedKVCache:
         if need is None:
             need = batch._bytes[key] = F.ftmoe_paged_attention_workspace_bytes(self._ref, ref, heads, window, causal,
                                                                                mass is not None)
-        handle = _handle(stream, self.device)
-        args = (self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal,
-                sinks.data_ptr() if sinks is not None else None, outr, lse.data_ptr() if lse is not None else None,
-                mass.data_ptr() if mass is not None else None, ms, mh)
-        if need:
-            with batch._lock:
-                ws = batch._workspace(need, handle, stream)
-                F.ftmoe_paged_attention(*args, ws.data_ptr(), need, handle)
-        else:
-            F.ftmoe_paged_attention(*args, None, 0, handle)
+        handle = _handle(stream, self._dev)
+        with batch._lock:
+            ws = batch._workspace(need, handle, stream) if need else None
+            F.ftmoe_paged_attention(self._ref, ref, qr, heads, self._scale if scale is None else scale, window, causal,
+                                    sinks.data_ptr() if sinks is not None else None, outr,
+                                    lse.data_ptr() if lse is not None else None,
+                                    mass.data_ptr() if mass is not None else None, ms, mh,
+                                    ws.data_ptr() if need else None, need, handle)
         return out
 
     def _mass(self, batch: KVBatch, mass: torch.Tensor):
-        if mass.dtype is not _F32 or not mass.is_cuda or mass.dim() != 3:
-            raise ValueError(f"mass: needs an fp32 device tensor [{batch.batch}, {self.kv_heads}, slots]")
+        if mass.dtype is not _F32 or mass.get_device() != self._dev or mass.dim() != 3:
+            raise ValueError(f"mass: needs an fp32 tensor [{batch.batch}, {self.kv_heads}, slots] on device {self._dev}")
         b, h, n = mass.shape
         ms, mh, m1 = mass.stride()
         if b != batch.batch or h != self.kv_heads or n < batch.max_kv or (n > 1 and m1 != 1):
@@ -319,8 +334,10 @@ class PagedKVCache:
         (int32 [batch, pages], pages that ``block_table`` does not name). Returns (kept int32
         [batch, kv_heads, budget], new_mass fp32 likewise, new_lens int32 [batch]); the old
         pages can be reused by later work on the same stream."""
+        if batch._dev != self._dev:
+            raise ValueError(f"batch on device {batch._dev}, cache on {self._dev}")
         ms, mh = self._mass(batch, mass)
-        if _ints(new_table, "new_table", 2).shape[0] != batch.batch:
+        if _ints(new_table, "new_table", 2, self._dev).shape[0] != batch.batch:
             raise ValueError(f"new_table has {new_table.shape[0]} rows for {batch.batch} sequences")
         shape = (batch.batch, self.kv_heads, budget)
         if budget < 1:
@@ -333,21 +350,26 @@ class PagedKVCache:
             new_lens = _new(batch.batch, torch.int32, self.device, stream)
         for name, t, sh, dt in (("kept", kept, shape, torch.int32), ("new_mass", new_mass, shape, _F32),
                                 ("new_lens", new_lens, shape[:1], torch.int32)):
-            if t.dtype is not dt or not t.is_cuda or t.shape != sh or not t.is_contiguous():
-                raise ValueError(f"{name}: needs a contiguous {dt} device tensor {list(sh)}")
+            if t.dtype is not dt or t.get_device() != self._dev or t.shape != sh or not t.is_contiguous():
+                raise ValueError(f"{name}: needs a contiguous {dt} tensor {list(sh)} on device {self._dev}")
         # the C call takes one row length for every row
         if new_table.shape[1] * self.page_size < min(budget, batch.max_kv):
             raise ValueError(f"new_table: {new_table.shape[1]} pages a row for {min(budget, batch.max_kv)} slots")
         stride = new_table.stride(0) if batch.batch > 1 else new_table.shape[1]
         F.ftmoe_kv_evict(self._ref, batch._ref(0), mass.data_ptr(), ms, mh, budget, recent, new_table.data_ptr(), stride,
-                         kept.data_ptr(), new_mass.data_ptr(), new_lens.data_ptr(), _handle(stream, self.device))
+                         kept.data_ptr(), new_mass.data_ptr(), new_lens.data_ptr(), _handle(stream, self._dev))
         return kept, new_mass, new_lens
+
+    def _on(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        return torch.cuda.ExternalStream(_stream(stream), device=self.device)
 
     def status(self, stream=None) -> int:
         """Sticky device status of this cache's calls (synchronises the stream)."""
-        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=self.device)):
+        with torch.cuda.stream(self._on(stream)):
             return int(self._status.item())
 
     def reset_status(self, stream=None) -> None:
-        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=self.device)):
+        with torch.cuda.stream(self._on(stream)):
             self._status.zero_()

@@ -8,7 +8,6 @@ from typing import Optional
 import torch
 
 from . import ftmoe as F
-from .cache import _stream
 from .kv_cache import _DTYPES, _handle, _new
 
 
@@ -31,28 +30,29 @@ class W4Weights:
             raise ValueError(f"group={group}: 32, 64 or 128, dividing K={self.K}")
         shape = (self.N, self.K // group)
         for name, t, dt in (("scales", scales, scales.dtype), ("zeros", zeros, torch.uint8)):
-            if t is not None and (t.dtype != dt or not t.is_cuda or t.shape != shape or not t.is_contiguous()):
-                raise ValueError(f"{name}: needs a contiguous {dt} device tensor {list(shape)}")
-        self.dtype, self.zeros, self.device = scales.dtype, zeros is not None, codes.device
+            if t is not None and (t.dtype != dt or t.get_device() != codes.get_device() or t.shape != shape or not t.is_contiguous()):
+                raise ValueError(f"{name}: needs a contiguous {dt} tensor {list(shape)} on the codes' device")
+        self.dtype, self.zeros, self.device, self._dev = scales.dtype, zeros is not None, codes.device, codes.get_device()
+        handle = _handle(stream, self._dev)
         nbytes = F.ftmoe_w4_packed_bytes(self.N, self.K, group, self.zeros)
         self.packed = _new(nbytes, torch.uint8, self.device, stream)
         F.ftmoe_w4_pack(codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if self.zeros else None, self.N, self.K,
-                        group, self.packed.data_ptr(), nbytes, _stream(stream))
+                        group, self.packed.data_ptr(), nbytes, handle)
         self._row = self.K + (-self.K) % 8  # a row stride that is never taken
         self._args = (self.packed.data_ptr(), self.N, self.K, group, self.zeros, _DTYPES[self.dtype])
 
     def matvec(self, x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """y [tokens, N] = x [tokens, K] times the weights' transpose."""
-        if x.dtype is not self.dtype or x.dim() != 2 or not x.is_cuda:
-            raise ValueError(f"x: needs a {self.dtype} device tensor [tokens, {self.K}] with contiguous rows")
+        if x.dtype is not self.dtype or x.dim() != 2 or x.get_device() != self._dev:
+            raise ValueError(f"x: needs a {self.dtype} tensor [tokens, {self.K}] on device {self._dev} with contiguous rows")
         n, k = x.shape
         xs, x1 = x.stride()
         if k != self.K or x1 != 1:
             raise ValueError(f"x: needs a {self.dtype} device tensor [tokens, {self.K}] with contiguous rows")
         if out is None:
             out = _new((n, self.N), self.dtype, self.device, stream)
-        elif out.dtype is not self.dtype or out.shape != (n, self.N) or not out.is_cuda or (self.N > 1 and out.stride(1) != 1):
-            raise ValueError(f"out: needs a {self.dtype} device tensor [{n}, {self.N}] with contiguous rows")
+        elif out.dtype is not self.dtype or out.shape != (n, self.N) or out.get_device() != self._dev or (self.N > 1 and out.stride(1) != 1):
+            raise ValueError(f"out: needs a {self.dtype} tensor [{n}, {self.N}] on device {self._dev} with contiguous rows")
         F.ftmoe_w4_matvec(*self._args, x.data_ptr(), xs if n > 1 else self._row, n, out.data_ptr(),
-                          out.stride(0) if n > 1 else self.N, _handle(stream, self.device))
+                          out.stride(0) if n > 1 else self.N, _handle(stream, self._dev))
         return out

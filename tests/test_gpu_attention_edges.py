@@ -156,3 +156,44 @@ def test_a_batch_keeps_no_large_workspace():
     del out
     assert torch.cuda.memory_allocated() - before <= 4 * mass.numel() + (1 << 20)
     check_attend(w, 0, None, True)
+
+
+def _calls(w):
+    """Every call that a cache, and 4-bit weights, take, by name."""
+    from expert_slot_cache_device_gb300.kv_cache import Rotary
+    from expert_slot_cache_device_gb300.w4 import W4Weights
+
+    k, v = (torch.zeros((w.tokens, w.kv_heads, w.dim), dtype=w.dtype, device="cuda") for _ in range(2))
+    pos = torch.zeros(w.tokens, dtype=torch.int32, device="cuda")
+    rotary, mass = Rotary(w.dim), torch.zeros((1, w.kv_heads, 64), device="cuda")
+    table = torch.tensor([[0, 0, 0, 0]], dtype=torch.int32, device="cuda")
+    codes, scales = torch.zeros((16, 64), dtype=torch.uint8, device="cuda"), torch.zeros((16, 1), dtype=BF, device="cuda")
+    weights, x = W4Weights(codes, scales), torch.zeros((2, 128), dtype=BF, device="cuda")
+    return {"append": lambda: w.cache.append(w.batch, rotary, w.q, k, v, pos), "attend": lambda: w.cache.attend(w.batch, w.q),
+            "evict": lambda: w.cache.evict(w.batch, mass, table, 64, 1), "pack": lambda: W4Weights(codes, scales),
+            "matvec": lambda: weights.matvec(x)}, weights
+
+
+def test_calls_with_another_device_current_are_refused(monkeypatch):
+    """Kernels go to the current device: a call on memory of another one is refused before anything is enqueued."""
+    from expert_slot_cache_device_gb300 import kv_cache
+
+    calls, _ = _calls(World([1], [20], 4, 2, 64, 16, BF))
+    for call in calls.values():
+        call()
+    monkeypatch.setattr(kv_cache, "_current_device", lambda: 1, raising=False)
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match="device"):
+            call()
+            pytest.fail(name)
+
+
+def test_tensors_of_another_device_are_refused():
+    """A cache and weights that say they are elsewhere than the arguments."""
+    w = World([1], [20], 4, 2, 64, 16, BF)
+    calls, weights = _calls(w)
+    w.cache._dev = weights._dev = 1
+    for name in ("append", "attend", "evict", "matvec"):
+        with pytest.raises(ValueError):
+            calls[name]()
+            pytest.fail(name)
