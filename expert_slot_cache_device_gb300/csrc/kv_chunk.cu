@@ -120,7 +120,7 @@ __device__ __forceinline__ bool take(Bars &bar, const Part *ring, uint32_t &n, P
 }
 
 // Total steps and this CTA's start. s_sum: kThreads entries.
-__device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *s_warp, int *s_sum, Walk *s_walk) {
+__device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *s_warp, long long *s_sum, Walk *s_walk) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!p.join) {  // a CTA an item that there can be, and no line to walk
         const int most = (p.bt.max_q + p.item_tokens - 1) / p.item_tokens, head = blockIdx.x / most;
@@ -132,7 +132,7 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
     long long sum = 0, total;
     for (int b0 = 0; b0 < p.bt.batch; b0 += kThreads) {
         for (int i = warp; i < kThreads; i += kWarps) {
-            int n = 0;
+            long long n = 0;
             if (b0 + i < p.bt.batch) {
                 const Seq s = seq_info(p.bt, b0 + i, blockIdx.x == 0 && lane == 0 ? p.c.status : nullptr);
                 n = seq_units(p, s, row_tiles(p, s));
@@ -156,12 +156,12 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
             for (int i = warp; i < kThreads; i += kWarps) {
                 if (b0 + i >= p.bt.batch) break;
                 const Seq s = seq_info(p.bt, b0 + i, nullptr);
-                const int n = seq_units(p, s, row_tiles(p, s));
+                const long long n = seq_units(p, s, row_tiles(p, s));
                 if (lane == 0) s_sum[i] = n;
             }
             __syncthreads();
         }
-        const long long n = b0 + tid < p.bt.batch ? (long long)s_sum[tid] * p.c.kv_heads : 0;
+        const long long n = b0 + tid < p.bt.batch ? s_sum[tid] * p.c.kv_heads : 0;
         const long long at = base + block_scan<kThreads>(n, total, s_warp);
         if (u0 >= at && u0 < at + n) {
             s_walk->b = b0 + tid;
@@ -174,29 +174,12 @@ __device__ __forceinline__ bool plan(const AttendParams &p, Walk &w, long long *
     if (warp == 0) {
         const int b = s_walk->b;
         const Seq s = seq_info(p.bt, b, nullptr);
-        const int n_qt = row_tiles(p, s), per = seq_units(p, s, n_qt);
-        const uint32_t at = (uint32_t)s_walk->left;  // within one sequence: below 2^32
-        const int hk = at / (uint32_t)per;
-        int rem = at - hk * per, found = -1, first = 0, before = 0;
-        for (int q0 = 0; q0 < n_qt && found < 0; q0 += 32) {
-            const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles + kItemCost : 0;
-            int x = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(~0u, x, o);
-                if (lane >= o) x += y;
-            }
-            const unsigned hit = __ballot_sync(~0u, n > 0 && rem >= before + x - n && rem < before + x);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                found = q0 + l;
-                first = rem - (before + __shfl_sync(~0u, x - n, l));
-            }
-            before += __shfl_sync(~0u, x, 31);
-        }
+        const int n_qt = row_tiles(p, s);
+        const long long per = seq_units(p, s, n_qt);
+        const Place at = place_of(p, s, n_qt, per, s_walk->left);
         __syncwarp();
         if (lane == 0) {
-            s_walk->hk = hk, s_walk->qt = found, s_walk->n_qt = n_qt, s_walk->at = first, s_walk->sq = s;
+            s_walk->hk = at.hk, s_walk->qt = at.qt, s_walk->n_qt = n_qt, s_walk->at = at.at, s_walk->sq = s;
             s_walk->left = u1 - u0;
         }
     }
@@ -228,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Bars bar;
     __shared__ uint32_t s_tmem;
     __shared__ long long s_warp[kWarps];
-    int *s_sum = reinterpret_cast<int *>(sm_raw);  // the ring is not in use yet
+    long long *s_sum = reinterpret_cast<long long *>(sm_raw);  // the ring is not in use yet
     __shared__ Walk s_walk;
     __shared__ Part s_part[kParts];
     __shared__ int64_t s_row[128];  // offset of a tile's row from its first token and head, -1 past the last

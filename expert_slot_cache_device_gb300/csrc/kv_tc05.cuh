@@ -222,11 +222,45 @@ __device__ __forceinline__ Item item_of(const AttendParams &p, const Seq &s, int
 // What an item adds to the line of work besides its steps: its start and end take about as long.
 constexpr int kItemCost = 2;
 
-// Units of one (sequence, key head) over its first end_qt items; the whole warp calls.
-__device__ __forceinline__ int seq_units(const AttendParams &p, const Seq &s, int end_qt) {
-    int n = 0;
+// Units of one (sequence, key head) over its first end_qt items; the whole warp calls. They are counted
+// in 64 bits: a prompt of a million tokens whose 128 query heads share a key head has 2^31. (The warp's 32-bit sums
+// take the low 16 bits and the rest apart, which lanes below 2^43 fit.)
+__device__ __forceinline__ long long seq_units(const AttendParams &p, const Seq &s, int end_qt) {
+    long long n = 0;
     for (int qt = threadIdx.x & 31; qt < end_qt; qt += 32) n += item_of(p, s, qt).tiles + kItemCost;
-    return __reduce_add_sync(~0u, n);
+    return ((long long)__reduce_add_sync(~0u, (uint32_t)(n >> 16)) << 16) + __reduce_add_sync(~0u, (uint32_t)n & 0xffffu);
+}
+
+// Where unit `at` of a sequence lies, whose key heads have `per` units each: key head, item, units into the item. The
+// whole warp calls.
+struct Place {
+    int hk, qt, at;
+};
+__device__ __forceinline__ Place place_of(const AttendParams &p, const Seq &s, int n_qt, long long per, long long at) {
+    const int lane = threadIdx.x & 31;
+    // (a 64-bit division takes longer than the rest)
+    const int hk = (at | per) >> 32 ? (int)(at / per) : (int)((uint32_t)at / (uint32_t)per);
+    const long long rem = at - hk * per;
+    long long before = 0;
+    Place w{hk, -1, 0};
+    for (int q0 = 0; q0 < n_qt && w.qt < 0; q0 += 32) {
+        const int n = q0 + lane < n_qt ? item_of(p, s, q0 + lane).tiles + kItemCost : 0;  // 32 of them: below 2^30
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        const long long r = rem - before;
+        const unsigned hit = __ballot_sync(~0u, n > 0 && r >= x - n && r < x);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            w.qt = q0 + l;
+            w.at = (int)(r - __shfl_sync(~0u, x - n, l));
+        }
+        before += __shfl_sync(~0u, x, 31);
+    }
+    return w;
 }
 
 // Tensor map of pages: [page][head][slot][element], boxes of 64 elements x box_slots slots.

@@ -197,3 +197,77 @@ def test_tensors_of_another_device_are_refused():
         with pytest.raises(ValueError):
             calls[name]()
             pytest.fail(name)
+
+
+PROBE = r"""
+#include "kv_tc05.cuh"
+using namespace ftmoe::kv;
+__global__ void probe(AttendParams p, Seq s, const long long *at, int n, long long *units, int4 *places) {
+    const int n_qt = row_tiles(p, s);
+    const long long per = seq_units(p, s, n_qt);
+    if (threadIdx.x == 0) *units = per;
+    for (int i = 0; i < n; i++) {
+        const Place x = place_of(p, s, n_qt, per, at[i]);
+        if (threadIdx.x == 0) places[i] = make_int4(x.hk, x.qt, x.at, 0);
+    }
+}
+extern "C" int place(int group, int window, int causal, int q_len, int kv_len, const long long *at, int n, long long *units, int4 *places) {
+    AttendParams p{};
+    p.group = group, p.window = window, p.causal = causal, p.item_tokens = 2 * (128 / group);
+    Seq s{0, q_len, kv_len};
+    probe<<<1, 32>>>(p, s, at, n, units, places);
+    return (int)cudaDeviceSynchronize();
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def place(tmp_path_factory):
+    import ctypes
+    import subprocess
+
+    from expert_slot_cache_device_gb300 import build as B
+
+    d = tmp_path_factory.mktemp("line")
+    src, lib = d / "probe.cu", d / "probe.so"
+    src.write_text(PROBE)
+    subprocess.run([B.nvcc(), *B.NVCC_FLAGS, "-shared", "-o", str(lib), str(src)], check=True)
+    f = ctypes.CDLL(str(lib)).place
+    f.argtypes = [ctypes.c_int] * 5 + [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]
+    return f
+
+
+@pytest.mark.parametrize("group,window,causal,q_len,kv_len,heads", [
+    (4, 0, 1, 1000, 4000, 2),
+    (17, 300, 1, 70, 5000, 3),
+    (1, 0, 0, 600, 129, 1),
+    (128, 0, 1, 1 << 20, 1 << 20, 1),          # 2^31 steps and some in one sequence and head
+    (8, 0, 1, 1 << 21, 1 << 21, 8),            # 2^32 and some in its eight heads
+    (128, 1 << 20, 1, 700001, (1 << 30) - 5, 2),
+    (128, 0, 0, 513, 1 << 30, 4),              # few items of 2^23 steps
+])
+def test_places_on_a_line_longer_than_32_bits(place, group, window, causal, q_len, kv_len, heads):
+    """The arithmetic that cuts the chunk kernel's work, at its places in long prompts (no attention is computed)."""
+    import numpy as np
+
+    t = 2 * (128 // group)
+    n = -(-q_len // t)
+    i0 = np.arange(n, dtype=np.int64) * t
+    i1 = np.minimum(i0 + t, q_len)
+    first = kv_len - q_len
+    hi = np.maximum(first + i1, 0) if causal else np.where(first + i1 > 0, kv_len, 0)
+    lo = np.maximum(first + i0 - window + 1, 0) if window else np.zeros_like(i0)
+    lo = np.minimum(lo, hi) // 128 * 128
+    units = np.maximum(-(-(hi - lo) // 128), 1) + 2  # an item's start and end count as two steps
+    ends = np.cumsum(units)
+    per = int(ends[-1])
+    rng = np.random.default_rng(q_len)
+    at = np.concatenate([rng.integers(0, per * heads, 40), [0, per - 1, per, per * heads - 1] if heads > 1 else [0, per - 1]])
+    d_at = torch.from_numpy(at).cuda()
+    d_units, d_places = torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros((len(at), 4), dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert place(group, window, causal, q_len, kv_len, d_at.data_ptr(), len(at), d_units.data_ptr(), d_places.data_ptr()) == 0
+    assert int(d_units) == per
+    qt = np.searchsorted(ends, at % per, side="right")
+    want = np.stack([at // per, qt, at % per - (ends - units)[qt]], 1)
+    assert (d_places[:, :3].cpu().numpy() == want).all()
