@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Bars bar;
     __shared__ uint32_t s_tmem;
     __shared__ long long s_warp[kWarps];
-    long long *s_sum = reinterpret_cast<long long *>(sm_raw);  // the ring is not in use yet
+    __shared__ long long s_sum[kThreads];  // (not over the ring: tensor copies are not ordered after plain stores to the same bytes)
     __shared__ Walk s_walk;
     __shared__ Part s_part[kParts];
     __shared__ int64_t s_row[128];  // offset of a tile's row from its first token and head, -1 past the last
