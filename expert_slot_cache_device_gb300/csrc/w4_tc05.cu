@@ -158,8 +158,8 @@ __global__ void __launch_bounds__(kBound, (Tile<GROUP, NT>::CTAS)) w4_tc05_kerne
         // the products of block j times their scales onto the sums
         auto finish = [&](int j) {
             if (!kv::warp_wait(&bar.d[team][j & 1], (j >> 1) & 1)) return false;
+            kv::fence_after();  // the block's A buffer is stored to next, whether its products are read here or with the next block's
             if (T::UB == 1 || (j & 1)) {
-                kv::fence_after();
 #pragma unroll
                 for (int g = 0; g < T::NG; g++) {
                     const uint64_t s2 = kv::pack2(s_old[0][g], s_old[0][g]);
