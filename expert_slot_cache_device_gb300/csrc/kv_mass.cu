@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto move_k = [&](uint32_t m) {
             const uint32_t to = tm + lanes + kKCol + 64 * (m & 1), row = tid & 127;
             if (!warp_wait(&bar.kfull, m & 1) || !warp_wait(&bar.kempty[m & 1], ((m >> 1) & 1) ^ 1)) return false;
+            fence_after();  // the products that read the buffer are done
 #pragma unroll
             for (int e = 0; e < D / 64; e++) {
                 uint32_t x[32];
