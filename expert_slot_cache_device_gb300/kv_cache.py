@@ -256,8 +256,6 @@ class PagedKVCache:
         vr, _, _ = self._rows(v, "v", self.kv_heads, n)
         if _ints(positions, "positions", 1, self._dev).numel() != n:
             raise ValueError(f"positions has {positions.numel()} entries for {n} tokens")
-        if n == 0:
-            return q
         qr = qo = None
         heads = 0
         if q is not None:
@@ -265,6 +263,8 @@ class PagedKVCache:
             if q_out is None:
                 q_out = _new(q.shape, q.dtype, q.device, stream)
             qo, _, _ = self._rows(q_out, "q_out", heads, n)
+        if n == 0:
+            return q_out
         F.ftmoe_rope_append(self._ref, batch._ref(n), rotary.ref, qr, qo, heads, kr, vr, positions.data_ptr(),
                             _handle(stream, self._dev))
         return q_out

@@ -271,3 +271,14 @@ def test_places_on_a_line_longer_than_32_bits(place, group, window, causal, q_le
     qt = np.searchsorted(ends, at % per, side="right")
     want = np.stack([at // per, qt, at % per - (ends - units)[qt]], 1)
     assert (d_places[:, :3].cpu().numpy() == want).all()
+
+
+def test_append_of_no_tokens_returns_its_output():
+    from expert_slot_cache_device_gb300.kv_cache import Rotary
+
+    w = World([0], [5], 4, 2, 64, 16, BF)
+    q, k = (torch.empty((0, h, 64), dtype=BF, device="cuda") for h in (4, 2))
+    pos, out = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty_like(q)
+    assert w.cache.append(w.batch, Rotary(64), q, k, k, pos, q_out=out) is out
+    assert w.cache.append(w.batch, Rotary(64), q, k, k, pos).shape == q.shape
+    assert w.cache.append(w.batch, Rotary(64), None, k, k, pos) is None
