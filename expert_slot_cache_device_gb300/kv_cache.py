@@ -168,8 +168,8 @@ class KVBatch:
         self.batch = block_table.shape[0]
         if kv_lens.numel() != self.batch or cu_q.numel() != self.batch + 1:
             raise ValueError(f"{self.batch} sequences: kv_lens has {kv_lens.numel()}, cu_q {cu_q.numel()} entries")
-        if max_q < 0 or max_kv < 0:
-            raise ValueError("max_q and max_kv must not be negative")
+        if not 0 <= max_q <= _INT_MAX or not 0 <= max_kv <= _INT_MAX:
+            raise ValueError(f"max_q={max_q}, max_kv={max_kv}: outside [0, {_INT_MAX}]")
         self.max_q, self.max_kv = int(max_q), int(max_kv)
         self.device = block_table.device
         stride = block_table.stride(0) if self.batch > 1 else block_table.shape[1]
@@ -340,8 +340,8 @@ class PagedKVCache:
         if _ints(new_table, "new_table", 2, self._dev).shape[0] != batch.batch:
             raise ValueError(f"new_table has {new_table.shape[0]} rows for {batch.batch} sequences")
         shape = (batch.batch, self.kv_heads, budget)
-        if budget < 1:
-            raise ValueError(f"budget={budget}")
+        if budget < 1 or budget > _INT_MAX or recent > _INT_MAX:
+            raise ValueError(f"budget={budget}, recent={recent}")
         if kept is None:
             kept = _new(shape, torch.int32, self.device, stream)
         if new_mass is None:

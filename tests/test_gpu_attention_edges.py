@@ -282,3 +282,18 @@ def test_append_of_no_tokens_returns_its_output():
     assert w.cache.append(w.batch, Rotary(64), q, k, k, pos, q_out=out) is out
     assert w.cache.append(w.batch, Rotary(64), q, k, k, pos).shape == q.shape
     assert w.cache.append(w.batch, Rotary(64), None, k, k, pos) is None
+
+
+def test_bounds_past_32_bits_are_refused():
+    """Host integers that the C views' 32 bits would cut: a bound of 2^32 would have become no token at all."""
+    from expert_slot_cache_device_gb300.kv_cache import KVBatch
+
+    w = World([1], [40], 4, 2, 64, 16, BF)
+    for q, n in ((2 ** 32, 40), (2 ** 31, 40), (1, 2 ** 32 + 40), (1, 2 ** 31)):
+        with pytest.raises(ValueError):
+            KVBatch(w.batch.block_table, w.batch.kv_lens, w.batch.cu_q, q, n)
+    mass, table = torch.zeros((1, 2, 40), device="cuda"), torch.zeros((1, 4), dtype=torch.int32, device="cuda")
+    for budget, recent in ((2 ** 32 + 8, 4), (8, 2 ** 32 + 4)):
+        with pytest.raises(ValueError):
+            w.cache.evict(w.batch, mass, table, budget, recent, kept=torch.zeros((1, 2, 8), dtype=torch.int32, device="cuda"),
+                          new_mass=torch.zeros((1, 2, 8), device="cuda"))
