@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import attention_reference as ref
 from test_gpu_attention import BF, HF, World, check_attend
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
@@ -297,3 +298,63 @@ def test_bounds_past_32_bits_are_refused():
         with pytest.raises(ValueError):
             w.cache.evict(w.batch, mass, table, budget, recent, kept=torch.zeros((1, 2, 8), dtype=torch.int32, device="cuda"),
                           new_mass=torch.zeros((1, 2, 8), device="cuda"))
+
+
+@pytest.mark.parametrize("layout", ["pages", "slots", "heads"])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [300, 17]), ([60, 2], [300, 17])])
+def test_keys_and_values_in_one_allocation(layout, q_lens, kv_lens):
+    """K and V as two halves of a page, of a slot or of a head: written, read and moved through their strides."""
+    from expert_slot_cache_device_gb300.kv_cache import PagedKVCache, Rotary
+
+    w = World(q_lens, kv_lens, 8, 2, 64, 16, BF, seed=14)
+    pages = w.cache.num_pages + 2
+    shape, at = {"pages": ((pages, 2, 16, 2, 64), 1), "slots": ((pages, 16, 2, 2, 64), 2), "heads": ((pages, 16, 2, 2, 64), 3)}[layout]
+    both = torch.zeros(shape, dtype=BF, device="cuda")
+    k, v = both.select(at, 0), both.select(at, 1)
+    k[:w.cache.num_pages], v[:w.cache.num_pages] = w.cache.k_pages, w.cache.v_pages
+    cache = PagedKVCache(pages, 16, 2, 64, BF, k_pages=k, v_pages=v)
+    apart, w.cache = w.cache, cache
+    check_attend(w, 0, None, True)
+    new_k, new_v = (torch.randn((w.tokens, 2, 64), generator=w.gen).to(BF).cuda() for _ in range(2))
+    pos = torch.arange(w.tokens, dtype=torch.int32, device="cuda")
+    got = [c.append(w.batch, Rotary(64), w.q, new_k, new_v, pos) for c in (cache, apart)]
+    assert torch.equal(*got)
+    for a, b in ((k, apart.k_pages), (v, apart.v_pages)):
+        assert torch.equal(a[:-2].nan_to_num(9.0), b.nan_to_num(9.0))
+    mass = torch.rand((2, 2, 300), device="cuda")
+    table = torch.tensor([[pages - 2], [pages - 1]], dtype=torch.int32, device="cuda")
+    kept, _, _ = cache.evict(w.batch, mass, table, 16, 3)
+    for i in range(2):
+        p, r = ref.cells(w.table[i], 16, kv_lens[i])
+        for h in range(2):
+            j = kept[i, h].cpu().long()
+            assert torch.equal(k[pages - 2 + i, :, h], k[p[j], r[j], h]) and torch.equal(v[pages - 2 + i, :, h], v[p[j], r[j], h])
+    assert cache.status() == 0
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,short", [([1, 1, 1], [5000, 17, 450], [300, 1, 449]), ([90, 1, 30], [2000, 17, 450], [700, 1, 449])])
+def test_captured_calls_with_mass(q_lens, kv_lens, short):
+    """Single tokens and chunks with mass in a graph, with another call of the batch after its capture: replays follow the
+    lengths and have workspaces of their own."""
+    w = World(q_lens, kv_lens, 8, 2, 64, 16, BF, seed=15)
+    n = max(kv_lens)
+    out, mass = torch.empty_like(w.q, memory_format=torch.contiguous_format), torch.zeros((3, 2, n), device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        w.cache.attend(w.batch, w.q, out=out, mass=mass)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            w.cache.attend(w.batch, w.q, out=out, mass=mass)
+    w.batch.kv_lens.copy_(torch.tensor(short, dtype=torch.int32))
+    want, _, want_mass = run(w)
+    for _ in range(2):
+        out.zero_(), mass.zero_()
+        graph.replay()
+        w.cache.attend(w.batch, w.q, mass=torch.zeros_like(mass))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(mass, want_mass)
+    for i, m in enumerate(short):
+        part = slice(w.cu[i], w.cu[i + 1])
+        o, _, _, ot, _, _ = ref.attention(w.q[part].cpu(), w.k_seq[i][:m], w.v_seq[i][:m], 64 ** -0.5, 0, True, None)
+        assert ((out[part].double().cpu() - o).abs() <= ot).all()

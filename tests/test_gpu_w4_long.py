@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import attention_reference as ref
-from test_gpu_w4 import BF, _weights
+from test_gpu_w4 import BF, HF, _weights
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 
@@ -32,3 +32,25 @@ def test_more_tokens_than_a_grid_has_tiles():
     # one rounding of y, and fp32 sums as in test_gpu_w4
     tol = ref.U[BF] * want.abs() + (k / 16 + k / 32 + 16) * 2.0 ** -22 * size + 2.0 ** -25
     assert ((y[at.cuda()].double().cpu() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n,k,group", [(300, 1344, 64), (144, 2880, 32), (1000, 7168, 128)])
+@pytest.mark.parametrize("tokens", [129, 200, 513, 1000])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_matvec_of_prompts(n, k, group, tokens, zeros):
+    from expert_slot_cache_device_gb300.w4 import W4Weights
+
+    for dt in (BF, HF):
+        g = torch.Generator().manual_seed(n + tokens)
+        codes, scales, z = _weights(n, k, group, zeros, dt, g)
+        w = W4Weights(codes.cuda(), scales.cuda(), z.cuda() if zeros else None, group)
+        x = torch.randn((tokens, k + 8), generator=g).to(dt)[:, :k]
+        out = torch.full((tokens, n + 1), 7.0, dtype=dt, device="cuda")
+        wide = torch.zeros((tokens, k + 8), dtype=dt, device="cuda")
+        wide[:, :k] = x.cuda()
+        y = w.matvec(wide[:, :k], out=out[:, :n])
+        want, size = ref.w4(x, codes, scales, z, group)
+        tol = ref.U[dt] * want.abs() + (k / 16 + k / group + 16) * 2.0 ** -22 * size + 2.0 ** -25  # as in test_gpu_w4
+        d = (y.double().cpu() - want).abs()
+        assert (d <= tol).all(), float((d / tol).max())
+        assert (out[:, n:] == 7.0).all()
