@@ -16,6 +16,14 @@ __device__ __forceinline__ void put_lse(const AttendParams &p, int64_t token, in
     if (p.lse2) p.lse2[token * p.q_heads + h] = lse2;
 }
 
+// 16 bytes to shared memory, zeros past the first `bytes` (0 or 16) of them; and all of them.
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // Clusters: this CTA's rank, a barrier of all, a read of another rank's shared memory.
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;

@@ -10,7 +10,9 @@
 //                   as 16-bit pairs, the first 64 slots as soon as they are formed. The maximum is
 //                   taken after that; one more than 2^8 above m raises m for the next step, which
 //                   first rescales O (in tensor memory). A half whose sum is too large for P's type (and
-//                   a row's first step) raises m at once. P, the sum and O always share one m.
+//                   a row's first step) raises m at once. P, the sum and O always share one m. P is rounded to
+//                   the cache's type because the tensor cores take it beside V in that type; the sum is
+//                   of P in fp32.
 //   warps 8, 10     tensor copies: K and V tiles (a box a page and 64 elements, 128-byte swizzle)
 //                   into a ring of stages, pages outside the visible range untouched; warp 8 also
 //                   the queries of the next item once the last S product has read the present ones.

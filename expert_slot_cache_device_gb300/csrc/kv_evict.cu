@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move(const EvictParams p) 
 
 cudaError_t launch_evict(const EvictParams &p, int num_sms, cudaStream_t st) {
     const dim3 grid(p.c.kv_heads, p.bt.batch);
-    // the fewest threads that hold the longest row at once: every count waits for all of them (1013 slots:
-    // 256 threads 7.7 us, 1024 threads 12.2)
+    // the fewest threads that hold the longest row at once: every count waits for all of them (two sequences of 1013
+    // slots: 256 threads 7.7 us, 1024 threads 12.2; of 8000 slots: 512 threads 16.7, 1024 threads 24.6)
     if (p.bt.max_kv <= 256 * 8)
         evict_select<256, 8><<<grid, 256, 0, st>>>(p);
     else if (p.bt.max_kv <= 512 * 16)

@@ -20,7 +20,7 @@ namespace kv {
 enum { kJoinNone = 0, kJoinOn = 1, kJoinEnd = 2 };
 
 struct Range {
-    int lo, hi;  // slots [lo, hi) that at least one row of the item sees; lo is cut down to a multiple of kAlign
+    int lo, hi;  // slots [lo, hi) that at least one row sees
 };
 
 // Visible slots of rows [i0, i1) (tokens) of a sequence: each token i, in slot kv_len - q_len + i,

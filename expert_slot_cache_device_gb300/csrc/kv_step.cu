@@ -4,12 +4,14 @@
 //
 // A CTA is four warps that share nothing while they read: warp w takes tiles w, w + 4, ... of 16
 // slots (4 KiB of K and of V of 128 elements a head, 2 KiB of 64) through its own ring of kStages
-// tiles filled by 16-byte cp.async, two CTAs an SM (four for 64), so about 128 KiB are in flight on an SM. Rows
+// tiles filled by 16-byte cp.async, two CTAs an SM (four for 64), so up to 192 KiB are in flight on an SM. Rows
 // past the visible range are zero-filled by the copy itself, so what such slots hold never
 // reaches a product. Rows are stored with 16-byte chunk c of row r at c ^ (r % 8), which makes the
 // eight rows of an ldmatrix distinct banks. Scores S = Q K^T and O += P V per tile; the softmax keeps
 // a running maximum that O is rescaled to only when it grew by more than 2^8 (the sum and P use
-// the same stale maximum, so the result is the same).
+// the same stale maximum, so the result is the same). P is rounded to the cache's type for P V, the type in which the tensor
+// cores take it beside V (errors against 64 bits of 2.0e-3 in place of 1.6e-3 in bf16, where the output's own rounding is most of
+// either); the sum, the log-sum-exp and the mass are of P in fp32.
 //
 // Work is cut by kv_split.cuh: one line of units of 64 slots over all (sequence, key head)s, an equal
 // part for each CTA; a cut inside an item of at most kSnap units moves to its start, since joining
@@ -19,7 +21,7 @@
 // mass kernel adds 2^(x - lse) once the log-sum-exp is known, reading 4 bytes a (row, slot)
 // instead of K again.
 //
-// 24 sequences of up to 16300 tokens, 4 key heads of 128, 16 query heads each (373 MB of K and V): 76 us, of which the
+// 24 sequences of up to 16300 tokens, 4 key heads of 128, 16 query heads each (373 MB of K and V): 77 us, of which the
 // first kernel takes 70 (5.3 TB/s, 0.79 of a plain copy) and the joining one the rest; with mass 95. SMs finish 10 us apart;
 // 160 such sequences reach 6.5 TB/s. One sequence of 777 tokens: 5.4 us, 64 with a window of 128: 9.4, both latency.
 #include "kv_split.cuh"
@@ -40,9 +42,6 @@ struct Shape {
 };
 constexpr float kSlack = 8.f;  // the maximum may lag by 2^8
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])

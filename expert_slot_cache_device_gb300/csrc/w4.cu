@@ -26,6 +26,7 @@ namespace ftmoe {
 namespace w4 {
 namespace {
 
+using kv::cp16;
 using kv::from_f;
 using kv::to_f;
 
@@ -87,9 +88,6 @@ struct Shape {
     static_assert(WK * TILE * 4 <= kStages * kWarps * WARP, "the sums fit the stages");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
 template <bool BF>
 __device__ __forceinline__ void mma_next(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if (BF)
@@ -174,17 +172,17 @@ __global__ void __launch_bounds__(kThreads, Shape<GROUP, TN, WK>::CTAS) matvec_k
 #pragma unroll
             for (int i = 0; i < S::KPW; i++) {
                 const bool ok = live_r && i < n;
-                cp16(st + mine + i * 512 + lane * 16, ok ? cp + i * 512 : p.packed, ok);
+                cp16(st + mine + i * 512 + lane * 16, ok ? cp + i * 512 : p.packed, ok ? 16 : 0);
             }
 #pragma unroll
             for (int q = 0; q < (PIECES > 32 ? 2 : 1); q++) {
-                if (lane + 32 * q < PIECES) cp16(st + mine + S::KPW * 512 + (lane + 32 * q) * 16, m_left[q] > 0 ? mp[q] : p.packed, m_left[q] > 0);
+                if (lane + 32 * q < PIECES) cp16(st + mine + S::KPW * 512 + (lane + 32 * q) * 16, m_left[q] > 0 ? mp[q] : p.packed, m_left[q] > 0 ? 16 : 0);
                 mp[q] += m_step[q], m_left[q] -= STEP;
             }
             const bool in = xk < k1;
 #pragma unroll
             for (int r = 0; r < 8 * TN; r += XR)
-                if (xr + r < live_x) cp16(st + xd + r * S::RS, in ? xp + (int64_t)r * p.x_stride : p.x, in);
+                if (xr + r < live_x) cp16(st + xd + r * S::RS, in ? xp + (int64_t)r * p.x_stride : p.x, in ? 16 : 0);
             cp += S::CB * 512, kb_next += S::CB, xk += S::CB * 64, xp += S::CB * 64;
         }
         asm volatile("cp.async.commit_group;" ::: "memory");

@@ -17,9 +17,11 @@
 // Up to eight CTAs of a cluster cut k and join their sums in rank order. Every wait is bounded; a CTA in which one runs
 // out gives NaN.
 //
-// Bound by the instructions that decode: about 230 a warp for 32 x 64 codes, 63 % of the issue slots at two CTAs an SM. 16384 x 7168
-// with 24 tokens takes 26.7 us (2.4 TB/s; with no codes decoded 21), with 128 tokens 45 us (0.67 PFLOP/s), where a
-// decoded block serves four times the tokens.
+// 16384 x 7168 with 24 tokens takes 26.7 us (2.4 TB/s). Decoding, about 230 instructions a warp for 32 x 64 codes, fills 63 % of the
+// issue slots at two CTAs an SM, but takes only 6 of the 26.7: with no codes decoded it is 21. The rest is each block's chain of
+// copy, store, product and read-back of every group's sums, and the cut: whole clusters take row groups, here 256 CTAs on 304
+// places, so SMs with two set the time. With 128 tokens 45 us (0.67 PFLOP/s), where a decoded block serves four
+// times the tokens and is decoded again for the next 128 (64 in groups of 32).
 #include <cmath>
 #include "kv_tc05.cuh"
 #include "w4.cuh"
@@ -28,6 +30,7 @@ namespace ftmoe {
 namespace w4 {
 namespace {
 
+using kv::cp16;
 using kv::from_f;
 using kv::to_f;
 
@@ -62,9 +65,6 @@ struct Bars {
     uint64_t a[2][2], d[2][2], xfull[kXStages], xempty[kXStages], done;
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
