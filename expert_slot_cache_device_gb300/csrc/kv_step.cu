@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) step_kernel(const A
 #pragma unroll
             for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_ml[w][row][0]);
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) L += s_ml[w][row][0] == -INFINITY ? 0.f : s_ml[w][row][1] * ex2(s_ml[w][row][0] - M);
+            for (int w = 0; w < kWarps; w++) L += s_ml[w][row][1] * (s_ml[w][row][0] == -INFINITY ? 0.f : ex2(s_ml[w][row][0] - M));  // (a NaN stays)
             float x[PER];
 #pragma unroll
             for (int e = 0; e < PER; e += 4) {

@@ -358,3 +358,21 @@ def test_captured_calls_with_mass(q_lens, kv_lens, short):
         part = slice(w.cu[i], w.cu[i + 1])
         o, _, _, ot, _, _ = ref.attention(w.q[part].cpu(), w.k_seq[i][:m], w.v_seq[i][:m], 64 ** -0.5, 0, True, None)
         assert ((out[part].double().cpu() - o).abs() <= ot).all()
+
+
+@pytest.mark.parametrize("q,n,heads,kv,dim", [(1, 1, 4, 2, 64), (1, 200, 8, 2, 128), (1, 9000, 16, 1, 64), (4, 300, 4, 2, 64),
+                                              (40, 300, 4, 2, 64), (300, 2000, 8, 2, 128)])
+def test_a_nan_that_a_row_sees_reaches_its_results(q, n, heads, kv, dim):
+    """Sixteen keys of one head are NaN: output and log-sum-exp of the rows that see them are too, the other head's and the other
+    sequence's rows are not."""
+    w = World([q, q], [n, n], heads, kv, dim, 16, BF, seed=q + n)
+    at = min(16, n - 1) if q == 1 else n - 2 * q if n > 2 * q else 0
+    p, r = ref.cells(w.table[0], 16, n)
+    bad = slice(at, min(at + 16, n - q + 1))  # every row sees these
+    w.cache.k_pages[p[bad], r[bad], 0] = math.nan
+    out, lse, mass = run(w)
+    per = heads // kv
+    assert torch.isnan(out[:q, :per]).all() and torch.isnan(lse[:q, :per]).all()
+    assert torch.isnan(mass[0, 0, :n]).all()
+    assert torch.isfinite(out[q:]).all() and torch.isfinite(lse[q:]).all() and torch.isfinite(mass[1]).all()
+    assert torch.isfinite(out[:q, per:]).all() and torch.isfinite(lse[:q, per:]).all() and torch.isfinite(mass[0, 1:]).all()
