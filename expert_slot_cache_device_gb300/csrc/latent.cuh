@@ -1,0 +1,119 @@
+// Device views of a paged latent cache and of expanded rows, parameters and launches of the
+// latent-attention kernels.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "kv.cuh"
+
+namespace ftmoe {
+namespace latent {
+
+using kv::Batch;
+using kv::Rows;
+
+constexpr int kGroup = 32;  // latents that share a power of two in 8 bits
+
+struct View {
+    unsigned char *pages;
+    int64_t page, slot;  // bytes
+    int32_t num_pages, page_shift, latent, rope, bits;
+    int32_t *status;
+};
+
+// Bytes of a slot before its rotary part, and the byte where its powers of two start.
+__host__ __device__ __forceinline__ int rope_at(int latent, int bits) {
+    return bits == 16 ? 2 * latent : latent + ((latent / kGroup + 15) & ~15);
+}
+
+// Page of a slot of sequence b, or -1 (recorded) where the table names none.
+__device__ __forceinline__ int page_of(const View &c, const Batch &bt, int b, int slot) {
+    const int page = bt.table[(int64_t)b * bt.table_stride + (slot >> c.page_shift)];
+    if ((uint32_t)page < (uint32_t)c.num_pages) return page;
+    kv::flag(c.status, FTMOE_ERR_ID_RANGE);
+    return -1;
+}
+__device__ __forceinline__ unsigned char *cell(const View &c, int page, int slot) {
+    return c.pages + page * c.page + (slot & ((1 << c.page_shift) - 1)) * c.slot;
+}
+
+// 2^e of a stored byte e + 127 (255: NaN).
+__device__ __forceinline__ float power(uint32_t byte) {
+    return byte == 255 ? __uint_as_float(0x7fc00000u) : (byte ? __uint_as_float(byte << 23) : __uint_as_float(0x00400000u));
+}
+// Two e4m3 codes (low byte first) as floats: exact, as binary16 holds every code.
+__device__ __forceinline__ float2 codes2(uint32_t u) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&h));
+}
+
+// ---------------------------------------------------------------- launches
+struct AppendParams {
+    View c;
+    Batch bt;
+    const uint16_t *lat, *key, *weight;  // weight nullable: no norm
+    int64_t lat_stride, key_stride;
+    float eps, factor;
+    Rows q, q_out;
+    int32_t q_heads, interleaved;
+    const float2 *freq;
+    const int32_t *pos;
+};
+cudaError_t launch_append(const AppendParams &p, bool bf16, cudaStream_t st);
+
+struct ReadParams {
+    View c;
+    Batch bt;
+    const int32_t *cu_rows;
+    int32_t rows;
+    uint16_t *out;
+    int64_t out_stride;
+};
+cudaError_t launch_read(const ReadParams &p, bool bf16, cudaStream_t st);
+
+struct AttendParams {
+    View c;
+    Batch bt;
+    Rows q, q_rope, out;
+    int32_t q_heads, causal;
+    float scale;
+    float *lse;  // [tokens, q_heads] (nullable)
+};
+// Bytes of workspace; with `base` the pointers of p are set into it.
+size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base);
+cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st);
+
+struct ExpandParams {
+    const int32_t *cu_q, *cu_kv;
+    int32_t batch, tokens, rows, max_q, max_kv;
+    int32_t *status;
+    Rows q, k, v, out;
+    const uint16_t *key;  // shared rotary parts
+    int64_t key_stride;
+    int32_t heads, nope, rope, vdim, causal;
+    float scale;
+    float *lse;
+};
+size_t expand_workspace(ExpandParams &p, int num_sms, unsigned char *base);
+cudaError_t launch_expand(const ExpandParams &p, bool bf16, int num_sms, cudaStream_t st);
+
+// Sequence b of an expanded call, each value cut to its range (a cut is recorded). `row0` is its first key row.
+struct RowSeq {
+    kv::Seq s;
+    int row0;
+};
+__device__ __forceinline__ RowSeq row_seq(const ExpandParams &p, int b, int32_t *status) {
+    Batch bt{};
+    bt.tokens = p.tokens, bt.max_q = p.max_q, bt.max_kv = p.max_kv;
+    const int a = p.cu_kv[b], e = p.cu_kv[b + 1];
+    RowSeq r;
+    r.row0 = a < 0 ? 0 : (a > p.rows ? p.rows : a);
+    const int end = e < r.row0 ? r.row0 : (e > p.rows ? p.rows : e);
+    if (r.row0 != a || end != e) kv::flag(status, FTMOE_ERR_STATE);
+    r.s = kv::seq_cut(bt, p.cu_q[b], p.cu_q[b + 1], end - r.row0, status);
+    return r;
+}
+
+}  // namespace latent
+}  // namespace ftmoe

@@ -39,6 +39,8 @@ EXPORTS = [
     "ftmoe_set_ffn_kernels", "ftmoe_ffn_kernels_for", "ftmoe_measure_cpu_read", "ftmoe_set_debug",
     "ftmoe_rope_append", "ftmoe_paged_attention_workspace_bytes", "ftmoe_paged_attention", "ftmoe_kv_evict",
     "ftmoe_w4_packed_bytes", "ftmoe_w4_pack", "ftmoe_w4_matvec",
+    "ftmoe_latent_append", "ftmoe_latent_read", "ftmoe_latent_attention_workspace_bytes", "ftmoe_latent_attention",
+    "ftmoe_expanded_attention_workspace_bytes", "ftmoe_expanded_attention",
 ]
 BACKEND_OFFLOAD, BACKEND_HYBRID = 0, 1
 NOALLOC_SCRATCH_BYTES = 16 << 20
@@ -87,6 +89,21 @@ class RotaryView(ctypes.Structure):
     """ftmoe_rotary: frequency table and the rotated part of a head."""
     _fields_ = [("d_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("factor", ctypes.c_float)]
+
+
+class LatentCacheView(ctypes.Structure):
+    """ftmoe_latent_cache: pages, strides in bytes, geometry, device status word."""
+    _fields_ = [("d_pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("bits", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("latent", ctypes.c_int32), ("rope", ctypes.c_int32),
+                ("d_status", ctypes.c_void_p)]
+
+
+class RowBatchView(ctypes.Structure):
+    """ftmoe_row_batch: the sequences of an expanded call."""
+    _fields_ = [("d_cu_q", ctypes.c_void_p), ("d_cu_kv", ctypes.c_void_p), ("batch", ctypes.c_int32),
+                ("tokens", ctypes.c_int32), ("rows", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("max_kv", ctypes.c_int32), ("d_status", ctypes.c_void_p)]
 
 
 _lib = None
@@ -138,6 +155,12 @@ def lib() -> ctypes.CDLL:
         "ftmoe_w4_packed_bytes": [i32, i32, i32, i32, ctypes.POINTER(sz)],
         "ftmoe_w4_pack": [P, P, P, i32, i32, i32, P, sz, P],
         "ftmoe_w4_matvec": [P, i32, i32, i32, i32, i32, P, i64, i32, P, i64, P],
+        "ftmoe_latent_append": [P, P, P, P, i64, P, i64, P, ctypes.c_float, P, P, i32, P, P],
+        "ftmoe_latent_read": [P, P, P, i32, P, i64, P],
+        "ftmoe_latent_attention_workspace_bytes": [P, P, i32, i32, ctypes.POINTER(sz)],
+        "ftmoe_latent_attention": [P, P, P, P, i32, ctypes.c_float, i32, P, P, P, sz, P],
+        "ftmoe_expanded_attention_workspace_bytes": [P, i32, i32, i32, i32, i32, i32, ctypes.POINTER(sz)],
+        "ftmoe_expanded_attention": [P, i32, i32, i32, i32, i32, P, P, P, i64, P, ctypes.c_float, i32, P, P, P, sz, P],
     }
     for name, args in sig.items():
         f = getattr(L, name)
@@ -374,3 +397,40 @@ def ftmoe_w4_pack(d_codes: int, d_scales: int, d_zeros: int, N: int, K: int, gro
 def ftmoe_w4_matvec(d_packed: int, N: int, K: int, group: int, has_zeros: bool, dtype: int, d_x: int, x_stride: int,
                     tokens: int, d_y: int, y_stride: int, stream: int) -> None:
     _check(lib().ftmoe_w4_matvec(d_packed, N, K, group, has_zeros, dtype, d_x, x_stride, tokens, d_y, y_stride, stream))
+
+
+# ---------------------------------------------------------------- latent attention
+def ftmoe_latent_append(kv, batch, rotary, d_c: int, c_stride: int, d_k_rope: int, k_stride: int, d_weight: int, eps: float,
+                        q, q_out, q_heads: int, d_positions: int, stream: int) -> None:
+    """kv, batch, rotary, q, q_out: ctypes references (byref) to their views; q and q_out None with q_heads = 0."""
+    _check(lib().ftmoe_latent_append(kv, batch, rotary, d_c, c_stride, d_k_rope, k_stride, d_weight, eps, q, q_out, q_heads,
+                                     d_positions, stream))
+
+
+def ftmoe_latent_read(kv, batch, d_cu_rows: int, rows: int, d_out: int, out_stride: int, stream: int) -> None:
+    _check(lib().ftmoe_latent_read(kv, batch, d_cu_rows, rows, d_out, out_stride, stream))
+
+
+def ftmoe_latent_attention_workspace_bytes(kv, batch, q_heads: int, causal: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ftmoe_latent_attention_workspace_bytes(kv, batch, q_heads, causal, ctypes.byref(out)))
+    return out.value
+
+
+def ftmoe_latent_attention(kv, batch, q, q_rope, q_heads: int, scale: float, causal: bool, out, d_lse: int, d_workspace: int,
+                           workspace_bytes: int, stream: int) -> None:
+    _check(lib().ftmoe_latent_attention(kv, batch, q, q_rope, q_heads, scale, causal, out, d_lse, d_workspace, workspace_bytes,
+                                        stream))
+
+
+def ftmoe_expanded_attention_workspace_bytes(batch, dtype: int, heads: int, nope: int, rope: int, v_dim: int, causal: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check(lib().ftmoe_expanded_attention_workspace_bytes(batch, dtype, heads, nope, rope, v_dim, causal, ctypes.byref(out)))
+    return out.value
+
+
+def ftmoe_expanded_attention(batch, dtype: int, heads: int, nope: int, rope: int, v_dim: int, q, k, d_k_rope: int,
+                             k_rope_stride: int, v, scale: float, causal: bool, out, d_lse: int, d_workspace: int,
+                             workspace_bytes: int, stream: int) -> None:
+    _check(lib().ftmoe_expanded_attention(batch, dtype, heads, nope, rope, v_dim, q, k, d_k_rope, k_rope_stride, v, scale, causal,
+                                          out, d_lse, d_workspace, workspace_bytes, stream))

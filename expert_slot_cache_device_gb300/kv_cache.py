@@ -150,7 +150,29 @@ class Rotary:
         self.ref = ctypes.byref(self._view)
 
 
-class KVBatch:
+class Workspaces:
+    """Device memory of one batch's calls, kept for the next."""
+
+    def __init__(self, device):
+        self.device = device
+        self._bytes, self._spaces = {}, {}
+        self._lock = threading.Lock()
+
+    def _workspace(self, need: int, handle: int, stream) -> torch.Tensor:
+        """At least ``need`` bytes for a call on stream ``handle``, kept for the next one there: a step's layers
+        run one after another (an allocation a call takes 4 us of its 12 on the host). A large one is not
+        kept: 64 sequences of 128k tokens with mass need 4 GB, and their call takes longer on the GPU than
+        the allocation on the host. A captured call gets its own, which lives with the graph. The caller holds ``_lock`` until the call's kernels are
+        enqueued: another thread's may not come between them, which share it."""
+        if need > _KEPT or torch.cuda.is_current_stream_capturing():
+            return _new(need, torch.uint8, self.device, stream)
+        t = self._spaces.get(handle)
+        if t is None or t.numel() < need:
+            t = self._spaces[handle] = _new(need, torch.uint8, self.device, stream)
+        return t
+
+
+class KVBatch(Workspaces):
     """The sequences of one call.
 
     block_table  int32 [batch, pages]: page of each block of page_size slots
@@ -171,11 +193,10 @@ class KVBatch:
         if not 0 <= max_q <= _INT_MAX or not 0 <= max_kv <= _INT_MAX:
             raise ValueError(f"max_q={max_q}, max_kv={max_kv}: outside [0, {_INT_MAX}]")
         self.max_q, self.max_kv = int(max_q), int(max_kv)
-        self.device = block_table.device
+        super().__init__(block_table.device)
         stride = block_table.stride(0) if self.batch > 1 else block_table.shape[1]
         self._args = (block_table.data_ptr(), stride, kv_lens.data_ptr(), cu_q.data_ptr(), self.batch)
-        self._views, self._bytes, self._spaces = {}, {}, {}
-        self._lock = threading.Lock()
+        self._views = {}
 
     def _ref(self, tokens: int):
         """Reference to the C view for token arrays of `tokens` rows."""
@@ -185,21 +206,29 @@ class KVBatch:
             v = self._views[tokens] = (ctypes.byref(v), v)
         return v[0]
 
-    def _workspace(self, need: int, handle: int, stream) -> torch.Tensor:
-        """At least ``need`` bytes for a call on stream ``handle``, kept for the next one there: a step's layers
-        run one after another (an allocation a call takes 4 us of its 12 on the host). A large one is not
-        kept: 64 sequences of 128k tokens with mass need 4 GB, and their call takes longer on the GPU than
-        the allocation on the host. A captured call gets its own, which lives with the graph. The caller holds ``_lock`` until the call's kernels are
-        enqueued: another thread's may not come between them, which share it."""
-        if need > _KEPT or torch.cuda.is_current_stream_capturing():
-            return _new(need, torch.uint8, self.device, stream)
-        t = self._spaces.get(handle)
-        if t is None or t.numel() < need:
-            t = self._spaces[handle] = _new(need, torch.uint8, self.device, stream)
-        return t
+
+class Status:
+    """Sticky device status word of an owner's calls."""
+
+    def __init__(self, device):
+        self._status = torch.zeros(1, dtype=torch.int32, device=device)
+
+    def _at(self, stream):
+        if stream is None:
+            return torch.cuda.current_stream(self.device)
+        return torch.cuda.ExternalStream(_stream(stream), device=self.device)
+
+    def status(self, stream=None) -> int:
+        """The first device error of the calls since the last reset, or 0 (synchronises the stream)."""
+        with torch.cuda.stream(self._at(stream)):
+            return int(self._status.item())
+
+    def reset_status(self, stream=None) -> None:
+        with torch.cuda.stream(self._at(stream)):
+            self._status.zero_()
 
 
-class PagedKVCache:
+class PagedKVCache(Status):
     """Keys and values of one layer in pages.
 
     num_pages, page_size (a power of two, 16..256), kv_heads, head_dim (attention: 64 or 128)
@@ -227,7 +256,7 @@ class PagedKVCache:
         self.num_pages, self.page_size, self.kv_heads, self.head_dim, self.dtype = *shape, dtype
         self.device = self.k_pages.device
         self._scale = head_dim ** -0.5
-        self._status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        super().__init__(self.device)
         self._view = F.KVCacheView(self.k_pages.data_ptr(), self.v_pages.data_ptr(), *self.k_pages.stride()[:3],
                                    *self.v_pages.stride()[:3], _DTYPES[dtype], num_pages, page_size, kv_heads, head_dim,
                                    self._status.data_ptr())
@@ -359,17 +388,3 @@ class PagedKVCache:
         F.ftmoe_kv_evict(self._ref, batch._ref(0), mass.data_ptr(), ms, mh, budget, recent, new_table.data_ptr(), stride,
                          kept.data_ptr(), new_mass.data_ptr(), new_lens.data_ptr(), _handle(stream, self._dev))
         return kept, new_mass, new_lens
-
-    def _on(self, stream):
-        if stream is None:
-            return torch.cuda.current_stream(self.device)
-        return torch.cuda.ExternalStream(_stream(stream), device=self.device)
-
-    def status(self, stream=None) -> int:
-        """Sticky device status of this cache's calls (synchronises the stream)."""
-        with torch.cuda.stream(self._on(stream)):
-            return int(self._status.item())
-
-    def reset_status(self, stream=None) -> None:
-        with torch.cuda.stream(self._on(stream)):
-            self._status.zero_()

@@ -568,6 +568,98 @@ int ftmoe_w4_pack(const void *d_codes, const void *d_scales, const void *d_zeros
 int ftmoe_w4_matvec(const void *d_packed, int32_t N, int32_t K, int32_t group, int32_t has_zeros, int32_t dtype,
                     const void *d_x, int64_t x_stride, int32_t tokens, void *d_y, int64_t y_stride, void *stream);
 
+/* ------------------------------------------------------------------------------------
+ * Latent attention: a cache of one shared vector a token (a normalised latent, from which the
+ * keys and values of every head are products, and one rotary part of the key that all heads
+ * share), its write, its reading back, and attention in the absorbed form (over the latents
+ * themselves) and in the expanded form (over each head's keys and values as rows). Ownership,
+ * capture and device status are as in the attention half above.
+ * ------------------------------------------------------------------------------------ */
+
+/* View of one layer's paged latent cache: num_pages pages of page_size slots; slot `row` of a
+ * page sits at page * page_stride + row * slot_stride bytes. A slot holds
+ *   bits 16: latent elements, then rope elements, of `dtype`;
+ *   bits 8:  latent e4m3 codes; a byte e + 127 for each 32 of them (the value of a code is
+ *            code * 2^e, rounded to dtype; byte 255: 32 NaNs), padded to 16 bytes; then rope elements of `dtype`.
+ * Base 16-byte aligned, strides positive multiples of 16.
+ *   dtype   FTMOE_DT_BF16 or FTMOE_DT_F16 (queries, new rows and outputs have it too);
+ *   latent  a multiple of 128, at most 512; rope: a multiple of 16 from 16 to 64;
+ *   page_size a power of two in [16, 256]; d_status as in ftmoe_kv_cache. */
+typedef struct {
+    void *d_pages;
+    int64_t page_stride, slot_stride; /* bytes */
+    int32_t dtype, bits, num_pages, page_size, latent, rope;
+    int32_t *d_status;
+} ftmoe_latent_cache;
+
+/* Write the new tokens to their slots and rotate their queries:
+ *   y = c * rsqrt(mean(c^2) + eps) * weight (c itself when d_weight is NULL), rounded to dtype;
+ *   with bits = 8 each 32 of y get the least e in [-127, 127] with max |y| <= 448 * 2^e and the codes
+ *   e4m3(y * 2^-e), to nearest even (y is cut to +-1.875 times the largest power of two of dtype
+ *   first, so that every code's value is finite; a group with an infinity or a NaN gets byte 255);
+ *   k_rope [tokens, rope] and q_rope [tokens, q_heads, rope] turn by d_positions (|position| < 2^24)
+ *   as in ftmoe_rope_append, with rotary->rot_dim = rope.
+ * c [tokens, latent] and k_rope have rows c_stride and k_stride elements apart (bases 16-byte
+ * aligned, strides multiples of eight); d_weight [latent], 16-byte aligned, of dtype. eps >= 0, finite. q_out may equal
+ * q (the same rows and strides); otherwise no array may overlap another. q_heads = 0 leaves the
+ * queries out. Norms, angles and products are formed in fp32. */
+int ftmoe_latent_append(const ftmoe_latent_cache *kv, const ftmoe_kv_batch *batch, const ftmoe_rotary *rotary,
+                        const void *d_c, int64_t c_stride, const void *d_k_rope, int64_t k_stride, const void *d_weight,
+                        float eps, const ftmoe_rows *q, const ftmoe_rows *q_out, int32_t q_heads,
+                        const int32_t *d_positions, void *stream);
+
+/* Cached tokens as rows: slot j of sequence b, latent and rope elements of dtype, goes to row
+ * d_cu_rows[b] + j of out (rows out_stride elements apart, 16-byte aligned, a multiple of eight).
+ * d_cu_rows int32 [batch + 1]: an entry below its predecessor or outside [0, rows], or a difference
+ * that is not kv_lens[b], gives FTMOE_ERR_STATE and is cut to its range (of two lengths the smaller
+ * is read). Rows that no sequence covers, and those of a bad page, are left alone. cu_q and tokens
+ * of the batch are not used. */
+int ftmoe_latent_read(const ftmoe_latent_cache *kv, const ftmoe_kv_batch *batch, const int32_t *d_cu_rows, int32_t rows,
+                      void *d_out, int64_t out_stride, void *stream);
+
+/* Absorbed attention of the new tokens over the cached ones:
+ *   s_j = scale * (q . c_j + q_rope . k_j), l = sum_j exp(s_j), out = sum_j exp(s_j) c_j / l,
+ *   lse = log l, over the slots j <= kv_len - q_len + i of new token i (causal != 0), or all below
+ *   kv_len (causal = 0). A row that sees nothing gives out = 0, lse = -inf.
+ *   q, out      [tokens, q_heads, latent]; out may be q itself (the same rows and strides; no other overlap);
+ *   q_rope      [tokens, q_heads, rope];
+ *   scale       positive and finite;
+ *   d_lse       fp32 [tokens, q_heads] or NULL;
+ *   d_workspace 256-byte aligned, at least what ftmoe_latent_attention_workspace_bytes gives for the
+ *               same arguments (0 for some: NULL will do); calls that overlap on the GPU need one each.
+ * Slots that no row sees may hold anything. Slots that some rows of a call see and others do not have to be finite.
+ * Scores, maxima, sums and outputs are kept in fp32; the probabilities are rounded to dtype for the
+ * product with the latents (not for l and lse). */
+int ftmoe_latent_attention_workspace_bytes(const ftmoe_latent_cache *kv, const ftmoe_kv_batch *batch, int32_t q_heads,
+                                           int32_t causal, size_t *bytes);
+int ftmoe_latent_attention(const ftmoe_latent_cache *kv, const ftmoe_kv_batch *batch, const ftmoe_rows *q,
+                           const ftmoe_rows *q_rope, int32_t q_heads, float scale, int32_t causal, const ftmoe_rows *out,
+                           float *d_lse, void *d_workspace, size_t workspace_bytes, void *stream);
+
+/* The sequences of an expanded call: sequence b has new tokens cu_q[b] .. cu_q[b + 1] - 1 of the token
+ * arrays and keys and values in rows cu_kv[b] .. cu_kv[b + 1] - 1, the new tokens' the last of them.
+ * Entries below their predecessor or out of range, and sequences longer than max_q or max_kv, give
+ * FTMOE_ERR_STATE in d_status (nullable, sticky) and are cut to their range. */
+typedef struct {
+    const int32_t *d_cu_q, *d_cu_kv; /* [batch + 1] */
+    int32_t batch, tokens, rows, max_q, max_kv;
+    int32_t *d_status;
+} ftmoe_row_batch;
+
+/* Expanded attention: s_j = scale * (q[:nope] . k_j + q[nope:] . kr_j), l, out and lse as above.
+ *   q       [tokens, heads, nope + rope];  k [rows, heads, nope];  v [rows, heads, v_dim];  out [tokens, heads, v_dim];
+ *   k_rope  [rows, rope], k_rope_stride elements apart (16-byte aligned, a multiple of eight), shared by the heads;
+ *   dtype   FTMOE_DT_BF16 or FTMOE_DT_F16, of all of them;
+ *   (nope, v_dim) is (128, 128) or (64, 64), rope a multiple of 16 from 16 to 64;
+ * out overlaps no other array. d_workspace as above. Rows of k, k_rope and v that no token sees may hold anything;
+ * those that some new tokens of a sequence see and others do not have to be finite. */
+int ftmoe_expanded_attention_workspace_bytes(const ftmoe_row_batch *batch, int32_t dtype, int32_t heads, int32_t nope,
+                                             int32_t rope, int32_t v_dim, int32_t causal, size_t *bytes);
+int ftmoe_expanded_attention(const ftmoe_row_batch *batch, int32_t dtype, int32_t heads, int32_t nope, int32_t rope,
+                             int32_t v_dim, const ftmoe_rows *q, const ftmoe_rows *k, const void *d_k_rope,
+                             int64_t k_rope_stride, const ftmoe_rows *v, float scale, int32_t causal, const ftmoe_rows *out,
+                             float *d_lse, void *d_workspace, size_t workspace_bytes, void *stream);
+
 /* Message of the last failing call on this thread. */
 const char *ftmoe_last_error(void);
 
