@@ -67,6 +67,10 @@ template <bool BF, int N, bool B_MN>
 constexpr uint32_t kInstr = (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) | ((B_MN ? 1u : 0u) << 16) |
                             ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 
+// The same with M given, and A stored with M consecutive where a_mn.
+template <bool BF, int M, int N, bool A_MN, bool B_MN>
+constexpr uint32_t kInstrM = (kInstr<BF, N, B_MN> & ~(31u << 24)) | ((A_MN ? 1u : 0u) << 15) | ((uint32_t)(M >> 4) << 24);
+
 // Operand of 128-byte rows with the 128-byte swizzle, groups of eight rows 1024 bytes apart
 // (stride offset), as the low word of its descriptor; the high word is kDescHi. K-major: rows are M
 // or N, a K = 16 step 32 bytes further in the row. MN-major: rows are K, the next 64 elements of
@@ -264,6 +268,11 @@ bool page_map(CUtensorMap &m, const View &c, bool keys, bool bf16, int box_slots
 bool query_map(CUtensorMap &m, const AttendParams &p, bool bf16);
 // Tensor map of rows: [row][column], boxes of 64 columns x box_rows rows; zeros past the ends.
 bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, int box_rows, bool bf16);
+// Tensor map of three axes, the first consecutive: elements of 8 bits or of a 16-bit type, strides in bytes, with the 128-byte
+// swizzle or none; zeros past the ends.
+enum class Elem { U8, BF16, F16 };
+bool box_map(CUtensorMap &m, Elem type, const void *x, const int64_t (&dims)[3], int64_t stride1, int64_t stride2, const int (&box)[3],
+             bool swizzle);
 
 }  // namespace kv
 }  // namespace ftmoe

@@ -72,6 +72,12 @@ struct ReadParams {
 };
 cudaError_t launch_read(const ReadParams &p, bool bf16, cudaStream_t st);
 
+// How a call's work is cut (latent_line.cuh): an item is item_tokens tokens of one sequence and one of `blocks` blocks of heads.
+struct Line {
+    int32_t batch, blocks, item_tokens, max_q, causal;
+    int4 *join;  // [CTAs] (kv_split.cuh), or NULL: a CTA an item, whole
+};
+
 struct AttendParams {
     View c;
     Batch bt;
@@ -79,6 +85,12 @@ struct AttendParams {
     int32_t q_heads, causal;
     float scale;
     float *lse;  // [tokens, q_heads] (nullable)
+    Line line;
+    int32_t heads;  // of a block
+    // workspace (attend_workspace): parts of split items
+    float *part_o;
+    float2 *part_ml;
+    __device__ __forceinline__ kv::Seq seq(int b, int32_t *status) const { return kv::seq_info(bt, b, status); }
 };
 // Bytes of workspace; with `base` the pointers of p are set into it.
 size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base);

@@ -1,0 +1,664 @@
+// Absorbed latent attention on the 5th-generation tensor cores. All heads read the same cached vectors, so the rows of an
+// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 64 slots. Both products have the cache as their A
+// operand, straight from shared memory in the one layout that the copies leave it in:
+//   S^T [64 slots, NR rows] = [C | K] [Q | Q_rope]^T     A: slots are M, latents K (K-major)
+//   O^T [latent, NR rows]  += C^T P^T                    A: latents are M = 128, slots K (M-major)
+// so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most; rows as M would take all of it), and few
+// rows cost few columns instead of an unused part of M = 128. P^T goes to shared memory as the B operand.
+//
+// Persistent, one CTA an SM, work cut by latent_line.cuh. Roles:
+//   warps 0-3   softmax of a tile: warp w has slots 16 w .. 16 w + 15 (tensor memory holds M = 64 in the first 16 lanes of
+//               each quarter), a thread two slots' values of every eighth pair of rows. P = 2^(s scale log2 e - m) in fp32
+//               with the maximum m of the tiles before; one vote of the four warps tells whether a score is more than 2^8
+//               above it, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to the cache's type, as
+//               the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at the item's end.
+//   warp 4      tensor copies: units of 128 latents x 64 slots (a box a page and 64 latents, 128-byte swizzle), rotary parts and queries.
+//   warp 5      issues tcgen05.mma: S of a tile, then O += C^T P^T, then S of the next.
+//   warp 6      walks the work and hands the parts out.
+//   warps 8-15  (8 bits) turn units of codes into units of elements.
+// Every wait is bounded; one that runs out is recorded and ends the role.
+#include "latent_line.cuh"
+
+namespace ftmoe {
+namespace latent {
+namespace {
+
+using kv::bar_expect;
+using kv::bar_init;
+using kv::commit;
+using kv::desc_lo;
+using kv::ex2;
+using kv::fence_after;
+using kv::fence_async;
+using kv::fence_before;
+using kv::from_f2;
+using kv::mma_ss;
+using kv::tma3;
+using kv::wait_bar;
+
+constexpr int kTile = 64;
+constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kConvWarps = 8;
+constexpr float kSlack = 8.f;
+constexpr int kChunk = kTile * 128;  // 64 elements of a tile's slots
+constexpr int kUnit = 2 * kChunk;    // 128 latents of a tile's slots
+
+template <bool Q8, int NR>
+struct Shape {
+    static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
+    static constexpr int kUnits = Q8 ? (NR == 64 ? 5 : NR == 32 ? 6 : 7) : (NR == 64 ? 8 : NR == 32 ? 10 : 11);
+    static constexpr int kRopes = NR == 64 ? 2 : 3;
+    static constexpr int kRaws = Q8 ? (NR == 64 ? 5 : 7) : 0;  // 128 codes of a tile's slots each
+    static constexpr int kRaw = kChunk, kScale = kTile * 16;
+    static constexpr int kQ = 9 * NR * 128;
+    static constexpr int kP = NR * 128 > 4096 ? NR * 128 : 4096;  // also scratch between tiles
+    static constexpr int kSmem = 1024 + kQ + kP + kUnits * kUnit + kRopes * kChunk + kRaws * kRaw + (Q8 ? kRopes * kScale : 0);
+    static constexpr uint32_t kS = 256;  // column of S; O is at 0
+};
+constexpr int kMaxUnits = 11, kMaxRopes = 3, kMaxRaws = 7;
+
+struct Maps {
+    CUtensorMap q, q_rope, lat, rope, scale;
+};
+
+struct Bars {
+    uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits], rope_full[kMaxRopes], rope_empty[kMaxRopes];
+    uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws], scale_full[kMaxRopes], scale_empty[kMaxRopes];
+    uint64_t qfull, qempty, s, p, o, done;
+};
+
+// A place in a ring of N and the phase of its barriers.
+template <int N>
+struct Turn {
+    int at = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, ph ^= 1;
+    }
+};
+
+// Slots of tensor memory as fragments: a thread's registers 4 j .. 4 j + 3 are rows 8 j + 2 (lane % 4), + 1 of slot
+// lane / 4, then of slot lane / 4 + 8.
+template <int NR>
+__device__ __forceinline__ void load_s(uint32_t a, uint32_t (&x)[NR / 2]) {
+    if constexpr (NR == 64) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+            "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : FTMOE_R32(x)
+            : "r"(a)
+            : "memory");
+    } else if constexpr (NR == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : FTMOE_R4(x, 0), FTMOE_R4(x, 4), FTMOE_R4(x, 8), FTMOE_R4(x, 12)
+            : "r"(a)
+            : "memory");
+    } else {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : FTMOE_R4(x, 0), FTMOE_R4(x, 4)
+            : "r"(a)
+            : "memory");
+    }
+}
+// 16 consecutive columns of this thread's lane.
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t *x) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : FTMOE_R4(x, 0), FTMOE_R4(x, 4), FTMOE_R4(x, 8), FTMOE_R4(x, 12)
+        : "r"(a)
+        : "memory");
+}
+
+// Barrier of the four softmax warps; true if any thread brings it.
+__device__ __forceinline__ bool vote(bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)mine)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ float ld_f(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+
+__device__ __forceinline__ int part_tiles(const Part &w) {
+    const int end = w.last * kStep < w.hi ? w.last * kStep : w.hi, n = (end - w.first * kStep + kTile - 1) / kTile;
+    return n > 0 ? n : 1;
+}
+
+template <bool BF, bool Q8, int NR>
+__global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const AttendParams p, const __grid_constant__ Maps maps) {
+    using S = Shape<Q8, NR>;
+    extern __shared__ __align__(1024) unsigned char sm_raw[];
+    __shared__ Bars bar;
+    __shared__ PartRing parts;
+    __shared__ uint32_t s_tmem;
+    __shared__ long long s_warp[S::kWarps];
+    __shared__ Walk<AttendParams> s_walk;
+    __shared__ uint16_t s_tok[NR];  // token of a row in its item
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + S::kUnits * kUnit, raws = ropes + S::kRopes * kChunk;
+    const uint32_t qs = raws + S::kRaws * S::kRaw, ps = qs + S::kQ, scales = ps + S::kP;
+    const int L = p.c.latent >> 7;  // units of a tile
+
+    if (tid == 0) {
+        for (int i = 0; i < S::kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvWarps : 1), bar_init(&bar.unit_empty[i], 1);
+        for (int i = 0; i < S::kRopes; i++) {
+            bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
+            bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
+        }
+        for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvWarps);
+        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], 6 + (Q8 ? kConvWarps : 0));
+        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.s, 1), bar_init(&bar.p, 4), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const int used = p.heads * p.line.item_tokens;  // rows of an item
+    if (tid < NR) s_tok[tid] = tid < used ? tid / p.heads : 0;
+    // rows past those are zeros: no copy writes them
+    for (int i = tid; i < 9 * (NR - used) * 8; i += S::kThreads) {
+        const int c = i / ((NR - used) * 8), r = i - c * ((NR - used) * 8);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qs + c * NR * 128 + used * 128 + r * 16), "r"(0) : "memory");
+    }
+    fence_async();
+    Walk<AttendParams> walk;
+    const bool any = plan<S::kWarps>(p, walk, s_warp, reinterpret_cast<long long *>(sm_raw + (ps - su32(sm_raw))), &s_walk, p.c.status);
+    asm volatile("griddepcontrol.launch_dependents;" :::);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(&s_tmem);
+    if (!any) {  // the whole CTA
+        if (tid == 0 && p.line.join) p.line.join[blockIdx.x] = make_int4(0, 0, 0, kv::kJoinNone);
+        if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+        return;
+    }
+    bool ok = true;
+    Part w;
+    uint32_t n_part = 0;
+
+    if (warp < 4) {  // ---------------------------------------------------- softmax
+        const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
+        const float c2 = p.scale * kv::kLog2e;
+        const int row0 = 16 * warp + (lane >> 2), col0 = 2 * (lane & 3);
+        constexpr int NB = NR / 8;
+        uint32_t ns = 0, no = 0;
+        Turn<S::kUnits> un;
+        while (!vote(!take(parts, n_part, w, ok))) {
+            const int nt = part_tiles(w);
+            const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
+            auto limit = [&](int c) {                       // slots that row c sees
+                const int t = s_tok[c], at = w.slot + t;
+                return t >= w.left || at < 0 ? 0 : (p.line.causal ? at + 1 : w.kv_len);
+            };
+            const int least = dead || w.slot < 0 ? 0 : (p.line.causal ? w.slot + 1 : w.kv_len);
+            float m[2 * NB], l[2 * NB];
+#pragma unroll
+            for (int i = 0; i < 2 * NB; i++) m[i] = -INFINITY, l[i] = 0.f;
+            for (int j = 0; j < nt; j++, ns++) {
+                const int s0 = w.first * kStep + j * kTile;
+                ok = ok && warp_wait(&bar.s, ns & 1);
+                fence_after();
+                uint32_t x[NR / 2];
+                load_s<NR>(lanes + S::kS, x);
+                if (s0 + kTile > least) {
+                    const int a = s0 + row0;
+#pragma unroll
+                    for (int i = 0; i < NB; i++)
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int lim = limit(8 * i + col0 + e);
+                            if (a >= lim) x[4 * i + e] = 0xff800000u;
+                            if (a + 8 >= lim) x[4 * i + 2 + e] = 0xff800000u;
+                        }
+                }
+                bool over = !ok;
+#pragma unroll
+                for (int i = 0; i < NB; i++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float t = fmaxf(__uint_as_float(x[4 * i + e]), __uint_as_float(x[4 * i + 2 + e])) * c2;
+                        over = over || t > m[2 * i + e] + kSlack;
+                    }
+                if (vote(over)) {
+                    if (vote(!ok)) break;
+                    // m to at least each row's maximum over the tile (P's place is free: the product that read it is done)
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; i++) {
+                        const int r = 4 * (i >> 1) + (i & 1);
+                        float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2])) * c2;
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
+                        if (lane < 4) st_f(ps + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
+                    }
+                    vote(false);
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; i++) {
+                        const uint32_t a = ps + (8 * (i >> 1) + col0 + (i & 1)) * 4;
+                        const float t = fmaxf(fmaxf(ld_f(a), ld_f(a + NR * 4)), fmaxf(ld_f(a + 2 * NR * 4), ld_f(a + 3 * NR * 4)));
+                        const float n = fmaxf(m[i], t), f = m[i] == -INFINITY ? 0.f : ex2(m[i] - n);
+                        m[i] = n, l[i] *= f;
+                        if (warp == 0 && lane < 4) st_f(a + 4 * NR * 4, f);
+                    }
+                    vote(false);
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int k = 0; k < L * NR; k += 16) {
+                            uint32_t y[16];
+                            tm_ld16(lanes + k, y);
+#pragma unroll
+                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(ps + (4 * NR + (k + e) % NR) * 4));
+                            kv::tm_st16(lanes + k, y);
+                        }
+                        kv::tm_st_wait();
+                    }
+                    vote(false);  // the scratch has been read
+                }
+#pragma unroll
+                for (int i = 0; i < NB; i += 2) {
+                    uint32_t y[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {  // rows 8 i, then 8 (i + 1); slots, then slots + 8
+                        const int r = 4 * (i + (k >> 1)) + 2 * (k & 1), c = 2 * (i + (k >> 1));
+                        const float z0 = m[c] == -INFINITY ? 0.f : -m[c], z1 = m[c + 1] == -INFINITY ? 0.f : -m[c + 1];
+                        const float a = ex2(fmaf(__uint_as_float(x[r]), c2, z0)), b = ex2(fmaf(__uint_as_float(x[r + 1]), c2, z1));
+                        l[c] += a, l[c + 1] += b;
+                        y[k] = from_f2<BF>(a, b);
+                    }
+                    // transposed: a row's slots consecutive, 16-byte piece c of row r at c ^ (r % 8)
+                    const int r = lane & 7, k = lane >> 3;
+                    const uint32_t at = ps + (8 * (i + (k >> 1)) + r) * 128 + (((2 * warp + (k & 1)) ^ r) << 4);
+                    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                                 "r"(y[3])
+                                 : "memory");
+                }
+                if (s0 + kTile > w.hi) {  // latents of slots that no row sees: what they hold must not reach 0 * C
+                    const int r0 = w.hi > s0 ? w.hi - s0 : 0;
+                    Turn<S::kUnits> t = un;
+                    for (int u = 0; u < L; u++, t.next()) {
+                        ok = ok && warp_wait(&bar.unit_full[t.at], t.ph);
+                        for (int i = tid; i < (kTile - r0) * 16; i += 128)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(units + t.at * kUnit + ((i >> 3) & 1) * kChunk + (r0 + (i >> 4)) * 128 + ((i & 7) << 4)),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                }
+                for (int u = 0; u < L; u++) un.next();
+                fence_async();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.p);
+            }
+            ok = ok && warp_wait(&bar.o, no++ & 1);
+            if (vote(!ok)) break;
+            fence_after();
+            const bool whole = w.first == 0 && w.last == w.steps;
+            const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
+#pragma unroll
+            for (int i = 0; i < 2 * NB; i++) {
+                float t = l[i];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
+                const int c = 8 * (i >> 1) + col0 + (i & 1);
+                if (lane < 4) st_f(ps + (warp * NR + c) * 4, t);
+                if (warp == 0 && lane < 4) st_f(ps + (5 * NR + c) * 4, m[i]);
+            }
+            vote(false);
+            if (tid < NR) {
+                const int c = tid, t = s_tok[c], h = w.block * p.heads + c - t * p.heads;
+                const float sum = (ld_f(ps + c * 4) + ld_f(ps + (NR + c) * 4)) + (ld_f(ps + (2 * NR + c) * 4) + ld_f(ps + (3 * NR + c) * 4));
+                const float top = ld_f(ps + (5 * NR + c) * 4);
+                if (!whole)
+                    p.part_ml[(int64_t)part * NR + c] = make_float2(top, sum);
+                else if (p.lse && c < used && t < w.left && h < p.q_heads)
+                    p.lse[(int64_t)(w.token + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                st_f(ps + (4 * NR + c) * 4, !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
+            }
+            vote(false);
+            // a warp has 32 latents of each unit, a lane one, columns are rows of the item
+            uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)w.block * p.heads * p.out.head;
+            float *po = p.part_o + (int64_t)part * NR * p.c.latent;
+#pragma unroll 1
+            for (int k = 0; k < L * NR; k += 16) {
+                uint32_t y[16];
+                tm_ld16(lanes + k, y);
+                const int at = (k / NR) * 128 + 32 * warp;
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const int c = k % NR + e;
+                    if (whole) {  // two lanes swap, so that each writes two latents of one row
+                        const float a = __uint_as_float(y[e]) * ld_f(ps + (4 * NR + c) * 4), b = __uint_as_float(y[e + 1]) * ld_f(ps + (4 * NR + c + 1) * 4);
+                        const float got = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
+                        const int r = c + (lane & 1), t = s_tok[r], h = r - t * p.heads;
+                        if (r < used && t < w.left && w.block * p.heads + h < p.q_heads)
+                            *reinterpret_cast<uint32_t *>(out + t * p.out.token + h * p.out.head + at + (lane & ~1)) =
+                                lane & 1 ? from_f2<BF>(got, b) : from_f2<BF>(a, got);
+                    } else {
+                        po[(int64_t)c * p.c.latent + at + lane] = __uint_as_float(y[e]);
+                        po[(int64_t)(c + 1) * p.c.latent + at + lane] = __uint_as_float(y[e + 1]);
+                    }
+                }
+            }
+            fence_before();  // O is read before the next part's first P is announced
+        }
+    } else if (warp == kCopyWarp) {  // ------------------------------------- cached tokens and queries
+        const int box = 1 << (p.c.page_shift < 6 ? p.c.page_shift : 6), boxes = kTile / box;
+        const int mine = lane % boxes, half = lane / boxes;
+        Turn<S::kUnits> un;
+        Turn<S::kRopes> ro;
+        Turn<Q8 ? S::kRaws : 1> ra;
+        uint32_t nq = 0;
+        while (ok && take(parts, n_part, w, ok)) {
+            const int nt = part_tiles(w), s1 = w.first * kStep;
+            const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
+            auto page_at = [&](int j) {
+                const int slot = s1 + j * kTile + mine * box;
+                return j < nt && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+            };
+            int next = page_at(0);
+            if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            nq++;
+            if (lane == 0) bar_expect(&bar.qfull, (2 * L + 1) * used * 128);
+            __syncwarp();
+            if (lane < 2 * L + 1)
+                tma3(qs + lane * NR * 128, lane < 2 * L ? &maps.q : &maps.q_rope, lane < 2 * L ? 64 * lane : 0, w.block * p.heads, w.token, &bar.qfull);
+            for (int j = 0; j < nt && ok; j++) {
+                int page = next;
+                next = page_at(j + 1);  // on its way while this tile waits for its places
+                const int slot = s1 + j * kTile + mine * box, row = slot & ((1 << p.c.page_shift) - 1);
+                if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
+                    if (slot < w.hi) kv::flag(p.c.status, FTMOE_ERR_ID_RANGE);
+                    page = -1;
+                }
+                const int valid = __popc(__ballot_sync(~0u, lane < boxes && page >= 0)) * box;  // slots that are copied
+                if (Q8) {
+                    ok = ok && warp_wait(&bar.scale_empty[ro.at], ro.ph ^ 1);
+                    if (!ok) break;
+                    if (lane == 0) bar_expect(&bar.scale_full[ro.at], valid * 16);
+                    __syncwarp();
+                    if (half == 0 && page >= 0) tma3(scales + ro.at * S::kScale + mine * box * 16, &maps.scale, 0, row, page, &bar.scale_full[ro.at]);
+                }
+                for (int u = 0; u < L; u++) {
+                    if (Q8) {
+                        ok = ok && warp_wait(&bar.raw_empty[ra.at], ra.ph ^ 1);
+                        if (!ok) break;
+                        if (lane == 0) bar_expect(&bar.raw_full[ra.at], valid * 128);
+                        __syncwarp();
+                        if (half == 0 && page >= 0) tma3(raws + ra.at * S::kRaw + mine * box * 128, &maps.lat, 128 * u, row, page, &bar.raw_full[ra.at]);
+                        ra.next();
+                    } else {
+                        ok = ok && warp_wait(&bar.unit_empty[un.at], un.ph ^ 1);
+                        if (!ok) break;
+                        if (lane == 0) bar_expect(&bar.unit_full[un.at], valid * 256);
+                        __syncwarp();
+                        if (half < 2 && page >= 0)
+                            tma3(units + un.at * kUnit + half * kChunk + mine * box * 128, &maps.lat, 128 * u + 64 * half, row, page, &bar.unit_full[un.at]);
+                        un.next();
+                    }
+                }
+                ok = ok && warp_wait(&bar.rope_empty[ro.at], ro.ph ^ 1);
+                if (!ok) break;
+                if (lane == 0) bar_expect(&bar.rope_full[ro.at], valid * 128);
+                __syncwarp();
+                if (half == 0 && page >= 0)
+                    tma3(ropes + ro.at * kChunk + mine * box * 128, Q8 ? &maps.rope : &maps.lat, Q8 ? 0 : p.c.latent, row, page, &bar.rope_full[ro.at]);
+                ro.next();
+            }
+        }
+        if (!ok) {  // wait (bounded) until the copies already issued have landed
+            if (nq > 0) wait_bar(&bar.qfull, (nq - 1) & 1);
+            for (int i = 0; i < S::kRopes; i++, ro.next()) {  // each place's last use (a place not used yet has no phase to wait for)
+                wait_bar(&bar.rope_full[ro.at], ro.ph ^ 1);
+                if (Q8) wait_bar(&bar.scale_full[ro.at], ro.ph ^ 1);
+            }
+            if (Q8)
+                for (int i = 0; i < S::kRaws; i++, ra.next()) wait_bar(&bar.raw_full[ra.at], ra.ph ^ 1);
+            else
+                for (int i = 0; i < S::kUnits; i++, un.next()) wait_bar(&bar.unit_full[un.at], un.ph ^ 1);
+        }
+    } else if (warp == kMmaWarp) {  // --------------------------------------- products
+        constexpr uint32_t IS = kv::kInstrM<BF, kTile, NR, false, false>, IO = kv::kInstrM<BF, 128, NR, true, false>;
+        const uint32_t one = kv::elect_one();
+        const uint32_t qd = desc_lo(qs, 16), pd = desc_lo(ps, 16), ud = desc_lo(units, 16), rd = desc_lo(ropes, 16), vd = desc_lo(units, kChunk);
+        const int rope_steps = p.c.rope >> 4;
+        uint32_t nq = 0, np = 0;
+        Turn<S::kUnits> us, uv;  // of the scores and of the outputs
+        Turn<S::kRopes> ro;
+        while (ok && take(parts, n_part, w, ok)) {
+            const int nt = __shfl_sync(~0u, part_tiles(w), 0);
+            ok = warp_wait(&bar.qfull, nq++ & 1);
+#pragma unroll 1
+            for (int j = 0; j < nt && ok; j++) {
+                uint32_t b = qd, acc = 0;
+#pragma unroll 1
+                for (int u = 0; u < L && ok; u++, us.next()) {
+                    ok = warp_wait(&bar.unit_full[us.at], us.ph);
+                    fence_after();
+                    uint32_t a = ud + us.at * (kUnit / 16);
+#pragma unroll 1
+                    for (int h = 0; h < 2; h++) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + 2 * k, b + 2 * k, acc);
+                        a += kChunk / 16, b += NR * 128 / 16;
+                    }
+                }
+                ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
+                if (!ok) break;
+                fence_after();
+#pragma unroll 1
+                for (int k = 0; k < rope_steps; k++) mma_ss<IS>(one, tm + S::kS, rd + ro.at * (kChunk / 16) + 2 * k, b + 2 * k, 1);
+                commit(one, &bar.s);
+                commit(one, &bar.rope_empty[ro.at]);
+                if (j + 1 == nt) commit(one, &bar.qempty);
+                ro.next();
+                ok = warp_wait(&bar.p, np++ & 1);
+                if (!ok) break;
+                fence_after();
+#pragma unroll 1
+                for (int u = 0; u < L; u++, uv.next()) {
+                    const uint32_t a = vd + uv.at * (kUnit / 16);
+                    acc = j > 0;
+#pragma unroll
+                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IO>(one, tm + u * NR, a + k * (2048 / 16), pd + 2 * k, acc);
+                    commit(one, &bar.unit_empty[uv.at]);
+                }
+            }
+            if (ok) commit(one, &bar.o);
+        }
+        commit(one, &bar.done);  // every product is done when this arrives
+        warp_wait(&bar.done, 0);
+    } else if (warp == kWalkWarp) {
+        ok = hand_out(p, parts, walk);
+    } else if (Q8 && warp >= 8) {  // --------------------------------------- codes to elements
+        // a thread has one group of 32 codes of each unit
+        const int slot = (tid - 256) >> 2, g = tid & 3, x7 = slot & 7;
+        Turn<S::kUnits> un;
+        Turn<S::kRopes> ro;
+        Turn<Q8 ? S::kRaws : 1> ra;
+        while (ok && take(parts, n_part, w, ok)) {
+            const int nt = part_tiles(w);
+            for (int j = 0; j < nt && ok; j++) {
+                ok = warp_wait(&bar.scale_full[ro.at], ro.ph);
+                if (!ok) break;
+                for (int u = 0; u < L; u++) {
+                    ok = ok && warp_wait(&bar.raw_full[ra.at], ra.ph) && warp_wait(&bar.unit_empty[un.at], un.ph ^ 1);
+                    if (!ok) break;
+                    uint32_t in[8], byte;
+                    const uint32_t from = raws + ra.at * S::kRaw + slot * 128;
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(in[4 * i]), "=r"(in[4 * i + 1]), "=r"(in[4 * i + 2]), "=r"(in[4 * i + 3])
+                                     : "r"(from + (((2 * g + i) ^ x7) << 4))
+                                     : "memory");
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scales + ro.at * S::kScale + slot * 16 + 4 * u + g) : "memory");
+                    const float f = power(byte);
+                    const uint32_t to = units + un.at * kUnit + (g >> 1) * kChunk + slot * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {  // pieces of eight elements; those of four lanes and two slots meet no bank twice
+                        const int e = i ^ (g & 2);
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const uint32_t c = e & 2 ? (e & 1 ? in[6 + k] : in[4 + k]) : (e & 1 ? in[2 + k] : in[k]);
+                            const float2 a = codes2(c & 0xffffu), b = codes2(c >> 16);
+                            y[2 * k] = from_f2<BF>(a.x * f, a.y * f), y[2 * k + 1] = from_f2<BF>(b.x * f, b.y * f);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((((g & 1) * 4 + e) ^ x7) << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                                     "r"(y[3])
+                                     : "memory");
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&bar.unit_full[un.at]), bar_arrive(&bar.raw_empty[ra.at]);
+                    un.next(), ra.next();
+                }
+                if (lane == 0) bar_arrive(&bar.scale_empty[ro.at]);
+                ro.next();
+            }
+        }
+    }
+    if (!ok && lane == 0) kv::flag(p.c.status, FTMOE_ERR_STATE);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
+}
+
+// Joins the parts of the item that CTA c of the kernel before started: a warp a row, a lane four latents at a time.
+constexpr int kJoinThreads = 256, kJoinRows = 8;
+
+template <bool BF>
+__global__ void __launch_bounds__(kJoinThreads) absorb_combine(const AttendParams p, int rows) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x, row = blockIdx.y * kJoinRows + warp;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 join = p.line.join[c];
+    const int t = row / p.heads, h = join.y * p.heads + row - t * p.heads;
+    if (t >= p.line.item_tokens || t >= join.x || h >= p.q_heads) return;
+    const int n = kv::count_parts(p.line.join, c, gridDim.x);
+    auto slot = [&](int k) { return (int64_t)(2 * (c + k) + (k == 0)) * rows + row; };
+    float M = -INFINITY;
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[slot(k)].x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    float sum = 0.f;
+    float4 x[4] = {};
+    for (int k = 0; k < n; k++) {
+        const float2 ml = p.part_ml[slot(k)];
+        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+        sum += ml.y * a;
+        const float4 *o = reinterpret_cast<const float4 *>(p.part_o + slot(k) * p.c.latent) + lane;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (128 * i >= p.c.latent) break;
+            const float4 v = o[32 * i];
+            x[i].x += v.x * a, x[i].y += v.y * a, x[i].z += v.z * a, x[i].w += v.w * a;
+        }
+    }
+    const float f = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t *out = p.out.d + (int64_t)(join.z + t) * p.out.token + (int64_t)h * p.out.head + 4 * lane;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        if (128 * i >= p.c.latent) break;
+        *reinterpret_cast<uint2 *>(out + 128 * i) = make_uint2(from_f2<BF>(x[i].x * f, x[i].y * f), from_f2<BF>(x[i].z * f, x[i].w * f));
+    }
+    if (lane == 0 && p.lse) p.lse[(int64_t)(join.z + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place.
+int rows_of(const AttendParams &p) {
+    const int64_t n = (int64_t)p.q_heads * p.bt.max_q;
+    return n <= 16 ? 16 : n <= 32 ? 32 : 64;
+}
+
+// Items, if no sequence has more tokens than max_q.
+int64_t most_items(const AttendParams &p) {
+    return (int64_t)((p.bt.max_q + p.line.item_tokens - 1) / p.line.item_tokens) * p.bt.batch * p.line.blocks;
+}
+bool cut(const AttendParams &p, int num_sms) {
+    const int64_t items = most_items(p), steps = ((int64_t)p.bt.max_kv + kStep - 1) / kStep;
+    return items > num_sms || steps > 2;
+}
+int ctas(const AttendParams &p, int num_sms) {
+    const int64_t items = most_items(p);
+    if (!cut(p, num_sms)) return (int)items;
+    const int64_t most = items * (p.bt.max_kv / kStep + 1 + kItemCost);
+    return (int)(most < num_sms ? (most > 0 ? most : 1) : num_sms);
+}
+
+template <bool BF, bool Q8, int NR>
+cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
+    using S = Shape<Q8, NR>;
+    const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
+    const int box = p.c.page_shift < 6 ? 1 << p.c.page_shift : 64, slots = 1 << p.c.page_shift;
+    Maps m;
+    bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, p.line.item_tokens}, true) &&
+              kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token,
+                          {64, p.heads, p.line.item_tokens}, true);
+    if (Q8)
+        ok = ok && kv::box_map(m.lat, kv::Elem::U8, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {128, box, 1}, true) &&
+             kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, false) &&
+             kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, 8), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+    else
+        ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent + p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+    if (!ok) return cudaErrorInvalidValue;
+    cudaError_t rc = kv::allow_smem<absorb_kernel<BF, Q8, NR>>(S::kSmem);
+    if (rc != cudaSuccess) return rc;
+    absorb_kernel<BF, Q8, NR><<<C, S::kThreads, S::kSmem, st>>>(p, m);
+    if ((rc = cudaGetLastError()) != cudaSuccess || !p.line.join) return rc;
+    return kv::launch_after(absorb_combine<BF>, dim3(C, NR / kJoinRows), kJoinThreads, 0, st, p, NR);
+}
+
+template <bool BF, bool Q8>
+cudaError_t launch_rows(const AttendParams &p, int C, cudaStream_t st) {
+    const int n = rows_of(p);
+    return n == 16 ? launch<BF, Q8, 16>(p, C, st) : n == 32 ? launch<BF, Q8, 32>(p, C, st) : launch<BF, Q8, 64>(p, C, st);
+}
+
+}  // namespace
+
+size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
+    const int rows = rows_of(p);
+    p.line.blocks = (p.q_heads + rows - 1) / rows, p.heads = (p.q_heads + p.line.blocks - 1) / p.line.blocks;
+    p.line.blocks = (p.q_heads + p.heads - 1) / p.heads;
+    p.line.item_tokens = rows / p.heads, p.line.batch = p.bt.batch, p.line.max_q = p.bt.max_q, p.line.causal = p.causal;
+    p.line.join = nullptr, p.part_o = nullptr, p.part_ml = nullptr;
+    if (!cut(p, num_sms)) return 0;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        unsigned char *at = base ? base + off : nullptr;
+        off += (bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    const size_t C = ctas(p, num_sms), n = 2 * C * rows;  // a part that starts an item and one that goes on with one for each CTA
+    p.part_o = reinterpret_cast<float *>(take(n * p.c.latent * 4));
+    p.part_ml = reinterpret_cast<float2 *>(take(n * 8));
+    p.line.join = reinterpret_cast<int4 *>(take(C * 16));
+    return off;
+}
+
+cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
+    const int C = ctas(p, num_sms);
+    if (p.c.bits == 8) return bf16 ? launch_rows<true, true>(p, C, st) : launch_rows<false, true>(p, C, st);
+    return bf16 ? launch_rows<true, false>(p, C, st) : launch_rows<false, false>(p, C, st);
+}
+
+}  // namespace latent
+}  // namespace ftmoe

@@ -1,4 +1,4 @@
-// Latent attention, absorbed (over the cache) and expanded (over rows), one CTA a (token, head).
+// Expanded latent attention, one CTA a (token, head).
 #include "kv_split.cuh"
 #include "latent.cuh"
 
@@ -45,36 +45,6 @@ __device__ void row_attend(const float *q, int kd, int vd, int n, float scale, u
 }
 
 template <bool BF>
-__global__ void __launch_bounds__(kThreads) attend_plain(const AttendParams p) {
-    __shared__ float s_q[576];
-    __shared__ int s_seq;
-    const int t = blockIdx.x / p.q_heads, h = blockIdx.x - t * p.q_heads, tid = threadIdx.x, latent = p.c.latent, rope = p.c.rope;
-    if (tid == 0) s_seq = -1;
-    __syncthreads();
-    for (int b = tid; b < p.bt.batch; b += kThreads) {
-        const kv::Seq s = kv::seq_info(p.bt, b, p.c.status);
-        if (t >= s.q0 && t < s.q0 + s.q_len) s_seq = b;
-    }
-    for (int e = tid; e < latent + rope; e += kThreads)
-        s_q[e] = to_f<BF>(e < latent ? p.q.d[t * p.q.token + h * p.q.head + e] : p.q_rope.d[t * p.q_rope.token + h * p.q_rope.head + e - latent]);
-    __syncthreads();
-    const int b = s_seq, at = rope_at(latent, p.c.bits);
-    if (b < 0) return;
-    const kv::Seq s = kv::seq_info(p.bt, b, nullptr);
-    const kv::Range seen = kv::visible(s, t - s.q0, t - s.q0 + 1, 0, p.causal);
-    auto key = [&](int j, int e) -> float {
-        const int page = page_of(p.c, p.bt, b, j);
-        if (page < 0) return 0.f;
-        const unsigned char *c = cell(p.c, page, j);
-        if (e >= latent) return to_f<BF>(reinterpret_cast<const uint16_t *>(c + at)[e - latent]);
-        if (p.c.bits == 16) return to_f<BF>(reinterpret_cast<const uint16_t *>(c)[e]);
-        return to_f<BF>(kv::from_f<BF>(codes2(c[e]).x * power(c[latent + e / kGroup])));
-    };
-    row_attend<BF>(s_q, latent + rope, latent, seen.hi, p.scale, p.out.d + t * p.out.token + h * p.out.head,
-                   p.lse ? p.lse + (int64_t)t * p.q_heads + h : nullptr, key, key);
-}
-
-template <bool BF>
 __global__ void __launch_bounds__(kThreads) expand_plain(const ExpandParams p) {
     __shared__ float s_q[192];
     __shared__ int s_seq;
@@ -102,13 +72,8 @@ __global__ void __launch_bounds__(kThreads) expand_plain(const ExpandParams p) {
 
 }  // namespace
 
-size_t attend_workspace(AttendParams &, int, unsigned char *) { return 0; }
 size_t expand_workspace(ExpandParams &, int, unsigned char *) { return 0; }
 
-cudaError_t launch_attend(const AttendParams &p, bool bf16, int, cudaStream_t st) {
-    (bf16 ? attend_plain<true> : attend_plain<false>)<<<(unsigned)((int64_t)p.bt.tokens * p.q_heads), kThreads, 0, st>>>(p);
-    return cudaGetLastError();
-}
 cudaError_t launch_expand(const ExpandParams &p, bool bf16, int, cudaStream_t st) {
     (bf16 ? expand_plain<true> : expand_plain<false>)<<<(unsigned)((int64_t)p.tokens * p.heads), kThreads, 0, st>>>(p);
     return cudaGetLastError();

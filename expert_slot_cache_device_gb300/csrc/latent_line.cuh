@@ -1,0 +1,216 @@
+// How the latent-attention kernels cut their work: as in kv_split.cuh, an item being a tile of tokens of one sequence and
+// one block of heads. Items stand in one line, sequence by sequence, block by block, tile by tile, each as long as its
+// visible slots have steps of 128 (and kItemCost for its start and end); CTA c of C takes an even piece of it. A warp of
+// each CTA walks its piece and hands the parts out through a small ring.
+#pragma once
+
+#include "kv_tc05.cuh"
+#include "latent.cuh"
+
+namespace ftmoe {
+namespace latent {
+
+using kv::bar_arrive;
+using kv::su32;
+using kv::warp_wait;
+
+constexpr int kStep = 128;    // slots of a step
+constexpr int kItemCost = 2;  // what an item's start and end take, in steps
+constexpr int kParts = 4;     // entries of the ring of parts
+
+__device__ __forceinline__ int item_count(const Line &l, const kv::Seq &s) {
+    return (int)((uint32_t)(s.q_len + l.item_tokens - 1) / (uint32_t)l.item_tokens);
+}
+// Slots [0, item_hi) are what at least one row of the item sees.
+__device__ __forceinline__ int item_hi(const Line &l, const kv::Seq &s, int qt) {
+    const int i0 = qt * l.item_tokens, i1 = l.item_tokens < s.q_len - i0 ? i0 + l.item_tokens : s.q_len;
+    const kv::Range r = kv::visible(s, i0, i1, 0, l.causal);
+    return r.hi;
+}
+__device__ __forceinline__ int item_steps(int hi) { return hi > 0 ? (hi + kStep - 1) / kStep : 1; }
+
+// Units of one (sequence, block) in its first `end` items; the whole warp calls. Counted in 64 bits; the warp's 32-bit sums
+// take the low 16 bits and the rest apart, which lanes below 2^43 fit.
+__device__ __forceinline__ long long seq_units(const Line &l, const kv::Seq &s, int end) {
+    long long n = 0;
+    for (int qt = threadIdx.x & 31; qt < end; qt += 32) n += item_steps(item_hi(l, s, qt)) + kItemCost;
+    return ((long long)__reduce_add_sync(~0u, (uint32_t)(n >> 16)) << 16) + __reduce_add_sync(~0u, (uint32_t)n & 0xffffu);
+}
+
+// A part of an item, as the roles take it from the ring.
+struct Part {
+    int b, block;
+    int token, left;         // first token row of the item; new tokens from there to the sequence's end
+    int slot, kv_len;        // the first token's slot
+    int hi;                  // item_hi
+    int first, last, steps;  // steps [first, last) of the item's; steps = 0: no more parts
+};
+
+// The walk along the line. P: `line`, and seq(b, status).
+template <class P>
+struct Walk {
+    long long left;
+    int b, block, qt, n_qt, at;  // at: units into the item (its kItemCost first)
+    kv::Seq sq;
+    __device__ __forceinline__ bool next(const P &p, Part &w) {
+        while (left > 0) {
+            const int hi = item_hi(p.line, sq, qt), steps = item_steps(hi);
+            const int n = steps + kItemCost, end = left < n - at && p.line.join ? at + (int)left : n;
+            w.b = b, w.block = block;
+            w.token = sq.q0 + qt * p.line.item_tokens, w.left = sq.q_len - qt * p.line.item_tokens;
+            w.slot = sq.kv_len - sq.q_len + qt * p.line.item_tokens, w.kv_len = sq.kv_len, w.hi = hi, w.steps = steps;
+            w.first = at > kItemCost ? at - kItemCost : 0, w.last = end - kItemCost;
+            left = p.line.join ? left - (end - at) : 0;
+            at = 0;
+            if (left > 0 && ++qt == n_qt) {
+                qt = 0;
+                if (++block == p.line.blocks) {
+                    block = 0;
+                    do {
+                        sq = p.seq(++b, nullptr);
+                        n_qt = item_count(p.line, sq);
+                    } while (n_qt == 0);
+                }
+            }
+            if (w.last > w.first) return true;
+        }
+        w.steps = 0;
+        return false;
+    }
+};
+
+// Total units and this CTA's start, for kWarps warps. s_sum: 32 kWarps entries, s_warp: kWarps.
+template <int kWarps, class P>
+__device__ __forceinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, long long *s_sum, Walk<P> *s_walk, int32_t *status) {
+    constexpr int T = kWarps * 32;
+    const Line &l = p.line;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (!l.join) {  // a CTA an item that there can be, and no line to walk
+        const int most = (l.max_q + l.item_tokens - 1) / l.item_tokens, block = blockIdx.x / most;
+        w.qt = blockIdx.x - block * most, w.b = block / l.blocks, w.block = block - w.b * l.blocks;
+        w.sq = p.seq(w.b, w.qt == 0 && w.block == 0 && tid == 0 ? status : nullptr);
+        w.n_qt = item_count(l, w.sq), w.at = 0, w.left = 1;
+        return w.qt < w.n_qt;
+    }
+    auto sums = [&](int b0, int32_t *st) {
+        for (int i = warp; i < T && b0 + i < l.batch; i += kWarps) {
+            const kv::Seq s = p.seq(b0 + i, lane == 0 ? st : nullptr);
+            const long long n = seq_units(l, s, item_count(l, s));
+            if (lane == 0) s_sum[i] = n;
+        }
+        __syncthreads();
+    };
+    long long sum = 0, total;
+    for (int b0 = 0; b0 < l.batch; b0 += T) {
+        sums(b0, blockIdx.x == 0 ? status : nullptr);
+        if (b0 + tid < l.batch) sum += s_sum[tid];
+        if (b0 + T < l.batch) __syncthreads();
+    }
+    kv::block_scan<T>(sum, total, s_warp);
+    const long long W = total * l.blocks;
+    const int C = kv::used_ctas(gridDim.x, W);
+    if (blockIdx.x >= C) return false;
+    const long long u0 = kv::unit_start(blockIdx.x, C, W), u1 = kv::unit_start(blockIdx.x + 1, C, W);
+    long long base = 0;
+    for (int b0 = 0; b0 < l.batch; b0 += T) {
+        if (l.batch > T) {  // the sums of the last round are not these
+            __syncthreads();
+            sums(b0, nullptr);
+        }
+        const long long n = b0 + tid < l.batch ? s_sum[tid] * l.blocks : 0;
+        const long long at = base + kv::block_scan<T>(n, total, s_warp);
+        if (u0 >= at && u0 < at + n) {
+            s_walk->b = b0 + tid;
+            s_walk->left = u0 - at;  // for now: the start within the sequence
+        }
+        base += total;
+        if (base > u0) break;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int b = s_walk->b;
+        const kv::Seq s = p.seq(b, nullptr);
+        const int n_qt = item_count(l, s);
+        const long long per = seq_units(l, s, n_qt), from = s_walk->left;
+        // (a 64-bit division takes longer than the rest)
+        const int block = (from | per) >> 32 ? (int)(from / per) : (int)((uint32_t)from / (uint32_t)per);
+        const long long rem = from - block * per;
+        long long before = 0;
+        int qt = -1, at = 0;
+        for (int q0 = 0; q0 < n_qt && qt < 0; q0 += 32) {
+            const int n = q0 + lane < n_qt ? item_steps(item_hi(l, s, q0 + lane)) + kItemCost : 0;  // 32 of them: below 2^30
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(~0u, x, o);
+                if (lane >= o) x += y;
+            }
+            const long long r = rem - before;
+            const unsigned hit = __ballot_sync(~0u, n > 0 && r >= x - n && r < x);
+            if (hit) {
+                const int k = __ffs(hit) - 1;
+                qt = q0 + k;
+                at = (int)(r - __shfl_sync(~0u, x - n, k));
+            }
+            before += __shfl_sync(~0u, x, 31);
+        }
+        __syncwarp();
+        if (lane == 0) {
+            s_walk->block = block, s_walk->qt = qt, s_walk->n_qt = n_qt, s_walk->at = at, s_walk->sq = s;
+            s_walk->left = u1 - u0;
+        }
+    }
+    __syncthreads();
+    w = *s_walk;
+    return true;
+}
+
+struct PartRing {
+    Part part[kParts];
+    uint64_t full[kParts], empty[kParts];
+};
+
+// Takes the next part; the whole warp calls. False at the end (or when the wait ran out: ok).
+__device__ __forceinline__ bool take(PartRing &ring, uint32_t &n, Part &w, bool &ok) {
+    const uint32_t e = n % kParts;
+    ok = warp_wait(&ring.full[e], (n / kParts) & 1);
+    if (!ok) return false;
+    w = ring.part[e];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(&ring.empty[e]);
+    n++;
+    return w.steps > 0;
+}
+
+// Hands out all parts of the walk and leaves what the joining kernel needs; the whole warp calls. False when a wait ran out.
+template <class P>
+__device__ __forceinline__ bool hand_out(const P &p, PartRing &ring, Walk<P> &walk) {
+    const int lane = threadIdx.x & 31;
+    int4 join = make_int4(0, 0, 0, kv::kJoinNone);
+    bool ok = true, more = true;
+    for (uint32_t n = 0; more; n++) {
+        if (n >= kParts && !warp_wait(&ring.empty[n % kParts], (n / kParts - 1) & 1)) {
+            ok = false;
+            break;
+        }
+        Part w;
+        more = walk.next(p, w);
+        if (more && (w.first > 0 || w.last < w.steps)) {
+            if (w.first == 0)
+                join.x = w.left, join.y = w.block, join.z = w.token;
+            else
+                join.w = w.last == w.steps ? kv::kJoinEnd : kv::kJoinOn;
+        }
+        __syncwarp();
+        if (lane == 0) {
+            ring.part[n % kParts] = w;
+            bar_arrive(&ring.full[n % kParts]);
+        }
+        __syncwarp();
+    }
+    if (lane == 0 && p.line.join) p.line.join[blockIdx.x] = join;
+    return ok;
+}
+
+}  // namespace latent
+}  // namespace ftmoe
