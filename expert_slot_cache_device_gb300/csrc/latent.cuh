@@ -106,26 +106,25 @@ struct ExpandParams {
     int32_t heads, nope, rope, vdim, causal;
     float scale;
     float *lse;
+    Line line;
+    // workspace (expand_workspace): parts of split items
+    float *part_o;
+    float2 *part_ml;
+    // First key row of sequence b, and the sequence, each value cut to its range (a cut is recorded).
+    __device__ __forceinline__ int first_row(int b) const {
+        const int a = cu_kv[b];
+        return a < 0 ? 0 : (a > rows ? rows : a);
+    }
+    __device__ __forceinline__ kv::Seq seq(int b, int32_t *st) const {
+        Batch bt{};
+        bt.tokens = tokens, bt.max_q = max_q, bt.max_kv = max_kv;
+        const int row0 = first_row(b), e = cu_kv[b + 1], end = e < row0 ? row0 : (e > rows ? rows : e);
+        if (cu_kv[b] != row0 || end != e) kv::flag(st, FTMOE_ERR_STATE);
+        return kv::seq_cut(bt, cu_q[b], cu_q[b + 1], end - row0, st);
+    }
 };
 size_t expand_workspace(ExpandParams &p, int num_sms, unsigned char *base);
 cudaError_t launch_expand(const ExpandParams &p, bool bf16, int num_sms, cudaStream_t st);
-
-// Sequence b of an expanded call, each value cut to its range (a cut is recorded). `row0` is its first key row.
-struct RowSeq {
-    kv::Seq s;
-    int row0;
-};
-__device__ __forceinline__ RowSeq row_seq(const ExpandParams &p, int b, int32_t *status) {
-    Batch bt{};
-    bt.tokens = p.tokens, bt.max_q = p.max_q, bt.max_kv = p.max_kv;
-    const int a = p.cu_kv[b], e = p.cu_kv[b + 1];
-    RowSeq r;
-    r.row0 = a < 0 ? 0 : (a > p.rows ? p.rows : a);
-    const int end = e < r.row0 ? r.row0 : (e > p.rows ? p.rows : e);
-    if (r.row0 != a || end != e) kv::flag(status, FTMOE_ERR_STATE);
-    r.s = kv::seq_cut(bt, p.cu_q[b], p.cu_q[b + 1], end - r.row0, status);
-    return r;
-}
 
 }  // namespace latent
 }  // namespace ftmoe

@@ -66,16 +66,6 @@ struct Bars {
     uint64_t qfull, qempty, s, p, o, done;
 };
 
-// A place in a ring of N and the phase of its barriers.
-template <int N>
-struct Turn {
-    int at = 0;
-    uint32_t ph = 0;
-    __device__ __forceinline__ void next() {
-        if (++at == N) at = 0, ph ^= 1;
-    }
-};
-
 // Slots of tensor memory as fragments: a thread's registers 4 j .. 4 j + 3 are rows 8 j + 2 (lane % 4), + 1 of slot
 // lane / 4, then of slot lane / 4 + 8.
 template <int NR>

@@ -165,6 +165,16 @@ __device__ __forceinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, 
     return true;
 }
 
+// A place in a ring of N and the phase of its barriers.
+template <int N>
+struct Turn {
+    int at = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) at = 0, ph ^= 1;
+    }
+};
+
 struct PartRing {
     Part part[kParts];
     uint64_t full[kParts], empty[kParts];
