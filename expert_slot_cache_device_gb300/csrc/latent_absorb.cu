@@ -23,6 +23,7 @@ namespace ftmoe {
 namespace latent {
 namespace {
 
+using kv::add2;
 using kv::bar_expect;
 using kv::bar_init;
 using kv::commit;
@@ -31,28 +32,32 @@ using kv::ex2;
 using kv::fence_after;
 using kv::fence_async;
 using kv::fence_before;
+using kv::fma2;
 using kv::from_f2;
 using kv::mma_ss;
+using kv::pack2;
 using kv::tma3;
+using kv::unpack2;
 using kv::wait_bar;
 
 constexpr int kTile = 64;
 constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kConvWarps = 8;
-constexpr float kSlack = 8.f;
+constexpr float kMost = 256.f;   // P that is let through without raising m
+constexpr float kNone = 3e38f;  // in place of -m before the first score
 constexpr int kChunk = kTile * 128;  // 64 elements of a tile's slots
 constexpr int kUnit = 2 * kChunk;    // 128 latents of a tile's slots
 
 template <bool Q8, int NR>
 struct Shape {
     static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
-    static constexpr int kUnits = Q8 ? (NR == 64 ? 5 : NR == 32 ? 6 : 7) : (NR == 64 ? 8 : NR == 32 ? 10 : 11);
-    static constexpr int kRopes = NR == 64 ? 2 : 3;
-    static constexpr int kRaws = Q8 ? (NR == 64 ? 5 : 7) : 0;  // 128 codes of a tile's slots each
+    static constexpr int kUnits = Q8 ? (NR == 64 ? 5 : 8) : (NR == 64 ? 8 : NR == 32 ? 10 : 11);
+    static constexpr int kRopes = Q8 ? 2 : (NR == 64 ? 1 : NR == 32 ? 2 : 3);
+    static constexpr int kRaws = Q8 ? (NR == 16 ? 6 : 4) : 0;  // 128 codes of a tile's slots each
     static constexpr int kRaw = kChunk, kScale = kTile * 16;
     static constexpr int kQ = 9 * NR * 128;
-    static constexpr int kP = NR * 128 > 4096 ? NR * 128 : 4096;  // also scratch between tiles
+    static constexpr int kP = 2 * NR * 128;  // two tiles' (each scratch before its P is formed; the plan's sums before)
     static constexpr int kSmem = 1024 + kQ + kP + kUnits * kUnit + kRopes * kChunk + kRaws * kRaw + (Q8 ? kRopes * kScale : 0);
-    static constexpr uint32_t kS = 256;  // column of S; O is at 0
+    static constexpr uint32_t kS = 256;  // columns of two tiles' S; O is at 0
 };
 constexpr int kMaxUnits = 11, kMaxRopes = 3, kMaxRaws = 7;
 
@@ -63,7 +68,7 @@ struct Maps {
 struct Bars {
     uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits], rope_full[kMaxRopes], rope_empty[kMaxRopes];
     uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws], scale_full[kMaxRopes], scale_empty[kMaxRopes];
-    uint64_t qfull, qempty, s, p, o, done;
+    uint64_t qfull, qempty, s[2], p[2], pv, o, done;
 };
 
 // Slots of tensor memory as fragments: a thread's registers 4 j .. 4 j + 3 are rows 8 j + 2 (lane % 4), + 1 of slot
@@ -137,7 +142,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     __shared__ long long s_warp[S::kWarps];
     __shared__ Walk<AttendParams> s_walk;
     __shared__ uint16_t s_tok[NR];  // token of a row in its item
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // (uniform, for the products' descriptors)
     const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + S::kUnits * kUnit, raws = ropes + S::kRopes * kChunk;
     const uint32_t qs = raws + S::kRaws * S::kRaw, ps = qs + S::kQ, scales = ps + S::kP;
     const int L = p.c.latent >> 7;  // units of a tile
@@ -150,7 +155,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         }
         for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvWarps);
         for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], 6 + (Q8 ? kConvWarps : 0));
-        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.s, 1), bar_init(&bar.p, 4), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
+        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.pv, 1), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
+        for (int i = 0; i < 2; i++) bar_init(&bar.s[i], 1), bar_init(&bar.p[i], 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kMmaWarp) {
@@ -187,7 +193,6 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         const int row0 = 16 * warp + (lane >> 2), col0 = 2 * (lane & 3);
         constexpr int NB = NR / 8;
         uint32_t ns = 0, no = 0;
-        Turn<S::kUnits> un;
         while (!vote(!take(parts, n_part, w, ok))) {
             const int nt = part_tiles(w);
             const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
@@ -196,16 +201,20 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 return t >= w.left || at < 0 ? 0 : (p.line.causal ? at + 1 : w.kv_len);
             };
             const int least = dead || w.slot < 0 ? 0 : (p.line.causal ? w.slot + 1 : w.kv_len);
-            float m[2 * NB], l[2 * NB];
+            // rows c and c + 1 of eight i: z = -m (kNone before the first score, which makes P of any score infinite), sums of P
+            float z[2 * NB];
+            uint64_t l[NB];
 #pragma unroll
-            for (int i = 0; i < 2 * NB; i++) m[i] = -INFINITY, l[i] = 0.f;
+            for (int i = 0; i < NB; i++) z[2 * i] = z[2 * i + 1] = kNone, l[i] = 0;
             for (int j = 0; j < nt; j++, ns++) {
                 const int s0 = w.first * kStep + j * kTile;
-                ok = ok && warp_wait(&bar.s, ns & 1);
+                const uint32_t tS = lanes + S::kS + NR * (ns & 1), pt = ps + NR * 128 * (ns & 1);
+                ok = ok && warp_wait(&bar.s[ns & 1], (ns >> 1) & 1);
                 fence_after();
                 uint32_t x[NR / 2];
-                load_s<NR>(lanes + S::kS, x);
-                if (s0 + kTile > least) {
+                auto scores = [&] {
+                    load_s<NR>(tS, x);
+                    if (s0 + kTile <= least) return;
                     const int a = s0 + row0;
 #pragma unroll
                     for (int i = 0; i < NB; i++)
@@ -215,70 +224,89 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                             if (a >= lim) x[4 * i + e] = 0xff800000u;
                             if (a + 8 >= lim) x[4 * i + 2 + e] = 0xff800000u;
                         }
-                }
-                bool over = !ok;
+                };
+                // P in place of the scores; whether one is above 2^8
+                auto form = [&] {
+                    float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < NB; i++)
+                    for (int i = 0; i < NB; i++)
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float t = fmaxf(__uint_as_float(x[4 * i + e]), __uint_as_float(x[4 * i + 2 + e])) * c2;
-                        over = over || t > m[2 * i + e] + kSlack;
-                    }
-                if (vote(over)) {
+                        for (int k = 4 * i; k < 4 * i + 4; k += 2) {
+                            const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
+                            const float a = ex2(f.x), b = ex2(f.y);
+                            top = kv::max3(top, a, b);
+                            x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
+                        }
+                    return top > kMost;
+                };
+                scores();
+                if (vote(form() || !ok)) {
                     if (vote(!ok)) break;
-                    // m to at least each row's maximum over the tile (P's place is free: the product that read it is done)
+                    scores();
+                    // m to at least each row's maximum over the tile
 #pragma unroll
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2])) * c2;
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
-                        if (lane < 4) st_f(ps + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
+                        if (lane < 4) st_f(pt + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
                     }
                     vote(false);
 #pragma unroll
-                    for (int i = 0; i < 2 * NB; i++) {
-                        const uint32_t a = ps + (8 * (i >> 1) + col0 + (i & 1)) * 4;
-                        const float t = fmaxf(fmaxf(ld_f(a), ld_f(a + NR * 4)), fmaxf(ld_f(a + 2 * NR * 4), ld_f(a + 3 * NR * 4)));
-                        const float n = fmaxf(m[i], t), f = m[i] == -INFINITY ? 0.f : ex2(m[i] - n);
-                        m[i] = n, l[i] *= f;
-                        if (warp == 0 && lane < 4) st_f(a + 4 * NR * 4, f);
+                    for (int i = 0; i < NB; i++) {
+                        float f[2];
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const uint32_t a = pt + (8 * i + col0 + e) * 4;
+                            const float t = fmaxf(fmaxf(ld_f(a), ld_f(a + NR * 4)), fmaxf(ld_f(a + 2 * NR * 4), ld_f(a + 3 * NR * 4)));
+                            float &zz = z[2 * i + e];
+                            const float m = zz == kNone ? -INFINITY : -zz, n = fmaxf(m, t);
+                            f[e] = m == -INFINITY ? 0.f : ex2(m - n);
+                            zz = n == -INFINITY ? kNone : -n;
+                            if (warp == 0 && lane < 4) st_f(a + 4 * NR * 4, f[e]);
+                        }
+                        const float2 y = unpack2(l[i]);
+                        l[i] = pack2(y.x * f[0], y.y * f[1]);
                     }
-                    vote(false);
+                    if (j > 0) ok = warp_wait(&bar.pv, (ns - 1) & 1);  // O holds all P so far
+                    if (vote(!ok)) break;
+                    fence_after();
                     if (j > 0) {
 #pragma unroll 1
                         for (int k = 0; k < L * NR; k += 16) {
                             uint32_t y[16];
                             tm_ld16(lanes + k, y);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(ps + (4 * NR + (k + e) % NR) * 4));
+                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(pt + (4 * NR + (k + e) % NR) * 4));
                             kv::tm_st16(lanes + k, y);
                         }
                         kv::tm_st_wait();
                     }
                     vote(false);  // the scratch has been read
+                    form();
                 }
 #pragma unroll
                 for (int i = 0; i < NB; i += 2) {
                     uint32_t y[4];
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {  // rows 8 i, then 8 (i + 1); slots, then slots + 8
-                        const int r = 4 * (i + (k >> 1)) + 2 * (k & 1), c = 2 * (i + (k >> 1));
-                        const float z0 = m[c] == -INFINITY ? 0.f : -m[c], z1 = m[c + 1] == -INFINITY ? 0.f : -m[c + 1];
-                        const float a = ex2(fmaf(__uint_as_float(x[r]), c2, z0)), b = ex2(fmaf(__uint_as_float(x[r + 1]), c2, z1));
-                        l[c] += a, l[c + 1] += b;
-                        y[k] = from_f2<BF>(a, b);
+                    for (int k = 0; k < 2; k++) {  // rows 8 i, then 8 (i + 1); slots, then slots + 8
+                        const uint32_t *v = x + 4 * (i + k);
+                        const float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]), c = __uint_as_float(v[2]), d = __uint_as_float(v[3]);
+                        l[i + k] = add2(l[i + k], add2(pack2(a, b), pack2(c, d)));
+                        y[2 * k] = from_f2<BF>(a, b), y[2 * k + 1] = from_f2<BF>(c, d);
                     }
                     // transposed: a row's slots consecutive, 16-byte piece c of row r at c ^ (r % 8)
                     const int r = lane & 7, k = lane >> 3;
-                    const uint32_t at = ps + (8 * (i + (k >> 1)) + r) * 128 + (((2 * warp + (k & 1)) ^ r) << 4);
+                    const uint32_t at = pt + (8 * (i + (k >> 1)) + r) * 128 + (((2 * warp + (k & 1)) ^ r) << 4);
                     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
                                  "r"(y[3])
                                  : "memory");
                 }
                 if (s0 + kTile > w.hi) {  // latents of slots that no row sees: what they hold must not reach 0 * C
                     const int r0 = w.hi > s0 ? w.hi - s0 : 0;
-                    Turn<S::kUnits> t = un;
+                    Turn<S::kUnits> t;
+                    t.at = (int)(ns * L % S::kUnits), t.ph = ns * L / S::kUnits & 1;
                     for (int u = 0; u < L; u++, t.next()) {
                         ok = ok && warp_wait(&bar.unit_full[t.at], t.ph);
                         for (int i = tid; i < (kTile - r0) * 16; i += 128)
@@ -287,11 +315,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                                          : "memory");
                     }
                 }
-                for (int u = 0; u < L; u++) un.next();
                 fence_async();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bar.p);
+                if (lane == 0) bar_arrive(&bar.p[ns & 1]);
             }
             ok = ok && warp_wait(&bar.o, no++ & 1);
             if (vote(!ok)) break;
@@ -299,13 +326,17 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             const bool whole = w.first == 0 && w.last == w.steps;
             const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
 #pragma unroll
-            for (int i = 0; i < 2 * NB; i++) {
-                float t = l[i];
+            for (int i = 0; i < NB; i++) {
+                const float2 y = unpack2(l[i]);
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
-                const int c = 8 * (i >> 1) + col0 + (i & 1);
-                if (lane < 4) st_f(ps + (warp * NR + c) * 4, t);
-                if (warp == 0 && lane < 4) st_f(ps + (5 * NR + c) * 4, m[i]);
+                for (int e = 0; e < 2; e++) {
+                    float t = e ? y.y : y.x;
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
+                    const int c = 8 * i + col0 + e;
+                    if (lane < 4) st_f(ps + (warp * NR + c) * 4, t);
+                    if (warp == 0 && lane < 4) st_f(ps + (5 * NR + c) * 4, z[2 * i + e] == kNone ? -INFINITY : -z[2 * i + e]);
+                }
             }
             vote(false);
             if (tid < NR) {
@@ -320,26 +351,43 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             }
             vote(false);
             // a warp has 32 latents of each unit, a lane one, columns are rows of the item
-            uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)w.block * p.heads * p.out.head;
-            float *po = p.part_o + (int64_t)part * NR * p.c.latent;
+            if (whole) {  // two lanes swap, so that each writes two latents of one row
+                uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)w.block * p.heads * p.out.head + 32 * warp + (lane & ~1);
+                const int rows = p.line.item_tokens < w.left ? used : w.left * p.heads, heads = p.q_heads - w.block * p.heads;
 #pragma unroll 1
-            for (int k = 0; k < L * NR; k += 16) {
-                uint32_t y[16];
-                tm_ld16(lanes + k, y);
-                const int at = (k / NR) * 128 + 32 * warp;
+                for (int k = 0; k < NR; k += 16) {
+                    float f[16];
+                    uint16_t *row[8];
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const int c = k % NR + e;
-                    if (whole) {  // two lanes swap, so that each writes two latents of one row
-                        const float a = __uint_as_float(y[e]) * ld_f(ps + (4 * NR + c) * 4), b = __uint_as_float(y[e + 1]) * ld_f(ps + (4 * NR + c + 1) * 4);
-                        const float got = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
-                        const int r = c + (lane & 1), t = s_tok[r], h = r - t * p.heads;
-                        if (r < used && t < w.left && w.block * p.heads + h < p.q_heads)
-                            *reinterpret_cast<uint32_t *>(out + t * p.out.token + h * p.out.head + at + (lane & ~1)) =
-                                lane & 1 ? from_f2<BF>(got, b) : from_f2<BF>(a, got);
-                    } else {
-                        po[(int64_t)c * p.c.latent + at + lane] = __uint_as_float(y[e]);
-                        po[(int64_t)(c + 1) * p.c.latent + at + lane] = __uint_as_float(y[e + 1]);
+                    for (int e = 0; e < 16; e++) f[e] = ld_f(ps + (4 * NR + k + e) * 4);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const int r = k + 2 * e + (lane & 1), t = s_tok[r], h = r - t * p.heads;
+                        row[e] = r < rows && h < heads ? out + t * p.out.token + h * p.out.head : nullptr;
+                    }
+#pragma unroll 1
+                    for (int u = 0; u < L; u++) {
+                        uint32_t y[16];
+                        tm_ld16(lanes + u * NR + k, y);
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const float a = __uint_as_float(y[e]) * f[e], b = __uint_as_float(y[e + 1]) * f[e + 1];
+                            const float got = __shfl_xor_sync(~0u, lane & 1 ? a : b, 1);
+                            if (row[e >> 1]) *reinterpret_cast<uint32_t *>(row[e >> 1] + 128 * u) = lane & 1 ? from_f2<BF>(got, b) : from_f2<BF>(a, got);
+                        }
+                    }
+                }
+            } else {
+                float *po = p.part_o + (int64_t)part * NR * p.c.latent + 32 * warp + lane;
+#pragma unroll 1
+                for (int u = 0; u < L; u++) {
+                    float *to = po + 128 * u;
+#pragma unroll 1
+                    for (int k = 0; k < NR; k += 16) {
+                        uint32_t y[16];
+                        tm_ld16(lanes + u * NR + k, y);
+#pragma unroll
+                        for (int e = 0; e < 16; e++, to += p.c.latent) *to = __uint_as_float(y[e]);
                     }
                 }
             }
@@ -428,47 +476,69 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         const uint32_t one = kv::elect_one();
         const uint32_t qd = desc_lo(qs, 16), pd = desc_lo(ps, 16), ud = desc_lo(units, 16), rd = desc_lo(ropes, 16), vd = desc_lo(units, kChunk);
         const int rope_steps = p.c.rope >> 4;
-        uint32_t nq = 0, np = 0;
-        Turn<S::kUnits> us, uv;  // of the scores and of the outputs
+        uint32_t nq = 0, n = 0, np = 0;  // items, tiles whose S and whose O product is issued
+        Turn<S::kUnits> us, uv;
         Turn<S::kRopes> ro;
+        auto scores = [&](bool rope_first) {
+            const uint32_t d = tm + S::kS + NR * (n & 1);
+            uint32_t acc = 0;
+            auto rope = [&] {
+                ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
+                if (!ok) return;
+                fence_after();
+                const uint32_t a = __shfl_sync(~0u, rd + ro.at * (kChunk / 16), 0), b = qd + L * (2 * NR * 128 / 16);
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    if (k < rope_steps) mma_ss<IS>(one, d, a + 2 * k, b + 2 * k, acc), acc = 1;
+                commit(one, &bar.rope_empty[ro.at]);
+                ro.next();
+            };
+            if (rope_first) rope();
+#pragma unroll 1
+            for (int u = 0; u < L && ok; u++, us.next()) {
+                ok = warp_wait(&bar.unit_full[us.at], us.ph);
+                fence_after();
+                const uint32_t a = __shfl_sync(~0u, ud + us.at * (kUnit / 16), 0), b = __shfl_sync(~0u, qd + u * (2 * NR * 128 / 16), 0);
+#pragma unroll
+                for (int k = 0; k < 8; k++, acc = 1)
+                    mma_ss<IS>(one, d, a + (k >> 2) * (kChunk / 16) + 2 * (k & 3), b + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
+            }
+            if (!rope_first && ok) rope();
+            if (ok) commit(one, &bar.s[n & 1]);
+            n++;
+        };
+        auto values = [&](uint32_t acc0) {
+            ok = ok && warp_wait(&bar.p[np & 1], (np >> 1) & 1);
+            if (!ok) return;
+            fence_after();
+            const uint32_t b = __shfl_sync(~0u, pd + (np & 1) * (NR * 128 / 16), 0);
+#pragma unroll 1
+            for (int u = 0; u < L; u++, uv.next()) {
+                const uint32_t a = __shfl_sync(~0u, vd + uv.at * (kUnit / 16), 0), d = __shfl_sync(~0u, tm + u * NR, 0);
+                uint32_t acc = acc0;
+#pragma unroll
+                for (int k = 0; k < 4; k++, acc = 1) mma_ss<IO>(one, d, a + k * (2048 / 16), b + 2 * k, acc);
+                commit(one, &bar.unit_empty[uv.at]);
+            }
+            commit(one, &bar.pv);
+            np++;
+        };
         while (ok && take(parts, n_part, w, ok)) {
             const int nt = __shfl_sync(~0u, part_tiles(w), 0);
             ok = warp_wait(&bar.qfull, nq++ & 1);
 #pragma unroll 1
-            for (int j = 0; j < nt && ok; j++) {
-                uint32_t b = qd, acc = 0;
-#pragma unroll 1
-                for (int u = 0; u < L && ok; u++, us.next()) {
-                    ok = warp_wait(&bar.unit_full[us.at], us.ph);
-                    fence_after();
-                    uint32_t a = ud + us.at * (kUnit / 16);
-#pragma unroll 1
-                    for (int h = 0; h < 2; h++) {
-#pragma unroll
-                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + 2 * k, b + 2 * k, acc);
-                        a += kChunk / 16, b += NR * 128 / 16;
-                    }
-                }
-                ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
-                if (!ok) break;
-                fence_after();
-#pragma unroll 1
-                for (int k = 0; k < rope_steps; k++) mma_ss<IS>(one, tm + S::kS, rd + ro.at * (kChunk / 16) + 2 * k, b + 2 * k, 1);
-                commit(one, &bar.s);
-                commit(one, &bar.rope_empty[ro.at]);
-                if (j + 1 == nt) commit(one, &bar.qempty);
-                ro.next();
-                ok = warp_wait(&bar.p, np++ & 1);
-                if (!ok) break;
-                fence_after();
-#pragma unroll 1
-                for (int u = 0; u < L; u++, uv.next()) {
-                    const uint32_t a = vd + uv.at * (kUnit / 16);
-                    acc = j > 0;
-#pragma unroll
-                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IO>(one, tm + u * NR, a + k * (2048 / 16), pd + 2 * k, acc);
-                    commit(one, &bar.unit_empty[uv.at]);
-                }
+            for (int j = 0; j < nt && ok;) {
+                // Two tiles' scores, then their outputs, where the second tile is there by then: its scores are formed during the first
+                // one's softmax. The second one's rotary part comes last, into the place that the first one's left.
+                scores(true);
+                Turn<S::kUnits> last = us;
+                for (int u = 1; u < L; u++) last.next();
+                const bool two = ok && j + 1 < nt && L * 2 <= S::kUnits && __all_sync(~0u, kv::test_bar(su32(&bar.unit_full[last.at]), last.ph));
+                if (two) scores(false);
+                if (j + 1 + two == nt) commit(one, &bar.qempty);
+                values(j > 0);
+                if (two) values(1);
+                j += 1 + two;
             }
             if (ok) commit(one, &bar.o);
         }

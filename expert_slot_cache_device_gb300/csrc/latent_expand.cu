@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const ExpandParams 
     __shared__ uint32_t s_tmem;
     __shared__ long long s_warp[kWarps];
     __shared__ Walk<ExpandParams> s_walk;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // (uniform, for the products' descriptors)
     const uint32_t ks = (su32(sm_raw) + 1023u) & ~1023u, vs = ks + S::kKRing * kChunk, qs = vs + S::kVRing * S::kV * kChunk, stage_out = qs + S::kQ;
 
     if (tid == 0) {

@@ -189,7 +189,7 @@ __device__ __forceinline__ bool take(PartRing &ring, uint32_t &n, Part &w, bool 
     __syncwarp();
     if ((threadIdx.x & 31) == 0) bar_arrive(&ring.empty[e]);
     n++;
-    return w.steps > 0;
+    return __shfl_sync(~0u, w.steps, 0) > 0;
 }
 
 // Hands out all parts of the walk and leaves what the joining kernel needs; the whole warp calls. False when a wait ran out.
