@@ -48,6 +48,20 @@ __device__ __forceinline__ float2 codes2(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
+// 16 codes of one group as elements.
+template <bool BF>
+__device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
+    const float s = power(byte);
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const float2 a = codes2(in[i] & 0xffffu), b = codes2(in[i] >> 16);
+        out[2 * i] = kv::from_f2<BF>(a.x * s, a.y * s), out[2 * i + 1] = kv::from_f2<BF>(b.x * s, b.y * s);
+    }
+    lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
 // ---------------------------------------------------------------- launches
 struct AppendParams {
     View c;
@@ -75,6 +89,7 @@ cudaError_t launch_read(const ReadParams &p, bool bf16, cudaStream_t st);
 // How a call's work is cut (latent_line.cuh): an item is item_tokens tokens of one sequence and one of `blocks` blocks of heads.
 struct Line {
     int32_t batch, blocks, item_tokens, max_q, causal;
+    int32_t pair;  // 1: CTAs 2 i and 2 i + 1 have the same place in the line and a block each of a pair of blocks (`blocks` counts pairs)
     int4 *join;  // [CTAs] (kv_split.cuh), or NULL: a CTA an item, whole
 };
 

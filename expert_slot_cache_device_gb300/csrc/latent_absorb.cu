@@ -12,10 +12,12 @@
 //               with the maximum m of the tiles before; one vote of the four warps tells whether a score is more than 2^8
 //               above it, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to the cache's type, as
 //               the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at the item's end.
-//   warp 4      tensor copies: units of 128 latents x 64 slots (a box a page and 64 latents, 128-byte swizzle), rotary parts and queries.
+//   warp 4      tensor copies of units of 128 latents x 64 slots (128-byte swizzle), a lane each: one lane after another, with a wait
+//               each, they took 450 cycles a unit and held everything up.
+//   warp 7      tensor copies of queries, rotary parts and powers of two.
 //   warp 5      issues tcgen05.mma: S of a tile, then O += C^T P^T, then S of the next.
 //   warp 6      walks the work and hands the parts out.
-//   warps 8-15  (8 bits) turn units of codes into units of elements.
+//   warps 8-15  (8 bits) turn units of codes into units of elements, two warps a unit.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 #include "latent_line.cuh"
 
@@ -41,7 +43,7 @@ using kv::unpack2;
 using kv::wait_bar;
 
 constexpr int kTile = 64;
-constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kConvWarps = 8;
+constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8, kConvPair = 2;
 constexpr float kMost = 256.f;   // P that is let through without raising m
 constexpr float kNone = 3e38f;  // in place of -m before the first score
 constexpr int kChunk = kTile * 128;  // 64 elements of a tile's slots
@@ -133,7 +135,7 @@ __device__ __forceinline__ int part_tiles(const Part &w) {
 }
 
 template <bool BF, bool Q8, int NR>
-__global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const AttendParams p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ Maps maps) {
     using S = Shape<Q8, NR>;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
@@ -146,19 +148,22 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + S::kUnits * kUnit, raws = ropes + S::kRopes * kChunk;
     const uint32_t qs = raws + S::kRaws * S::kRaw, ps = qs + S::kQ, scales = ps + S::kP;
     const int L = p.c.latent >> 7;  // units of a tile
+    const int pair = p.line.pair, rank = pair & blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < S::kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvWarps : 1), bar_init(&bar.unit_empty[i], 1);
+        for (int i = 0; i < S::kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvPair : 1), bar_init(&bar.unit_empty[i], 1);
         for (int i = 0; i < S::kRopes; i++) {
             bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
             bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
         }
-        for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvWarps);
-        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], 6 + (Q8 ? kConvWarps : 0));
+        for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvPair);
+        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], 7 + (Q8 ? kConvWarps : 0));
         bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.pv, 1), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
         for (int i = 0; i < 2; i++) bar_init(&bar.s[i], 1), bar_init(&bar.p[i], 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == kCopyWarp && lane < 5)  // (their first use would wait for them)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps) + lane * sizeof(CUtensorMap)) : "memory");
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -179,7 +184,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     fence_after();
     const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(&s_tmem);
     if (!any) {  // the whole CTA
-        if (tid == 0 && p.line.join) p.line.join[blockIdx.x] = make_int4(0, 0, 0, kv::kJoinNone);
+        if (tid == 0 && p.line.join) p.line.join[where(p.line).id] = make_int4(0, 0, 0, kv::kJoinNone);
         if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
         return;
     }
@@ -194,6 +199,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         constexpr int NB = NR / 8;
         uint32_t ns = 0, no = 0;
         while (!vote(!take(parts, n_part, w, ok))) {
+            const int block = (w.block << pair) + rank;
             const int nt = part_tiles(w);
             const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
             auto limit = [&](int c) {                       // slots that row c sees
@@ -324,7 +330,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             if (vote(!ok)) break;
             fence_after();
             const bool whole = w.first == 0 && w.last == w.steps;
-            const int part = 2 * blockIdx.x + (w.first == 0 ? 1 : 0);
+            const int part = 2 * where(p.line).id + (w.first == 0 ? 1 : 0);
 #pragma unroll
             for (int i = 0; i < NB; i++) {
                 const float2 y = unpack2(l[i]);
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             }
             vote(false);
             if (tid < NR) {
-                const int c = tid, t = s_tok[c], h = w.block * p.heads + c - t * p.heads;
+                const int c = tid, t = s_tok[c], h = block * p.heads + c - t * p.heads;
                 const float sum = (ld_f(ps + c * 4) + ld_f(ps + (NR + c) * 4)) + (ld_f(ps + (2 * NR + c) * 4) + ld_f(ps + (3 * NR + c) * 4));
                 const float top = ld_f(ps + (5 * NR + c) * 4);
                 if (!whole)
@@ -352,8 +358,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             vote(false);
             // a warp has 32 latents of each unit, a lane one, columns are rows of the item
             if (whole) {  // two lanes swap, so that each writes two latents of one row
-                uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)w.block * p.heads * p.out.head + 32 * warp + (lane & ~1);
-                const int rows = p.line.item_tokens < w.left ? used : w.left * p.heads, heads = p.q_heads - w.block * p.heads;
+                uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)block * p.heads * p.out.head + 32 * warp + (lane & ~1);
+                const int rows = p.line.item_tokens < w.left ? used : w.left * p.heads, heads = p.q_heads - block * p.heads;
 #pragma unroll 1
                 for (int k = 0; k < NR; k += 16) {
                     float f[16];
@@ -393,19 +399,69 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             }
             fence_before();  // O is read before the next part's first P is announced
         }
-    } else if (warp == kCopyWarp) {  // ------------------------------------- cached tokens and queries
+    } else if (warp == kCopyWarp) {  // ------------------------------------- latents
+        // a lane a copy: unit u of the tile, half h of its latents where a page is less than a tile (else one copy has both), page
+        // blk of the tile's
         const int box = 1 << (p.c.page_shift < 6 ? p.c.page_shift : 6), boxes = kTile / box;
-        const int mine = lane % boxes, half = lane / boxes;
-        Turn<S::kUnits> un;
+        const int u = lane >> 3, h = lane >> 2 & 1, blk = lane & 3;
+        const bool lead = (lane & 7) == 0, mine = u < L && blk < boxes && (h == 0 || (!Q8 && boxes > 1));
+        constexpr int N = Q8 ? S::kRaws : S::kUnits, kBytes = Q8 ? S::kRaw : kUnit;
+        uint64_t *full = Q8 ? bar.raw_full : bar.unit_full, *empty = Q8 ? bar.raw_empty : bar.unit_empty;
+        const uint32_t to = (Q8 ? raws : units) + h * kChunk + blk * box * 128;
+        Turn<N> un;
+        while (ok && take(parts, n_part, w, ok)) {
+            const int nt = part_tiles(w), s1 = w.first * kStep;
+            const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
+            auto page_at = [&](int j) {
+                const int slot = s1 + j * kTile + blk * box;
+                return j < nt && mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+            };
+            int next = page_at(0);
+            for (int j = 0; j < nt && ok; j++) {
+                int page = next;
+                next = page_at(j + 1);  // on its way while this tile waits for its places
+                const int slot = s1 + j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
+                if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
+                    if (mine && slot < w.hi) kv::flag(p.c.status, FTMOE_ERR_ID_RANGE);
+                    page = -1;
+                }
+                const int valid = __popc(__ballot_sync(~0u, lane < 4 && page >= 0)) * box;  // slots that are copied
+                const int over = un.at + u >= N, at = un.at + u - (over ? N : 0);
+                // units go out as their places come free, those that are free already together
+                bool todo = u < L;
+                for (int k = 0; k <= L; k++) {
+                    const unsigned ready = __ballot_sync(~0u, todo && lead && kv::test_bar(su32(&empty[at]), un.ph ^ over ^ 1));
+                    const bool go = todo && (ready >> (lane & ~7) & 1);
+                    if (go && lead) bar_expect(&full[at], valid * (Q8 ? 128 : 256));
+                    __syncwarp();
+                    if (go && page >= 0 && mine) {
+                        if (Q8)
+                            tma3(to + at * kBytes, &maps.lat, 128 * u, row, page, &full[at]);
+                        else
+                            kv::tma4(to + at * kBytes, &maps.lat, 0, row, 2 * u + h, page, &full[at]);
+                    }
+                    todo = todo && !go;
+                    const unsigned left = __ballot_sync(~0u, todo);
+                    if (!left) break;
+                    const int first = __shfl_sync(~0u, at, __ffs(left) - 1), phase = __shfl_sync(~0u, (int)un.ph ^ over, __ffs(left) - 1);
+                    ok = warp_wait(&empty[first], phase ^ 1);
+                    if (!ok) break;
+                }
+                for (int k = 0; k < L; k++) un.next();
+            }
+        }
+        if (!ok)  // wait (bounded) until the copies already issued have landed
+            for (int i = 0; i < N; i++, un.next()) wait_bar(&full[un.at], un.ph ^ 1);
+    } else if (warp == kRopeWarp) {  // ------------------------------------- queries, rotary parts, powers of two
+        const int box = 1 << (p.c.page_shift < 6 ? p.c.page_shift : 6), boxes = kTile / box;
         Turn<S::kRopes> ro;
-        Turn<Q8 ? S::kRaws : 1> ra;
         uint32_t nq = 0;
         while (ok && take(parts, n_part, w, ok)) {
             const int nt = part_tiles(w), s1 = w.first * kStep;
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
             auto page_at = [&](int j) {
-                const int slot = s1 + j * kTile + mine * box;
-                return j < nt && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                const int slot = s1 + j * kTile + lane * box;
+                return j < nt && lane < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
             int next = page_at(0);
             if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
@@ -416,60 +472,33 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             if (lane == 0) bar_expect(&bar.qfull, (2 * L + 1) * used * 128);
             __syncwarp();
             if (lane < 2 * L + 1)
-                tma3(qs + lane * NR * 128, lane < 2 * L ? &maps.q : &maps.q_rope, lane < 2 * L ? 64 * lane : 0, w.block * p.heads, w.token, &bar.qfull);
+                tma3(qs + lane * NR * 128, lane < 2 * L ? &maps.q : &maps.q_rope, lane < 2 * L ? 64 * lane : 0, ((w.block << pair) + rank) * p.heads, w.token, &bar.qfull);
             for (int j = 0; j < nt && ok; j++) {
-                int page = next;
-                next = page_at(j + 1);  // on its way while this tile waits for its places
-                const int slot = s1 + j * kTile + mine * box, row = slot & ((1 << p.c.page_shift) - 1);
-                if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
-                    if (slot < w.hi) kv::flag(p.c.status, FTMOE_ERR_ID_RANGE);
-                    page = -1;
-                }
-                const int valid = __popc(__ballot_sync(~0u, lane < boxes && page >= 0)) * box;  // slots that are copied
+                const int page = (uint32_t)next < (uint32_t)p.c.num_pages ? next : -1;
+                next = page_at(j + 1);
+                const int row = (s1 + j * kTile + lane * box) & ((1 << p.c.page_shift) - 1);
+                const int valid = __popc(__ballot_sync(~0u, page >= 0)) * box;
                 if (Q8) {
-                    ok = ok && warp_wait(&bar.scale_empty[ro.at], ro.ph ^ 1);
+                    ok = warp_wait(&bar.scale_empty[ro.at], ro.ph ^ 1);
                     if (!ok) break;
                     if (lane == 0) bar_expect(&bar.scale_full[ro.at], valid * 16);
                     __syncwarp();
-                    if (half == 0 && page >= 0) tma3(scales + ro.at * S::kScale + mine * box * 16, &maps.scale, 0, row, page, &bar.scale_full[ro.at]);
+                    if (page >= 0) tma3(scales + ro.at * S::kScale + lane * box * 16, &maps.scale, 0, row, page, &bar.scale_full[ro.at]);
                 }
-                for (int u = 0; u < L; u++) {
-                    if (Q8) {
-                        ok = ok && warp_wait(&bar.raw_empty[ra.at], ra.ph ^ 1);
-                        if (!ok) break;
-                        if (lane == 0) bar_expect(&bar.raw_full[ra.at], valid * 128);
-                        __syncwarp();
-                        if (half == 0 && page >= 0) tma3(raws + ra.at * S::kRaw + mine * box * 128, &maps.lat, 128 * u, row, page, &bar.raw_full[ra.at]);
-                        ra.next();
-                    } else {
-                        ok = ok && warp_wait(&bar.unit_empty[un.at], un.ph ^ 1);
-                        if (!ok) break;
-                        if (lane == 0) bar_expect(&bar.unit_full[un.at], valid * 256);
-                        __syncwarp();
-                        if (half < 2 && page >= 0)
-                            tma3(units + un.at * kUnit + half * kChunk + mine * box * 128, &maps.lat, 128 * u + 64 * half, row, page, &bar.unit_full[un.at]);
-                        un.next();
-                    }
-                }
-                ok = ok && warp_wait(&bar.rope_empty[ro.at], ro.ph ^ 1);
+                ok = warp_wait(&bar.rope_empty[ro.at], ro.ph ^ 1);
                 if (!ok) break;
                 if (lane == 0) bar_expect(&bar.rope_full[ro.at], valid * 128);
                 __syncwarp();
-                if (half == 0 && page >= 0)
-                    tma3(ropes + ro.at * kChunk + mine * box * 128, Q8 ? &maps.rope : &maps.lat, Q8 ? 0 : p.c.latent, row, page, &bar.rope_full[ro.at]);
+                if (page >= 0) tma3(ropes + ro.at * kChunk + lane * box * 128, &maps.rope, 0, row, page, &bar.rope_full[ro.at]);
                 ro.next();
             }
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed
             if (nq > 0) wait_bar(&bar.qfull, (nq - 1) & 1);
-            for (int i = 0; i < S::kRopes; i++, ro.next()) {  // each place's last use (a place not used yet has no phase to wait for)
+            for (int i = 0; i < S::kRopes; i++, ro.next()) {
                 wait_bar(&bar.rope_full[ro.at], ro.ph ^ 1);
                 if (Q8) wait_bar(&bar.scale_full[ro.at], ro.ph ^ 1);
             }
-            if (Q8)
-                for (int i = 0; i < S::kRaws; i++, ra.next()) wait_bar(&bar.raw_full[ra.at], ra.ph ^ 1);
-            else
-                for (int i = 0; i < S::kUnits; i++, un.next()) wait_bar(&bar.unit_full[un.at], un.ph ^ 1);
         }
     } else if (warp == kMmaWarp) {  // --------------------------------------- products
         constexpr uint32_t IS = kv::kInstrM<BF, kTile, NR, false, false>, IO = kv::kInstrM<BF, 128, NR, true, false>;
@@ -479,14 +508,29 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         uint32_t nq = 0, n = 0, np = 0;  // items, tiles whose S and whose O product is issued
         Turn<S::kUnits> us, uv;
         Turn<S::kRopes> ro;
+        // Whether the units of the tile that starts at `t` (and its rotary part) are there: a lane a barrier.
+        auto there = [&](Turn<S::kUnits> t, bool rope) {
+            bool x = true;
+            if (lane < L) {
+                const int at = t.at + lane, over = at >= S::kUnits;
+                x = kv::test_bar(su32(&bar.unit_full[over ? at - S::kUnits : at]), t.ph ^ over);
+            } else if (rope && lane == L) {
+                x = kv::test_bar(su32(&bar.rope_full[ro.at]), ro.ph);
+            }
+            return __all_sync(~0u, x) != 0;
+        };
         auto scores = [&](bool rope_first) {
             const uint32_t d = tm + S::kS + NR * (n & 1);
+            const bool all = there(us, true);  // else each is waited for
             uint32_t acc = 0;
+            fence_after();
             auto rope = [&] {
-                ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
-                if (!ok) return;
-                fence_after();
-                const uint32_t a = __shfl_sync(~0u, rd + ro.at * (kChunk / 16), 0), b = qd + L * (2 * NR * 128 / 16);
+                if (!all) {
+                    ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
+                    if (!ok) return;
+                    fence_after();
+                }
+                const uint32_t a = rd + ro.at * (kChunk / 16), b = qd + L * (2 * NR * 128 / 16);
 #pragma unroll
                 for (int k = 0; k < 4; k++)
                     if (k < rope_steps) mma_ss<IS>(one, d, a + 2 * k, b + 2 * k, acc), acc = 1;
@@ -494,11 +538,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 ro.next();
             };
             if (rope_first) rope();
+            uint32_t b = qd;
 #pragma unroll 1
-            for (int u = 0; u < L && ok; u++, us.next()) {
-                ok = warp_wait(&bar.unit_full[us.at], us.ph);
-                fence_after();
-                const uint32_t a = __shfl_sync(~0u, ud + us.at * (kUnit / 16), 0), b = __shfl_sync(~0u, qd + u * (2 * NR * 128 / 16), 0);
+            for (int u = 0; u < L && ok; u++, us.next(), b += 2 * NR * 128 / 16) {
+                if (!all) {
+                    ok = warp_wait(&bar.unit_full[us.at], us.ph);
+                    fence_after();
+                }
+                const uint32_t a = ud + us.at * (kUnit / 16);
 #pragma unroll
                 for (int k = 0; k < 8; k++, acc = 1)
                     mma_ss<IS>(one, d, a + (k >> 2) * (kChunk / 16) + 2 * (k & 3), b + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
@@ -511,10 +558,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             ok = ok && warp_wait(&bar.p[np & 1], (np >> 1) & 1);
             if (!ok) return;
             fence_after();
-            const uint32_t b = __shfl_sync(~0u, pd + (np & 1) * (NR * 128 / 16), 0);
+            const uint32_t b = pd + (np & 1) * (NR * 128 / 16);
 #pragma unroll 1
             for (int u = 0; u < L; u++, uv.next()) {
-                const uint32_t a = __shfl_sync(~0u, vd + uv.at * (kUnit / 16), 0), d = __shfl_sync(~0u, tm + u * NR, 0);
+                const uint32_t a = vd + uv.at * (kUnit / 16), d = tm + u * NR;
                 uint32_t acc = acc0;
 #pragma unroll
                 for (int k = 0; k < 4; k++, acc = 1) mma_ss<IO>(one, d, a + k * (2048 / 16), b + 2 * k, acc);
@@ -529,11 +576,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 #pragma unroll 1
             for (int j = 0; j < nt && ok;) {
                 // Two tiles' scores, then their outputs, where the second tile is there by then: its scores are formed during the first
-                // one's softmax. The second one's rotary part comes last, into the place that the first one's left.
-                scores(true);
-                Turn<S::kUnits> last = us;
-                for (int u = 1; u < L; u++) last.next();
-                const bool two = ok && j + 1 < nt && L * 2 <= S::kUnits && __all_sync(~0u, kv::test_bar(su32(&bar.unit_full[last.at]), last.ph));
+                // one's softmax. The rotary part of every second tile comes last, into the place that the other's left; which tiles that
+                // is must not hang on what was there when, or sums would be rounded differently from call to call.
+                scores((j & 1) == 0);
+                const bool two = ok && (j & 1) == 0 && j + 1 < nt && L * 2 <= S::kUnits && there(us, false);
                 if (two) scores(false);
                 if (j + 1 + two == nt) commit(one, &bar.qempty);
                 values(j > 0);
@@ -547,48 +593,37 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     } else if (warp == kWalkWarp) {
         ok = hand_out(p, parts, walk);
     } else if (Q8 && warp >= 8) {  // --------------------------------------- codes to elements
-        // a thread has one group of 32 codes of each unit
-        const int slot = (tid - 256) >> 2, g = tid & 3, x7 = slot & 7;
-        Turn<S::kUnits> un;
+        // two warps a unit, every fourth of them, a thread a slot: their waits and latencies overlap (all eight on one
+        // unit after another took 700 cycles each)
+        const int slot = (tid - 256) & 63, group = (warp - 8) >> 1, x7 = slot & 7;
+        uint32_t n = 0;  // units before this tile
         Turn<S::kRopes> ro;
-        Turn<Q8 ? S::kRaws : 1> ra;
         while (ok && take(parts, n_part, w, ok)) {
             const int nt = part_tiles(w);
-            for (int j = 0; j < nt && ok; j++) {
+            for (int j = 0; j < nt && ok; j++, n += L) {
                 ok = warp_wait(&bar.scale_full[ro.at], ro.ph);
-                if (!ok) break;
-                for (int u = 0; u < L; u++) {
-                    ok = ok && warp_wait(&bar.raw_full[ra.at], ra.ph) && warp_wait(&bar.unit_empty[un.at], un.ph ^ 1);
+                for (int u = (group - (int)n) & 3; u < L && ok; u += 4) {
+                    const uint32_t un = (n + u) % S::kUnits, ra = (n + u) % (S::kRaws + !Q8);
+                    ok = warp_wait(&bar.raw_full[ra], (n + u) / (S::kRaws + !Q8) & 1) && warp_wait(&bar.unit_empty[un], (n + u) / S::kUnits & 1 ^ 1);
                     if (!ok) break;
-                    uint32_t in[8], byte;
-                    const uint32_t from = raws + ra.at * S::kRaw + slot * 128;
+                    const uint32_t from = raws + ra * S::kRaw + slot * 128, to = units + un * kUnit + slot * 128;
+                    uint32_t powers;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(powers) : "r"(scales + ro.at * S::kScale + slot * 16 + 4 * u) : "memory");
 #pragma unroll
-                    for (int i = 0; i < 2; i++)
+                    for (int i = 0; i < 8; i++) {  // 16 codes, two pieces of eight elements
+                        uint4 in, lo, hi;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(in[4 * i]), "=r"(in[4 * i + 1]), "=r"(in[4 * i + 2]), "=r"(in[4 * i + 3])
-                                     : "r"(from + (((2 * g + i) ^ x7) << 4))
+                                     : "=r"(in.x), "=r"(in.y), "=r"(in.z), "=r"(in.w)
+                                     : "r"(from + ((i ^ x7) << 4))
                                      : "memory");
-                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(scales + ro.at * S::kScale + slot * 16 + 4 * u + g) : "memory");
-                    const float f = power(byte);
-                    const uint32_t to = units + un.at * kUnit + (g >> 1) * kChunk + slot * 128;
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {  // pieces of eight elements; those of four lanes and two slots meet no bank twice
-                        const int e = i ^ (g & 2);
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const uint32_t c = e & 2 ? (e & 1 ? in[6 + k] : in[4 + k]) : (e & 1 ? in[2 + k] : in[k]);
-                            const float2 a = codes2(c & 0xffffu), b = codes2(c >> 16);
-                            y[2 * k] = from_f2<BF>(a.x * f, a.y * f), y[2 * k + 1] = from_f2<BF>(b.x * f, b.y * f);
-                        }
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + ((((g & 1) * 4 + e) ^ x7) << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]),
-                                     "r"(y[3])
-                                     : "memory");
+                        decode16<BF>(in, powers >> (8 * (i >> 1)) & 0xff, lo, hi);
+                        const uint32_t at = to + (i >> 2) * kChunk;
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((2 * i & 7) ^ x7) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((2 * i + 1 & 7) ^ x7) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
                     }
                     fence_async();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&bar.unit_full[un.at]), bar_arrive(&bar.raw_empty[ra.at]);
-                    un.next(), ra.next();
+                    if (lane == 0) bar_arrive(&bar.unit_full[un]), bar_arrive(&bar.raw_empty[ra]);
                 }
                 if (lane == 0) bar_arrive(&bar.scale_empty[ro.at]);
                 ro.next();
@@ -610,9 +645,10 @@ __global__ void __launch_bounds__(kJoinThreads) absorb_combine(const AttendParam
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x, row = blockIdx.y * kJoinRows + warp;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 join = p.line.join[c];
-    const int t = row / p.heads, h = join.y * p.heads + row - t * p.heads;
+    const int of = gridDim.x >> p.line.pair, rank = p.line.pair && c >= of ? 1 : 0;  // (Where)
+    const int t = row / p.heads, h = ((join.y << p.line.pair) + rank) * p.heads + row - t * p.heads;
     if (t >= p.line.item_tokens || t >= join.x || h >= p.q_heads) return;
-    const int n = kv::count_parts(p.line.join, c, gridDim.x);
+    const int n = kv::count_parts(p.line.join, c, (rank + 1) * of);
     auto slot = [&](int k) { return (int64_t)(2 * (c + k) + (k == 0)) * rows + row; };
     float M = -INFINITY;
     for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[slot(k)].x);
@@ -648,19 +684,19 @@ int rows_of(const AttendParams &p) {
     return n <= 16 ? 16 : n <= 32 ? 32 : 64;
 }
 
-// Items, if no sequence has more tokens than max_q.
+// Items (or pairs of them), if no sequence has more tokens than max_q.
 int64_t most_items(const AttendParams &p) {
     return (int64_t)((p.bt.max_q + p.line.item_tokens - 1) / p.line.item_tokens) * p.bt.batch * p.line.blocks;
 }
 bool cut(const AttendParams &p, int num_sms) {
     const int64_t items = most_items(p), steps = ((int64_t)p.bt.max_kv + kStep - 1) / kStep;
-    return items > num_sms || steps > 2;
+    return items > num_sms >> p.line.pair || steps > 2;
 }
 int ctas(const AttendParams &p, int num_sms) {
     const int64_t items = most_items(p);
-    if (!cut(p, num_sms)) return (int)items;
-    const int64_t most = items * (p.bt.max_kv / kStep + 1 + kItemCost);
-    return (int)(most < num_sms ? (most > 0 ? most : 1) : num_sms);
+    if (!cut(p, num_sms)) return (int)items << p.line.pair;
+    const int64_t most = items * (p.bt.max_kv / kStep + 1 + kItemCost), have = num_sms >> p.line.pair;
+    return (int)(most < have ? (most > 0 ? most : 1) : have) << p.line.pair;
 }
 
 template <bool BF, bool Q8, int NR>
@@ -674,10 +710,10 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
                           {64, p.heads, p.line.item_tokens}, true);
     if (Q8)
         ok = ok && kv::box_map(m.lat, kv::Elem::U8, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {128, box, 1}, true) &&
-             kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, false) &&
-             kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, 8), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+             kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, false);
     else
-        ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent + p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+        ok = ok && kv::box_map4(m.lat, e, p.c.pages, {64, slots, p.c.latent / 64, p.c.num_pages}, p.c.slot, 128, p.c.page, {64, box, box == kTile ? 2 : 1, 1});
+    ok = ok && kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<absorb_kernel<BF, Q8, NR>>(S::kSmem);
     if (rc != cudaSuccess) return rc;
@@ -699,6 +735,10 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
     p.line.blocks = (p.q_heads + rows - 1) / rows, p.heads = (p.q_heads + p.line.blocks - 1) / p.line.blocks;
     p.line.blocks = (p.q_heads + p.heads - 1) / p.heads;
     p.line.item_tokens = rows / p.heads, p.line.batch = p.bt.batch, p.line.max_q = p.bt.max_q, p.line.causal = p.causal;
+    // Two blocks of heads read the same cached tokens at the same time, on two SMs: one of them mostly finds them in L2 (one after the
+    // other, 128 heads read them from memory twice).
+    p.line.pair = p.line.blocks % 2 == 0 ? 1 : 0;
+    p.line.blocks >>= p.line.pair;
     p.line.join = nullptr, p.part_o = nullptr, p.part_ml = nullptr;
     if (!cut(p, num_sms)) return 0;
     size_t off = 0;

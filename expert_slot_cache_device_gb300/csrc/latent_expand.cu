@@ -85,7 +85,7 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float a) {
 }
 
 template <bool BF, int D>
-__global__ void __launch_bounds__(kThreads, 1) expand_kernel(const ExpandParams p, const __grid_constant__ Maps maps) {
+__global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_constant__ ExpandParams p, const __grid_constant__ Maps maps) {
     using S = Shape<D>;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const ExpandParams 
     fence_after();
     const uint32_t tm = *reinterpret_cast<volatile uint32_t *>(&s_tmem);
     if (!any) {  // the whole CTA
-        if (tid == 0 && p.line.join) p.line.join[blockIdx.x] = make_int4(0, 0, 0, kv::kJoinNone);
+        if (tid == 0 && p.line.join) p.line.join[where(p.line).id] = make_int4(0, 0, 0, kv::kJoinNone);
         if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
         return;
     }
@@ -530,7 +530,7 @@ int ctas(const ExpandParams &p, int num_sms) {
 
 size_t expand_workspace(ExpandParams &p, int num_sms, unsigned char *base) {
     p.line.batch = p.batch, p.line.blocks = p.heads, p.line.item_tokens = kRows, p.line.max_q = p.max_q, p.line.causal = p.causal;
-    p.line.join = nullptr, p.part_o = nullptr, p.part_ml = nullptr;
+    p.line.pair = 0, p.line.join = nullptr, p.part_o = nullptr, p.part_ml = nullptr;
     if (!cut(p, num_sms)) return 0;
     size_t off = 0;
     auto take = [&](size_t bytes) {

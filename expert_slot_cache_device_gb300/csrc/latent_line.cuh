@@ -79,20 +79,42 @@ struct Walk {
     }
 };
 
+// Where this CTA stands: its place in the line, the places there are, and its index in join, where those of one line follow one
+// another (a pair's CTAs have the same place, and a line each).
+struct Where {
+    int at, of, id;
+};
+__device__ __forceinline__ Where where(const Line &l) {
+    const int at = blockIdx.x >> l.pair, of = gridDim.x >> l.pair;
+    return Where{at, of, l.pair ? (int)(blockIdx.x & 1) * of + at : at};
+}
+
 // Total units and this CTA's start, for kWarps warps. s_sum: 32 kWarps entries, s_warp: kWarps.
 template <int kWarps, class P>
-__device__ __forceinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, long long *s_sum, Walk<P> *s_walk, int32_t *status) {
+__device__ __noinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, long long *s_sum, Walk<P> *s_walk, int32_t *status) {
     constexpr int T = kWarps * 32;
     const Line &l = p.line;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const Where me = where(l);
     if (!l.join) {  // a CTA an item that there can be, and no line to walk
-        const int most = (l.max_q + l.item_tokens - 1) / l.item_tokens, block = blockIdx.x / most;
-        w.qt = blockIdx.x - block * most, w.b = block / l.blocks, w.block = block - w.b * l.blocks;
+        const int most = (l.max_q + l.item_tokens - 1) / l.item_tokens, block = me.at / most;
+        w.qt = me.at - block * most, w.b = block / l.blocks, w.block = block - w.b * l.blocks;
         w.sq = p.seq(w.b, w.qt == 0 && w.block == 0 && tid == 0 ? status : nullptr);
         w.n_qt = item_count(l, w.sq), w.at = 0, w.left = 1;
         return w.qt < w.n_qt;
     }
+    // one item a sequence at most: a thread a sequence, which then knows its start without reading it again
+    const bool single = l.max_q <= l.item_tokens;
+    kv::Seq mine{};
     auto sums = [&](int b0, int32_t *st) {
+        if (single) {
+            if (b0 + tid < l.batch) {
+                mine = p.seq(b0 + tid, st);
+                s_sum[tid] = mine.q_len > 0 ? item_steps(item_hi(l, mine, 0)) + kItemCost : 0;
+            }
+            __syncthreads();
+            return;
+        }
         for (int i = warp; i < T && b0 + i < l.batch; i += kWarps) {
             const kv::Seq s = p.seq(b0 + i, lane == 0 ? st : nullptr);
             const long long n = seq_units(l, s, item_count(l, s));
@@ -102,15 +124,15 @@ __device__ __forceinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, 
     };
     long long sum = 0, total;
     for (int b0 = 0; b0 < l.batch; b0 += T) {
-        sums(b0, blockIdx.x == 0 ? status : nullptr);
+        sums(b0, me.at == 0 ? status : nullptr);
         if (b0 + tid < l.batch) sum += s_sum[tid];
         if (b0 + T < l.batch) __syncthreads();
     }
     kv::block_scan<T>(sum, total, s_warp);
     const long long W = total * l.blocks;
-    const int C = kv::used_ctas(gridDim.x, W);
-    if (blockIdx.x >= C) return false;
-    const long long u0 = kv::unit_start(blockIdx.x, C, W), u1 = kv::unit_start(blockIdx.x + 1, C, W);
+    const int C = kv::used_ctas(me.of, W);
+    if (me.at >= C) return false;
+    const long long u0 = kv::unit_start(me.at, C, W), u1 = kv::unit_start(me.at + 1, C, W);
     long long base = 0;
     for (int b0 = 0; b0 < l.batch; b0 += T) {
         if (l.batch > T) {  // the sums of the last round are not these
@@ -122,12 +144,18 @@ __device__ __forceinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, 
         if (u0 >= at && u0 < at + n) {
             s_walk->b = b0 + tid;
             s_walk->left = u0 - at;  // for now: the start within the sequence
+            if (single) {
+                const uint32_t from = (uint32_t)(u0 - at), per = (uint32_t)s_sum[tid];  // below 2^16 blocks of 2^24 units
+                const long long block = l.blocks == 1 ? 0 : (u0 - at) >> 32 ? (u0 - at) / per : from / per;
+                s_walk->block = (int)block, s_walk->qt = 0, s_walk->n_qt = 1, s_walk->at = (int)(u0 - at - block * per), s_walk->sq = mine;
+                s_walk->left = u1 - u0;
+            }
         }
         base += total;
         if (base > u0) break;
     }
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0 && !single) {
         const int b = s_walk->b;
         const kv::Seq s = p.seq(b, nullptr);
         const int n_qt = item_count(l, s);
@@ -218,7 +246,7 @@ __device__ __forceinline__ bool hand_out(const P &p, PartRing &ring, Walk<P> &wa
         }
         __syncwarp();
     }
-    if (lane == 0 && p.line.join) p.line.join[blockIdx.x] = join;
+    if (lane == 0 && p.line.join) p.line.join[where(p.line).id] = join;
     return ok;
 }
 

@@ -154,20 +154,6 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     }
 }
 
-// 16 codes of one group as elements.
-template <bool BF>
-__device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
-    const float s = power(byte);
-    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-    uint32_t out[8];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 a = codes2(in[i] & 0xffffu), b = codes2(in[i] >> 16);
-        out[2 * i] = from_f2<BF>(a.x * s, a.y * s), out[2 * i + 1] = from_f2<BF>(b.x * s, b.y * s);
-    }
-    lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
-}
-
 // A CTA copies kReadRows slots of one sequence; a thread takes 16 bytes of a slot at a time.
 constexpr int kReadRows = 32, kReadThreads = 256;
 
