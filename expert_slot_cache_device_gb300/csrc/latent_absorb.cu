@@ -1,23 +1,24 @@
 // Absorbed latent attention on the 5th-generation tensor cores. All heads read the same cached vectors, so the rows of an
-// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 64 slots. Both products have the cache as their A
+// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots. Both products have the cache as their A
 // operand, straight from shared memory in the one layout that the copies leave it in:
-//   S^T [64 slots, NR rows] = [C | K] [Q | Q_rope]^T     A: slots are M, latents K (K-major)
+//   S^T [128 slots, NR rows] = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
 //   O^T [latent, NR rows]  += C^T P^T                    A: latents are M = 128, slots K (M-major)
 // so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most; rows as M would take all of it), and few
 // rows cost few columns instead of an unused part of M = 128. P^T goes to shared memory as the B operand.
 //
 // Persistent, one CTA an SM, work cut by latent_line.cuh. Roles:
-//   warps 0-3   softmax of a tile: warp w has slots 16 w .. 16 w + 15 (tensor memory holds M = 64 in the first 16 lanes of
-//               each quarter), a thread two slots' values of every eighth pair of rows. P = 2^(s scale log2 e - m) in fp32
-//               with the maximum m of the tiles before; one vote of the four warps tells whether a score is more than 2^8
-//               above it, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to the cache's type, as
-//               the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at the item's end.
-//   warp 4      tensor copies of units of 128 latents x 64 slots (128-byte swizzle), a lane each: one lane after another, with a wait
+//   warps 0-3   softmax of a tile: warp w has slots 32 w .. 32 w + 31, a thread four slots' values of every eighth pair of rows.
+//               P = 2^(s scale log2 e - m) in fp32 with the maximum m of the tiles before; one vote of the four warps tells whether a
+//               P is above 2^8, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to
+//               the cache's type, as the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at
+//               the item's end.
+//   warp 4      tensor copies of units of 64 latents x 128 slots (128-byte swizzle), a lane each: one lane after another, with a wait
 //               each, they took 450 cycles a unit and held everything up.
-//   warp 7      tensor copies of queries, rotary parts and powers of two.
-//   warp 5      issues tcgen05.mma: S of a tile, then O += C^T P^T, then S of the next.
+//   warp 5      issues tcgen05.mma: S of a tile, then O += C^T P^T, then S of the next. The warp's number comes from a shuffle, by which
+//               the compiler knows its branches to be uniform and keeps descriptors in uniform registers (without: 70 cycles a product).
 //   warp 6      walks the work and hands the parts out.
-//   warps 8-15  (8 bits) turn units of codes into units of elements, two warps a unit.
+//   warp 7      tensor copies of queries, rotary parts and powers of two.
+//   warps 8-15  (8 bits) turn units of codes into units of elements, four warps a unit.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 #include "latent_line.cuh"
 
@@ -42,41 +43,41 @@ using kv::tma3;
 using kv::unpack2;
 using kv::wait_bar;
 
-constexpr int kTile = 64;
-constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8, kConvPair = 2;
+constexpr int kTile = kStep;
+constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8, kConvGroup = 4;
 constexpr float kMost = 256.f;   // P that is let through without raising m
 constexpr float kNone = 3e38f;  // in place of -m before the first score
-constexpr int kChunk = kTile * 128;  // 64 elements of a tile's slots
-constexpr int kUnit = 2 * kChunk;    // 128 latents of a tile's slots
+constexpr int kUnit = kTile * 128;  // 64 latents of a tile's slots
 
 template <bool Q8, int NR>
 struct Shape {
     static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
-    static constexpr int kUnits = Q8 ? (NR == 64 ? 5 : 8) : (NR == 64 ? 8 : NR == 32 ? 10 : 11);
-    static constexpr int kRopes = Q8 ? 2 : (NR == 64 ? 1 : NR == 32 ? 2 : 3);
-    static constexpr int kRaws = Q8 ? (NR == 16 ? 6 : 4) : 0;  // 128 codes of a tile's slots each
-    static constexpr int kRaw = kChunk, kScale = kTile * 16;
+    static constexpr int kUnits = Q8 || NR == 64 ? 8 : 10;  // an even number: two units are an operand of the second product
+    static constexpr int kRopes = NR == 16 && !Q8 ? 2 : 1, kScales = Q8 ? 2 : 0;
+    static constexpr int kRaws = Q8 ? (NR == 16 ? 6 : 4) : 0, kRaw = kTile * 64, kScale = kTile * 16;
     static constexpr int kQ = 9 * NR * 128;
-    static constexpr int kP = 2 * NR * 128;  // two tiles' (each scratch before its P is formed; the plan's sums before)
-    static constexpr int kSmem = 1024 + kQ + kP + kUnits * kUnit + kRopes * kChunk + kRaws * kRaw + (Q8 ? kRopes * kScale : 0);
-    static constexpr uint32_t kS = 256;  // columns of two tiles' S; O is at 0
+    // P lies over the rotary part, which S has read by then, where shared memory would not hold both
+    static constexpr bool kOver = NR == 64;
+    static constexpr int kP = kOver ? 0 : NR * 256, kScratch = kOver ? 2048 : 0;
+    static constexpr int kSmem = 1024 + kUnits * kUnit + kRopes * kUnit + kRaws * kRaw + kQ + kP + kScratch + kScales * kScale;
+    static constexpr uint32_t kS = 256;  // column of S; O is at 0
 };
-constexpr int kMaxUnits = 11, kMaxRopes = 3, kMaxRaws = 7;
+constexpr int kMaxUnits = 10, kMaxRopes = 2, kMaxRaws = 6, kMaxScales = 2;
 
 struct Maps {
     CUtensorMap q, q_rope, lat, rope, scale;
 };
 
 struct Bars {
-    uint64_t unit_full[kMaxUnits], unit_empty[kMaxUnits], rope_full[kMaxRopes], rope_empty[kMaxRopes];
-    uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws], scale_full[kMaxRopes], scale_empty[kMaxRopes];
-    uint64_t qfull, qempty, s[2], p[2], pv, o, done;
+    uint64_t unit_full[kMaxUnits], pair_empty[kMaxUnits / 2], rope_full[kMaxRopes], rope_empty[kMaxRopes];
+    uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws], scale_full[kMaxScales], scale_empty[kMaxScales];
+    uint64_t qfull, qempty, s, p, o, done;
 };
 
-// Slots of tensor memory as fragments: a thread's registers 4 j .. 4 j + 3 are rows 8 j + 2 (lane % 4), + 1 of slot
-// lane / 4, then of slot lane / 4 + 8.
+// Sixteen lanes of tensor memory as fragments: a thread's registers 4 j .. 4 j + 3 are columns 8 j + 2 (lane % 4), + 1 of lane
+// lane / 4, then of lane / 4 + 8.
 template <int NR>
-__device__ __forceinline__ void load_s(uint32_t a, uint32_t (&x)[NR / 2]) {
+__device__ __forceinline__ void load_s(uint32_t a, uint32_t *x) {
     if constexpr (NR == 64) {
         asm volatile(
             "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
@@ -129,11 +130,6 @@ __device__ __forceinline__ float ld_f(uint32_t a) {
 }
 __device__ __forceinline__ void st_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 
-__device__ __forceinline__ int part_tiles(const Part &w) {
-    const int end = w.last * kStep < w.hi ? w.last * kStep : w.hi, n = (end - w.first * kStep + kTile - 1) / kTile;
-    return n > 0 ? n : 1;
-}
-
 template <bool BF, bool Q8, int NR>
 __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ Maps maps) {
     using S = Shape<Q8, NR>;
@@ -145,21 +141,20 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     __shared__ Walk<AttendParams> s_walk;
     __shared__ uint16_t s_tok[NR];  // token of a row in its item
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // (uniform, for the products' descriptors)
-    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + S::kUnits * kUnit, raws = ropes + S::kRopes * kChunk;
-    const uint32_t qs = raws + S::kRaws * S::kRaw, ps = qs + S::kQ, scales = ps + S::kP;
-    const int L = p.c.latent >> 7;  // units of a tile
+    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + S::kUnits * kUnit, raws = ropes + S::kRopes * kUnit;
+    const uint32_t qs = raws + S::kRaws * S::kRaw, ps = S::kOver ? ropes : qs + S::kQ, scratch = S::kOver ? qs + S::kQ : ps;
+    const uint32_t scales = qs + S::kQ + S::kP + S::kScratch;
+    const int L = p.c.latent >> 6;  // units of a tile
     const int pair = p.line.pair, rank = pair & blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < S::kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvPair : 1), bar_init(&bar.unit_empty[i], 1);
-        for (int i = 0; i < S::kRopes; i++) {
-            bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
-            bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
-        }
-        for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvPair);
+        for (int i = 0; i < S::kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvGroup : 1);
+        for (int i = 0; i < S::kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
+        for (int i = 0; i < S::kRopes; i++) bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
+        for (int i = 0; i < S::kScales; i++) bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
+        for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvGroup);
         for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], 7 + (Q8 ? kConvWarps : 0));
-        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.pv, 1), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
-        for (int i = 0; i < 2; i++) bar_init(&bar.s[i], 1), bar_init(&bar.p[i], 4);
+        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.s, 1), bar_init(&bar.p, 4), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kCopyWarp && lane < 5)  // (their first use would wait for them)
@@ -175,9 +170,9 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         const int c = i / ((NR - used) * 8), r = i - c * ((NR - used) * 8);
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qs + c * NR * 128 + used * 128 + r * 16), "r"(0) : "memory");
     }
-    fence_async();
     Walk<AttendParams> walk;
     const bool any = plan<S::kWarps>(p, walk, s_warp, reinterpret_cast<long long *>(sm_raw + (ps - su32(sm_raw))), &s_walk, p.c.status);
+    fence_async();  // of the zeros above, and of the plan's sums, over which tensor copies may go
     asm volatile("griddepcontrol.launch_dependents;" :::);
     fence_before();
     __syncthreads();
@@ -195,12 +190,11 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     if (warp < 4) {  // ---------------------------------------------------- softmax
         const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
         const float c2 = p.scale * kv::kLog2e;
-        const int row0 = 16 * warp + (lane >> 2), col0 = 2 * (lane & 3);
+        const int row0 = 32 * warp + (lane >> 2), col0 = 2 * (lane & 3);
         constexpr int NB = NR / 8;
         uint32_t ns = 0, no = 0;
         while (!vote(!take(parts, n_part, w, ok))) {
             const int block = (w.block << pair) + rank;
-            const int nt = part_tiles(w);
             const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
             auto limit = [&](int c) {                       // slots that row c sees
                 const int t = s_tok[c], at = w.slot + t;
@@ -212,37 +206,34 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             uint64_t l[NB];
 #pragma unroll
             for (int i = 0; i < NB; i++) z[2 * i] = z[2 * i + 1] = kNone, l[i] = 0;
-            for (int j = 0; j < nt; j++, ns++) {
-                const int s0 = w.first * kStep + j * kTile;
-                const uint32_t tS = lanes + S::kS + NR * (ns & 1), pt = ps + NR * 128 * (ns & 1);
-                ok = ok && warp_wait(&bar.s[ns & 1], (ns >> 1) & 1);
+            for (int j = w.first; j < w.last; j++, ns++) {
+                const int s0 = j * kTile;
+                ok = ok && warp_wait(&bar.s, ns & 1);
                 fence_after();
-                uint32_t x[NR / 2];
+                uint32_t x[NR];  // slots of the warp's first 16 lanes, then of the others
                 auto scores = [&] {
-                    load_s<NR>(tS, x);
+                    load_s<NR>(lanes + S::kS, x);
+                    load_s<NR>(lanes + (16u << 16) + S::kS, x + NR / 2);
                     if (s0 + kTile <= least) return;
-                    const int a = s0 + row0;
 #pragma unroll
-                    for (int i = 0; i < NB; i++)
+                    for (int k = 0; k < 4; k++)
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const int lim = limit(8 * i + col0 + e);
-                            if (a >= lim) x[4 * i + e] = 0xff800000u;
-                            if (a + 8 >= lim) x[4 * i + 2 + e] = 0xff800000u;
-                        }
+                        for (int i = 0; i < NB; i++)
+#pragma unroll
+                            for (int e = 0; e < 2; e++)
+                                if (s0 + row0 + 8 * k >= limit(8 * i + col0 + e)) x[(k >> 1) * (NR / 2) + 4 * i + 2 * (k & 1) + e] = 0xff800000u;
                 };
                 // P in place of the scores; whether one is above 2^8
                 auto form = [&] {
                     float top = 0.f;
 #pragma unroll
-                    for (int i = 0; i < NB; i++)
-#pragma unroll
-                        for (int k = 4 * i; k < 4 * i + 4; k += 2) {
-                            const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
-                            const float a = ex2(f.x), b = ex2(f.y);
-                            top = kv::max3(top, a, b);
-                            x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
-                        }
+                    for (int k = 0; k < NR; k += 2) {
+                        const int i = (k % (NR / 2)) >> 2;
+                        const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
+                        const float a = ex2(f.x), b = ex2(f.y);
+                        top = kv::max3(top, a, b);
+                        x[k] = __float_as_uint(a), x[k + 1] = __float_as_uint(b);
+                    }
                     return top > kMost;
                 };
                 scores();
@@ -253,10 +244,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 #pragma unroll
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
-                        float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2])) * c2;
+                        float t = kv::max3(fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2])), __uint_as_float(x[NR / 2 + r]), __uint_as_float(x[NR / 2 + r + 2])) * c2;
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
-                        if (lane < 4) st_f(pt + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
+                        if (lane < 4) st_f(scratch + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
                     }
                     vote(false);
 #pragma unroll
@@ -264,7 +255,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         float f[2];
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
-                            const uint32_t a = pt + (8 * i + col0 + e) * 4;
+                            const uint32_t a = scratch + (8 * i + col0 + e) * 4;
                             const float t = fmaxf(fmaxf(ld_f(a), ld_f(a + NR * 4)), fmaxf(ld_f(a + 2 * NR * 4), ld_f(a + 3 * NR * 4)));
                             float &zz = z[2 * i + e];
                             const float m = zz == kNone ? -INFINITY : -zz, n = fmaxf(m, t);
@@ -275,16 +266,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         const float2 y = unpack2(l[i]);
                         l[i] = pack2(y.x * f[0], y.y * f[1]);
                     }
-                    if (j > 0) ok = warp_wait(&bar.pv, (ns - 1) & 1);  // O holds all P so far
-                    if (vote(!ok)) break;
-                    fence_after();
-                    if (j > 0) {
+                    vote(false);
+                    if (j > w.first) {  // (the product with the last P was done before this tile's S)
 #pragma unroll 1
-                        for (int k = 0; k < L * NR; k += 16) {
+                        for (int k = 0; k < (L >> 1) * NR; k += 16) {
                             uint32_t y[16];
                             tm_ld16(lanes + k, y);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(pt + (4 * NR + (k + e) % NR) * 4));
+                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(scratch + (4 * NR + (k + e) % NR) * 4));
                             kv::tm_st16(lanes + k, y);
                         }
                         kv::tm_st_wait();
@@ -293,38 +282,37 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     form();
                 }
 #pragma unroll
-                for (int i = 0; i < NB; i += 2) {
-                    uint32_t y[4];
+                for (int h = 0; h < 2; h++)
 #pragma unroll
-                    for (int k = 0; k < 2; k++) {  // rows 8 i, then 8 (i + 1); slots, then slots + 8
-                        const uint32_t *v = x + 4 * (i + k);
-                        const float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]), c = __uint_as_float(v[2]), d = __uint_as_float(v[3]);
-                        l[i + k] = add2(l[i + k], add2(pack2(a, b), pack2(c, d)));
-                        y[2 * k] = from_f2<BF>(a, b), y[2 * k + 1] = from_f2<BF>(c, d);
+                    for (int i = 0; i < NB; i += 2) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {  // rows 8 i, then 8 (i + 1); slots, then slots + 8
+                            const uint32_t *v = x + h * (NR / 2) + 4 * (i + k);
+                            const float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]), c = __uint_as_float(v[2]), d = __uint_as_float(v[3]);
+                            l[i + k] = add2(l[i + k], add2(pack2(a, b), pack2(c, d)));
+                            y[2 * k] = from_f2<BF>(a, b), y[2 * k + 1] = from_f2<BF>(c, d);
+                        }
+                        // transposed: a row's slots consecutive, 64 in 128 bytes, 16-byte piece c of row r at c ^ (r % 8)
+                        const int r = lane & 7, k = lane >> 3;
+                        const uint32_t at = ps + (warp >> 1) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((4 * (warp & 1) + 2 * h + (k & 1)) ^ r) << 4);
+                        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
+                                     "r"(y[3])
+                                     : "memory");
                     }
-                    // transposed: a row's slots consecutive, 16-byte piece c of row r at c ^ (r % 8)
-                    const int r = lane & 7, k = lane >> 3;
-                    const uint32_t at = pt + (8 * (i + (k >> 1)) + r) * 128 + (((2 * warp + (k & 1)) ^ r) << 4);
-                    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
-                                 "r"(y[3])
-                                 : "memory");
-                }
                 if (s0 + kTile > w.hi) {  // latents of slots that no row sees: what they hold must not reach 0 * C
                     const int r0 = w.hi > s0 ? w.hi - s0 : 0;
-                    Turn<S::kUnits> t;
-                    t.at = (int)(ns * L % S::kUnits), t.ph = ns * L / S::kUnits & 1;
-                    for (int u = 0; u < L; u++, t.next()) {
-                        ok = ok && warp_wait(&bar.unit_full[t.at], t.ph);
-                        for (int i = tid; i < (kTile - r0) * 16; i += 128)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(units + t.at * kUnit + ((i >> 3) & 1) * kChunk + (r0 + (i >> 4)) * 128 + ((i & 7) << 4)),
-                                         "r"(0)
-                                         : "memory");
+                    for (int u = 0; u < L; u++) {
+                        const uint32_t n = ns * L + u, at = n % S::kUnits;
+                        ok = ok && warp_wait(&bar.unit_full[at], n / S::kUnits & 1);
+                        for (int i = tid; i < (kTile - r0) * 8; i += 128)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(units + at * kUnit + r0 * 128 + i * 16), "r"(0) : "memory");
                     }
                 }
                 fence_async();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bar.p[ns & 1]);
+                if (lane == 0) bar_arrive(&bar.p);
             }
             ok = ok && warp_wait(&bar.o, no++ & 1);
             if (vote(!ok)) break;
@@ -340,23 +328,23 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
                     const int c = 8 * i + col0 + e;
-                    if (lane < 4) st_f(ps + (warp * NR + c) * 4, t);
-                    if (warp == 0 && lane < 4) st_f(ps + (5 * NR + c) * 4, z[2 * i + e] == kNone ? -INFINITY : -z[2 * i + e]);
+                    if (lane < 4) st_f(scratch + (warp * NR + c) * 4, t);
+                    if (warp == 0 && lane < 4) st_f(scratch + (5 * NR + c) * 4, z[2 * i + e] == kNone ? -INFINITY : -z[2 * i + e]);
                 }
             }
             vote(false);
             if (tid < NR) {
                 const int c = tid, t = s_tok[c], h = block * p.heads + c - t * p.heads;
-                const float sum = (ld_f(ps + c * 4) + ld_f(ps + (NR + c) * 4)) + (ld_f(ps + (2 * NR + c) * 4) + ld_f(ps + (3 * NR + c) * 4));
-                const float top = ld_f(ps + (5 * NR + c) * 4);
+                const float sum = (ld_f(scratch + c * 4) + ld_f(scratch + (NR + c) * 4)) + (ld_f(scratch + (2 * NR + c) * 4) + ld_f(scratch + (3 * NR + c) * 4));
+                const float top = ld_f(scratch + (5 * NR + c) * 4);
                 if (!whole)
                     p.part_ml[(int64_t)part * NR + c] = make_float2(top, sum);
                 else if (p.lse && c < used && t < w.left && h < p.q_heads)
                     p.lse[(int64_t)(w.token + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-                st_f(ps + (4 * NR + c) * 4, !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
+                st_f(scratch + (4 * NR + c) * 4, !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
             }
             vote(false);
-            // a warp has 32 latents of each unit, a lane one, columns are rows of the item
+            // a warp has 32 latents of each 128, a lane one, columns are rows of the item
             if (whole) {  // two lanes swap, so that each writes two latents of one row
                 uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)block * p.heads * p.out.head + 32 * warp + (lane & ~1);
                 const int rows = p.line.item_tokens < w.left ? used : w.left * p.heads, heads = p.q_heads - block * p.heads;
@@ -365,14 +353,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     float f[16];
                     uint16_t *row[8];
 #pragma unroll
-                    for (int e = 0; e < 16; e++) f[e] = ld_f(ps + (4 * NR + k + e) * 4);
+                    for (int e = 0; e < 16; e++) f[e] = ld_f(scratch + (4 * NR + k + e) * 4);
 #pragma unroll
                     for (int e = 0; e < 8; e++) {
                         const int r = k + 2 * e + (lane & 1), t = s_tok[r], h = r - t * p.heads;
                         row[e] = r < rows && h < heads ? out + t * p.out.token + h * p.out.head : nullptr;
                     }
 #pragma unroll 1
-                    for (int u = 0; u < L; u++) {
+                    for (int u = 0; u < L >> 1; u++) {
                         uint32_t y[16];
                         tm_ld16(lanes + u * NR + k, y);
 #pragma unroll
@@ -386,7 +374,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             } else {
                 float *po = p.part_o + (int64_t)part * NR * p.c.latent + 32 * warp + lane;
 #pragma unroll 1
-                for (int u = 0; u < L; u++) {
+                for (int u = 0; u < L >> 1; u++) {
                     float *to = po + 128 * u;
 #pragma unroll 1
                     for (int k = 0; k < NR; k += 16) {
@@ -400,191 +388,154 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             fence_before();  // O is read before the next part's first P is announced
         }
     } else if (warp == kCopyWarp) {  // ------------------------------------- latents
-        // a lane a copy: unit u of the tile, half h of its latents where a page is less than a tile (else one copy has both), page
-        // blk of the tile's
-        const int box = 1 << (p.c.page_shift < 6 ? p.c.page_shift : 6), boxes = kTile / box;
-        const int u = lane >> 3, h = lane >> 2 & 1, blk = lane & 3;
-        const bool lead = (lane & 7) == 0, mine = u < L && blk < boxes && (h == 0 || (!Q8 && boxes > 1));
-        constexpr int N = Q8 ? S::kRaws : S::kUnits, kBytes = Q8 ? S::kRaw : kUnit;
-        uint64_t *full = Q8 ? bar.raw_full : bar.unit_full, *empty = Q8 ? bar.raw_empty : bar.unit_empty;
-        const uint32_t to = (Q8 ? raws : units) + h * kChunk + blk * box * 128;
-        Turn<N> un;
+        // four units at a time, eight lanes a unit, a page of the tile each
+        const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTile / box;
+        const int blk = lane & 7;
+        const bool lead = blk == 0, mine = blk < boxes;
+        constexpr int N = Q8 ? S::kRaws : S::kUnits, kBytes = Q8 ? S::kRaw : kUnit, kRow = Q8 ? 64 : 128;
+        uint64_t *full = Q8 ? bar.raw_full : bar.unit_full, *empty = Q8 ? bar.raw_empty : bar.pair_empty;
+        const uint32_t to = (Q8 ? raws : units) + blk * box * kRow;
+        uint32_t n = 0, sent = 0;  // units before this tile, those of this tile that went out
         while (ok && take(parts, n_part, w, ok)) {
-            const int nt = part_tiles(w), s1 = w.first * kStep;
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
             auto page_at = [&](int j) {
-                const int slot = s1 + j * kTile + blk * box;
-                return j < nt && mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                const int slot = j * kTile + blk * box;
+                return j < w.last && mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            int next = page_at(0);
-            for (int j = 0; j < nt && ok; j++) {
+            int next = page_at(w.first);
+            for (int j = w.first; j < w.last && ok; j++, n += L, sent = 0) {
                 int page = next;
                 next = page_at(j + 1);  // on its way while this tile waits for its places
-                const int slot = s1 + j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
+                const int slot = j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
                 if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
                     if (mine && slot < w.hi) kv::flag(p.c.status, FTMOE_ERR_ID_RANGE);
                     page = -1;
                 }
-                const int valid = __popc(__ballot_sync(~0u, lane < 4 && page >= 0)) * box;  // slots that are copied
-                const int over = un.at + u >= N, at = un.at + u - (over ? N : 0);
-                // units go out as their places come free, those that are free already together
-                bool todo = u < L;
-                for (int k = 0; k <= L; k++) {
-                    const unsigned ready = __ballot_sync(~0u, todo && lead && kv::test_bar(su32(&empty[at]), un.ph ^ over ^ 1));
-                    const bool go = todo && (ready >> (lane & ~7) & 1);
-                    if (go && lead) bar_expect(&full[at], valid * (Q8 ? 128 : 256));
-                    __syncwarp();
-                    if (go && page >= 0 && mine) {
-                        if (Q8)
-                            tma3(to + at * kBytes, &maps.lat, 128 * u, row, page, &full[at]);
-                        else
-                            kv::tma4(to + at * kBytes, &maps.lat, 0, row, 2 * u + h, page, &full[at]);
+                const int bytes = __popc(__ballot_sync(~0u, lane < 8 && page >= 0)) * box * kRow;  // of a unit
+                for (int u0 = 0; u0 < L && ok; u0 += 4) {
+                    const int u = u0 + (lane >> 3), at = (n + u) % N, ph = (n + u) / N & 1;
+                    uint64_t *free = &empty[Q8 ? at : at >> 1];
+                    // units go out as their places come free, those that are free already together
+                    bool todo = u < L;
+                    for (int k = 0; k < 5; k++) {
+                        const unsigned ready = __ballot_sync(~0u, todo && lead && kv::test_bar(su32(free), ph ^ 1));
+                        const bool go = todo && (ready >> (lane & ~7) & 1);
+                        if (go && lead) bar_expect(&full[at], bytes);
+                        __syncwarp();
+                        if (go && page >= 0) tma3(to + at * kBytes, &maps.lat, 64 * u, row, page, &full[at]);
+                        sent |= (ready & 1) << u0 | (ready >> 8 & 1) << (u0 + 1) | (ready >> 16 & 1) << (u0 + 2) | (ready >> 24 & 1) << (u0 + 3);
+                        todo = todo && !go;
+                        const unsigned left = __ballot_sync(~0u, todo);
+                        if (!left) break;
+                        const int from = __ffs(left) - 1, first = __shfl_sync(~0u, Q8 ? at : at >> 1, from), phase = __shfl_sync(~0u, ph, from);
+                        ok = warp_wait(&empty[first], phase ^ 1);
+                        if (!ok) break;
                     }
-                    todo = todo && !go;
-                    const unsigned left = __ballot_sync(~0u, todo);
-                    if (!left) break;
-                    const int first = __shfl_sync(~0u, at, __ffs(left) - 1), phase = __shfl_sync(~0u, (int)un.ph ^ over, __ffs(left) - 1);
-                    ok = warp_wait(&empty[first], phase ^ 1);
-                    if (!ok) break;
                 }
-                for (int k = 0; k < L; k++) un.next();
             }
         }
-        if (!ok)  // wait (bounded) until the copies already issued have landed
-            for (int i = 0; i < N; i++, un.next()) wait_bar(&full[un.at], un.ph ^ 1);
+        if (!ok) {  // wait (bounded) until the copies already issued have landed: each place's last
+            for (int i = 0; i < N; i++) {
+                int last = -1;
+                for (int x = (int)n + i - N; x < (int)n + 8; x += N)
+                    if (x >= 0 && (x < (int)n || (sent >> (x - n) & 1))) last = x;
+                if (last >= 0) wait_bar(&full[last % N], last / N & 1);
+            }
+        }
     } else if (warp == kRopeWarp) {  // ------------------------------------- queries, rotary parts, powers of two
-        const int box = 1 << (p.c.page_shift < 6 ? p.c.page_shift : 6), boxes = kTile / box;
+        const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTile / box;
         Turn<S::kRopes> ro;
+        Turn<S::kScales + !Q8> sc;
         uint32_t nq = 0;
         while (ok && take(parts, n_part, w, ok)) {
-            const int nt = part_tiles(w), s1 = w.first * kStep;
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
             auto page_at = [&](int j) {
-                const int slot = s1 + j * kTile + lane * box;
-                return j < nt && lane < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                const int slot = j * kTile + lane * box;
+                return j < w.last && lane < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            int next = page_at(0);
+            int next = page_at(w.first);
             if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
                 ok = false;
                 break;
             }
             nq++;
-            if (lane == 0) bar_expect(&bar.qfull, (2 * L + 1) * used * 128);
+            if (lane == 0) bar_expect(&bar.qfull, (L + 1) * used * 128);
             __syncwarp();
-            if (lane < 2 * L + 1)
-                tma3(qs + lane * NR * 128, lane < 2 * L ? &maps.q : &maps.q_rope, lane < 2 * L ? 64 * lane : 0, ((w.block << pair) + rank) * p.heads, w.token, &bar.qfull);
-            for (int j = 0; j < nt && ok; j++) {
+            if (lane <= L)
+                tma3(qs + lane * NR * 128, lane < L ? &maps.q : &maps.q_rope, lane < L ? 64 * lane : 0, ((w.block << pair) + rank) * p.heads, w.token, &bar.qfull);
+            for (int j = w.first; j < w.last && ok; j++) {
                 const int page = (uint32_t)next < (uint32_t)p.c.num_pages ? next : -1;
                 next = page_at(j + 1);
-                const int row = (s1 + j * kTile + lane * box) & ((1 << p.c.page_shift) - 1);
+                const int row = (j * kTile + lane * box) & ((1 << p.c.page_shift) - 1);
                 const int valid = __popc(__ballot_sync(~0u, page >= 0)) * box;
                 if (Q8) {
-                    ok = warp_wait(&bar.scale_empty[ro.at], ro.ph ^ 1);
+                    ok = warp_wait(&bar.scale_empty[sc.at], sc.ph ^ 1);
                     if (!ok) break;
-                    if (lane == 0) bar_expect(&bar.scale_full[ro.at], valid * 16);
+                    if (lane == 0) bar_expect(&bar.scale_full[sc.at], valid * 16);
                     __syncwarp();
-                    if (page >= 0) tma3(scales + ro.at * S::kScale + lane * box * 16, &maps.scale, 0, row, page, &bar.scale_full[ro.at]);
+                    if (page >= 0) tma3(scales + sc.at * S::kScale + lane * box * 16, &maps.scale, 0, row, page, &bar.scale_full[sc.at]);
+                    sc.next();
                 }
                 ok = warp_wait(&bar.rope_empty[ro.at], ro.ph ^ 1);
                 if (!ok) break;
                 if (lane == 0) bar_expect(&bar.rope_full[ro.at], valid * 128);
                 __syncwarp();
-                if (page >= 0) tma3(ropes + ro.at * kChunk + lane * box * 128, &maps.rope, 0, row, page, &bar.rope_full[ro.at]);
+                if (page >= 0) tma3(ropes + ro.at * kUnit + lane * box * 128, &maps.rope, 0, row, page, &bar.rope_full[ro.at]);
                 ro.next();
             }
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed
             if (nq > 0) wait_bar(&bar.qfull, (nq - 1) & 1);
-            for (int i = 0; i < S::kRopes; i++, ro.next()) {
-                wait_bar(&bar.rope_full[ro.at], ro.ph ^ 1);
-                if (Q8) wait_bar(&bar.scale_full[ro.at], ro.ph ^ 1);
-            }
+            for (int i = 0; i < S::kRopes; i++, ro.next()) wait_bar(&bar.rope_full[ro.at], ro.ph ^ 1);
+            for (int i = 0; i < S::kScales; i++, sc.next()) wait_bar(&bar.scale_full[sc.at], sc.ph ^ 1);
         }
     } else if (warp == kMmaWarp) {  // --------------------------------------- products
         constexpr uint32_t IS = kv::kInstrM<BF, kTile, NR, false, false>, IO = kv::kInstrM<BF, 128, NR, true, false>;
         const uint32_t one = kv::elect_one();
-        const uint32_t qd = desc_lo(qs, 16), pd = desc_lo(ps, 16), ud = desc_lo(units, 16), rd = desc_lo(ropes, 16), vd = desc_lo(units, kChunk);
+        const uint32_t qd = desc_lo(qs, 16), pd = desc_lo(ps, 16), ud = desc_lo(units, 16), rd = desc_lo(ropes, 16), vd = desc_lo(units, kUnit);
         const int rope_steps = p.c.rope >> 4;
-        uint32_t nq = 0, n = 0, np = 0;  // items, tiles whose S and whose O product is issued
-        Turn<S::kUnits> us, uv;
+        uint32_t nq = 0, n = 0;  // items, tiles
+        Turn<S::kUnits> us, uv;  // of the scores and of the outputs
         Turn<S::kRopes> ro;
-        // Whether the units of the tile that starts at `t` (and its rotary part) are there: a lane a barrier.
-        auto there = [&](Turn<S::kUnits> t, bool rope) {
-            bool x = true;
-            if (lane < L) {
-                const int at = t.at + lane, over = at >= S::kUnits;
-                x = kv::test_bar(su32(&bar.unit_full[over ? at - S::kUnits : at]), t.ph ^ over);
-            } else if (rope && lane == L) {
-                x = kv::test_bar(su32(&bar.rope_full[ro.at]), ro.ph);
-            }
-            return __all_sync(~0u, x) != 0;
-        };
-        auto scores = [&](bool rope_first) {
-            const uint32_t d = tm + S::kS + NR * (n & 1);
-            const bool all = there(us, true);  // else each is waited for
-            uint32_t acc = 0;
-            fence_after();
-            auto rope = [&] {
-                if (!all) {
-                    ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
-                    if (!ok) return;
-                    fence_after();
-                }
-                const uint32_t a = rd + ro.at * (kChunk / 16), b = qd + L * (2 * NR * 128 / 16);
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    if (k < rope_steps) mma_ss<IS>(one, d, a + 2 * k, b + 2 * k, acc), acc = 1;
-                commit(one, &bar.rope_empty[ro.at]);
-                ro.next();
-            };
-            if (rope_first) rope();
-            uint32_t b = qd;
-#pragma unroll 1
-            for (int u = 0; u < L && ok; u++, us.next(), b += 2 * NR * 128 / 16) {
-                if (!all) {
-                    ok = warp_wait(&bar.unit_full[us.at], us.ph);
-                    fence_after();
-                }
-                const uint32_t a = ud + us.at * (kUnit / 16);
-#pragma unroll
-                for (int k = 0; k < 8; k++, acc = 1)
-                    mma_ss<IS>(one, d, a + (k >> 2) * (kChunk / 16) + 2 * (k & 3), b + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
-            }
-            if (!rope_first && ok) rope();
-            if (ok) commit(one, &bar.s[n & 1]);
-            n++;
-        };
-        auto values = [&](uint32_t acc0) {
-            ok = ok && warp_wait(&bar.p[np & 1], (np >> 1) & 1);
-            if (!ok) return;
-            fence_after();
-            const uint32_t b = pd + (np & 1) * (NR * 128 / 16);
-#pragma unroll 1
-            for (int u = 0; u < L; u++, uv.next()) {
-                const uint32_t a = vd + uv.at * (kUnit / 16), d = tm + u * NR;
-                uint32_t acc = acc0;
-#pragma unroll
-                for (int k = 0; k < 4; k++, acc = 1) mma_ss<IO>(one, d, a + k * (2048 / 16), b + 2 * k, acc);
-                commit(one, &bar.unit_empty[uv.at]);
-            }
-            commit(one, &bar.pv);
-            np++;
-        };
         while (ok && take(parts, n_part, w, ok)) {
-            const int nt = __shfl_sync(~0u, part_tiles(w), 0);
+            const int nt = __shfl_sync(~0u, w.last - w.first, 0);
             ok = warp_wait(&bar.qfull, nq++ & 1);
 #pragma unroll 1
-            for (int j = 0; j < nt && ok;) {
-                // Two tiles' scores, then their outputs, where the second tile is there by then: its scores are formed during the first
-                // one's softmax. The rotary part of every second tile comes last, into the place that the other's left; which tiles that
-                // is must not hang on what was there when, or sums would be rounded differently from call to call.
-                scores((j & 1) == 0);
-                const bool two = ok && (j & 1) == 0 && j + 1 < nt && L * 2 <= S::kUnits && there(us, false);
-                if (two) scores(false);
-                if (j + 1 + two == nt) commit(one, &bar.qempty);
-                values(j > 0);
-                if (two) values(1);
-                j += 1 + two;
+            for (int j = 0; j < nt && ok; j++, n++) {
+                uint32_t b = qd, acc = 0;
+#pragma unroll 1
+                for (int u = 0; u < L && ok; u++, us.next(), b += NR * 128 / 16) {
+                    ok = warp_wait(&bar.unit_full[us.at], us.ph);
+                    fence_after();
+                    const uint32_t a = ud + us.at * (kUnit / 16);
+#pragma unroll
+                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + 2 * k, b + 2 * k, acc);
+                }
+                ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
+                if (!ok) break;
+                fence_after();
+                const uint32_t r = rd + ro.at * (kUnit / 16);
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    if (k < rope_steps) mma_ss<IS>(one, tm + S::kS, r + 2 * k, b + 2 * k, 1);
+                commit(one, &bar.s);
+                if (!S::kOver) commit(one, &bar.rope_empty[ro.at]);
+                if (j + 1 == nt) commit(one, &bar.qempty);
+                ok = warp_wait(&bar.p, n & 1);
+                if (!ok) break;
+                fence_after();
+#pragma unroll 1
+                for (int u = 0; u < L; u += 2) {
+                    const uint32_t a = vd + uv.at * (kUnit / 16), d = tm + (u >> 1) * NR;
+                    acc = j > 0;
+#pragma unroll
+                    for (int k = 0; k < 8; k++, acc = 1)
+                        mma_ss<IO>(one, d, a + k * (2048 / 16), pd + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
+                    commit(one, &bar.pair_empty[uv.at >> 1]);
+                    uv.next(), uv.next();
+                }
+                if (S::kOver) commit(one, &bar.rope_empty[ro.at]);
+                ro.next();
             }
             if (ok) commit(one, &bar.o);
         }
@@ -593,40 +544,41 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     } else if (warp == kWalkWarp) {
         ok = hand_out(p, parts, walk);
     } else if (Q8 && warp >= 8) {  // --------------------------------------- codes to elements
-        // two warps a unit, every fourth of them, a thread a slot: their waits and latencies overlap (all eight on one
-        // unit after another took 700 cycles each)
-        const int slot = (tid - 256) & 63, group = (warp - 8) >> 1, x7 = slot & 7;
+        // four warps a unit, every second of them, a thread a slot
+        constexpr int R = S::kRaws + !Q8;
+        const int slot = (tid - 256) & 127, group = (warp - 8) >> 2;
         uint32_t n = 0;  // units before this tile
-        Turn<S::kRopes> ro;
+        Turn<S::kScales + !Q8> sc;
         while (ok && take(parts, n_part, w, ok)) {
-            const int nt = part_tiles(w);
-            for (int j = 0; j < nt && ok; j++, n += L) {
-                ok = warp_wait(&bar.scale_full[ro.at], ro.ph);
-                for (int u = (group - (int)n) & 3; u < L && ok; u += 4) {
-                    const uint32_t un = (n + u) % S::kUnits, ra = (n + u) % (S::kRaws + !Q8);
-                    ok = warp_wait(&bar.raw_full[ra], (n + u) / (S::kRaws + !Q8) & 1) && warp_wait(&bar.unit_empty[un], (n + u) / S::kUnits & 1 ^ 1);
+            for (int j = w.first; j < w.last && ok; j++, n += L) {
+                ok = warp_wait(&bar.scale_full[sc.at], sc.ph);
+                for (int u = (group ^ (int)n) & 1; u < L && ok; u += 2) {
+                    const uint32_t un = (n + u) % S::kUnits, ra = (n + u) % R;
+                    ok = warp_wait(&bar.raw_full[ra], (n + u) / R & 1) && warp_wait(&bar.pair_empty[un >> 1], (n + u) / S::kUnits & 1 ^ 1);
                     if (!ok) break;
-                    const uint32_t from = raws + ra * S::kRaw + slot * 128, to = units + un * kUnit + slot * 128;
+                    const uint32_t from = raws + ra * S::kRaw + slot * 64, to = units + un * kUnit + slot * 128;
                     uint32_t powers;
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(powers) : "r"(scales + ro.at * S::kScale + slot * 16 + 4 * u) : "memory");
+                    asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}"
+                                 : "=r"(powers)
+                                 : "r"(scales + sc.at * S::kScale + slot * 16 + 2 * u)
+                                 : "memory");
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {  // 16 codes, two pieces of eight elements
+                    for (int i = 0; i < 4; i++) {  // 16 codes (64-byte swizzle), two pieces of eight elements
                         uint4 in, lo, hi;
                         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(in.x), "=r"(in.y), "=r"(in.z), "=r"(in.w)
-                                     : "r"(from + ((i ^ x7) << 4))
+                                     : "r"(from + ((i ^ (slot >> 1 & 3)) << 4))
                                      : "memory");
                         decode16<BF>(in, powers >> (8 * (i >> 1)) & 0xff, lo, hi);
-                        const uint32_t at = to + (i >> 2) * kChunk;
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((2 * i & 7) ^ x7) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + (((2 * i + 1 & 7) ^ x7) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * i) ^ (slot & 7)) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * i + 1) ^ (slot & 7)) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
                     }
                     fence_async();
                     __syncwarp();
                     if (lane == 0) bar_arrive(&bar.unit_full[un]), bar_arrive(&bar.raw_empty[ra]);
                 }
-                if (lane == 0) bar_arrive(&bar.scale_empty[ro.at]);
-                ro.next();
+                if (lane == 0) bar_arrive(&bar.scale_empty[sc.at]);
+                sc.next();
             }
         }
     }
@@ -678,10 +630,11 @@ __global__ void __launch_bounds__(kJoinThreads) absorb_combine(const AttendParam
     if (lane == 0 && p.lse) p.lse[(int64_t)(join.z + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place.
+// Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place. With 8 bits
+// 32 at most: codes, elements and more queries do not fit shared memory.
 int rows_of(const AttendParams &p) {
     const int64_t n = (int64_t)p.q_heads * p.bt.max_q;
-    return n <= 16 ? 16 : n <= 32 ? 32 : 64;
+    return n <= 16 ? 16 : n <= 32 || p.c.bits == 8 ? 32 : 64;
 }
 
 // Items (or pairs of them), if no sequence has more tokens than max_q.
@@ -703,17 +656,16 @@ template <bool BF, bool Q8, int NR>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     using S = Shape<Q8, NR>;
     const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
-    const int box = p.c.page_shift < 6 ? 1 << p.c.page_shift : 64, slots = 1 << p.c.page_shift;
+    const int box = p.c.page_shift < 7 ? 1 << p.c.page_shift : kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
     Maps m;
-    bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, p.line.item_tokens}, true) &&
-              kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token,
-                          {64, p.heads, p.line.item_tokens}, true);
+    bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, 128) &&
+              kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, 128) &&
+              kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 128);
     if (Q8)
-        ok = ok && kv::box_map(m.lat, kv::Elem::U8, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {128, box, 1}, true) &&
-             kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, false);
+        ok = ok && kv::box_map(m.lat, kv::Elem::U8, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 64) &&
+             kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, 0);
     else
-        ok = ok && kv::box_map4(m.lat, e, p.c.pages, {64, slots, p.c.latent / 64, p.c.num_pages}, p.c.slot, 128, p.c.page, {64, box, box == kTile ? 2 : 1, 1});
-    ok = ok && kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+        ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 128);
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<absorb_kernel<BF, Q8, NR>>(S::kSmem);
     if (rc != cudaSuccess) return rc;
@@ -722,10 +674,11 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     return kv::launch_after(absorb_combine<BF>, dim3(C, NR / kJoinRows), kJoinThreads, 0, st, p, NR);
 }
 
-template <bool BF, bool Q8>
+template <bool BF>
 cudaError_t launch_rows(const AttendParams &p, int C, cudaStream_t st) {
     const int n = rows_of(p);
-    return n == 16 ? launch<BF, Q8, 16>(p, C, st) : n == 32 ? launch<BF, Q8, 32>(p, C, st) : launch<BF, Q8, 64>(p, C, st);
+    if (p.c.bits == 8) return n == 16 ? launch<BF, true, 16>(p, C, st) : launch<BF, true, 32>(p, C, st);
+    return n == 16 ? launch<BF, false, 16>(p, C, st) : n == 32 ? launch<BF, false, 32>(p, C, st) : launch<BF, false, 64>(p, C, st);
 }
 
 }  // namespace
@@ -756,8 +709,7 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
 
 cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
     const int C = ctas(p, num_sms);
-    if (p.c.bits == 8) return bf16 ? launch_rows<true, true>(p, C, st) : launch_rows<false, true>(p, C, st);
-    return bf16 ? launch_rows<true, false>(p, C, st) : launch_rows<false, false>(p, C, st);
+    return bf16 ? launch_rows<true>(p, C, st) : launch_rows<false>(p, C, st);
 }
 
 }  // namespace latent
