@@ -48,12 +48,12 @@ constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWa
 constexpr float kMost = 256.f;   // P that is let through without raising m
 constexpr float kNone = 3e38f;  // in place of -m before the first score
 constexpr int kUnit = kTile * 128;  // 64 latents of a tile's slots
+constexpr int kUnits = 8;           // places for them; two are an operand of the second product
 
 template <bool Q8, int NR>
 struct Shape {
     static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
-    static constexpr int kUnits = Q8 || NR == 64 ? 8 : 10;  // an even number: two units are an operand of the second product
-    static constexpr int kRopes = NR == 16 && !Q8 ? 2 : 1, kScales = Q8 ? 2 : 0;
+    static constexpr int kRopes = NR == 64 || Q8 ? 1 : 2, kScales = Q8 ? 2 : 0;
     static constexpr int kRaws = Q8 ? (NR == 16 ? 6 : 4) : 0, kRaw = kTile * 64, kScale = kTile * 16;
     static constexpr int kQ = 9 * NR * 128;
     // P lies over the rotary part, which S has read by then, where shared memory would not hold both
@@ -62,14 +62,14 @@ struct Shape {
     static constexpr int kSmem = 1024 + kUnits * kUnit + kRopes * kUnit + kRaws * kRaw + kQ + kP + kScratch + kScales * kScale;
     static constexpr uint32_t kS = 256;  // column of S; O is at 0
 };
-constexpr int kMaxUnits = 10, kMaxRopes = 2, kMaxRaws = 6, kMaxScales = 2;
+constexpr int kMaxRopes = 2, kMaxRaws = 6, kMaxScales = 2;
 
 struct Maps {
-    CUtensorMap q, q_rope, lat, rope, scale;
+    CUtensorMap q, q_rope, lat, rope, all, scale;  // all: whole slots, for prefetches
 };
 
 struct Bars {
-    uint64_t unit_full[kMaxUnits], pair_empty[kMaxUnits / 2], rope_full[kMaxRopes], rope_empty[kMaxRopes];
+    uint64_t unit_full[kUnits], pair_empty[kUnits / 2], rope_full[kMaxRopes], rope_empty[kMaxRopes];
     uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws], scale_full[kMaxScales], scale_empty[kMaxScales];
     uint64_t qfull, qempty, s, p, o, done;
 };
@@ -130,6 +130,12 @@ __device__ __forceinline__ float ld_f(uint32_t a) {
 }
 __device__ __forceinline__ void st_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 
+__device__ __forceinline__ void prefetch(const CUtensorMap *map, int x, int y, int z) {
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+constexpr int kWide = 192;  // 16-bit elements of a slot that one prefetch has
+
 template <bool BF, bool Q8, int NR>
 __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ Maps maps) {
     using S = Shape<Q8, NR>;
@@ -141,15 +147,15 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     __shared__ Walk<AttendParams> s_walk;
     __shared__ uint16_t s_tok[NR];  // token of a row in its item
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // (uniform, for the products' descriptors)
-    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + S::kUnits * kUnit, raws = ropes + S::kRopes * kUnit;
+    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + kUnits * kUnit, raws = ropes + S::kRopes * kUnit;
     const uint32_t qs = raws + S::kRaws * S::kRaw, ps = S::kOver ? ropes : qs + S::kQ, scratch = S::kOver ? qs + S::kQ : ps;
     const uint32_t scales = qs + S::kQ + S::kP + S::kScratch;
     const int L = p.c.latent >> 6;  // units of a tile
     const int pair = p.line.pair, rank = pair & blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < S::kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvGroup : 1);
-        for (int i = 0; i < S::kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
+        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvGroup : 1);
+        for (int i = 0; i < kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
         for (int i = 0; i < S::kRopes; i++) bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
         for (int i = 0; i < S::kScales; i++) bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
         for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvGroup);
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.s, 1), bar_init(&bar.p, 4), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kCopyWarp && lane < 5)  // (their first use would wait for them)
+    if (warp == kCopyWarp && lane < 6)  // (their first use would wait for them)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps) + lane * sizeof(CUtensorMap)) : "memory");
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
@@ -303,8 +309,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 if (s0 + kTile > w.hi) {  // latents of slots that no row sees: what they hold must not reach 0 * C
                     const int r0 = w.hi > s0 ? w.hi - s0 : 0;
                     for (int u = 0; u < L; u++) {
-                        const uint32_t n = ns * L + u, at = n % S::kUnits;
-                        ok = ok && warp_wait(&bar.unit_full[at], n / S::kUnits & 1);
+                        const uint32_t n = ns * L + u, at = n % kUnits;
+                        ok = ok && warp_wait(&bar.unit_full[at], n / kUnits & 1);
                         for (int i = tid; i < (kTile - r0) * 8; i += 128)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(units + at * kUnit + r0 * 128 + i * 16), "r"(0) : "memory");
                     }
@@ -392,7 +398,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTile / box;
         const int blk = lane & 7;
         const bool lead = blk == 0, mine = blk < boxes;
-        constexpr int N = Q8 ? S::kRaws : S::kUnits, kBytes = Q8 ? S::kRaw : kUnit, kRow = Q8 ? 64 : 128;
+        const int wide = ((rope_at(p.c.latent, p.c.bits) >> 1) + p.c.rope + kWide - 1) / kWide;  // copies of kWide elements of a slot: 4 at most
+        constexpr int N = Q8 ? S::kRaws : kUnits, kBytes = Q8 ? S::kRaw : kUnit, kRow = Q8 ? 64 : 128;
         uint64_t *full = Q8 ? bar.raw_full : bar.unit_full, *empty = Q8 ? bar.raw_empty : bar.pair_empty;
         const uint32_t to = (Q8 ? raws : units) + blk * box * kRow;
         uint32_t n = 0, sent = 0;  // units before this tile, those of this tile that went out
@@ -432,6 +439,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         if (!ok) break;
                     }
                 }
+                // The next tile on its way to L2: shared memory holds one, and what comes from memory once its places are free comes
+                // too late.
+                if (lane >> 3 < wide && (uint32_t)next < (uint32_t)p.c.num_pages)
+                    prefetch(&maps.all, kWide * (lane >> 3), (slot + kTile) & ((1 << p.c.page_shift) - 1), next);
             }
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed: each place's last
@@ -495,23 +506,39 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         const uint32_t qd = desc_lo(qs, 16), pd = desc_lo(ps, 16), ud = desc_lo(units, 16), rd = desc_lo(ropes, 16), vd = desc_lo(units, kUnit);
         const int rope_steps = p.c.rope >> 4;
         uint32_t nq = 0, n = 0;  // items, tiles
-        Turn<S::kUnits> us, uv;  // of the scores and of the outputs
+        Turn<kUnits> us, uv;  // of the scores and of the outputs
         Turn<S::kRopes> ro;
         while (ok && take(parts, n_part, w, ok)) {
             const int nt = __shfl_sync(~0u, w.last - w.first, 0);
             ok = warp_wait(&bar.qfull, nq++ & 1);
 #pragma unroll 1
             for (int j = 0; j < nt && ok; j++, n++) {
+                // each unit's barrier is tested while the products of the one before are issued (a test takes 100 cycles)
                 uint32_t b = qd, acc = 0;
-#pragma unroll 1
-                for (int u = 0; u < L && ok; u++, us.next(), b += NR * 128 / 16) {
-                    ok = warp_wait(&bar.unit_full[us.at], us.ph);
-                    fence_after();
-                    const uint32_t a = ud + us.at * (kUnit / 16);
+                bool there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
+                if (L == kUnits) {  // places and descriptors known here: 50 cycles a product, what it runs, against 77
 #pragma unroll
-                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + 2 * k, b + 2 * k, acc);
+                    for (int u = 0; u < kUnits; u++) {
+                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.unit_full[u], us.ph);
+                        fence_after();
+                        there = kv::test_bar(su32(u + 1 < kUnits ? &bar.unit_full[u + 1] : &bar.rope_full[ro.at]), u + 1 < kUnits ? us.ph : ro.ph);
+#pragma unroll
+                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, ud + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
+                    }
+                    us.ph ^= 1, b = qd + kUnits * (NR * 128 / 16);
+                } else {
+#pragma unroll 1
+                    for (int u = 0; u < L && ok; u++, b += NR * 128 / 16) {
+                        if (!__all_sync(~0u, there)) ok = warp_wait(&bar.unit_full[us.at], us.ph);
+                        fence_after();
+                        const uint32_t a = ud + us.at * (kUnit / 16);
+                        us.next();
+                        there = kv::test_bar(su32(u + 1 < L ? &bar.unit_full[us.at] : &bar.rope_full[ro.at]), u + 1 < L ? us.ph : ro.ph);
+#pragma unroll
+                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + 2 * k, b + 2 * k, acc);
+                    }
                 }
-                ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
+                if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
                 if (!ok) break;
                 fence_after();
                 const uint32_t r = rd + ro.at * (kUnit / 16);
@@ -553,8 +580,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             for (int j = w.first; j < w.last && ok; j++, n += L) {
                 ok = warp_wait(&bar.scale_full[sc.at], sc.ph);
                 for (int u = (group ^ (int)n) & 1; u < L && ok; u += 2) {
-                    const uint32_t un = (n + u) % S::kUnits, ra = (n + u) % R;
-                    ok = warp_wait(&bar.raw_full[ra], (n + u) / R & 1) && warp_wait(&bar.pair_empty[un >> 1], (n + u) / S::kUnits & 1 ^ 1);
+                    const uint32_t un = (n + u) % kUnits, ra = (n + u) % R;
+                    ok = warp_wait(&bar.raw_full[ra], (n + u) / R & 1) && warp_wait(&bar.pair_empty[un >> 1], (n + u) / kUnits & 1 ^ 1);
                     if (!ok) break;
                     const uint32_t from = raws + ra * S::kRaw + slot * 64, to = units + un * kUnit + slot * 128;
                     uint32_t powers;
@@ -661,6 +688,8 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, 128) &&
               kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, 128) &&
               kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 128);
+    const int row = rope_at(p.c.latent, p.c.bits) / 2 + p.c.rope;
+    ok = ok && kv::box_map(m.all, e, p.c.pages, {row, slots, p.c.num_pages}, p.c.slot, p.c.page, {kWide, box, 1}, 0);
     if (Q8)
         ok = ok && kv::box_map(m.lat, kv::Elem::U8, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 64) &&
              kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, 0);

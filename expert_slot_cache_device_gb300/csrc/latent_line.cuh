@@ -103,6 +103,49 @@ __device__ __noinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, lon
         w.n_qt = item_count(l, w.sq), w.at = 0, w.left = 1;
         return w.qt < w.n_qt;
     }
+    if (l.max_q <= l.item_tokens && l.batch <= 128) {
+        // one item a sequence at most, and few sequences: every warp for itself, four to a lane, without a barrier
+        long long n[4], mine = 0, before = 0;
+        kv::Seq s[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const int b = 4 * lane + k;
+            s[k] = b < l.batch ? p.seq(b, me.at == 0 && warp == 0 ? status : nullptr) : kv::Seq{0, 0, 0};
+            n[k] = s[k].q_len > 0 ? (long long)(item_steps(item_hi(l, s[k], 0)) + kItemCost) * l.blocks : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) mine += n[k];
+        long long x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        const long long W = __shfl_sync(~0u, x, 31);
+        const int C = kv::used_ctas(me.of, W);
+        if (me.at >= C) return false;
+        const long long u0 = kv::unit_start(me.at, C, W), u1 = kv::unit_start(me.at + 1, C, W);
+        before = x - mine;
+        int hit = -1;
+        long long from = 0;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if (u0 >= before && u0 < before + n[k]) hit = k, from = u0 - before;
+            before += n[k];
+        }
+        const int owner = __ffs(__ballot_sync(~0u, hit >= 0)) - 1;
+        hit = __shfl_sync(~0u, hit, owner), from = __shfl_sync(~0u, from, owner);
+        kv::Seq sq = s[0];
+        long long per = n[0];
+#pragma unroll
+        for (int k = 1; k < 4; k++)
+            if (hit == k) sq = s[k], per = n[k];
+        sq.q0 = __shfl_sync(~0u, sq.q0, owner), sq.q_len = __shfl_sync(~0u, sq.q_len, owner), sq.kv_len = __shfl_sync(~0u, sq.kv_len, owner);
+        per = __shfl_sync(~0u, per, owner);
+        const long long block = l.blocks == 1 ? 0 : from / (per / l.blocks);
+        w.b = 4 * owner + hit, w.block = (int)block, w.qt = 0, w.n_qt = 1, w.at = (int)(from - block * (per / l.blocks)), w.sq = sq, w.left = u1 - u0;
+        return true;
+    }
     // one item a sequence at most: a thread a sequence, which then knows its start without reading it again
     const bool single = l.max_q <= l.item_tokens;
     kv::Seq mine{};
