@@ -268,11 +268,11 @@ bool page_map(CUtensorMap &m, const View &c, bool keys, bool bf16, int box_slots
 bool query_map(CUtensorMap &m, const AttendParams &p, bool bf16);
 // Tensor map of rows: [row][column], boxes of 64 columns x box_rows rows; zeros past the ends.
 bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, int box_rows, bool bf16);
-// Tensor map of three axes, the first consecutive: elements of 8 bits or of a 16-bit type, strides in bytes, swizzled in `swizzle`
-// bytes (128, 64 or 0: not); zeros past the ends.
+// Tensor map of three axes, the first consecutive: elements of 8 bits or of a 16-bit type, strides in bytes, with the 128-byte
+// swizzle or none; zeros past the ends.
 enum class Elem { U8, BF16, F16 };
 bool box_map(CUtensorMap &m, Elem type, const void *x, const int64_t (&dims)[3], int64_t stride1, int64_t stride2, const int (&box)[3],
-             int swizzle);
+             bool swizzle);
 
 }  // namespace kv
 }  // namespace ftmoe

@@ -50,33 +50,38 @@ __device__ __forceinline__ float2 codes2(uint32_t u) {
 
 // 16 codes of one group as elements. A code's exponent and fraction, put under the element type's, are its value times
 // 2^-120 (bf16) or 2^-8 (f16), subnormals too, and one product with a power of two gives the element. Powers whose factor the type
-// does not hold, and codes that are NaN, go by floats.
+// does not hold (not plain_power) go by floats. (A group with a NaN has the power NaN; the codes 0x7f and 0xff are not written.)
 template <bool BF>
-__device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
+__device__ __forceinline__ bool plain_power(uint32_t byte) {
+    return (BF || byte >= 127 - 22) && byte <= 127 + 7;
+}
+template <bool BF>
+__device__ __forceinline__ void decode16_plain(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
     uint32_t out[8];
-    uint32_t nan = 0;  // 0x80 where a code is 0x7f or 0xff
+    // the factor twice: bf16 2^(e + 120), f16 2^(e + 8)
+    const uint32_t f = BF ? (byte + 120) * 0x00800080u : (byte - 127 + 8 + 15) * 0x04000400u;
 #pragma unroll
-    for (int i = 0; i < 4; i++) nan |= (in[i] & 0x7f7f7f7fu) + 0x01010101u;
-    if ((BF || byte >= 127 - 22) && byte <= 127 + 7 && !(nan & 0x80808080u)) {
-        // the factor twice: bf16 2^(e + 120), f16 2^(e + 8)
-        const uint32_t f = BF ? (byte + 120) * 0x00800080u : (byte - 127 + 8 + 15) * 0x04000400u;
+    for (int i = 0; i < 8; i++) {
+        const uint32_t x = __byte_perm(in[i >> 1], 0, i & 1 ? 0x3424 : 0x1404);  // codes in the high bytes
+        const uint32_t y = (x & 0x80008000u) | (BF ? x >> 4 & 0x07f007f0u : x >> 1 & 0x3f803f80u);
+        if (BF)
+            asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(y), "r"(f));
+        else
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(y), "r"(f));
+    }
+    lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+template <bool BF>
+__device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
+    if (plain_power<BF>(byte)) return decode16_plain<BF>(u, byte, lo, hi);
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+    uint32_t out[8];
+    const float s = power(byte);
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const uint32_t x = __byte_perm(in[i >> 1], 0, i & 1 ? 0x3424 : 0x1404);  // codes in the high bytes
-            const uint32_t y = (x & 0x80008000u) | (BF ? x >> 4 & 0x07f007f0u : x >> 1 & 0x3f803f80u);
-            if (BF)
-                asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(y), "r"(f));
-            else
-                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(out[i]) : "r"(y), "r"(f));
-        }
-    } else {
-        const float s = power(byte);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const float2 a = codes2(in[i] & 0xffffu), b = codes2(in[i] >> 16);
-            out[2 * i] = kv::from_f2<BF>(a.x * s, a.y * s), out[2 * i + 1] = kv::from_f2<BF>(b.x * s, b.y * s);
-        }
+    for (int i = 0; i < 4; i++) {
+        const float2 a = codes2(in[i] & 0xffffu), b = codes2(in[i] >> 16);
+        out[2 * i] = kv::from_f2<BF>(a.x * s, a.y * s), out[2 * i + 1] = kv::from_f2<BF>(b.x * s, b.y * s);
     }
     lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
 }

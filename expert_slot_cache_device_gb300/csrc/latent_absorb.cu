@@ -1,13 +1,13 @@
 // Absorbed latent attention on the 5th-generation tensor cores. All heads read the same cached vectors, so the rows of an
-// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots. Both products have the cache as their A
+// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots (64 of an 8-bit cache). Both products have the cache as their A
 // operand, straight from shared memory in the one layout that the copies leave it in:
-//   S^T [128 slots, NR rows] = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
+//   S^T [slots, NR rows]     = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
 //   O^T [latent, NR rows]  += C^T P^T                    A: latents are M = 128, slots K (M-major)
 // so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most; rows as M would take all of it), and few
 // rows cost few columns instead of an unused part of M = 128. P^T goes to shared memory as the B operand.
 //
 // Persistent, one CTA an SM, work cut by latent_line.cuh. Roles:
-//   warps 0-3   softmax of a tile: warp w has slots 32 w .. 32 w + 31, a thread four slots' values of every eighth pair of rows.
+//   warps 0-3   softmax of a tile: a warp has a quarter of the slots, a thread four (two) slots' values of every eighth pair of rows.
 //               P = 2^(s scale log2 e - m) in fp32 with the maximum m of the tiles before; one vote of the four warps tells whether a
 //               P is above 2^8, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to
 //               the cache's type, as the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at
@@ -18,7 +18,8 @@
 //               the compiler knows its branches to be uniform and keeps descriptors in uniform registers (without: 70 cycles a product).
 //   warp 6      walks the work and hands the parts out.
 //   warp 7      tensor copies of queries, rotary parts and powers of two.
-//   warps 8-15  (8 bits) turn units of codes into units of elements, four warps a unit.
+//   warps 8-15  (8 bits, instead of warp 4) load codes, a warp a unit, and turn them into units of elements. Codes stay in registers on
+//               their way: shared memory has no place for more than a quarter of a tile's, which let too few be under way.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 #include "latent_line.cuh"
 
@@ -43,34 +44,36 @@ using kv::tma3;
 using kv::unpack2;
 using kv::wait_bar;
 
-constexpr int kTile = kStep;
-constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8, kConvGroup = 4;
+constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8;
 constexpr float kMost = 256.f;   // P that is let through without raising m
-constexpr float kNone = 3e38f;  // in place of -m before the first score
-constexpr int kUnit = kTile * 128;  // 64 latents of a tile's slots
-constexpr int kUnits = 8;           // places for them; two are an operand of the second product
+constexpr float kLeast = 5.9604645e-8f;  // 2^-24
 
 template <bool Q8, int NR>
 struct Shape {
     static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
-    static constexpr int kRopes = NR == 64 || Q8 ? 1 : 2, kScales = Q8 ? 2 : 0;
-    static constexpr int kRaws = Q8 ? (NR == 16 ? 6 : 4) : 0, kRaw = kTile * 64, kScale = kTile * 16;
+    static constexpr int kRopes = NR == 64 ? 1 : 2, kScales = Q8 ? 2 : 0;
+    // Slots of a tile: 128 read least from shared memory; of codes 64, as only two tiles of elements let one be filled while the other is
+    // worked on.
+    static constexpr int kTile = Q8 ? 64 : 128, kHalves = kTile / 64;
+    static constexpr int kUnit = kTile * 128;       // 64 latents of a tile's slots
+    static constexpr int kUnits = Q8 ? 16 : 8;      // places for them; two are an operand of the second product
+    static constexpr int kScale = kTile * 16;
     static constexpr int kQ = 9 * NR * 128;
     // P lies over the rotary part, which S has read by then, where shared memory would not hold both
     static constexpr bool kOver = NR == 64;
-    static constexpr int kP = kOver ? 0 : NR * 256, kScratch = kOver ? 2048 : 0;
-    static constexpr int kSmem = 1024 + kUnits * kUnit + kRopes * kUnit + kRaws * kRaw + kQ + kP + kScratch + kScales * kScale;
+    static constexpr int kP = kOver ? 0 : NR * 2 * kTile > 4096 ? NR * 2 * kTile : 4096, kScratch = kOver ? 2048 : 0;
+    static constexpr int kSmem = 1024 + kUnits * kUnit + kRopes * kUnit + kQ + kP + kScratch + kScales * kScale;
     static constexpr uint32_t kS = 256;  // column of S; O is at 0
 };
-constexpr int kMaxRopes = 2, kMaxRaws = 6, kMaxScales = 2;
+constexpr int kMaxRopes = 2, kMaxScales = 2;
 
 struct Maps {
     CUtensorMap q, q_rope, lat, rope, all, scale;  // all: whole slots, for prefetches
 };
 
 struct Bars {
-    uint64_t unit_full[kUnits], pair_empty[kUnits / 2], rope_full[kMaxRopes], rope_empty[kMaxRopes];
-    uint64_t raw_full[kMaxRaws], raw_empty[kMaxRaws], scale_full[kMaxScales], scale_empty[kMaxScales];
+    uint64_t unit_full[16], pair_empty[8], rope_full[kMaxRopes], rope_empty[kMaxRopes];
+    uint64_t scale_full[kMaxScales], scale_empty[kMaxScales];
     uint64_t qfull, qempty, s, p, o, done;
 };
 
@@ -136,9 +139,21 @@ __device__ __forceinline__ void prefetch(const CUtensorMap *map, int x, int y, i
 }
 constexpr int kWide = 192;  // 16-bit elements of a slot that one prefetch has
 
+// Tiles of a part.
+template <int kTile>
+struct Tiles {
+    int first, last;
+    __device__ __forceinline__ explicit Tiles(const Part &w) {
+        first = w.first * (kStep / kTile), last = w.last * (kStep / kTile);
+        const int end = (w.hi + kTile - 1) / kTile;
+        if (last > end) last = end > first ? end : first + 1;
+    }
+};
+
 template <bool BF, bool Q8, int NR>
 __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ Maps maps) {
     using S = Shape<Q8, NR>;
+    constexpr int kTile = S::kTile, kUnit = S::kUnit, kUnits = S::kUnits;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
     __shared__ PartRing parts;
@@ -147,23 +162,22 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     __shared__ Walk<AttendParams> s_walk;
     __shared__ uint16_t s_tok[NR];  // token of a row in its item
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // (uniform, for the products' descriptors)
-    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + kUnits * kUnit, raws = ropes + S::kRopes * kUnit;
-    const uint32_t qs = raws + S::kRaws * S::kRaw, ps = S::kOver ? ropes : qs + S::kQ, scratch = S::kOver ? qs + S::kQ : ps;
+    const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + kUnits * kUnit;
+    const uint32_t qs = ropes + S::kRopes * kUnit, ps = S::kOver ? ropes : qs + S::kQ, scratch = S::kOver ? qs + S::kQ : ps;
     const uint32_t scales = qs + S::kQ + S::kP + S::kScratch;
     const int L = p.c.latent >> 6;  // units of a tile
     const int pair = p.line.pair, rank = pair & blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvGroup : 1);
+        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], 1);
         for (int i = 0; i < kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
         for (int i = 0; i < S::kRopes; i++) bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
         for (int i = 0; i < S::kScales; i++) bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
-        for (int i = 0; i < S::kRaws; i++) bar_init(&bar.raw_full[i], 1), bar_init(&bar.raw_empty[i], kConvGroup);
-        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], 7 + (Q8 ? kConvWarps : 0));
+        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], Q8 ? 6 + kConvWarps : 7);
         bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.s, 1), bar_init(&bar.p, 4), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kCopyWarp && lane < 6)  // (their first use would wait for them)
+    if (warp == kCopyWarp && lane < 6 && (lane != 5 || Q8) && (lane != 2 || !Q8))  // (their first use would wait for them)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps) + lane * sizeof(CUtensorMap)) : "memory");
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
@@ -177,7 +191,11 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(qs + c * NR * 128 + used * 128 + r * 16), "r"(0) : "memory");
     }
     Walk<AttendParams> walk;
-    const bool any = plan<S::kWarps>(p, walk, s_warp, reinterpret_cast<long long *>(sm_raw + (ps - su32(sm_raw))), &s_walk, p.c.status);
+    bool any = true;
+    if (!plans_alone(p.line))
+        any = plan<S::kWarps>(p, walk, s_warp, reinterpret_cast<long long *>(sm_raw + (ps - su32(sm_raw))), &s_walk, p.c.status);
+    else if (warp == kWalkWarp)
+        plan_alone(p, walk, p.c.status);
     fence_async();  // of the zeros above, and of the plan's sums, over which tensor copies may go
     asm volatile("griddepcontrol.launch_dependents;" :::);
     fence_before();
@@ -193,13 +211,16 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     Part w;
     uint32_t n_part = 0;
 
+    const int wide = ((rope_at(p.c.latent, p.c.bits) >> 1) + p.c.rope + kWide - 1) / kWide;  // copies of kWide elements of a slot: 4 at most
+
     if (warp < 4) {  // ---------------------------------------------------- softmax
         const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
         const float c2 = p.scale * kv::kLog2e;
-        const int row0 = 32 * warp + (lane >> 2), col0 = 2 * (lane & 3);
+        const int row0 = kTile / 4 * warp + (lane >> 2), col0 = 2 * (lane & 3);
         constexpr int NB = NR / 8;
         uint32_t ns = 0, no = 0;
         while (!vote(!take(parts, n_part, w, ok))) {
+            const Tiles<kTile> tl(w);
             const int block = (w.block << pair) + rank;
             const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
             auto limit = [&](int c) {                       // slots that row c sees
@@ -207,22 +228,24 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 return t >= w.left || at < 0 ? 0 : (p.line.causal ? at + 1 : w.kv_len);
             };
             const int least = dead || w.slot < 0 ? 0 : (p.line.causal ? w.slot + 1 : w.kv_len);
-            // rows c and c + 1 of eight i: z = -m (kNone before the first score, which makes P of any score infinite), sums of P
+            // Rows c and c + 1 of eight i: z = -m, sums of P. m starts at 0: a first tile whose P are neither above 2^8 nor, for any thread
+            // and row, all below 2^-24 needs no maximum (bf16: P keeps its precision there; f16 would lose it below 2^-14).
             float z[2 * NB];
             uint64_t l[NB];
 #pragma unroll
-            for (int i = 0; i < NB; i++) z[2 * i] = z[2 * i + 1] = kNone, l[i] = 0;
-            for (int j = w.first; j < w.last; j++, ns++) {
+            for (int i = 0; i < NB; i++) z[2 * i] = z[2 * i + 1] = 0.f, l[i] = 0;
+            for (int j = tl.first; j < tl.last; j++, ns++) {
                 const int s0 = j * kTile;
                 ok = ok && warp_wait(&bar.s, ns & 1);
                 fence_after();
-                uint32_t x[NR];  // slots of the warp's first 16 lanes, then of the others
+                constexpr int X = S::kHalves * NR / 2;
+                uint32_t x[X];  // slots of the warp's first 16 lanes, then of the others
                 auto scores = [&] {
                     load_s<NR>(lanes + S::kS, x);
-                    load_s<NR>(lanes + (16u << 16) + S::kS, x + NR / 2);
+                    if (S::kHalves == 2) load_s<NR>(lanes + (16u << 16) + S::kS, x + X - NR / 2);
                     if (s0 + kTile <= least) return;
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
+                    for (int k = 0; k < 2 * S::kHalves; k++)
 #pragma unroll
                         for (int i = 0; i < NB; i++)
 #pragma unroll
@@ -233,7 +256,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 auto form = [&] {
                     float top = 0.f;
 #pragma unroll
-                    for (int k = 0; k < NR; k += 2) {
+                    for (int k = 0; k < X; k += 2) {
                         const int i = (k % (NR / 2)) >> 2;
                         const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
                         const float a = ex2(f.x), b = ex2(f.y);
@@ -243,14 +266,27 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     return top > kMost;
                 };
                 scores();
-                if (vote(form() || !ok)) {
+                const bool fresh = j == tl.first;
+                bool raise = form() || !ok || (fresh && !BF);
+                if (fresh) {
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; i++) {
+                        const int r = 4 * (i >> 1) + (i & 1);
+                        float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
+                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
+                        raise = raise || t < kLeast;
+                    }
+                }
+                if (vote(raise)) {
                     if (vote(!ok)) break;
                     scores();
                     // m to at least each row's maximum over the tile
 #pragma unroll
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
-                        float t = kv::max3(fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2])), __uint_as_float(x[NR / 2 + r]), __uint_as_float(x[NR / 2 + r + 2])) * c2;
+                        float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
+                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
+                        t *= c2;
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
                         if (lane < 4) st_f(scratch + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
@@ -263,17 +299,16 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         for (int e = 0; e < 2; e++) {
                             const uint32_t a = scratch + (8 * i + col0 + e) * 4;
                             const float t = fmaxf(fmaxf(ld_f(a), ld_f(a + NR * 4)), fmaxf(ld_f(a + 2 * NR * 4), ld_f(a + 3 * NR * 4)));
-                            float &zz = z[2 * i + e];
-                            const float m = zz == kNone ? -INFINITY : -zz, n = fmaxf(m, t);
-                            f[e] = m == -INFINITY ? 0.f : ex2(m - n);
-                            zz = n == -INFINITY ? kNone : -n;
+                            const float m = -z[2 * i + e], n = fresh ? (t == -INFINITY ? 0.f : t) : fmaxf(m, t);
+                            f[e] = fresh ? 0.f : ex2(m - n);
+                            z[2 * i + e] = -n;
                             if (warp == 0 && lane < 4) st_f(a + 4 * NR * 4, f[e]);
                         }
                         const float2 y = unpack2(l[i]);
                         l[i] = pack2(y.x * f[0], y.y * f[1]);
                     }
                     vote(false);
-                    if (j > w.first) {  // (the product with the last P was done before this tile's S)
+                    if (!fresh) {  // (the product with the last P was done before this tile's S)
 #pragma unroll 1
                         for (int k = 0; k < (L >> 1) * NR; k += 16) {
                             uint32_t y[16];
@@ -288,7 +323,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     form();
                 }
 #pragma unroll
-                for (int h = 0; h < 2; h++)
+                for (int h = 0; h < S::kHalves; h++)
 #pragma unroll
                     for (int i = 0; i < NB; i += 2) {
                         uint32_t y[4];
@@ -301,7 +336,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         }
                         // transposed: a row's slots consecutive, 64 in 128 bytes, 16-byte piece c of row r at c ^ (r % 8)
                         const int r = lane & 7, k = lane >> 3;
-                        const uint32_t at = ps + (warp >> 1) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((4 * (warp & 1) + 2 * h + (k & 1)) ^ r) << 4);
+                        const int piece = 2 * S::kHalves * warp + 2 * h + (k & 1);
+                        const uint32_t at = ps + (piece >> 3) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((piece & 7) ^ r) << 4);
                         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
                                      "r"(y[3])
                                      : "memory");
@@ -335,7 +371,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
                     const int c = 8 * i + col0 + e;
                     if (lane < 4) st_f(scratch + (warp * NR + c) * 4, t);
-                    if (warp == 0 && lane < 4) st_f(scratch + (5 * NR + c) * 4, z[2 * i + e] == kNone ? -INFINITY : -z[2 * i + e]);
+                    if (warp == 0 && lane < 4) st_f(scratch + (5 * NR + c) * 4, -z[2 * i + e]);
                 }
             }
             vote(false);
@@ -344,7 +380,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 const float sum = (ld_f(scratch + c * 4) + ld_f(scratch + (NR + c) * 4)) + (ld_f(scratch + (2 * NR + c) * 4) + ld_f(scratch + (3 * NR + c) * 4));
                 const float top = ld_f(scratch + (5 * NR + c) * 4);
                 if (!whole)
-                    p.part_ml[(int64_t)part * NR + c] = make_float2(top, sum);
+                    p.part_ml[(int64_t)part * NR + c] = make_float2(sum == 0.f ? -INFINITY : top, sum);
                 else if (p.lse && c < used && t < w.left && h < p.q_heads)
                     p.lse[(int64_t)(w.token + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
                 st_f(scratch + (4 * NR + c) * 4, !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
@@ -393,78 +429,74 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             }
             fence_before();  // O is read before the next part's first P is announced
         }
-    } else if (warp == kCopyWarp) {  // ------------------------------------- latents
+    } else if (!Q8 && warp == kCopyWarp) {  // ------------------------------------- latents
         // four units at a time, eight lanes a unit, a page of the tile each
-        const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTile / box;
+        const int box = 1 << p.c.page_shift < kTile ? 1 << p.c.page_shift : kTile, boxes = kTile / box;
         const int blk = lane & 7;
         const bool lead = blk == 0, mine = blk < boxes;
-        const int wide = ((rope_at(p.c.latent, p.c.bits) >> 1) + p.c.rope + kWide - 1) / kWide;  // copies of kWide elements of a slot: 4 at most
-        constexpr int N = Q8 ? S::kRaws : kUnits, kBytes = Q8 ? S::kRaw : kUnit, kRow = Q8 ? 64 : 128;
-        uint64_t *full = Q8 ? bar.raw_full : bar.unit_full, *empty = Q8 ? bar.raw_empty : bar.pair_empty;
-        const uint32_t to = (Q8 ? raws : units) + blk * box * kRow;
+        const uint32_t to = units + blk * box * 128;
         uint32_t n = 0, sent = 0;  // units before this tile, those of this tile that went out
         while (ok && take(parts, n_part, w, ok)) {
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
             auto page_at = [&](int j) {
                 const int slot = j * kTile + blk * box;
-                return j < w.last && mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                return mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            int next = page_at(w.first);
-            for (int j = w.first; j < w.last && ok; j++, n += L, sent = 0) {
-                int page = next;
+            const Tiles<kTile> tl(w);
+            int next = page_at(tl.first);
+            for (int j = tl.first; j < tl.last && ok; j++, n += L, sent = 0) {
+                const int page = (uint32_t)next < (uint32_t)p.c.num_pages ? next : -1;  // (warp 7 records bad ones)
                 next = page_at(j + 1);  // on its way while this tile waits for its places
-                const int slot = j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
-                if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
-                    if (mine && slot < w.hi) kv::flag(p.c.status, FTMOE_ERR_ID_RANGE);
-                    page = -1;
-                }
-                const int bytes = __popc(__ballot_sync(~0u, lane < 8 && page >= 0)) * box * kRow;  // of a unit
+                const int row = (j * kTile + blk * box) & ((1 << p.c.page_shift) - 1);
+                const int bytes = __popc(__ballot_sync(~0u, lane < 8 && page >= 0)) * box * 128;  // of a unit
                 for (int u0 = 0; u0 < L && ok; u0 += 4) {
-                    const int u = u0 + (lane >> 3), at = (n + u) % N, ph = (n + u) / N & 1;
-                    uint64_t *free = &empty[Q8 ? at : at >> 1];
+                    const int u = u0 + (lane >> 3), at = (n + u) % kUnits, ph = (n + u) / kUnits & 1;
+                    uint64_t *free = &bar.pair_empty[at >> 1];
                     // units go out as their places come free, those that are free already together
                     bool todo = u < L;
                     for (int k = 0; k < 5; k++) {
                         const unsigned ready = __ballot_sync(~0u, todo && lead && kv::test_bar(su32(free), ph ^ 1));
                         const bool go = todo && (ready >> (lane & ~7) & 1);
-                        if (go && lead) bar_expect(&full[at], bytes);
+                        if (go && lead) bar_expect(&bar.unit_full[at], bytes);
                         __syncwarp();
-                        if (go && page >= 0) tma3(to + at * kBytes, &maps.lat, 64 * u, row, page, &full[at]);
+                        if (go && page >= 0) tma3(to + at * kUnit, &maps.lat, 64 * u, row, page, &bar.unit_full[at]);
                         sent |= (ready & 1) << u0 | (ready >> 8 & 1) << (u0 + 1) | (ready >> 16 & 1) << (u0 + 2) | (ready >> 24 & 1) << (u0 + 3);
                         todo = todo && !go;
                         const unsigned left = __ballot_sync(~0u, todo);
                         if (!left) break;
-                        const int from = __ffs(left) - 1, first = __shfl_sync(~0u, Q8 ? at : at >> 1, from), phase = __shfl_sync(~0u, ph, from);
-                        ok = warp_wait(&empty[first], phase ^ 1);
+                        const int from = __ffs(left) - 1, first = __shfl_sync(~0u, at >> 1, from), phase = __shfl_sync(~0u, ph, from);
+                        ok = warp_wait(&bar.pair_empty[first], phase ^ 1);
                         if (!ok) break;
                     }
                 }
-                // The next tile on its way to L2: shared memory holds one, and what comes from memory once its places are free comes
-                // too late.
+                // The next tile on its way to L2: shared memory holds one, and what comes from memory only when its places are
+                // free comes too late. (After this tile's copies, which would queue behind it.)
                 if (lane >> 3 < wide && (uint32_t)next < (uint32_t)p.c.num_pages)
-                    prefetch(&maps.all, kWide * (lane >> 3), (slot + kTile) & ((1 << p.c.page_shift) - 1), next);
+                    prefetch(&maps.all, kWide * (lane >> 3), ((j + 1) * kTile + blk * box) & ((1 << p.c.page_shift) - 1), next);
             }
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed: each place's last
-            for (int i = 0; i < N; i++) {
+            for (int i = 0; i < kUnits; i++) {
                 int last = -1;
-                for (int x = (int)n + i - N; x < (int)n + 8; x += N)
+                for (int x = (int)n + i - kUnits; x < (int)n + kUnits; x += kUnits)
                     if (x >= 0 && (x < (int)n || (sent >> (x - n) & 1))) last = x;
-                if (last >= 0) wait_bar(&full[last % N], last / N & 1);
+                if (last >= 0) wait_bar(&bar.unit_full[last % kUnits], last / kUnits & 1);
             }
         }
     } else if (warp == kRopeWarp) {  // ------------------------------------- queries, rotary parts, powers of two
-        const int box = 1 << (p.c.page_shift < 7 ? p.c.page_shift : 7), boxes = kTile / box;
+        const int box = 1 << p.c.page_shift < kTile ? 1 << p.c.page_shift : kTile, boxes = kTile / box;
+        const int blk = lane & 7;
         Turn<S::kRopes> ro;
         Turn<S::kScales + !Q8> sc;
         uint32_t nq = 0;
         while (ok && take(parts, n_part, w, ok)) {
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
             auto page_at = [&](int j) {
-                const int slot = j * kTile + lane * box;
-                return j < w.last && lane < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                const int slot = j * kTile + blk * box;
+                return blk < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            int next = page_at(w.first);
+            const Tiles<kTile> tl(w);
+            int next = page_at(tl.first);
             if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
                 ok = false;
                 break;
@@ -474,25 +506,32 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             __syncwarp();
             if (lane <= L)
                 tma3(qs + lane * NR * 128, lane < L ? &maps.q : &maps.q_rope, lane < L ? 64 * lane : 0, ((w.block << pair) + rank) * p.heads, w.token, &bar.qfull);
-            for (int j = w.first; j < w.last && ok; j++) {
-                const int page = (uint32_t)next < (uint32_t)p.c.num_pages ? next : -1;
+            for (int j = tl.first; j < tl.last && ok; j++) {
+                const int slot = j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
+                int page = next;
                 next = page_at(j + 1);
-                const int row = (j * kTile + lane * box) & ((1 << p.c.page_shift) - 1);
-                const int valid = __popc(__ballot_sync(~0u, page >= 0)) * box;
+                if ((uint32_t)page >= (uint32_t)p.c.num_pages) {
+                    if (blk < boxes && slot < w.hi) kv::flag(p.c.status, FTMOE_ERR_ID_RANGE);
+                    page = -1;
+                }
+                const bool mine = lane < 8 && page >= 0;
+                const int valid = __popc(__ballot_sync(~0u, mine)) * box;
                 if (Q8) {
                     ok = warp_wait(&bar.scale_empty[sc.at], sc.ph ^ 1);
                     if (!ok) break;
                     if (lane == 0) bar_expect(&bar.scale_full[sc.at], valid * 16);
                     __syncwarp();
-                    if (page >= 0) tma3(scales + sc.at * S::kScale + lane * box * 16, &maps.scale, 0, row, page, &bar.scale_full[sc.at]);
+                    if (mine) tma3(scales + sc.at * S::kScale + lane * box * 16, &maps.scale, 0, row, page, &bar.scale_full[sc.at]);
                     sc.next();
                 }
                 ok = warp_wait(&bar.rope_empty[ro.at], ro.ph ^ 1);
                 if (!ok) break;
                 if (lane == 0) bar_expect(&bar.rope_full[ro.at], valid * 128);
                 __syncwarp();
-                if (page >= 0) tma3(ropes + ro.at * kUnit + lane * box * 128, &maps.rope, 0, row, page, &bar.rope_full[ro.at]);
+                if (mine) tma3(ropes + ro.at * kUnit + lane * box * 128, &maps.rope, 0, row, page, &bar.rope_full[ro.at]);
                 ro.next();
+                if (Q8 && lane >> 3 < wide && (uint32_t)next < (uint32_t)p.c.num_pages)  // (as warp 4 does)
+                    prefetch(&maps.all, kWide * (lane >> 3), (slot + kTile) & ((1 << p.c.page_shift) - 1), next);
             }
         }
         if (!ok) {  // wait (bounded) until the copies already issued have landed
@@ -509,23 +548,27 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         Turn<kUnits> us, uv;  // of the scores and of the outputs
         Turn<S::kRopes> ro;
         while (ok && take(parts, n_part, w, ok)) {
-            const int nt = __shfl_sync(~0u, w.last - w.first, 0);
+            const Tiles<kTile> tl(w);
+            const int nt = __shfl_sync(~0u, tl.last - tl.first, 0);
             ok = warp_wait(&bar.qfull, nq++ & 1);
 #pragma unroll 1
             for (int j = 0; j < nt && ok; j++, n++) {
                 // each unit's barrier is tested while the products of the one before are issued (a test takes 100 cycles)
                 uint32_t b = qd, acc = 0;
                 bool there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
-                if (L == kUnits) {  // places and descriptors known here: 50 cycles a product, what it runs, against 77
+                if (L == 8) {  // places known here but for the first: 50 cycles a product, what it runs, against 77
+                    uint64_t *full = &bar.unit_full[us.at];
+                    const uint32_t a = ud + us.at * (kUnit / 16);
 #pragma unroll
-                    for (int u = 0; u < kUnits; u++) {
-                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.unit_full[u], us.ph);
+                    for (int u = 0; u < 8; u++) {
+                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&full[u], us.ph);
                         fence_after();
-                        there = kv::test_bar(su32(u + 1 < kUnits ? &bar.unit_full[u + 1] : &bar.rope_full[ro.at]), u + 1 < kUnits ? us.ph : ro.ph);
+                        there = kv::test_bar(su32(u + 1 < 8 ? &full[u + 1] : &bar.rope_full[ro.at]), u + 1 < 8 ? us.ph : ro.ph);
 #pragma unroll
-                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, ud + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
+                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
                     }
-                    us.ph ^= 1, b = qd + kUnits * (NR * 128 / 16);
+                    us.at += 8, b = qd + 8 * (NR * 128 / 16);
+                    if (us.at == kUnits) us.at = 0, us.ph ^= 1;
                 } else {
 #pragma unroll 1
                     for (int u = 0; u < L && ok; u++, b += NR * 128 / 16) {
@@ -556,7 +599,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     const uint32_t a = vd + uv.at * (kUnit / 16), d = tm + (u >> 1) * NR;
                     acc = j > 0;
 #pragma unroll
-                    for (int k = 0; k < 8; k++, acc = 1)
+                    for (int k = 0; k < kTile / 16; k++, acc = 1)
                         mma_ss<IO>(one, d, a + k * (2048 / 16), pd + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
                     commit(one, &bar.pair_empty[uv.at >> 1]);
                     uv.next(), uv.next();
@@ -571,42 +614,92 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     } else if (warp == kWalkWarp) {
         ok = hand_out(p, parts, walk);
     } else if (Q8 && warp >= 8) {  // --------------------------------------- codes to elements
-        // four warps a unit, every second of them, a thread a slot
-        constexpr int R = S::kRaws + !Q8;
-        const int slot = (tid - 256) & 127, group = (warp - 8) >> 2;
-        uint32_t n = 0;  // units before this tile
-        Turn<S::kScales + !Q8> sc;
-        while (ok && take(parts, n_part, w, ok)) {
-            for (int j = w.first; j < w.last && ok; j++, n += L) {
-                ok = warp_wait(&bar.scale_full[sc.at], sc.ph);
-                for (int u = (group ^ (int)n) & 1; u < L && ok; u += 2) {
-                    const uint32_t un = (n + u) % kUnits, ra = (n + u) % R;
-                    ok = warp_wait(&bar.raw_full[ra], (n + u) / R & 1) && warp_wait(&bar.pair_empty[un >> 1], (n + u) / kUnits & 1 ^ 1);
-                    if (!ok) break;
-                    const uint32_t from = raws + ra * S::kRaw + slot * 64, to = units + un * kUnit + slot * 128;
-                    uint32_t powers;
-                    asm volatile("{\n\t.reg .u16 x;\n\tld.shared.u16 x, [%1];\n\tcvt.u32.u16 %0, x;\n\t}"
-                                 : "=r"(powers)
-                                 : "r"(scales + sc.at * S::kScale + slot * 16 + 2 * u)
-                                 : "memory");
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {  // 16 codes (64-byte swizzle), two pieces of eight elements
-                        uint4 in, lo, hi;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(in.x), "=r"(in.y), "=r"(in.z), "=r"(in.w)
-                                     : "r"(from + ((i ^ (slot >> 1 & 3)) << 4))
-                                     : "memory");
-                        decode16<BF>(in, powers >> (8 * (i >> 1)) & 0xff, lo, hi);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * i) ^ (slot & 7)) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * i + 1) ^ (slot & 7)) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
-                    }
-                    fence_async();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(&bar.unit_full[un]), bar_arrive(&bar.raw_empty[ra]);
-                }
-                if (lane == 0) bar_arrive(&bar.scale_empty[sc.at]);
-                sc.next();
+        // every eighth unit a warp; four lanes have a slot's 64 codes, a warp eight slots at a time. The next unit's codes are loaded while
+        // this one's are turned, and the place of the one after that looked up.
+        const int sub = lane >> 2, q = lane & 3;
+        constexpr int kScales = S::kScales + !Q8;
+        uint32_t n = 0, nt = 0, seen = 0;  // units and tiles before this part, tiles whose powers this warp has done with
+        // every warp takes part in every tile's powers, whether it has a unit of it or not: a wait is never two phases off
+        auto pass = [&](uint32_t upto) {
+            for (; seen < upto && ok; seen++) {
+                ok = warp_wait(&bar.scale_full[seen % kScales], seen / kScales & 1);
+                if (lane == 0) bar_arrive(&bar.scale_empty[seen % kScales]);
             }
+        };
+        while (ok && take(parts, n_part, w, ok)) {
+            const Tiles<kTile> tl(w);
+            const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
+            const uint32_t end = n + (tl.last - tl.first) * L;
+            auto place_of = [&](uint32_t x) -> const unsigned char * {  // of 16 slots of unit x's tile from 16 (lane % 4) on; or NULL
+                const uint32_t t = (x - n) / L;
+                const int slot = (tl.first + (int)t) * kTile + 16 * (lane & 3);
+                const int page = x < end && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                if ((uint32_t)page >= (uint32_t)p.c.num_pages) return nullptr;
+                return cell(p.c, page, slot) + 64 * (x - n - t * L);
+            };
+            const int64_t off = sub * p.c.slot + 16 * q, off8 = off + 8 * p.c.slot;
+            auto load = [&](const unsigned char *place, uint4 (&in)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const unsigned char *at = reinterpret_cast<const unsigned char *>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(place), i >> 1));
+#pragma unroll
+                    for (int k = 0; k < 2; k++)
+                        asm volatile(
+                            "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                            "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                            : "=&r"(in[i + k].x), "=&r"(in[i + k].y), "=&r"(in[i + k].z), "=&r"(in[i + k].w)
+                            : "l"(at + (k ? off8 : off)), "l"(at));
+                }
+            };
+            auto turn = [&](uint32_t x, const uint4 (&in)[8]) {
+                const uint32_t t = (x - n) / L, u = x - n - t * L, un = x % kUnits, sc = (nt + t) % kScales;
+                pass(nt + t);
+                ok = ok && warp_wait(&bar.scale_full[sc], (nt + t) / kScales & 1);
+                if (!ok) return;
+                const uint32_t from = scales + sc * S::kScale + sub * 16 + 2 * u + (q >> 1), to = units + un * kUnit + sub * 128;
+                uint32_t byte[8];
+                bool plain = true;
+#pragma unroll
+                for (int i = 0; i < 8; i++)
+                    asm volatile("{\n\t.reg .u8 x;\n\tld.shared.u8 x, [%1];\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(byte[i]) : "r"(from + 128 * i) : "memory");
+#pragma unroll
+                for (int i = 0; i < 8; i++) plain = plain && plain_power<BF>(byte[i]);
+                plain = __all_sync(~0u, plain);
+                ok = warp_wait(&bar.pair_empty[un >> 1], x / kUnits & 1 ^ 1);
+                if (!ok) return;
+                auto put = [&](int i, const uint4 &lo, const uint4 &hi) {
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 1024 * i + (((2 * q) ^ sub) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 1024 * i + (((2 * q + 1) ^ sub) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                                 : "memory");
+                };
+                uint4 lo, hi;
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) decode16_plain<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) decode16<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.unit_full[un]), bar_arrive(&bar.scale_empty[sc]);
+                seen++;
+            };
+            uint32_t x = n + ((warp - 8 - n) & 7);
+            uint4 a[8], b[8];
+            load(place_of(x), a);
+            const unsigned char *next = place_of(x + 8);
+            for (; x < end && ok; x += 16) {
+                load(next, b);
+                next = place_of(x + 16);
+                turn(x, a);
+                if (x + 8 >= end || !ok) break;
+                load(next, a);
+                next = place_of(x + 24);
+                turn(x + 8, b);
+            }
+            n = end, nt += tl.last - tl.first;
+            pass(nt);
         }
     }
     if (!ok && lane == 0) kv::flag(p.c.status, FTMOE_ERR_STATE);
@@ -683,18 +776,17 @@ template <bool BF, bool Q8, int NR>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     using S = Shape<Q8, NR>;
     const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
-    const int box = p.c.page_shift < 7 ? 1 << p.c.page_shift : kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
+    const int box = 1 << p.c.page_shift < S::kTile ? 1 << p.c.page_shift : S::kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
     Maps m;
-    bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, 128) &&
-              kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, 128) &&
-              kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 128);
+    bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, true) &&
+              kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, true) &&
+              kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     const int row = rope_at(p.c.latent, p.c.bits) / 2 + p.c.rope;
-    ok = ok && kv::box_map(m.all, e, p.c.pages, {row, slots, p.c.num_pages}, p.c.slot, p.c.page, {kWide, box, 1}, 0);
+    ok = ok && kv::box_map(m.all, e, p.c.pages, {row, slots, p.c.num_pages}, p.c.slot, p.c.page, {kWide, box, 1}, false);
     if (Q8)
-        ok = ok && kv::box_map(m.lat, kv::Elem::U8, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 64) &&
-             kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, 0);
+        ok = ok && kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, false);
     else
-        ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, 128);
+        ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<absorb_kernel<BF, Q8, NR>>(S::kSmem);
     if (rc != cudaSuccess) return rc;

@@ -112,7 +112,11 @@ __global__ void __launch_bounds__(kThreads, 1) expand_kernel(const __grid_consta
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     Walk<ExpandParams> walk;
-    const bool any = plan<kWarps>(p, walk, s_warp, reinterpret_cast<long long *>(sm_raw + (stage_out - su32(sm_raw))), &s_walk, p.status);
+    bool any = true;
+    if (!plans_alone(p.line))
+        any = plan<kWarps>(p, walk, s_warp, reinterpret_cast<long long *>(sm_raw + (stage_out - su32(sm_raw))), &s_walk, p.status);
+    else if (warp == kWalkWarp)
+        plan_alone(p, walk, p.status);
     asm volatile("griddepcontrol.launch_dependents;" :::);
     fence_before();
     __syncthreads();
@@ -502,10 +506,10 @@ cudaError_t launch(const ExpandParams &p, int C, cudaStream_t st) {
     Maps m;
     const bool keys = p.rows > 0;  // (without one, no chunk's rows are ever seen)
     const void *some = p.q.d;
-    if (!kv::box_map(m.q, e, p.q.d, {p.nope + p.rope, p.heads, p.tokens}, 2 * p.q.head, 2 * p.q.token, {64, 1, 128}, 128) ||
-        !kv::box_map(m.k, e, keys ? p.k.d : some, {p.nope, p.heads, keys ? p.rows : 1}, keys ? 2 * p.k.head : 16, keys ? 2 * p.k.token : 16, {64, 1, 128}, 128) ||
-        !kv::box_map(m.v, e, keys ? p.v.d : some, {p.vdim, p.heads, keys ? p.rows : 1}, keys ? 2 * p.v.head : 16, keys ? 2 * p.v.token : 16, {64, 1, 128}, 128) ||
-        !kv::box_map(m.key, e, keys ? p.key : some, {p.rope, keys ? p.rows : 1, 1}, keys ? 2 * p.key_stride : 16, keys ? 2 * p.key_stride : 16, {64, 128, 1}, 128))
+    if (!kv::box_map(m.q, e, p.q.d, {p.nope + p.rope, p.heads, p.tokens}, 2 * p.q.head, 2 * p.q.token, {64, 1, 128}, true) ||
+        !kv::box_map(m.k, e, keys ? p.k.d : some, {p.nope, p.heads, keys ? p.rows : 1}, keys ? 2 * p.k.head : 16, keys ? 2 * p.k.token : 16, {64, 1, 128}, true) ||
+        !kv::box_map(m.v, e, keys ? p.v.d : some, {p.vdim, p.heads, keys ? p.rows : 1}, keys ? 2 * p.v.head : 16, keys ? 2 * p.v.token : 16, {64, 1, 128}, true) ||
+        !kv::box_map(m.key, e, keys ? p.key : some, {p.rope, keys ? p.rows : 1, 1}, keys ? 2 * p.key_stride : 16, keys ? 2 * p.key_stride : 16, {64, 128, 1}, true))
         return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<expand_kernel<BF, D>>(S::kSmem);
     if (rc != cudaSuccess) return rc;

@@ -89,6 +89,57 @@ __device__ __forceinline__ Where where(const Line &l) {
     return Where{at, of, l.pair ? (int)(blockIdx.x & 1) * of + at : at};
 }
 
+// Calls whose walk one warp finds by itself, while the others set up: a CTA an item (no line to walk), or few sequences of one
+// item each at most. A start of 2 us less than plan's, whose loads, barriers and scans all warps wait for.
+__device__ __forceinline__ bool plans_alone(const Line &l) { return !l.join || (l.max_q <= l.item_tokens && l.batch <= 256); }
+
+template <class P>
+__device__ __forceinline__ void plan_alone(const P &p, Walk<P> &w, int32_t *status) {
+    const Line &l = p.line;
+    const Where me = where(l);
+    const int lane = threadIdx.x & 31;
+    if (!l.join) {
+        const int most = (l.max_q + l.item_tokens - 1) / l.item_tokens, block = me.at / most;
+        w.qt = me.at - block * most, w.b = block / l.blocks, w.block = block - w.b * l.blocks;
+        w.sq = p.seq(w.b, w.qt == 0 && w.block == 0 && lane == 0 ? status : nullptr);
+        w.n_qt = item_count(l, w.sq), w.at = 0, w.left = w.qt < w.n_qt;
+        return;
+    }
+    auto units = [&](const kv::Seq &x) { return x.q_len > 0 ? item_steps(item_hi(l, x, 0)) + kItemCost : 0; };  // of a block
+    long long W = 0;
+    for (int b = lane; b < l.batch; b += 32) W += units(p.seq(b, me.at == 0 ? status : nullptr));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(~0u, W, o);
+    W *= l.blocks;
+    const int C = kv::used_ctas(me.of, W);
+    w.left = 0, w.n_qt = 1, w.qt = 0;
+    if (me.at >= C) return;
+    const long long u0 = kv::unit_start(me.at, C, W), u1 = kv::unit_start(me.at + 1, C, W);
+    long long before = 0;  // units of the sequences before this round's
+    for (int b0 = 0; b0 < l.batch; b0 += 32) {
+        const kv::Seq s = b0 + lane < l.batch ? p.seq(b0 + lane, nullptr) : kv::Seq{0, 0, 0};
+        const int per = units(s);
+        long long x = (long long)per * l.blocks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(~0u, x, o);
+            if (lane >= o) x += y;
+        }
+        const unsigned past = __ballot_sync(~0u, u0 < before + x);
+        if (past) {
+            const int owner = __ffs(past) - 1;
+            long long rest = u0 - (before + x - (long long)per * l.blocks);
+            int block = 0;
+            if (l.blocks > 1 && lane == owner) block = (int)(rest / per), rest -= (long long)block * per;
+            w.b = b0 + owner, w.block = __shfl_sync(~0u, block, owner), w.at = __shfl_sync(~0u, (int)rest, owner);
+            w.sq.q0 = __shfl_sync(~0u, s.q0, owner), w.sq.q_len = __shfl_sync(~0u, s.q_len, owner), w.sq.kv_len = __shfl_sync(~0u, s.kv_len, owner);
+            w.left = u1 - u0;
+            return;
+        }
+        before += __shfl_sync(~0u, x, 31);
+    }
+}
+
 // Total units and this CTA's start, for kWarps warps. s_sum: 32 kWarps entries, s_warp: kWarps.
 template <int kWarps, class P>
 __device__ __noinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, long long *s_sum, Walk<P> *s_walk, int32_t *status) {
@@ -96,56 +147,6 @@ __device__ __noinline__ bool plan(const P &p, Walk<P> &w, long long *s_warp, lon
     const Line &l = p.line;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const Where me = where(l);
-    if (!l.join) {  // a CTA an item that there can be, and no line to walk
-        const int most = (l.max_q + l.item_tokens - 1) / l.item_tokens, block = me.at / most;
-        w.qt = me.at - block * most, w.b = block / l.blocks, w.block = block - w.b * l.blocks;
-        w.sq = p.seq(w.b, w.qt == 0 && w.block == 0 && tid == 0 ? status : nullptr);
-        w.n_qt = item_count(l, w.sq), w.at = 0, w.left = 1;
-        return w.qt < w.n_qt;
-    }
-    if (l.max_q <= l.item_tokens && l.batch <= 128) {
-        // one item a sequence at most, and few sequences: every warp for itself, four to a lane, without a barrier
-        long long n[4], mine = 0, before = 0;
-        kv::Seq s[4];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const int b = 4 * lane + k;
-            s[k] = b < l.batch ? p.seq(b, me.at == 0 && warp == 0 ? status : nullptr) : kv::Seq{0, 0, 0};
-            n[k] = s[k].q_len > 0 ? (long long)(item_steps(item_hi(l, s[k], 0)) + kItemCost) * l.blocks : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 4; k++) mine += n[k];
-        long long x = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(~0u, x, o);
-            if (lane >= o) x += y;
-        }
-        const long long W = __shfl_sync(~0u, x, 31);
-        const int C = kv::used_ctas(me.of, W);
-        if (me.at >= C) return false;
-        const long long u0 = kv::unit_start(me.at, C, W), u1 = kv::unit_start(me.at + 1, C, W);
-        before = x - mine;
-        int hit = -1;
-        long long from = 0;
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            if (u0 >= before && u0 < before + n[k]) hit = k, from = u0 - before;
-            before += n[k];
-        }
-        const int owner = __ffs(__ballot_sync(~0u, hit >= 0)) - 1;
-        hit = __shfl_sync(~0u, hit, owner), from = __shfl_sync(~0u, from, owner);
-        kv::Seq sq = s[0];
-        long long per = n[0];
-#pragma unroll
-        for (int k = 1; k < 4; k++)
-            if (hit == k) sq = s[k], per = n[k];
-        sq.q0 = __shfl_sync(~0u, sq.q0, owner), sq.q_len = __shfl_sync(~0u, sq.q_len, owner), sq.kv_len = __shfl_sync(~0u, sq.kv_len, owner);
-        per = __shfl_sync(~0u, per, owner);
-        const long long block = l.blocks == 1 ? 0 : from / (per / l.blocks);
-        w.b = 4 * owner + hit, w.block = (int)block, w.qt = 0, w.n_qt = 1, w.at = (int)(from - block * (per / l.blocks)), w.sq = sq, w.left = u1 - u0;
-        return true;
-    }
     // one item a sequence at most: a thread a sequence, which then knows its start without reading it again
     const bool single = l.max_q <= l.item_tokens;
     kv::Seq mine{};

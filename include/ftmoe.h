@@ -580,7 +580,8 @@ int ftmoe_w4_matvec(const void *d_packed, int32_t N, int32_t K, int32_t group, i
  * page sits at page * page_stride + row * slot_stride bytes. A slot holds
  *   bits 16: latent elements, then rope elements, of `dtype`;
  *   bits 8:  latent e4m3 codes; a byte e + 127 for each 32 of them (the value of a code is
- *            code * 2^e, rounded to dtype; byte 255: 32 NaNs), padded to 16 bytes; then rope elements of `dtype`.
+ *            code * 2^e, rounded to dtype; byte 255: 32 NaNs; the codes 0x7f and 0xff are
+ *            not written, and not specified), padded to 16 bytes; then rope elements of `dtype`.
  * Base 16-byte aligned, strides positive multiples of 16.
  *   dtype   FTMOE_DT_BF16 or FTMOE_DT_F16 (queries, new rows and outputs have it too);
  *   latent  a multiple of 128, at most 512; rope: a multiple of 16 from 16 to 64;
