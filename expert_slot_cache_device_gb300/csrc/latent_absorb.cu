@@ -1,13 +1,13 @@
 // Absorbed latent attention on the 5th-generation tensor cores. All heads read the same cached vectors, so the rows of an
-// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots (64 of an 8-bit cache). Both products have the cache as their A
+// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots. Both products have the cache as their A
 // operand, straight from shared memory in the one layout that the copies leave it in:
-//   S^T [slots, NR rows]     = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
+//   S^T [128 slots, NR rows] = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
 //   O^T [latent, NR rows]  += C^T P^T                    A: latents are M = 128, slots K (M-major)
 // so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most; rows as M would take all of it), and few
 // rows cost few columns instead of an unused part of M = 128. P^T goes to shared memory as the B operand.
 //
 // Persistent, one CTA an SM, work cut by latent_line.cuh. Roles:
-//   warps 0-3   softmax of a tile: a warp has a quarter of the slots, a thread four (two) slots' values of every eighth pair of rows.
+//   warps 0-3   softmax of a tile: warp w has slots 32 w .. 32 w + 31, a thread four slots' values of every eighth pair of rows.
 //               P = 2^(s scale log2 e - m) in fp32 with the maximum m of the tiles before; one vote of the four warps tells whether a
 //               P is above 2^8, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to
 //               the cache's type, as the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at
@@ -18,7 +18,7 @@
 //               the compiler knows its branches to be uniform and keeps descriptors in uniform registers (without: 70 cycles a product).
 //   warp 6      walks the work and hands the parts out.
 //   warp 7      tensor copies of queries, rotary parts and powers of two.
-//   warps 8-15  (8 bits, instead of warp 4) load codes, a warp a unit, and turn them into units of elements. Codes stay in registers on
+//   warps 8-15  (8 bits, instead of warp 4) load codes, a pair of units at a time, and turn them into elements. Codes stay in registers on
 //               their way: shared memory has no place for more than a quarter of a tile's, which let too few be under way.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 #include "latent_line.cuh"
@@ -45,6 +45,9 @@ using kv::unpack2;
 using kv::wait_bar;
 
 constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8;
+constexpr int kTile = kStep;
+constexpr int kUnit = kTile * 128;  // 64 latents of a tile's slots
+constexpr int kUnits = 8;           // places for them; two are an operand of the second product
 constexpr float kMost = 256.f;   // P that is let through without raising m
 constexpr float kLeast = 5.9604645e-8f;  // 2^-24
 
@@ -52,11 +55,6 @@ template <bool Q8, int NR>
 struct Shape {
     static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
     static constexpr int kRopes = NR == 64 ? 1 : 2, kScales = Q8 ? 2 : 0;
-    // Slots of a tile: 128 read least from shared memory; of codes 64, as only two tiles of elements let one be filled while the other is
-    // worked on.
-    static constexpr int kTile = Q8 ? 64 : 128, kHalves = kTile / 64;
-    static constexpr int kUnit = kTile * 128;       // 64 latents of a tile's slots
-    static constexpr int kUnits = Q8 ? 16 : 8;      // places for them; two are an operand of the second product
     static constexpr int kScale = kTile * 16;
     static constexpr int kQ = 9 * NR * 128;
     // P lies over the rotary part, which S has read by then, where shared memory would not hold both
@@ -72,7 +70,7 @@ struct Maps {
 };
 
 struct Bars {
-    uint64_t unit_full[16], pair_empty[8], rope_full[kMaxRopes], rope_empty[kMaxRopes];
+    uint64_t unit_full[kUnits], pair_empty[kUnits / 2], rope_full[kMaxRopes], rope_empty[kMaxRopes];
     uint64_t scale_full[kMaxScales], scale_empty[kMaxScales];
     uint64_t qfull, qempty, s, p, o, done;
 };
@@ -139,21 +137,9 @@ __device__ __forceinline__ void prefetch(const CUtensorMap *map, int x, int y, i
 }
 constexpr int kWide = 192;  // 16-bit elements of a slot that one prefetch has
 
-// Tiles of a part.
-template <int kTile>
-struct Tiles {
-    int first, last;
-    __device__ __forceinline__ explicit Tiles(const Part &w) {
-        first = w.first * (kStep / kTile), last = w.last * (kStep / kTile);
-        const int end = (w.hi + kTile - 1) / kTile;
-        if (last > end) last = end > first ? end : first + 1;
-    }
-};
-
 template <bool BF, bool Q8, int NR>
 __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ Maps maps) {
     using S = Shape<Q8, NR>;
-    constexpr int kTile = S::kTile, kUnit = S::kUnit, kUnits = S::kUnits;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
     __shared__ PartRing parts;
@@ -169,7 +155,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     const int pair = p.line.pair, rank = pair & blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], 1);
+        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvWarps : 1);
         for (int i = 0; i < kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
         for (int i = 0; i < S::kRopes; i++) bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
         for (int i = 0; i < S::kScales; i++) bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
@@ -216,11 +202,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     if (warp < 4) {  // ---------------------------------------------------- softmax
         const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
         const float c2 = p.scale * kv::kLog2e;
-        const int row0 = kTile / 4 * warp + (lane >> 2), col0 = 2 * (lane & 3);
+        const int row0 = 32 * warp + (lane >> 2), col0 = 2 * (lane & 3);
         constexpr int NB = NR / 8;
         uint32_t ns = 0, no = 0;
         while (!vote(!take(parts, n_part, w, ok))) {
-            const Tiles<kTile> tl(w);
             const int block = (w.block << pair) + rank;
             const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
             auto limit = [&](int c) {                       // slots that row c sees
@@ -234,18 +219,17 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             uint64_t l[NB];
 #pragma unroll
             for (int i = 0; i < NB; i++) z[2 * i] = z[2 * i + 1] = 0.f, l[i] = 0;
-            for (int j = tl.first; j < tl.last; j++, ns++) {
+            for (int j = w.first; j < w.last; j++, ns++) {
                 const int s0 = j * kTile;
                 ok = ok && warp_wait(&bar.s, ns & 1);
                 fence_after();
-                constexpr int X = S::kHalves * NR / 2;
-                uint32_t x[X];  // slots of the warp's first 16 lanes, then of the others
+                uint32_t x[NR];  // slots of the warp's first 16 lanes, then of the others
                 auto scores = [&] {
                     load_s<NR>(lanes + S::kS, x);
-                    if (S::kHalves == 2) load_s<NR>(lanes + (16u << 16) + S::kS, x + X - NR / 2);
+                    load_s<NR>(lanes + (16u << 16) + S::kS, x + NR / 2);
                     if (s0 + kTile <= least) return;
 #pragma unroll
-                    for (int k = 0; k < 2 * S::kHalves; k++)
+                    for (int k = 0; k < 4; k++)
 #pragma unroll
                         for (int i = 0; i < NB; i++)
 #pragma unroll
@@ -256,7 +240,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 auto form = [&] {
                     float top = 0.f;
 #pragma unroll
-                    for (int k = 0; k < X; k += 2) {
+                    for (int k = 0; k < NR; k += 2) {
                         const int i = (k % (NR / 2)) >> 2;
                         const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
                         const float a = ex2(f.x), b = ex2(f.y);
@@ -266,14 +250,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     return top > kMost;
                 };
                 scores();
-                const bool fresh = j == tl.first;
+                const bool fresh = j == w.first;
                 bool raise = form() || !ok || (fresh && !BF);
                 if (fresh) {
 #pragma unroll
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
-                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
+                        t = kv::max3(t, __uint_as_float(x[NR / 2 + r]), __uint_as_float(x[NR / 2 + r + 2]));
                         raise = raise || t < kLeast;
                     }
                 }
@@ -285,7 +269,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
-                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
+                        t = kv::max3(t, __uint_as_float(x[NR / 2 + r]), __uint_as_float(x[NR / 2 + r + 2]));
                         t *= c2;
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
@@ -323,7 +307,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     form();
                 }
 #pragma unroll
-                for (int h = 0; h < S::kHalves; h++)
+                for (int h = 0; h < 2; h++)
 #pragma unroll
                     for (int i = 0; i < NB; i += 2) {
                         uint32_t y[4];
@@ -336,7 +320,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         }
                         // transposed: a row's slots consecutive, 64 in 128 bytes, 16-byte piece c of row r at c ^ (r % 8)
                         const int r = lane & 7, k = lane >> 3;
-                        const int piece = 2 * S::kHalves * warp + 2 * h + (k & 1);
+                        const int piece = 4 * warp + 2 * h + (k & 1);
                         const uint32_t at = ps + (piece >> 3) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((piece & 7) ^ r) << 4);
                         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
                                      "r"(y[3])
@@ -442,9 +426,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 const int slot = j * kTile + blk * box;
                 return mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            const Tiles<kTile> tl(w);
-            int next = page_at(tl.first);
-            for (int j = tl.first; j < tl.last && ok; j++, n += L, sent = 0) {
+            int next = page_at(w.first);
+            for (int j = w.first; j < w.last && ok; j++, n += L, sent = 0) {
                 const int page = (uint32_t)next < (uint32_t)p.c.num_pages ? next : -1;  // (warp 7 records bad ones)
                 next = page_at(j + 1);  // on its way while this tile waits for its places
                 const int row = (j * kTile + blk * box) & ((1 << p.c.page_shift) - 1);
@@ -495,8 +478,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 const int slot = j * kTile + blk * box;
                 return blk < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            const Tiles<kTile> tl(w);
-            int next = page_at(tl.first);
+            int next = page_at(w.first);
             if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
                 ok = false;
                 break;
@@ -506,7 +488,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             __syncwarp();
             if (lane <= L)
                 tma3(qs + lane * NR * 128, lane < L ? &maps.q : &maps.q_rope, lane < L ? 64 * lane : 0, ((w.block << pair) + rank) * p.heads, w.token, &bar.qfull);
-            for (int j = tl.first; j < tl.last && ok; j++) {
+            for (int j = w.first; j < w.last && ok; j++) {
                 const int slot = j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
                 int page = next;
                 next = page_at(j + 1);
@@ -548,27 +530,23 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         Turn<kUnits> us, uv;  // of the scores and of the outputs
         Turn<S::kRopes> ro;
         while (ok && take(parts, n_part, w, ok)) {
-            const Tiles<kTile> tl(w);
-            const int nt = __shfl_sync(~0u, tl.last - tl.first, 0);
+            const int nt = __shfl_sync(~0u, w.last - w.first, 0);
             ok = warp_wait(&bar.qfull, nq++ & 1);
 #pragma unroll 1
             for (int j = 0; j < nt && ok; j++, n++) {
                 // each unit's barrier is tested while the products of the one before are issued (a test takes 100 cycles)
                 uint32_t b = qd, acc = 0;
                 bool there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
-                if (L == 8) {  // places known here but for the first: 50 cycles a product, what it runs, against 77
-                    uint64_t *full = &bar.unit_full[us.at];
-                    const uint32_t a = ud + us.at * (kUnit / 16);
+                if (L == kUnits) {  // places and descriptors known here: 50 cycles a product, what it runs, against 77
 #pragma unroll
-                    for (int u = 0; u < 8; u++) {
-                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&full[u], us.ph);
+                    for (int u = 0; u < kUnits; u++) {
+                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.unit_full[u], us.ph);
                         fence_after();
-                        there = kv::test_bar(su32(u + 1 < 8 ? &full[u + 1] : &bar.rope_full[ro.at]), u + 1 < 8 ? us.ph : ro.ph);
+                        there = kv::test_bar(su32(u + 1 < kUnits ? &bar.unit_full[u + 1] : &bar.rope_full[ro.at]), u + 1 < kUnits ? us.ph : ro.ph);
 #pragma unroll
-                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
+                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, ud + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
                     }
-                    us.at += 8, b = qd + 8 * (NR * 128 / 16);
-                    if (us.at == kUnits) us.at = 0, us.ph ^= 1;
+                    us.ph ^= 1, b = qd + kUnits * (NR * 128 / 16);
                 } else {
 #pragma unroll 1
                     for (int u = 0; u < L && ok; u++, b += NR * 128 / 16) {
@@ -614,92 +592,86 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     } else if (warp == kWalkWarp) {
         ok = hand_out(p, parts, walk);
     } else if (Q8 && warp >= 8) {  // --------------------------------------- codes to elements
-        // every eighth unit a warp; four lanes have a slot's 64 codes, a warp eight slots at a time. The next unit's codes are loaded while
-        // this one's are turned, and the place of the one after that looked up.
-        const int sub = lane >> 2, q = lane & 3;
-        constexpr int kScales = S::kScales + !Q8;
-        uint32_t n = 0, nt = 0, seen = 0;  // units and tiles before this part, tiles whose powers this warp has done with
-        // every warp takes part in every tile's powers, whether it has a unit of it or not: a wait is never two phases off
-        auto pass = [&](uint32_t upto) {
-            for (; seen < upto && ok; seen++) {
-                ok = warp_wait(&bar.scale_full[seen % kScales], seen / kScales & 1);
-                if (lane == 0) bar_arrive(&bar.scale_empty[seen % kScales]);
+        // All of them take one pair of units after another, 16 slots each, so that the first is there soonest; four lanes have a slot's 64 codes
+        // of a unit. The next tile's codes are loaded pair by pair as this one's are turned (48 KB and more under way: with the next pair's
+        // alone, 16 KB, the loads' latency was the time); a tile's pages are looked up a tile before that.
+        const int sub = lane >> 2, q = lane & 3, slot0 = 16 * (warp & 7), LP = L >> 1;
+        const int64_t off = sub * p.c.slot + 16 * q, off8 = off + 8 * p.c.slot;
+        const uint32_t at0 = units + (slot0 + sub) * 128 + (((2 * q) ^ sub) << 4), at1 = units + (slot0 + sub) * 128 + (((2 * q + 1) ^ sub) << 4);
+        const uint32_t from0 = scales + (slot0 + sub) * 16 + (q >> 1);
+        Turn<S::kScales + !Q8> sc;
+        Turn<kUnits / 2> pl;
+        auto load = [&](const unsigned char *at, uint4 (&in)[4]) {  // (unit of the pair, eight slots)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                uint4 &v = in[i];
+                asm volatile(
+                    "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+                    "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                    : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+                    : "l"(at + (i & 1 ? off8 : off) + 64 * (i >> 1)), "l"(at));
             }
         };
-        while (ok && take(parts, n_part, w, ok)) {
-            const Tiles<kTile> tl(w);
-            const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
-            const uint32_t end = n + (tl.last - tl.first) * L;
-            auto place_of = [&](uint32_t x) -> const unsigned char * {  // of 16 slots of unit x's tile from 16 (lane % 4) on; or NULL
-                const uint32_t t = (x - n) / L;
-                const int slot = (tl.first + (int)t) * kTile + 16 * (lane & 3);
-                const int page = x < end && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
-                if ((uint32_t)page >= (uint32_t)p.c.num_pages) return nullptr;
-                return cell(p.c, page, slot) + 64 * (x - n - t * L);
+        auto turn = [&](int m, const uint4 (&in)[4]) {
+            const bool free = kv::test_bar(su32(&bar.pair_empty[pl.at]), pl.ph ^ 1);
+            uint32_t byte[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                asm volatile("{\n\t.reg .u8 x;\n\tld.shared.u8 x, [%1];\n\tcvt.u32.u8 %0, x;\n\t}"
+                             : "=r"(byte[i])
+                             : "r"(from0 + sc.at * S::kScale + 4 * m + 2 * (i >> 1) + 128 * (i & 1))
+                             : "memory");
+            if (!__all_sync(~0u, free)) ok = ok && warp_wait(&bar.pair_empty[pl.at], pl.ph ^ 1);
+            if (!ok) return;
+            bool plain = true;
+#pragma unroll
+            for (int i = 0; i < 4; i++) plain = plain && plain_power<BF>(byte[i]);
+            auto put = [&](int i, const uint4 &lo, const uint4 &hi) {
+                const uint32_t o = pl.at * (2 * kUnit) + (i >> 1) * kUnit + 1024 * (i & 1);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at0 + o), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at1 + o), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
             };
-            const int64_t off = sub * p.c.slot + 16 * q, off8 = off + 8 * p.c.slot;
-            auto load = [&](const unsigned char *place, uint4 (&in)[8]) {
+            uint4 lo, hi;
+            if (__all_sync(~0u, plain)) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const unsigned char *at = reinterpret_cast<const unsigned char *>(__shfl_sync(~0u, reinterpret_cast<unsigned long long>(place), i >> 1));
+                for (int i = 0; i < 4; i++) decode16_plain<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 2; k++)
-                        asm volatile(
-                            "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-                            "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-                            : "=&r"(in[i + k].x), "=&r"(in[i + k].y), "=&r"(in[i + k].z), "=&r"(in[i + k].w)
-                            : "l"(at + (k ? off8 : off)), "l"(at));
-                }
-            };
-            auto turn = [&](uint32_t x, const uint4 (&in)[8]) {
-                const uint32_t t = (x - n) / L, u = x - n - t * L, un = x % kUnits, sc = (nt + t) % kScales;
-                pass(nt + t);
-                ok = ok && warp_wait(&bar.scale_full[sc], (nt + t) / kScales & 1);
-                if (!ok) return;
-                const uint32_t from = scales + sc * S::kScale + sub * 16 + 2 * u + (q >> 1), to = units + un * kUnit + sub * 128;
-                uint32_t byte[8];
-                bool plain = true;
-#pragma unroll
-                for (int i = 0; i < 8; i++)
-                    asm volatile("{\n\t.reg .u8 x;\n\tld.shared.u8 x, [%1];\n\tcvt.u32.u8 %0, x;\n\t}" : "=r"(byte[i]) : "r"(from + 128 * i) : "memory");
-#pragma unroll
-                for (int i = 0; i < 8; i++) plain = plain && plain_power<BF>(byte[i]);
-                plain = __all_sync(~0u, plain);
-                ok = warp_wait(&bar.pair_empty[un >> 1], x / kUnits & 1 ^ 1);
-                if (!ok) return;
-                auto put = [&](int i, const uint4 &lo, const uint4 &hi) {
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 1024 * i + (((2 * q) ^ sub) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 1024 * i + (((2 * q + 1) ^ sub) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
-                                 : "memory");
-                };
-                uint4 lo, hi;
-                if (plain) {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) decode16_plain<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; i++) decode16<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&bar.unit_full[un]), bar_arrive(&bar.scale_empty[sc]);
-                seen++;
-            };
-            uint32_t x = n + ((warp - 8 - n) & 7);
-            uint4 a[8], b[8];
-            load(place_of(x), a);
-            const unsigned char *next = place_of(x + 8);
-            for (; x < end && ok; x += 16) {
-                load(next, b);
-                next = place_of(x + 16);
-                turn(x, a);
-                if (x + 8 >= end || !ok) break;
-                load(next, a);
-                next = place_of(x + 24);
-                turn(x + 8, b);
+                for (int i = 0; i < 4; i++) decode16<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
             }
-            n = end, nt += tl.last - tl.first;
-            pass(nt);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&bar.unit_full[2 * pl.at]), bar_arrive(&bar.unit_full[2 * pl.at + 1]);
+            pl.next();
+        };
+        while (ok && take(parts, n_part, w, ok)) {
+            const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
+            auto page_at = [&](int j) {
+                const int slot = j * kTile + slot0;
+                return j < w.last && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+            };
+            auto place = [&](int j, int page) -> const unsigned char * {
+                return (uint32_t)page < (uint32_t)p.c.num_pages ? cell(p.c, page, j * kTile + slot0) : nullptr;
+            };
+            const unsigned char *here = place(w.first, page_at(w.first));
+            int next = page_at(w.first + 1);
+            uint4 in[4][4];
+#pragma unroll
+            for (int m = 0; m < 4; m++)
+                if (m < LP) load(here ? here + 128 * m : nullptr, in[m]);
+            for (int j = w.first; j < w.last && ok; j++) {
+                const unsigned char *then = place(j + 1, next);
+                next = page_at(j + 2);
+                ok = warp_wait(&bar.scale_full[sc.at], sc.ph);
+#pragma unroll
+                for (int m = 0; m < 4; m++)
+                    if (m < LP && ok) {
+                        turn(m, in[m]);
+                        load(then ? then + 128 * m : nullptr, in[m]);
+                    }
+                if (lane == 0) bar_arrive(&bar.scale_empty[sc.at]);
+                sc.next();
+            }
         }
     }
     if (!ok && lane == 0) kv::flag(p.c.status, FTMOE_ERR_STATE);
@@ -776,7 +748,7 @@ template <bool BF, bool Q8, int NR>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     using S = Shape<Q8, NR>;
     const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
-    const int box = 1 << p.c.page_shift < S::kTile ? 1 << p.c.page_shift : S::kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
+    const int box = 1 << p.c.page_shift < kTile ? 1 << p.c.page_shift : kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
     Maps m;
     bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, true) &&
               kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, true) &&
