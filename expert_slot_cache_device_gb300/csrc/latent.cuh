@@ -73,8 +73,7 @@ __device__ __forceinline__ void decode16_plain(const uint4 u, uint32_t byte, uin
     lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
 }
 template <bool BF>
-__device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
-    if (plain_power<BF>(byte)) return decode16_plain<BF>(u, byte, lo, hi);
+__device__ __forceinline__ void decode16_floats(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
     uint32_t out[8];
     const float s = power(byte);
@@ -84,6 +83,13 @@ __device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo
         out[2 * i] = kv::from_f2<BF>(a.x * s, a.y * s), out[2 * i + 1] = kv::from_f2<BF>(b.x * s, b.y * s);
     }
     lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
+}
+template <bool BF>
+__device__ __forceinline__ void decode16(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
+    if (plain_power<BF>(byte))
+        decode16_plain<BF>(u, byte, lo, hi);
+    else
+        decode16_floats<BF>(u, byte, lo, hi);
 }
 
 // ---------------------------------------------------------------- launches

@@ -131,6 +131,11 @@ __device__ __forceinline__ float ld_f(uint32_t a) {
 }
 __device__ __forceinline__ void st_f(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 
+// Out of line: rare, and copies of it between the plain ones' cost instruction fetches.
+template <bool BF>
+__device__ __noinline__ void decode16_far(const uint4 u, uint32_t byte, uint4 &lo, uint4 &hi) {
+    decode16_floats<BF>(u, byte, lo, hi);
+}
 __device__ __forceinline__ void prefetch(const CUtensorMap *map, int x, int y, int z) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z)
                  : "memory");
@@ -637,7 +642,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 for (int i = 0; i < 4; i++) decode16_plain<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; i++) decode16<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
+                for (int i = 0; i < 4; i++) decode16_far<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
             }
             fence_async();
             __syncwarp();
