@@ -407,13 +407,15 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 #pragma unroll 1
                 for (int u = 0; u < L >> 1; u++) {
                     float *to = po + 128 * u;
-#pragma unroll 1
-                    for (int k = 0; k < NR; k += 16) {
-                        uint32_t y[16];
-                        tm_ld16(lanes + u * NR + k, y);
+                    uint32_t y[NR];
+                    if constexpr (NR == 64)
+                        kv::tm_ld64(lanes + u * NR, y), kv::tm_ld_wait(y);
+                    else if constexpr (NR == 32)
+                        kv::tm_ld32(lanes + u * NR, y);
+                    else
+                        tm_ld16(lanes + u * NR, y);
 #pragma unroll
-                        for (int e = 0; e < 16; e++, to += p.c.latent) *to = __uint_as_float(y[e]);
-                    }
+                    for (int e = 0; e < NR; e++, to += p.c.latent) *to = __uint_as_float(y[e]);
                 }
             }
             fence_before();  // O is read before the next part's first P is announced
@@ -686,45 +688,69 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     if (warp == kMmaWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm) : "memory");
 }
 
-// Joins the parts of the item that CTA c of the kernel before started: a warp a row, a lane four latents at a time.
+// Joins the parts of the item that CTA c of the kernel before started: a warp a row, a lane four latents at a time. What the
+// first FIRST parts may have is loaded before it is known how many there are, one trip instead of four: eight where the grid is
+// small and has nothing else to wait for, else the two that an item that is joined has, in few registers (seven parts of one
+// sequence, 16 heads: 13.5 us with the kernel before, two first 15.5; 48 sequences of 128 heads: 97 us, 100 with four first).
 constexpr int kJoinThreads = 256, kJoinRows = 8;
 
-template <bool BF>
-__global__ void __launch_bounds__(kJoinThreads) absorb_combine(const AttendParams p, int rows) {
+template <bool BF, int FIRST>
+__global__ void __launch_bounds__(kJoinThreads, FIRST == 2 ? 4 : 1) absorb_combine(const AttendParams p, int rows) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x, row = blockIdx.y * kJoinRows + warp;
+    const int of = gridDim.x >> p.line.pair, rank = p.line.pair && c >= of ? 1 : 0, end = (rank + 1) * of;  // (Where)
+    const int t = row / p.heads;
+    if (t >= p.line.item_tokens) return;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 join = p.line.join[c];
-    const int of = gridDim.x >> p.line.pair, rank = p.line.pair && c >= of ? 1 : 0;  // (Where)
-    const int t = row / p.heads, h = ((join.y << p.line.pair) + rank) * p.heads + row - t * p.heads;
-    if (t >= p.line.item_tokens || t >= join.x || h >= p.q_heads) return;
-    const int n = kv::count_parts(p.line.join, c, (rank + 1) * of);
+    const int4 mine = c + lane < end ? p.line.join[c + lane] : make_int4(0, 0, 0, kv::kJoinEnd);
     auto slot = [&](int k) { return (int64_t)(2 * (c + k) + (k == 0)) * rows + row; };
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, p.part_ml[slot(k)].x);
+    auto part = [&](int k) { return reinterpret_cast<const float4 *>(p.part_o + slot(k) * p.c.latent) + lane; };
+    const float2 none = make_float2(-INFINITY, 0.f);
+    float2 ml = c + lane < end ? p.part_ml[slot(lane)] : none;
+    float4 v[FIRST][4];
+    auto fetch = [&](int k) {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (128 * i < p.c.latent) v[k][i] = part(k)[32 * i];
+    };
+#pragma unroll
+    for (int k = 0; k < FIRST; k++)
+        if (c + k < end) fetch(k);
+    const int left = __shfl_sync(~0u, mine.x, 0), block = __shfl_sync(~0u, mine.y, 0), token = __shfl_sync(~0u, mine.z, 0);
+    const int h = ((block << p.line.pair) + rank) * p.heads + row - t * p.heads;
+    if (t >= left || h >= p.q_heads) return;
+    const unsigned ends = __ballot_sync(~0u, lane > 0 && mine.w == kv::kJoinEnd);
+    const int n = ends ? __ffs(ends) : kv::count_parts(p.line.join, c, end);
+    if (lane >= n) ml = none;
+    float M = ml.x;
+    for (int k = lane + 32; k < n; k += 32) M = fmaxf(M, p.part_ml[slot(k)].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
     float sum = 0.f;
     float4 x[4] = {};
-    for (int k = 0; k < n; k++) {
-        const float2 ml = p.part_ml[slot(k)];
-        const float a = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-        sum += ml.y * a;
-        const float4 *o = reinterpret_cast<const float4 *>(p.part_o + slot(k) * p.c.latent) + lane;
+    auto add = [&](float2 y, const float4 *o, int step) {
+        const float a = y.x == -INFINITY ? 0.f : ex2(y.x - M);
+        sum += y.y * a;
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             if (128 * i >= p.c.latent) break;
-            const float4 v = o[32 * i];
-            x[i].x += v.x * a, x[i].y += v.y * a, x[i].z += v.z * a, x[i].w += v.w * a;
+            const float4 f = o[step * i];
+            x[i].x += f.x * a, x[i].y += f.y * a, x[i].z += f.z * a, x[i].w += f.w * a;
         }
+    };
+#pragma unroll
+    for (int k = 0; k < FIRST; k++) {
+        const float2 y = make_float2(__shfl_sync(~0u, ml.x, k), __shfl_sync(~0u, ml.y, k));
+        if (k < n) add(y, v[k], 1);
     }
+    for (int k = FIRST; k < n; k++) add(p.part_ml[slot(k)], part(k), 32);
     const float f = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t *out = p.out.d + (int64_t)(join.z + t) * p.out.token + (int64_t)h * p.out.head + 4 * lane;
+    uint16_t *out = p.out.d + (int64_t)(token + t) * p.out.token + (int64_t)h * p.out.head + 4 * lane;
 #pragma unroll
     for (int i = 0; i < 4; i++) {
         if (128 * i >= p.c.latent) break;
         *reinterpret_cast<uint2 *>(out + 128 * i) = make_uint2(from_f2<BF>(x[i].x * f, x[i].y * f), from_f2<BF>(x[i].z * f, x[i].w * f));
     }
-    if (lane == 0 && p.lse) p.lse[(int64_t)(join.z + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
+    if (lane == 0 && p.lse) p.lse[(int64_t)(token + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place. With 8 bits
@@ -769,7 +795,7 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     if (rc != cudaSuccess) return rc;
     absorb_kernel<BF, Q8, NR><<<C, S::kThreads, S::kSmem, st>>>(p, m);
     if ((rc = cudaGetLastError()) != cudaSuccess || !p.line.join) return rc;
-    return kv::launch_after(absorb_combine<BF>, dim3(C, NR / kJoinRows), kJoinThreads, 0, st, p, NR);
+    return kv::launch_after(C * (NR / kJoinRows) <= 304 ? absorb_combine<BF, 8> : absorb_combine<BF, 2>, dim3(C, NR / kJoinRows), kJoinThreads, 0, st, p, NR);
 }
 
 template <bool BF>

@@ -89,9 +89,9 @@ __device__ __forceinline__ Where where(const Line &l) {
     return Where{at, of, l.pair ? (int)(blockIdx.x & 1) * of + at : at};
 }
 
-// Calls whose walk one warp finds by itself, while the others set up: a CTA an item (no line to walk), or few sequences of one
-// item each at most. A start of 2 us less than plan's, whose loads, barriers and scans all warps wait for.
-__device__ __forceinline__ bool plans_alone(const Line &l) { return !l.join || (l.max_q <= l.item_tokens && l.batch <= 256); }
+// Calls whose walk one warp finds by itself, while the others set up: a CTA an item (no line to walk), or few sequences of few
+// items each, which a lane counts for its sequence. A start of 2 us less than plan's, whose loads, barriers and scans all warps wait for.
+__device__ __forceinline__ bool plans_alone(const Line &l) { return !l.join || (l.max_q <= 16 * l.item_tokens && l.batch <= 256); }
 
 template <class P>
 __device__ __forceinline__ void plan_alone(const P &p, Walk<P> &w, int32_t *status) {
@@ -105,14 +105,18 @@ __device__ __forceinline__ void plan_alone(const P &p, Walk<P> &w, int32_t *stat
         w.n_qt = item_count(l, w.sq), w.at = 0, w.left = w.qt < w.n_qt;
         return;
     }
-    auto units = [&](const kv::Seq &x) { return x.q_len > 0 ? item_steps(item_hi(l, x, 0)) + kItemCost : 0; };  // of a block
+    auto units = [&](const kv::Seq &x) {  // of a block
+        int n = 0;
+        for (int qt = 0; qt < item_count(l, x); qt++) n += item_steps(item_hi(l, x, qt)) + kItemCost;
+        return n;
+    };
     long long W = 0;
     for (int b = lane; b < l.batch; b += 32) W += units(p.seq(b, me.at == 0 ? status : nullptr));
 #pragma unroll
     for (int o = 16; o; o >>= 1) W += __shfl_xor_sync(~0u, W, o);
     W *= l.blocks;
     const int C = kv::used_ctas(me.of, W);
-    w.left = 0, w.n_qt = 1, w.qt = 0;
+    w.left = 0;
     if (me.at >= C) return;
     const long long u0 = kv::unit_start(me.at, C, W), u1 = kv::unit_start(me.at + 1, C, W);
     long long before = 0;  // units of the sequences before this round's
@@ -129,9 +133,14 @@ __device__ __forceinline__ void plan_alone(const P &p, Walk<P> &w, int32_t *stat
         if (past) {
             const int owner = __ffs(past) - 1;
             long long rest = u0 - (before + x - (long long)per * l.blocks);
-            int block = 0;
-            if (l.blocks > 1 && lane == owner) block = (int)(rest / per), rest -= (long long)block * per;
-            w.b = b0 + owner, w.block = __shfl_sync(~0u, block, owner), w.at = __shfl_sync(~0u, (int)rest, owner);
+            int block = 0, qt = 0, at = 0;
+            if (lane == owner) {
+                if (l.blocks > 1) block = (int)(rest / per);
+                at = (int)(rest - (long long)block * per);
+                for (int n; at >= (n = item_steps(item_hi(l, s, qt)) + kItemCost); qt++) at -= n;
+            }
+            w.b = b0 + owner, w.block = __shfl_sync(~0u, block, owner), w.at = __shfl_sync(~0u, at, owner);
+            w.qt = __shfl_sync(~0u, qt, owner), w.n_qt = __shfl_sync(~0u, item_count(l, s), owner);
             w.sq.q0 = __shfl_sync(~0u, s.q0, owner), w.sq.q_len = __shfl_sync(~0u, s.q_len, owner), w.sq.kv_len = __shfl_sync(~0u, s.kv_len, owner);
             w.left = u1 - u0;
             return;
