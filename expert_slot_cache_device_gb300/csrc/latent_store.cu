@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 }
 
 // A CTA copies kReadRows slots of one sequence; a thread takes 16 bytes of a slot at a time.
-constexpr int kReadRows = 32, kReadThreads = 256;
+constexpr int kReadRows = 32, kReadThreads = 256, kReadAhead = 5;
 
 template <bool BF, bool Q8>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) {
@@ -174,21 +174,35 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const ReadParams p) 
     }
     __syncthreads();
     const int latent = p.c.latent, at = rope_at(latent, p.c.bits);
-    const int lat = Q8 ? latent >> 4 : latent >> 3, per = lat + (p.c.rope >> 3);  // 16-byte pieces of a slot
-    for (int i = tid; i < here * per; i += kReadThreads) {
-        const int r = i / per, c = i - r * per;
-        if (s_src[r] < 0) continue;
-        const unsigned char *src = p.c.pages + s_src[r];
-        uint16_t *dst = p.out + (int64_t)(r0 + j0 + r) * p.out_stride;
-        if (c >= lat)
-            *reinterpret_cast<uint4 *>(dst + latent + 8 * (c - lat)) = *reinterpret_cast<const uint4 *>(src + at + 16 * (c - lat));
-        else if (!Q8)
-            *reinterpret_cast<uint4 *>(dst + 8 * c) = *reinterpret_cast<const uint4 *>(src + 16 * c);
-        else {
-            uint4 lo, hi;
-            decode16<BF>(*reinterpret_cast<const uint4 *>(src + 16 * c), src[latent + (c >> 1)], lo, hi);
-            *reinterpret_cast<uint4 *>(dst + 16 * c) = lo;
-            *reinterpret_cast<uint4 *>(dst + 16 * c + 8) = hi;
+    const int lat = Q8 ? latent >> 4 : latent >> 3, per = lat + (p.c.rope >> 3);  // 16-byte pieces of a slot, 72 at most
+    const uint32_t inv = ((1u << 20) + per - 1) / per;                            // i / per = i * inv >> 20 for i * per < 2^20
+    for (int i0 = tid; i0 < here * per; i0 += kReadAhead * kReadThreads) {
+        uint4 x[kReadAhead];
+        uint32_t byte[kReadAhead];
+        int row[kReadAhead], col[kReadAhead];  // row -1: none
+#pragma unroll
+        for (int k = 0; k < kReadAhead; k++) {
+            const int i = i0 + k * kReadThreads, r = i * inv >> 20, c = i - r * per;
+            const int64_t from = i < here * per ? s_src[r] : -1;
+            row[k] = from < 0 ? -1 : r, col[k] = c, x[k] = make_uint4(0, 0, 0, 0), byte[k] = 0;
+            if (from < 0) continue;
+            const unsigned char *src = p.c.pages + from;
+            x[k] = *reinterpret_cast<const uint4 *>(src + (c < lat ? 16 * c : at + 16 * (c - lat)));
+            if (Q8 && c < lat) byte[k] = src[latent + (c >> 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < kReadAhead; k++) {
+            if (row[k] < 0) continue;
+            uint16_t *dst = p.out + (int64_t)(r0 + j0 + row[k]) * p.out_stride;
+            const int c = col[k];
+            if (!Q8 || c >= lat)
+                *reinterpret_cast<uint4 *>(dst + (Q8 ? latent + 8 * (c - lat) : 8 * c)) = x[k];
+            else {
+                uint4 lo, hi;
+                decode16<BF>(x[k], byte[k], lo, hi);
+                *reinterpret_cast<uint4 *>(dst + 16 * c) = lo;
+                *reinterpret_cast<uint4 *>(dst + 16 * c + 8) = hi;
+            }
         }
     }
 }
