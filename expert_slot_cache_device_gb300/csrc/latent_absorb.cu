@@ -1,13 +1,13 @@
 // Absorbed latent attention on the 5th-generation tensor cores. All heads read the same cached vectors, so the rows of an
-// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots. Both products have the cache as their A
+// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots (64 of an 8-bit cache). Both products have the cache as their A
 // operand, straight from shared memory in the one layout that the copies leave it in:
-//   S^T [128 slots, NR rows] = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
+//   S^T [slots, NR rows]     = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
 //   O^T [latent, NR rows]  += C^T P^T                    A: latents are M = 128, slots K (M-major)
 // so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most; rows as M would take all of it), and few
 // rows cost few columns instead of an unused part of M = 128. P^T goes to shared memory as the B operand.
 //
 // Persistent, one CTA an SM, work cut by latent_line.cuh. Roles:
-//   warps 0-3   softmax of a tile: warp w has slots 32 w .. 32 w + 31, a thread four slots' values of every eighth pair of rows.
+//   warps 0-3   softmax of a tile: a warp has a quarter of the slots, a thread four (two) slots' values of every eighth pair of rows.
 //               P = 2^(s scale log2 e - m) in fp32 with the maximum m of the tiles before; one vote of the four warps tells whether a
 //               P is above 2^8, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to
 //               the cache's type, as the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at
@@ -18,7 +18,7 @@
 //               the compiler knows its branches to be uniform and keeps descriptors in uniform registers (without: 70 cycles a product).
 //   warp 6      walks the work and hands the parts out.
 //   warp 7      tensor copies of queries, rotary parts and powers of two.
-//   warps 8-15  (8 bits, instead of warp 4) load codes, a pair of units at a time, and turn them into elements. Codes stay in registers on
+//   warps 8-15  (8 bits, instead of warp 4) load codes, a warp a unit, and turn them into elements. Codes stay in registers on
 //               their way: shared memory has no place for more than a quarter of a tile's, which let too few be under way.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 #include "latent_line.cuh"
@@ -45,34 +45,35 @@ using kv::unpack2;
 using kv::wait_bar;
 
 constexpr int kCopyWarp = 4, kMmaWarp = 5, kWalkWarp = 6, kRopeWarp = 7, kConvWarps = 8;
-constexpr int kTile = kStep;
-constexpr int kUnit = kTile * 128;  // 64 latents of a tile's slots
-constexpr int kUnits = 8;           // places for them; two are an operand of the second product
 constexpr float kMost = 256.f;   // P that is let through without raising m
 constexpr float kLeast = 5.9604645e-8f;  // 2^-24
 
 template <bool Q8, int NR>
 struct Shape {
     static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
-    static constexpr int kRopes = NR == 64 ? 1 : 2, kScales = Q8 ? 2 : 0;
-    static constexpr int kScale = kTile * 16;
+    // Slots of a tile: 128 read least from shared memory. Of codes 64, and a place for two tiles, so that one is turned into elements while
+    // the other is worked on, and two tiles' products in turn.
+    static constexpr int kTile = Q8 ? 64 : 128, kHalves = kTile / 64;
+    static constexpr bool kTwo = Q8;
+    static constexpr int kUnit = kTile * 128;   // 64 latents of a tile's slots
+    static constexpr int kUnits = Q8 ? 16 : 8;  // places for them; two are an operand of the second product
+    static constexpr int kRopes = NR == 64 ? 1 : 2;
     static constexpr int kQ = 9 * NR * 128;
     // P lies over the rotary part, which S has read by then, where shared memory would not hold both
     static constexpr bool kOver = NR == 64;
-    static constexpr int kP = kOver ? 0 : NR * 2 * kTile > 4096 ? NR * 2 * kTile : 4096, kScratch = kOver ? 2048 : 0;
-    static constexpr int kSmem = 1024 + kUnits * kUnit + kRopes * kUnit + kQ + kP + kScratch + kScales * kScale;
-    static constexpr uint32_t kS = 256;  // column of S; O is at 0
+    static constexpr int kPOne = NR * 2 * kTile, kP = kOver ? 0 : kTwo ? 2 * kPOne : kPOne, kScratch = kOver ? 2048 : 0;
+    static constexpr int kSmem = 1024 + kUnits * kUnit + kRopes * kUnit + kQ + kP + kScratch;
+    static constexpr uint32_t kS = 256, kSTwo = kTwo ? NR : 0;  // column of S, from one tile's to the next one's; O is at 0
 };
-constexpr int kMaxRopes = 2, kMaxScales = 2;
+constexpr int kMaxRopes = 2;
 
 struct Maps {
-    CUtensorMap q, q_rope, lat, rope, all, scale;  // all: whole slots, for prefetches
+    CUtensorMap q, q_rope, lat, rope, all;  // all: whole slots, for prefetches
 };
 
 struct Bars {
-    uint64_t unit_full[kUnits], pair_empty[kUnits / 2], rope_full[kMaxRopes], rope_empty[kMaxRopes];
-    uint64_t scale_full[kMaxScales], scale_empty[kMaxScales];
-    uint64_t qfull, qempty, s, p, o, done;
+    uint64_t unit_full[16], pair_empty[8], rope_full[kMaxRopes], rope_empty[kMaxRopes];
+    uint64_t qfull, qempty, s[2], p[2], pv, o, done;
 };
 
 // Sixteen lanes of tensor memory as fragments: a thread's registers 4 j .. 4 j + 3 are columns 8 j + 2 (lane % 4), + 1 of lane
@@ -142,9 +143,21 @@ __device__ __forceinline__ void prefetch(const CUtensorMap *map, int x, int y, i
 }
 constexpr int kWide = 192;  // 16-bit elements of a slot that one prefetch has
 
+// Tiles of a part.
+template <int kTile>
+struct Tiles {
+    int first, last;
+    __device__ __forceinline__ explicit Tiles(const Part &w) {
+        first = w.first * (kStep / kTile), last = w.last * (kStep / kTile);
+        const int end = (w.hi + kTile - 1) / kTile;
+        if (last > end) last = end > first ? end : first + 1;
+    }
+};
+
 template <bool BF, bool Q8, int NR>
 __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(const __grid_constant__ AttendParams p, const __grid_constant__ Maps maps) {
     using S = Shape<Q8, NR>;
+    constexpr int kTile = S::kTile, kUnit = S::kUnit, kUnits = S::kUnits;
     extern __shared__ __align__(1024) unsigned char sm_raw[];
     __shared__ Bars bar;
     __shared__ PartRing parts;
@@ -155,20 +168,19 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     const int tid = threadIdx.x, warp = __shfl_sync(~0u, tid >> 5, 0), lane = tid & 31;  // (uniform, for the products' descriptors)
     const uint32_t units = (su32(sm_raw) + 1023u) & ~1023u, ropes = units + kUnits * kUnit;
     const uint32_t qs = ropes + S::kRopes * kUnit, ps = S::kOver ? ropes : qs + S::kQ, scratch = S::kOver ? qs + S::kQ : ps;
-    const uint32_t scales = qs + S::kQ + S::kP + S::kScratch;
     const int L = p.c.latent >> 6;  // units of a tile
     const int pair = p.line.pair, rank = pair & blockIdx.x;
 
     if (tid == 0) {
-        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], Q8 ? kConvWarps : 1);
+        for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], 1);
         for (int i = 0; i < kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
         for (int i = 0; i < S::kRopes; i++) bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
-        for (int i = 0; i < S::kScales; i++) bar_init(&bar.scale_full[i], 1), bar_init(&bar.scale_empty[i], kConvWarps);
         for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], Q8 ? 6 + kConvWarps : 7);
-        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.s, 1), bar_init(&bar.p, 4), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
+        bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.pv, 1), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
+        for (int i = 0; i < 2; i++) bar_init(&bar.s[i], 1), bar_init(&bar.p[i], 4);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kCopyWarp && lane < 6 && (lane != 5 || Q8) && (lane != 2 || !Q8))  // (their first use would wait for them)
+    if (warp == kCopyWarp && lane < 5 && (lane != 2 || !Q8))  // (their first use would wait for them)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps) + lane * sizeof(CUtensorMap)) : "memory");
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(su32(&s_tmem)) : "memory");
@@ -207,10 +219,11 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     if (warp < 4) {  // ---------------------------------------------------- softmax
         const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
         const float c2 = p.scale * kv::kLog2e;
-        const int row0 = 32 * warp + (lane >> 2), col0 = 2 * (lane & 3);
+        const int row0 = kTile / 4 * warp + (lane >> 2), col0 = 2 * (lane & 3);
         constexpr int NB = NR / 8;
         uint32_t ns = 0, no = 0;
         while (!vote(!take(parts, n_part, w, ok))) {
+            const Tiles<kTile> tl(w);
             const int block = (w.block << pair) + rank;
             const bool dead = w.left < p.line.item_tokens;  // some of the item's tokens are none
             auto limit = [&](int c) {                       // slots that row c sees
@@ -224,17 +237,21 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             uint64_t l[NB];
 #pragma unroll
             for (int i = 0; i < NB; i++) z[2 * i] = z[2 * i + 1] = 0.f, l[i] = 0;
-            for (int j = w.first; j < w.last; j++, ns++) {
+            for (int j = tl.first; j < tl.last; j++, ns++) {
                 const int s0 = j * kTile;
-                ok = ok && warp_wait(&bar.s, ns & 1);
+                const int turn = S::kTwo ? ns & 1 : 0;
+                const uint32_t phase = S::kTwo ? ns >> 1 & 1 : ns & 1;
+                const uint32_t tS = lanes + S::kS + turn * S::kSTwo, pt = ps + turn * S::kPOne, sp = S::kOver ? scratch : pt;
+                ok = ok && warp_wait(&bar.s[turn], phase);
                 fence_after();
-                uint32_t x[NR];  // slots of the warp's first 16 lanes, then of the others
+                constexpr int X = S::kHalves * NR / 2;
+                uint32_t x[X];  // slots of the warp's first 16 lanes, then of the others
                 auto scores = [&] {
-                    load_s<NR>(lanes + S::kS, x);
-                    load_s<NR>(lanes + (16u << 16) + S::kS, x + NR / 2);
+                    load_s<NR>(tS, x);
+                    if (S::kHalves == 2) load_s<NR>(tS + (16u << 16), x + X - NR / 2);
                     if (s0 + kTile <= least) return;
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
+                    for (int k = 0; k < 2 * S::kHalves; k++)
 #pragma unroll
                         for (int i = 0; i < NB; i++)
 #pragma unroll
@@ -245,7 +262,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 auto form = [&] {
                     float top = 0.f;
 #pragma unroll
-                    for (int k = 0; k < NR; k += 2) {
+                    for (int k = 0; k < X; k += 2) {
                         const int i = (k % (NR / 2)) >> 2;
                         const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
                         const float a = ex2(f.x), b = ex2(f.y);
@@ -255,14 +272,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     return top > kMost;
                 };
                 scores();
-                const bool fresh = j == w.first;
+                const bool fresh = j == tl.first;
                 bool raise = form() || !ok || (fresh && !BF);
                 if (fresh) {
 #pragma unroll
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
-                        t = kv::max3(t, __uint_as_float(x[NR / 2 + r]), __uint_as_float(x[NR / 2 + r + 2]));
+                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
                         raise = raise || t < kLeast;
                     }
                 }
@@ -274,11 +291,11 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
-                        t = kv::max3(t, __uint_as_float(x[NR / 2 + r]), __uint_as_float(x[NR / 2 + r + 2]));
+                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
                         t *= c2;
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
-                        if (lane < 4) st_f(scratch + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
+                        if (lane < 4) st_f(sp + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
                     }
                     vote(false);
 #pragma unroll
@@ -286,7 +303,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         float f[2];
 #pragma unroll
                         for (int e = 0; e < 2; e++) {
-                            const uint32_t a = scratch + (8 * i + col0 + e) * 4;
+                            const uint32_t a = sp + (8 * i + col0 + e) * 4;
                             const float t = fmaxf(fmaxf(ld_f(a), ld_f(a + NR * 4)), fmaxf(ld_f(a + 2 * NR * 4), ld_f(a + 3 * NR * 4)));
                             const float m = -z[2 * i + e], n = fresh ? (t == -INFINITY ? 0.f : t) : fmaxf(m, t);
                             f[e] = fresh ? 0.f : ex2(m - n);
@@ -296,14 +313,16 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         const float2 y = unpack2(l[i]);
                         l[i] = pack2(y.x * f[0], y.y * f[1]);
                     }
-                    vote(false);
-                    if (!fresh) {  // (the product with the last P was done before this tile's S)
+                    if (!fresh) ok = warp_wait(&bar.pv, (ns - 1) & 1);  // O holds all P so far
+                    if (vote(!ok)) break;
+                    fence_after();
+                    if (!fresh) {
 #pragma unroll 1
                         for (int k = 0; k < (L >> 1) * NR; k += 16) {
                             uint32_t y[16];
                             tm_ld16(lanes + k, y);
 #pragma unroll
-                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(scratch + (4 * NR + (k + e) % NR) * 4));
+                            for (int e = 0; e < 16; e++) y[e] = __float_as_uint(__uint_as_float(y[e]) * ld_f(sp + (4 * NR + (k + e) % NR) * 4));
                             kv::tm_st16(lanes + k, y);
                         }
                         kv::tm_st_wait();
@@ -312,7 +331,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     form();
                 }
 #pragma unroll
-                for (int h = 0; h < 2; h++)
+                for (int h = 0; h < S::kHalves; h++)
 #pragma unroll
                     for (int i = 0; i < NB; i += 2) {
                         uint32_t y[4];
@@ -325,8 +344,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         }
                         // transposed: a row's slots consecutive, 64 in 128 bytes, 16-byte piece c of row r at c ^ (r % 8)
                         const int r = lane & 7, k = lane >> 3;
-                        const int piece = 4 * warp + 2 * h + (k & 1);
-                        const uint32_t at = ps + (piece >> 3) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((piece & 7) ^ r) << 4);
+                        const int piece = 2 * S::kHalves * warp + 2 * h + (k & 1);
+                        const uint32_t at = pt + (piece >> 3) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((piece & 7) ^ r) << 4);
                         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
                                      "r"(y[3])
                                      : "memory");
@@ -343,7 +362,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 fence_async();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&bar.p);
+                if (lane == 0) bar_arrive(&bar.p[turn]);
             }
             ok = ok && warp_wait(&bar.o, no++ & 1);
             if (vote(!ok)) break;
@@ -433,8 +452,9 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 const int slot = j * kTile + blk * box;
                 return mine && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            int next = page_at(w.first);
-            for (int j = w.first; j < w.last && ok; j++, n += L, sent = 0) {
+            const Tiles<kTile> tl(w);
+            int next = page_at(tl.first);
+            for (int j = tl.first; j < tl.last && ok; j++, n += L, sent = 0) {
                 const int page = (uint32_t)next < (uint32_t)p.c.num_pages ? next : -1;  // (warp 7 records bad ones)
                 next = page_at(j + 1);  // on its way while this tile waits for its places
                 const int row = (j * kTile + blk * box) & ((1 << p.c.page_shift) - 1);
@@ -477,7 +497,6 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         const int box = 1 << p.c.page_shift < kTile ? 1 << p.c.page_shift : kTile, boxes = kTile / box;
         const int blk = lane & 7;
         Turn<S::kRopes> ro;
-        Turn<S::kScales + !Q8> sc;
         uint32_t nq = 0;
         while (ok && take(parts, n_part, w, ok)) {
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
@@ -485,7 +504,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 const int slot = j * kTile + blk * box;
                 return blk < boxes && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
             };
-            int next = page_at(w.first);
+            const Tiles<kTile> tl(w);
+            int next = page_at(tl.first);
             if (nq > 0 && !warp_wait(&bar.qempty, (nq - 1) & 1)) {
                 ok = false;
                 break;
@@ -495,7 +515,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             __syncwarp();
             if (lane <= L)
                 tma3(qs + lane * NR * 128, lane < L ? &maps.q : &maps.q_rope, lane < L ? 64 * lane : 0, ((w.block << pair) + rank) * p.heads, w.token, &bar.qfull);
-            for (int j = w.first; j < w.last && ok; j++) {
+            for (int j = tl.first; j < tl.last && ok; j++) {
                 const int slot = j * kTile + blk * box, row = slot & ((1 << p.c.page_shift) - 1);
                 int page = next;
                 next = page_at(j + 1);
@@ -505,14 +525,6 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 }
                 const bool mine = lane < 8 && page >= 0;
                 const int valid = __popc(__ballot_sync(~0u, mine)) * box;
-                if (Q8) {
-                    ok = warp_wait(&bar.scale_empty[sc.at], sc.ph ^ 1);
-                    if (!ok) break;
-                    if (lane == 0) bar_expect(&bar.scale_full[sc.at], valid * 16);
-                    __syncwarp();
-                    if (mine) tma3(scales + sc.at * S::kScale + lane * box * 16, &maps.scale, 0, row, page, &bar.scale_full[sc.at]);
-                    sc.next();
-                }
                 ok = warp_wait(&bar.rope_empty[ro.at], ro.ph ^ 1);
                 if (!ok) break;
                 if (lane == 0) bar_expect(&bar.rope_full[ro.at], valid * 128);
@@ -526,71 +538,103 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         if (!ok) {  // wait (bounded) until the copies already issued have landed
             if (nq > 0) wait_bar(&bar.qfull, (nq - 1) & 1);
             for (int i = 0; i < S::kRopes; i++, ro.next()) wait_bar(&bar.rope_full[ro.at], ro.ph ^ 1);
-            for (int i = 0; i < S::kScales; i++, sc.next()) wait_bar(&bar.scale_full[sc.at], sc.ph ^ 1);
         }
     } else if (warp == kMmaWarp) {  // --------------------------------------- products
         constexpr uint32_t IS = kv::kInstrM<BF, kTile, NR, false, false>, IO = kv::kInstrM<BF, 128, NR, true, false>;
         const uint32_t one = kv::elect_one();
         const uint32_t qd = desc_lo(qs, 16), pd = desc_lo(ps, 16), ud = desc_lo(units, 16), rd = desc_lo(ropes, 16), vd = desc_lo(units, kUnit);
         const int rope_steps = p.c.rope >> 4;
-        uint32_t nq = 0, n = 0;  // items, tiles
+        uint32_t nq = 0, n = 0, np = 0;  // items, tiles whose S and whose O product is issued
         Turn<kUnits> us, uv;  // of the scores and of the outputs
         Turn<S::kRopes> ro;
+        // each unit's barrier is tested while the products of the one before are issued (a test takes 100 cycles)
+        auto scores = [&](bool last) {
+            const int turn = S::kTwo ? n & 1 : 0;
+            const uint32_t d = tm + S::kS + turn * S::kSTwo;
+            uint32_t b = qd, acc = 0;
+            // one test of all that this tile needs (a test takes 100 cycles), a lane each
+            const uint32_t mine = lane < L ? su32(&bar.unit_full[us.at + lane < kUnits ? us.at + lane : us.at + lane - kUnits]) : su32(&bar.rope_full[ro.at]);
+            const uint32_t ph = lane < L ? us.ph ^ (us.at + lane >= kUnits) : ro.ph;
+            bool there = __all_sync(~0u, kv::test_bar(mine, ph)) != 0;
+            if (there && L == 8) {
+                fence_after();
+                const uint32_t a = ud + us.at * (kUnit / 16);
+#pragma unroll
+                for (int u = 0; u < 8; u++) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, d, a + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
+                }
+                us.at += 8, b = qd + 8 * (NR * 128 / 16);
+                if (us.at == kUnits) us.at = 0, us.ph ^= 1;
+            } else {
+#pragma unroll 1
+                for (int u = 0; u < L && ok; u++, b += NR * 128 / 16) {
+                    if (u == 0) there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
+                    if (!__all_sync(~0u, there)) ok = warp_wait(&bar.unit_full[us.at], us.ph);
+                    fence_after();
+                    const uint32_t a = ud + us.at * (kUnit / 16);
+                    us.next();
+                    there = kv::test_bar(su32(u + 1 < L ? &bar.unit_full[us.at] : &bar.rope_full[ro.at]), u + 1 < L ? us.ph : ro.ph);
+#pragma unroll
+                    for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, d, a + 2 * k, b + 2 * k, acc);
+                }
+            }
+            if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
+            if (!ok) return;
+            fence_after();
+            const uint32_t r = rd + ro.at * (kUnit / 16);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                if (k < rope_steps) mma_ss<IS>(one, d, r + 2 * k, b + 2 * k, 1);
+            commit(one, &bar.s[turn]);
+            if (!S::kOver) commit(one, &bar.rope_empty[ro.at]), ro.next();
+            if (last) commit(one, &bar.qempty);
+            n++;
+        };
+        auto values = [&](uint32_t acc0) {
+            const int turn = S::kTwo ? np & 1 : 0;
+            ok = ok && warp_wait(&bar.p[turn], S::kTwo ? np >> 1 & 1 : np & 1);
+            if (!ok) return;
+            fence_after();
+            const uint32_t b = pd + turn * (S::kPOne / 16);
+#pragma unroll 1
+            for (int u = 0; u < L; u += 2) {
+                const uint32_t a = vd + uv.at * (kUnit / 16), d = tm + (u >> 1) * NR;
+                uint32_t acc = acc0;
+#pragma unroll
+                for (int k = 0; k < kTile / 16; k++, acc = 1)
+                    mma_ss<IO>(one, d, a + k * (2048 / 16), b + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
+                commit(one, &bar.pair_empty[uv.at >> 1]);
+                uv.next(), uv.next();
+            }
+            if (S::kOver) commit(one, &bar.rope_empty[ro.at]), ro.next();
+            commit(one, &bar.pv);
+            np++;
+        };
         while (ok && take(parts, n_part, w, ok)) {
-            const int nt = __shfl_sync(~0u, w.last - w.first, 0);
+            const Tiles<kTile> tl(w);
+            const int nt = __shfl_sync(~0u, tl.last - tl.first, 0);
             ok = warp_wait(&bar.qfull, nq++ & 1);
+            fence_after();
 #pragma unroll 1
-            for (int j = 0; j < nt && ok; j++, n++) {
-                // each unit's barrier is tested while the products of the one before are issued (a test takes 100 cycles)
-                uint32_t b = qd, acc = 0;
-                bool there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
-                if (L == kUnits) {  // places and descriptors known here: 50 cycles a product, what it runs, against 77
-#pragma unroll
-                    for (int u = 0; u < kUnits; u++) {
-                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.unit_full[u], us.ph);
-                        fence_after();
-                        there = kv::test_bar(su32(u + 1 < kUnits ? &bar.unit_full[u + 1] : &bar.rope_full[ro.at]), u + 1 < kUnits ? us.ph : ro.ph);
-#pragma unroll
-                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, ud + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
+            for (int j = 0; j < nt && ok;) {
+                scores(j + 1 == nt);
+                // the next tile's scores too, if it is there before this one's P: they are formed during its softmax
+                bool two = false;
+                if (S::kTwo && j + 1 < nt && ok) {
+                    const int at = us.at + lane, over = at >= kUnits;
+                    const uint32_t watch = lane < L ? su32(&bar.unit_full[over ? at - kUnits : at]) : su32(&bar.p[np & 1]);
+                    const uint32_t phase = lane < L ? us.ph ^ over : np >> 1 & 1;
+                    for (int i = 0; i < 1 << 21; i++) {
+                        const unsigned there = __ballot_sync(~0u, kv::test_bar(watch, phase));
+                        two = (there & ((1u << L) - 1)) == (1u << L) - 1;
+                        if (two || there >> 31) break;
                     }
-                    us.ph ^= 1, b = qd + kUnits * (NR * 128 / 16);
-                } else {
-#pragma unroll 1
-                    for (int u = 0; u < L && ok; u++, b += NR * 128 / 16) {
-                        if (!__all_sync(~0u, there)) ok = warp_wait(&bar.unit_full[us.at], us.ph);
-                        fence_after();
-                        const uint32_t a = ud + us.at * (kUnit / 16);
-                        us.next();
-                        there = kv::test_bar(su32(u + 1 < L ? &bar.unit_full[us.at] : &bar.rope_full[ro.at]), u + 1 < L ? us.ph : ro.ph);
-#pragma unroll
-                        for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, tm + S::kS, a + 2 * k, b + 2 * k, acc);
-                    }
+                    if (two) scores(j + 2 == nt);
                 }
-                if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.rope_full[ro.at], ro.ph);
-                if (!ok) break;
-                fence_after();
-                const uint32_t r = rd + ro.at * (kUnit / 16);
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    if (k < rope_steps) mma_ss<IS>(one, tm + S::kS, r + 2 * k, b + 2 * k, 1);
-                commit(one, &bar.s);
-                if (!S::kOver) commit(one, &bar.rope_empty[ro.at]);
-                if (j + 1 == nt) commit(one, &bar.qempty);
-                ok = warp_wait(&bar.p, n & 1);
-                if (!ok) break;
-                fence_after();
-#pragma unroll 1
-                for (int u = 0; u < L; u += 2) {
-                    const uint32_t a = vd + uv.at * (kUnit / 16), d = tm + (u >> 1) * NR;
-                    acc = j > 0;
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; k++, acc = 1)
-                        mma_ss<IO>(one, d, a + k * (2048 / 16), pd + (k >> 2) * (NR * 128 / 16) + 2 * (k & 3), acc);
-                    commit(one, &bar.pair_empty[uv.at >> 1]);
-                    uv.next(), uv.next();
-                }
-                if (S::kOver) commit(one, &bar.rope_empty[ro.at]);
-                ro.next();
+                values(j > 0);
+                if (two) values(1);
+                j += 1 + two;
             }
             if (ok) commit(one, &bar.o);
         }
@@ -599,86 +643,95 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
     } else if (warp == kWalkWarp) {
         ok = hand_out(p, parts, walk);
     } else if (Q8 && warp >= 8) {  // --------------------------------------- codes to elements
-        // All of them take one pair of units after another, 16 slots each, so that the first is there soonest; four lanes have a slot's 64 codes
-        // of a unit. The next tile's codes are loaded pair by pair as this one's are turned (48 KB and more under way: with the next pair's
-        // alone, 16 KB, the loads' latency was the time); a tile's pages are looked up a tile before that.
-        const int sub = lane >> 2, q = lane & 3, slot0 = 16 * (warp & 7), LP = L >> 1;
-        const int64_t off = sub * p.c.slot + 16 * q, off8 = off + 8 * p.c.slot;
-        const uint32_t at0 = units + (slot0 + sub) * 128 + (((2 * q) ^ sub) << 4), at1 = units + (slot0 + sub) * 128 + (((2 * q + 1) ^ sub) << 4);
-        const uint32_t from0 = scales + (slot0 + sub) * 16 + (q >> 1);
-        Turn<S::kScales + !Q8> sc;
-        Turn<kUnits / 2> pl;
-        auto load = [&](const unsigned char *at, uint4 (&in)[4]) {  // (unit of the pair, eight slots)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                uint4 &v = in[i];
-                asm volatile(
-                    "{\n\t.reg .pred p;\n\tsetp.ne.u64 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-                    "@p ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-                    : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-                    : "l"(at + (i & 1 ? off8 : off) + 64 * (i >> 1)), "l"(at));
-            }
-        };
-        auto turn = [&](int m, const uint4 (&in)[4]) {
-            const bool free = kv::test_bar(su32(&bar.pair_empty[pl.at]), pl.ph ^ 1);
-            uint32_t byte[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                asm volatile("{\n\t.reg .u8 x;\n\tld.shared.u8 x, [%1];\n\tcvt.u32.u8 %0, x;\n\t}"
-                             : "=r"(byte[i])
-                             : "r"(from0 + sc.at * S::kScale + 4 * m + 2 * (i >> 1) + 128 * (i & 1))
-                             : "memory");
-            if (!__all_sync(~0u, free)) ok = ok && warp_wait(&bar.pair_empty[pl.at], pl.ph ^ 1);
-            if (!ok) return;
-            bool plain = true;
-#pragma unroll
-            for (int i = 0; i < 4; i++) plain = plain && plain_power<BF>(byte[i]);
-            auto put = [&](int i, const uint4 &lo, const uint4 &hi) {
-                const uint32_t o = pl.at * (2 * kUnit) + (i >> 1) * kUnit + 1024 * (i & 1);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at0 + o), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at1 + o), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
-            };
-            uint4 lo, hi;
-            if (__all_sync(~0u, plain)) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) decode16_plain<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; i++) decode16_far<BF>(in[i], byte[i], lo, hi), put(i, lo, hi);
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&bar.unit_full[2 * pl.at]), bar_arrive(&bar.unit_full[2 * pl.at + 1]);
-            pl.next();
-        };
+        // every eighth unit a warp; four lanes have a slot's 64 codes, a warp eight slots at a time. The next unit's codes are loaded while
+        // this one's are turned, and the pages of the one after that looked up.
+        const int sub = lane >> 2, q = lane & 3;
+        const int steps = 8 / L, rest = 8 - steps * L;  // tiles from a unit to this warp's next, and units
+        const int64_t off = sub * p.c.slot + 16 * q, off8 = off + 8 * p.c.slot, offp = (lane & 15) * p.c.slot + p.c.latent;
+        const uint32_t at0 = units + sub * 128 + (((2 * q) ^ sub) << 4), at1 = units + sub * 128 + (((2 * q + 1) ^ sub) << 4);
+        uint32_t n = 0;  // units before this part
         while (ok && take(parts, n_part, w, ok)) {
+            const Tiles<kTile> tl(w);
             const int32_t *tab = p.bt.table + (int64_t)w.b * p.bt.table_stride;
-            auto page_at = [&](int j) {
-                const int slot = j * kTile + slot0;
-                return j < w.last && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+            struct Unit {  // tile and unit in it, pages of its 4 x 16 slots (-1: none)
+                int j, m, page[4];
             };
-            auto place = [&](int j, int page) -> const unsigned char * {
-                return (uint32_t)page < (uint32_t)p.c.num_pages ? cell(p.c, page, j * kTile + slot0) : nullptr;
+            auto find = [&](Unit &x) {
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const int slot = x.j * kTile + 16 * k;
+                    x.page[k] = x.j < tl.last && slot < w.hi ? tab[slot >> p.c.page_shift] : -1;
+                }
             };
-            const unsigned char *here = place(w.first, page_at(w.first));
-            int next = page_at(w.first + 1);
-            uint4 in[4][4];
+            auto after = [&](const Unit &x) {
+                Unit y;
+                y.j = x.j + steps, y.m = x.m + rest;
+                if (y.m >= L) y.m -= L, y.j++;
+                find(y);
+                return y;
+            };
+            auto load = [&](const Unit &x, uint4 (&in)[8], uint32_t (&power)[2]) {  // (of page 0 where there is none: not used)
+                const unsigned char *at[4];
 #pragma unroll
-            for (int m = 0; m < 4; m++)
-                if (m < LP) load(here ? here + 128 * m : nullptr, in[m]);
-            for (int j = w.first; j < w.last && ok; j++) {
-                const unsigned char *then = place(j + 1, next);
-                next = page_at(j + 2);
-                ok = warp_wait(&bar.scale_full[sc.at], sc.ph);
+                for (int k = 0; k < 4; k++) {
+                    at[k] = cell(p.c, (uint32_t)x.page[k] < (uint32_t)p.c.num_pages ? x.page[k] : 0, x.j * kTile + 16 * k) + 64 * x.m;
 #pragma unroll
-                for (int m = 0; m < 4; m++)
-                    if (m < LP && ok) {
-                        turn(m, in[m]);
-                        load(then ? then + 128 * m : nullptr, in[m]);
+                    for (int i = 0; i < 2; i++) {
+                        uint4 &v = in[2 * k + i];
+                        asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "l"(at[k] + (i ? off8 : off)));
                     }
-                if (lane == 0) bar_arrive(&bar.scale_empty[sc.at]);
-                sc.next();
+                }
+#pragma unroll
+                for (int k = 0; k < 2; k++)  // both powers of a slot's two groups, slots lane and lane + 32
+                    asm volatile("ld.global.u16 %0, [%1];" : "=r"(power[k]) : "l"((lane & 16 ? at[2 * k + 1] : at[2 * k]) + (offp - 62 * x.m)));
+            };
+            uint32_t x = n + ((warp - 8 - n) & 7);  // of all units
+            auto turn = [&](const uint4 (&in)[8], const uint32_t (&power)[2]) {
+                const uint32_t un = x % kUnits;
+                const bool free = kv::test_bar(su32(&bar.pair_empty[un >> 1]), x / kUnits & 1 ^ 1);
+                bool plain = true;
+#pragma unroll
+                for (int k = 0; k < 2; k++) plain = plain && plain_power<BF>(power[k] & 255) && plain_power<BF>(power[k] >> 8);
+                plain = __all_sync(~0u, plain);
+                if (!__all_sync(~0u, free)) ok = ok && warp_wait(&bar.pair_empty[un >> 1], x / kUnits & 1 ^ 1);
+                if (!ok) return;
+                auto byte = [&](int i) { return __shfl_sync(~0u, power[i >> 2], 8 * (i & 3) + sub) >> (q & 2) * 4 & 255; };
+                auto put = [&](int i, const uint4 &lo, const uint4 &hi) {
+                    const uint32_t o = un * kUnit + 1024 * i;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at0 + o), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at1 + o), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+                };
+                uint4 lo, hi;
+                if (plain) {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) decode16_plain<BF>(in[i], byte(i), lo, hi), put(i, lo, hi);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) decode16_far<BF>(in[i], byte(i), lo, hi), put(i, lo, hi);
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&bar.unit_full[un]);
+                x += 8;
+            };
+            Unit y{tl.first + (int)(x - n) / L, (int)(x - n) % L, {-1, -1, -1, -1}};
+            find(y);
+            uint4 a[8], b[8];
+            uint32_t pa[2], pb[2];
+            load(y, a, pa);
+            Unit z = after(y);
+            while (y.j < tl.last && ok) {
+                load(z, b, pb);
+                y = after(z);
+                turn(a, pa);
+                if (z.j >= tl.last || !ok) break;
+                load(y, a, pa);
+                z = after(y);
+                turn(b, pb);
             }
+            n += (tl.last - tl.first) * L;
         }
     }
     if (!ok && lane == 0) kv::flag(p.c.status, FTMOE_ERR_STATE);
@@ -779,16 +832,14 @@ template <bool BF, bool Q8, int NR>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     using S = Shape<Q8, NR>;
     const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
-    const int box = 1 << p.c.page_shift < kTile ? 1 << p.c.page_shift : kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
+    const int box = 1 << p.c.page_shift < S::kTile ? 1 << p.c.page_shift : S::kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
     Maps m;
     bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, true) &&
               kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, true) &&
               kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     const int row = rope_at(p.c.latent, p.c.bits) / 2 + p.c.rope;
     ok = ok && kv::box_map(m.all, e, p.c.pages, {row, slots, p.c.num_pages}, p.c.slot, p.c.page, {kWide, box, 1}, false);
-    if (Q8)
-        ok = ok && kv::box_map(m.scale, kv::Elem::U8, p.c.pages + p.c.latent, {16, slots, p.c.num_pages}, p.c.slot, p.c.page, {16, box, 1}, false);
-    else
+    if (!Q8)
         ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<absorb_kernel<BF, Q8, NR>>(S::kSmem);
