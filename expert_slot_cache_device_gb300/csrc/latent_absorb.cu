@@ -313,9 +313,9 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         const float2 y = unpack2(l[i]);
                         l[i] = pack2(y.x * f[0], y.y * f[1]);
                     }
-                    if (!fresh) ok = warp_wait(&bar.pv, (ns - 1) & 1);  // O holds all P so far
+                    if (S::kTwo && !fresh) ok = warp_wait(&bar.pv, (ns - 1) & 1);  // O holds all P so far (one tile: before this one's S)
                     if (vote(!ok)) break;
-                    fence_after();
+                    if (S::kTwo) fence_after();
                     if (!fresh) {
 #pragma unroll 1
                         for (int k = 0; k < (L >> 1) * NR; k += 16) {
@@ -552,15 +552,26 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             const int turn = S::kTwo ? n & 1 : 0;
             const uint32_t d = tm + S::kS + turn * S::kSTwo;
             uint32_t b = qd, acc = 0;
-            // one test of all that this tile needs (a test takes 100 cycles), a lane each
-            const uint32_t mine = lane < L ? su32(&bar.unit_full[us.at + lane < kUnits ? us.at + lane : us.at + lane - kUnits]) : su32(&bar.rope_full[ro.at]);
-            const uint32_t ph = lane < L ? us.ph ^ (us.at + lane >= kUnits) : ro.ph;
-            bool there = __all_sync(~0u, kv::test_bar(mine, ph)) != 0;
-            if (there && L == 8) {
-                fence_after();
+            // Two tiles' places: one test of all that this tile needs, a lane each (a test takes 100 cycles); it is mostly there. Else each
+            // unit's barrier is tested while the products of the one before are issued.
+            bool there;
+            if (S::kTwo) {
+                const int at = us.at + lane, over = at >= kUnits;
+                const uint32_t mine = lane < L ? su32(&bar.unit_full[over ? at - kUnits : at]) : su32(&bar.rope_full[ro.at]);
+                there = __all_sync(~0u, kv::test_bar(mine, lane < L ? us.ph ^ over : ro.ph)) != 0;
+            } else {
+                there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
+            }
+            if (L == 8 && (there || !S::kTwo)) {  // places known here but for the first: 50 cycles a product, what it runs, against 77
+                if (S::kTwo) fence_after();
                 const uint32_t a = ud + us.at * (kUnit / 16);
 #pragma unroll
                 for (int u = 0; u < 8; u++) {
+                    if (!S::kTwo) {
+                        if (!__all_sync(~0u, there)) ok = ok && warp_wait(&bar.unit_full[u], us.ph);
+                        fence_after();
+                        there = kv::test_bar(su32(u < 7 ? &bar.unit_full[u + 1] : &bar.rope_full[ro.at]), u < 7 ? us.ph : ro.ph);
+                    }
 #pragma unroll
                     for (int k = 0; k < 4; k++, acc = 1) mma_ss<IS>(one, d, a + u * (kUnit / 16) + 2 * k, qd + u * (NR * 128 / 16) + 2 * k, acc);
                 }
@@ -569,7 +580,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             } else {
 #pragma unroll 1
                 for (int u = 0; u < L && ok; u++, b += NR * 128 / 16) {
-                    if (u == 0) there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
+                    if (S::kTwo && u == 0) there = kv::test_bar(su32(&bar.unit_full[us.at]), us.ph);
                     if (!__all_sync(~0u, there)) ok = warp_wait(&bar.unit_full[us.at], us.ph);
                     fence_after();
                     const uint32_t a = ud + us.at * (kUnit / 16);
@@ -608,7 +619,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 uv.next(), uv.next();
             }
             if (S::kOver) commit(one, &bar.rope_empty[ro.at]), ro.next();
-            commit(one, &bar.pv);
+            if (S::kTwo) commit(one, &bar.pv);
             np++;
         };
         while (ok && take(parts, n_part, w, ok)) {
