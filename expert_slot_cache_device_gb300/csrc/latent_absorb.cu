@@ -50,7 +50,10 @@ constexpr float kLeast = 5.9604645e-8f;  // 2^-24
 
 template <bool Q8, int NR>
 struct Shape {
-    static constexpr int kWarps = Q8 ? 16 : 8, kThreads = kWarps * 32;
+    // Softmax warps, and the columns (rows of the item) of each: of 64 columns a warp takes half, two warps a quarter of the lanes
+    // (48 x 9000 tokens, 128 heads: 93.4 us, 99.3 with all 64 in one).
+    static constexpr int kCols = NR == 64 ? 32 : NR, kSoft = 4 * NR / kCols;
+    static constexpr int kWarps = Q8 ? 16 : 4 + kSoft, kThreads = kWarps * 32;
     // Slots of a tile: 128 read least from shared memory. Of codes 64, and a place for two tiles, so that one is turned into elements while
     // the other is worked on, and two tiles' products in turn.
     static constexpr int kTile = Q8 ? 64 : 128, kHalves = kTile / 64;
@@ -80,15 +83,7 @@ struct Bars {
 // lane / 4, then of lane / 4 + 8.
 template <int NR>
 __device__ __forceinline__ void load_s(uint32_t a, uint32_t *x) {
-    if constexpr (NR == 64) {
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-            "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-            "tcgen05.wait::ld.sync.aligned;"
-            : FTMOE_R32(x)
-            : "r"(a)
-            : "memory");
-    } else if constexpr (NR == 32) {
+    if constexpr (NR == 32) {
         asm volatile(
             "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
             "tcgen05.wait::ld.sync.aligned;"
@@ -114,14 +109,15 @@ __device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t *x) {
         : "memory");
 }
 
-// Barrier of the four softmax warps; true if any thread brings it.
-__device__ __forceinline__ bool vote(bool mine) {
+// Barrier of the softmax warps' N threads; true if any thread brings it.
+template <int N>
+__device__ __forceinline__ bool vote_of(bool mine) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)mine)
+        : "r"((uint32_t)mine), "n"(N)
         : "memory");
     return r != 0;
 }
@@ -175,9 +171,9 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
         for (int i = 0; i < kUnits; i++) bar_init(&bar.unit_full[i], 1);
         for (int i = 0; i < kUnits / 2; i++) bar_init(&bar.pair_empty[i], 1);
         for (int i = 0; i < S::kRopes; i++) bar_init(&bar.rope_full[i], 1), bar_init(&bar.rope_empty[i], 1);
-        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], Q8 ? 6 + kConvWarps : 7);
+        for (int i = 0; i < kParts; i++) bar_init(&parts.full[i], 1), bar_init(&parts.empty[i], S::kSoft + (Q8 ? 2 + kConvWarps : 3));
         bar_init(&bar.qfull, 1), bar_init(&bar.qempty, 1), bar_init(&bar.pv, 1), bar_init(&bar.o, 1), bar_init(&bar.done, 1);
-        for (int i = 0; i < 2; i++) bar_init(&bar.s[i], 1), bar_init(&bar.p[i], 4);
+        for (int i = 0; i < 2; i++) bar_init(&bar.s[i], 1), bar_init(&bar.p[i], S::kSoft);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == kCopyWarp && lane < 5 && (lane != 2 || !Q8))  // (their first use would wait for them)
@@ -216,11 +212,15 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 
     const int wide = ((rope_at(p.c.latent, p.c.bits) >> 1) + p.c.rope + kWide - 1) / kWide;  // copies of kWide elements of a slot: 4 at most
 
-    if (warp < 4) {  // ---------------------------------------------------- softmax
-        const uint32_t lanes = tm + ((uint32_t)(32 * warp) << 16);
+    if (warp < 4 || (S::kSoft == 8 && warp >= 8)) {  // ---------------------------------------------------- softmax
+        constexpr int W = S::kCols, kThreads = 32 * S::kSoft;
+        auto vote = [](bool mine) { return vote_of<kThreads>(mine); };
+        // quarter of the lanes, first column, thread of the group
+        const int quarter = warp & 3, half = S::kSoft == 8 ? warp >> 3 : 0, cb = half * W, st = half * 128 + (tid & 127);
+        const uint32_t lanes = tm + ((uint32_t)(32 * quarter) << 16);
         const float c2 = p.scale * kv::kLog2e;
-        const int row0 = kTile / 4 * warp + (lane >> 2), col0 = 2 * (lane & 3);
-        constexpr int NB = NR / 8;
+        const int row0 = kTile / 4 * quarter + (lane >> 2), col0 = cb + 2 * (lane & 3);
+        constexpr int NB = W / 8;
         uint32_t ns = 0, no = 0;
         while (!vote(!take(parts, n_part, w, ok))) {
             const Tiles<kTile> tl(w);
@@ -241,14 +241,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                 const int s0 = j * kTile;
                 const int turn = S::kTwo ? ns & 1 : 0;
                 const uint32_t phase = S::kTwo ? ns >> 1 & 1 : ns & 1;
-                const uint32_t tS = lanes + S::kS + turn * S::kSTwo, pt = ps + turn * S::kPOne, sp = S::kOver ? scratch : pt;
+                const uint32_t tS = lanes + S::kS + turn * S::kSTwo + cb, pt = ps + turn * S::kPOne, sp = S::kOver ? scratch : pt;
                 ok = ok && warp_wait(&bar.s[turn], phase);
                 fence_after();
-                constexpr int X = S::kHalves * NR / 2;
+                constexpr int X = S::kHalves * W / 2;
                 uint32_t x[X];  // slots of the warp's first 16 lanes, then of the others
                 auto scores = [&] {
-                    load_s<NR>(tS, x);
-                    if (S::kHalves == 2) load_s<NR>(tS + (16u << 16), x + X - NR / 2);
+                    load_s<W>(tS, x);
+                    if (S::kHalves == 2) load_s<W>(tS + (16u << 16), x + X - W / 2);
                     if (s0 + kTile <= least) return;
 #pragma unroll
                     for (int k = 0; k < 2 * S::kHalves; k++)
@@ -256,14 +256,14 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         for (int i = 0; i < NB; i++)
 #pragma unroll
                             for (int e = 0; e < 2; e++)
-                                if (s0 + row0 + 8 * k >= limit(8 * i + col0 + e)) x[(k >> 1) * (NR / 2) + 4 * i + 2 * (k & 1) + e] = 0xff800000u;
+                                if (s0 + row0 + 8 * k >= limit(8 * i + col0 + e)) x[(k >> 1) * (W / 2) + 4 * i + 2 * (k & 1) + e] = 0xff800000u;
                 };
                 // P in place of the scores; whether one is above 2^8
                 auto form = [&] {
                     float top = 0.f;
 #pragma unroll
                     for (int k = 0; k < X; k += 2) {
-                        const int i = (k % (NR / 2)) >> 2;
+                        const int i = (k % (W / 2)) >> 2;
                         const float2 f = unpack2(fma2(pack2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), pack2(c2, c2), pack2(z[2 * i], z[2 * i + 1])));
                         const float a = ex2(f.x), b = ex2(f.y);
                         top = kv::max3(top, a, b);
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
-                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
+                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - W / 2 + r]), __uint_as_float(x[X - W / 2 + r + 2]));
                         raise = raise || t < kLeast;
                     }
                 }
@@ -291,11 +291,11 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     for (int i = 0; i < 2 * NB; i++) {
                         const int r = 4 * (i >> 1) + (i & 1);
                         float t = fmaxf(__uint_as_float(x[r]), __uint_as_float(x[r + 2]));
-                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - NR / 2 + r]), __uint_as_float(x[X - NR / 2 + r + 2]));
+                        if (S::kHalves == 2) t = kv::max3(t, __uint_as_float(x[X - W / 2 + r]), __uint_as_float(x[X - W / 2 + r + 2]));
                         t *= c2;
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
-                        if (lane < 4) st_f(sp + (warp * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
+                        if (lane < 4) st_f(sp + (quarter * NR + 8 * (i >> 1) + col0 + (i & 1)) * 4, t);
                     }
                     vote(false);
 #pragma unroll
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                             const float m = -z[2 * i + e], n = fresh ? (t == -INFINITY ? 0.f : t) : fmaxf(m, t);
                             f[e] = fresh ? 0.f : ex2(m - n);
                             z[2 * i + e] = -n;
-                            if (warp == 0 && lane < 4) st_f(a + 4 * NR * 4, f[e]);
+                            if (quarter == 0 && lane < 4) st_f(a + 4 * NR * 4, f[e]);
                         }
                         const float2 y = unpack2(l[i]);
                         l[i] = pack2(y.x * f[0], y.y * f[1]);
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     if (S::kTwo) fence_after();
                     if (!fresh) {
 #pragma unroll 1
-                        for (int k = 0; k < (L >> 1) * NR; k += 16) {
+                        for (int k = 16 * half; k < (L >> 1) * NR; k += 4 * S::kSoft) {
                             uint32_t y[16];
                             tm_ld16(lanes + k, y);
 #pragma unroll
@@ -337,15 +337,15 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                         uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 2; k++) {  // rows 8 i, then 8 (i + 1); slots, then slots + 8
-                            const uint32_t *v = x + h * (NR / 2) + 4 * (i + k);
+                            const uint32_t *v = x + h * (W / 2) + 4 * (i + k);
                             const float a = __uint_as_float(v[0]), b = __uint_as_float(v[1]), c = __uint_as_float(v[2]), d = __uint_as_float(v[3]);
                             l[i + k] = add2(l[i + k], add2(pack2(a, b), pack2(c, d)));
                             y[2 * k] = from_f2<BF>(a, b), y[2 * k + 1] = from_f2<BF>(c, d);
                         }
                         // transposed: a row's slots consecutive, 64 in 128 bytes, 16-byte piece c of row r at c ^ (r % 8)
                         const int r = lane & 7, k = lane >> 3;
-                        const int piece = 2 * S::kHalves * warp + 2 * h + (k & 1);
-                        const uint32_t at = pt + (piece >> 3) * (NR * 128) + (8 * (i + (k >> 1)) + r) * 128 + (((piece & 7) ^ r) << 4);
+                        const int piece = 2 * S::kHalves * quarter + 2 * h + (k & 1);
+                        const uint32_t at = pt + (piece >> 3) * (NR * 128) + (cb + 8 * (i + (k >> 1)) + r) * 128 + (((piece & 7) ^ r) << 4);
                         asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]),
                                      "r"(y[3])
                                      : "memory");
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     for (int u = 0; u < L; u++) {
                         const uint32_t n = ns * L + u, at = n % kUnits;
                         ok = ok && warp_wait(&bar.unit_full[at], n / kUnits & 1);
-                        for (int i = tid; i < (kTile - r0) * 8; i += 128)
+                        for (int i = st; i < (kTile - r0) * 8; i += kThreads)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(units + at * kUnit + r0 * 128 + i * 16), "r"(0) : "memory");
                     }
                 }
@@ -378,8 +378,8 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) t += __shfl_xor_sync(~0u, t, o);
                     const int c = 8 * i + col0 + e;
-                    if (lane < 4) st_f(scratch + (warp * NR + c) * 4, t);
-                    if (warp == 0 && lane < 4) st_f(scratch + (5 * NR + c) * 4, -z[2 * i + e]);
+                    if (lane < 4) st_f(scratch + (quarter * NR + c) * 4, t);
+                    if (quarter == 0 && lane < 4) st_f(scratch + (5 * NR + c) * 4, -z[2 * i + e]);
                 }
             }
             vote(false);
@@ -396,10 +396,10 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
             vote(false);
             // a warp has 32 latents of each 128, a lane one, columns are rows of the item
             if (whole) {  // two lanes swap, so that each writes two latents of one row
-                uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)block * p.heads * p.out.head + 32 * warp + (lane & ~1);
+                uint16_t *out = p.out.d + (int64_t)w.token * p.out.token + (int64_t)block * p.heads * p.out.head + 32 * quarter + (lane & ~1);
                 const int rows = p.line.item_tokens < w.left ? used : w.left * p.heads, heads = p.q_heads - block * p.heads;
 #pragma unroll 1
-                for (int k = 0; k < NR; k += 16) {
+                for (int k = 16 * half; k < NR; k += 4 * S::kSoft) {
                     float f[16];
                     uint16_t *row[8];
 #pragma unroll
@@ -422,19 +422,17 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
                     }
                 }
             } else {
-                float *po = p.part_o + (int64_t)part * NR * p.c.latent + 32 * warp + lane;
+                float *po = p.part_o + ((int64_t)part * NR + cb) * p.c.latent + 32 * quarter + lane;
 #pragma unroll 1
                 for (int u = 0; u < L >> 1; u++) {
                     float *to = po + 128 * u;
-                    uint32_t y[NR];
-                    if constexpr (NR == 64)
-                        kv::tm_ld64(lanes + u * NR, y), kv::tm_ld_wait(y);
-                    else if constexpr (NR == 32)
-                        kv::tm_ld32(lanes + u * NR, y);
+                    uint32_t y[W];
+                    if constexpr (W == 32)
+                        kv::tm_ld32(lanes + u * NR + cb, y);
                     else
                         tm_ld16(lanes + u * NR, y);
 #pragma unroll
-                    for (int e = 0; e < NR; e++, to += p.c.latent) *to = __uint_as_float(y[e]);
+                    for (int e = 0; e < W; e++, to += p.c.latent) *to = __uint_as_float(y[e]);
                 }
             }
             fence_before();  // O is read before the next part's first P is announced
@@ -830,7 +828,7 @@ int64_t most_items(const AttendParams &p) {
 }
 bool cut(const AttendParams &p, int num_sms) {
     const int64_t items = most_items(p), steps = ((int64_t)p.bt.max_kv + kStep - 1) / kStep;
-    return items > num_sms >> p.line.pair || steps > 2;
+    return items > num_sms >> p.line.pair || steps > 1;
 }
 int ctas(const AttendParams &p, int num_sms) {
     const int64_t items = most_items(p);
