@@ -1,26 +1,32 @@
 // Absorbed latent attention on the 5th-generation tensor cores. All heads read the same cached vectors, so the rows of an
-// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots (64 of an 8-bit cache). Both products have the cache as their A
-// operand, straight from shared memory in the one layout that the copies leave it in:
-//   S^T [slots, NR rows]     = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
-//   O^T [latent, NR rows]  += C^T P^T                    A: latents are M = 128, slots K (M-major)
-// so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most; rows as M would take all of it), and few
-// rows cost few columns instead of an unused part of M = 128. P^T goes to shared memory as the B operand.
+// item are (token, head) pairs, NR = 16, 32 or 64 of them, and a tile is 128 slots (64 of an 8-bit cache). Both products have the
+// cache as their A operand, straight from shared memory in the one layout that the copies leave it in:
+//   S^T [slots, NR rows]   = [C | K] [Q | Q_rope]^T    A: slots are M, latents K (K-major)
+//   O^T [latent, NR rows] += C^T P^T                   A: latents are M = 128, slots K (M-major)
+// so that O takes latent / 128 * NR columns of tensor memory (256 of 512 at most), and few rows cost few columns instead of an
+// unused part of M = 128. (128 rows would take all 512 columns for O and leave none for S.) P^T goes to shared memory as B.
 //
 // Persistent, one CTA an SM, work cut by latent_line.cuh. Roles:
-//   warps 0-3   softmax of a tile: a warp has a quarter of the slots, a thread four (two) slots' values of every eighth pair of rows.
-//               P = 2^(s scale log2 e - m) in fp32 with the maximum m of the tiles before; one vote of the four warps tells whether a
-//               P is above 2^8, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to
+//   warps 0-3   (64 rows: 8-11 too, which take the last 32) softmax of a tile: a warp has a quarter of the slots, a thread four (two)
+//               slots of every eighth pair of rows. P = 2^(s scale log2 e - m) in fp32 with the maximum m of the tiles before; one vote tells
+//               whether a P is above 2^8, and only then maxima are taken across the slots, m is raised and O multiplied. P is rounded to
 //               the cache's type, as the tensor cores take it; the sums are of P in fp32, kept by each thread for its slots and added at
 //               the item's end.
-//   warp 4      tensor copies of units of 64 latents x 128 slots (128-byte swizzle), a lane each: one lane after another, with a wait
-//               each, they took 450 cycles a unit and held everything up.
-//   warp 5      issues tcgen05.mma: S of a tile, then O += C^T P^T, then S of the next. The warp's number comes from a shuffle, by which
-//               the compiler knows its branches to be uniform and keeps descriptors in uniform registers (without: 70 cycles a product).
+//   warp 4      (16 bits) tensor copies of units of 64 latents of a tile (128-byte swizzle), a lane each: one lane after another, with a wait
+//               each, they took 450 cycles a unit and held everything up. Then the next tile's prefetch to L2.
+//   warp 5      issues tcgen05.mma. The warp's number comes from a shuffle, by which the compiler knows its branches to be uniform and
+//               keeps descriptors in uniform registers (without: 70 cycles a product).
 //   warp 6      walks the work and hands the parts out.
-//   warp 7      tensor copies of queries, rotary parts and powers of two.
-//   warps 8-15  (8 bits, instead of warp 4) load codes, a warp a unit, and turn them into elements. Codes stay in registers on
+//   warp 7      tensor copies of queries and rotary parts.
+//   warps 8-15  (8 bits, instead of warp 4) load codes and powers, a warp a unit, and turn them into elements. Codes stay in registers on
 //               their way: shared memory has no place for more than a quarter of a tile's, which let too few be under way.
 // Every wait is bounded; one that runs out is recorded and ends the role.
+//
+// Measured: 48 sequences of 9000 tokens, 128 heads: 94 us (85, and 9 for the join), 3.2 TB/s of the 6.8 of a plain copy, DRAM read
+// once (307 MB), the tensor pipe 29 % busy. Shared memory holds one tile (128 KB) beside 72 KB of queries, so an SM's time is the chain of a
+// tile: its scores (36 products of 50 cycles: M128 N64 runs no faster), softmax, outputs (32), and the refill behind them. 8 bits, 96
+// of 7000, 32 heads: 98 us, 2.3 TB/s; there the chain is conversion (about 1500 cycles of 64 slots), scores, softmax, outputs over two places,
+// and shared memory passes 4 KB a slot, half its bandwidth over the call. One sequence of 777: 12 us, latency (launch, plan, two tiles, join).
 #include "latent_line.cuh"
 
 namespace ftmoe {
@@ -54,8 +60,9 @@ struct Shape {
     // (48 x 9000 tokens, 128 heads: 93.4 us, 99.3 with all 64 in one).
     static constexpr int kCols = NR == 64 ? 32 : NR, kSoft = 4 * NR / kCols;
     static constexpr int kWarps = Q8 ? 16 : 4 + kSoft, kThreads = kWarps * 32;
-    // Slots of a tile: 128 read least from shared memory. Of codes 64, and a place for two tiles, so that one is turned into elements while
-    // the other is worked on, and two tiles' products in turn.
+    // Slots of a tile. 128 issue the fewest products (16 heads, 64 x 2000: 39 us, 46 with 64; 64 rows, 48 x 9000: 94, 113 with 64 slots
+    // and four softmax warps). Of codes 64, with places for two tiles: one is turned into elements while the other is worked on (98 us,
+    // 108 with 128), and its scores are formed during the other's softmax (104 without).
     static constexpr int kTile = Q8 ? 64 : 128, kHalves = kTile / 64;
     static constexpr bool kTwo = Q8;
     static constexpr int kUnit = kTile * 128;   // 64 latents of a tile's slots
@@ -815,8 +822,9 @@ __global__ void __launch_bounds__(kJoinThreads, FIRST == 2 ? 4 : 1) absorb_combi
     if (lane == 0 && p.lse) p.lse[(int64_t)(token + t) * p.q_heads + h] = sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place. With 8 bits
-// 32 at most: codes, elements and more queries do not fit shared memory.
+// Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place (64 x 2000 tokens: 16
+// heads 39 us, 43 as 32 rows, 53 as 64; 32 heads 42, 54 as 64). With 8 bits 32 at most: two tiles of elements and more queries do not fit
+// shared memory.
 int rows_of(const AttendParams &p) {
     const int64_t n = (int64_t)p.q_heads * p.bt.max_q;
     return n <= 16 ? 16 : n <= 32 || p.c.bits == 8 ? 32 : 64;
@@ -826,9 +834,10 @@ int rows_of(const AttendParams &p) {
 int64_t most_items(const AttendParams &p) {
     return (int64_t)((p.bt.max_q + p.line.item_tokens - 1) / p.line.item_tokens) * p.bt.batch * p.line.blocks;
 }
+// One sequence of 16 heads and two steps 9.6 us cut, 10.1 whole; 64 sequences of four steps 20.4 and 16.0, of 16 steps 39.7 and 45.9; 152
+// of eight steps 47.0 and 39.2; two waves: 256 of eight steps 69.8 and 63.6, 160 of 16 steps 76.6 and 100.
 bool cut(const AttendParams &p, int num_sms) {
-    const int64_t items = most_items(p), steps = ((int64_t)p.bt.max_kv + kStep - 1) / kStep;
-    return items > num_sms >> p.line.pair || steps > 1;
+    return cut_pays(most_items(p), ((int64_t)p.bt.max_kv + kStep - 1) / kStep, num_sms >> p.line.pair, 2, 0);
 }
 int ctas(const AttendParams &p, int num_sms) {
     const int64_t items = most_items(p);
@@ -873,7 +882,7 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
     p.line.blocks = (p.q_heads + p.heads - 1) / p.heads;
     p.line.item_tokens = rows / p.heads, p.line.batch = p.bt.batch, p.line.max_q = p.bt.max_q, p.line.causal = p.causal;
     // Two blocks of heads read the same cached tokens at the same time, on two SMs: one of them mostly finds them in L2 (one after the
-    // other, 128 heads read them from memory twice).
+    // other, 128 heads read them from memory twice: 32 x 4000 tokens 74 us, in pairs 61; 64 x 2000 of 32 heads are one block).
     p.line.pair = p.line.blocks % 2 == 0 ? 1 : 0;
     p.line.blocks >>= p.line.pair;
     p.line.join = nullptr, p.part_o = nullptr, p.part_ml = nullptr;

@@ -11,6 +11,10 @@
 //   warp 9          issues tcgen05.mma, tile 0's and tile 1's in turn: O_t += P_t V, then S_t = Q_t K^T of the next step.
 //   warp 11         walks the work and hands the parts out.
 // Every wait is bounded; one that runs out is recorded and ends the role.
+//
+// Measured: a prompt of 4096, 32 heads: 132 us, 1.30 PFLOP/s of the 1.94 of a large library product (tensor pipe 60 % busy: 32 heads x 16
+// items of unequal length, their starts and ends, and 6 us of join); 2048 tokens over 25000 rows, 16 heads: 336 us, 1.50 PFLOP/s; five
+// chunks of at most 301: 26 us, cold starts of two kernels and a few steps' latency.
 #include "latent_line.cuh"
 
 namespace ftmoe {
@@ -519,10 +523,9 @@ cudaError_t launch(const ExpandParams &p, int C, cudaStream_t st) {
 }
 
 int64_t most_items(const ExpandParams &p) { return (int64_t)((p.max_q + kRows - 1) / kRows) * p.batch * p.heads; }
-bool cut(const ExpandParams &p, int num_sms) {
-    const int64_t items = most_items(p), steps = ((int64_t)p.max_kv + kStep - 1) / kStep;
-    return items > num_sms || steps > 6 || steps > (items * (steps + kItemCost) + num_sms - 1) / num_sms + 1;
-}
+// 8 items of two steps 10.9 us cut, 9.2 whole, of four 11.4 and 12.8; 64 of eight steps 23.9 and 20.8, of 16 steps 32.0 and 34.0; 152 of 16
+// steps 38.9 and 35.5; 304 of four, two waves, 34.7 and 36.5.
+bool cut(const ExpandParams &p, int num_sms) { return cut_pays(most_items(p), ((int64_t)p.max_kv + kStep - 1) / kStep, num_sms, 1, 1); }
 int ctas(const ExpandParams &p, int num_sms) {
     const int64_t items = most_items(p);
     if (!cut(p, num_sms)) return (int)items;

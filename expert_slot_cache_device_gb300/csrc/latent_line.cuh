@@ -15,8 +15,18 @@ using kv::su32;
 using kv::warp_wait;
 
 constexpr int kStep = 128;    // slots of a step
-constexpr int kItemCost = 2;  // what an item's start and end take, in steps
+constexpr int kItemCost = 2;  // what an item's start and end take, in steps (its queries, its first S, its outputs: 6000 to 9000 cycles)
 constexpr int kParts = 4;     // entries of the ring of parts
+
+// Whether `items` of at most `steps` steps are cut evenly for `have` places and joined, or each goes whole to a place, in as many waves. The
+// join, and starts in the middle of items, cost about 8 steps where every place has a part (what an item's joining kernel reads), less with
+// fewer. The host knows bounds of the lengths only: a mean of 3/4 is assumed. `waves`: the most that whole items may need.
+inline bool cut_pays(int64_t items, int64_t steps, int64_t have, int64_t waves, int64_t extra) {
+    const int64_t n = (items + have - 1) / have;
+    if (n > waves) return true;
+    const int64_t share = (items * (3 * steps / 4 + kItemCost) + have - 1) / have;
+    return n * (steps + kItemCost) > share + kItemCost + 8 * (items < have ? items : have) / have + extra;
+}
 
 __device__ __forceinline__ int item_count(const Line &l, const kv::Seq &s) {
     return (int)((uint32_t)(s.q_len + l.item_tokens - 1) / (uint32_t)l.item_tokens);

@@ -621,7 +621,8 @@ int ftmoe_latent_read(const ftmoe_latent_cache *kv, const ftmoe_kv_batch *batch,
 /* Absorbed attention of the new tokens over the cached ones:
  *   s_j = scale * (q . c_j + q_rope . k_j), l = sum_j exp(s_j), out = sum_j exp(s_j) c_j / l,
  *   lse = log l, over the slots j <= kv_len - q_len + i of new token i (causal != 0), or all below
- *   kv_len (causal = 0). A row that sees nothing gives out = 0, lse = -inf.
+ *   kv_len (causal = 0). A row that sees nothing gives out = 0, lse = -inf; so does, causal or not, a new
+ *   token without a slot of its own (kv_len - q_len + i < 0).
  *   q, out      [tokens, q_heads, latent]; out may be q itself (the same rows and strides; no other overlap);
  *   q_rope      [tokens, q_heads, rope];
  *   scale       positive and finite;

@@ -33,6 +33,10 @@ def _built():
     ([1, 2], [900, 40], 200, 512, 16, BF, 16),                                      # four: pairs of blocks
     ([2, 1], [90, 1500], 600, 128, 256, HF, 16),
     ([1], [40000], 128, 512, 64, BF, 8),                                            # one sequence over all SMs
+    ([1] * 100, [(67 * i) % 640 for i in range(100)], 16, 256, 64, BF, 16),         # whole items of several steps
+    ([1] * 60, [300 + (89 * i) % 400 for i in range(60)], 128, 256, 32, HF, 16),    # pairs of them
+    ([1] * 250, [(31 * i) % 513 for i in range(250)], 32, 128, 16, BF, 8),          # two waves
+    ([2] * 70, [2 + (57 * i) % 500 for i in range(70)], 130, 128, 16, BF, 16),
 ])
 def test_attend_plans(q_lens, kv_lens, heads, latent, page, dt, bits):
     check_attend(World(q_lens, kv_lens, latent, 32, page, dt, bits, seed=heads), heads)
@@ -50,7 +54,8 @@ def test_nothing_cached(bits):
 
 @pytest.mark.parametrize("q_lens,kv_lens,heads", [([5] * 450, [3 + (23 * i) % 120 for i in range(450)], 1),
                                                   ([i % 7 for i in range(900)], [(11 * i) % 90 for i in range(900)], 2),
-                                                  ([5000], [5000], 1), ([4200, 300], [4300, 400], 2)])
+                                                  ([5000], [5000], 1), ([4200, 300], [4300, 400], 2),
+                                                  ([100, 256, 7], [700, 1000, 500], 40), ([200] * 9, [1100, 200, 900, 201, 345, 600, 777, 1024, 1023], 16)])
 def test_expand_plans(q_lens, kv_lens, heads):
     check_expand(q_lens, kv_lens, heads, 64, 16, BF, seed=heads)
 
