@@ -129,7 +129,7 @@ __device__ __forceinline__ void plan_alone(const P &p, Walk<P> &w, int32_t *stat
     w.left = 0;
     if (me.at >= C) return;
     const long long u0 = kv::unit_start(me.at, C, W), u1 = kv::unit_start(me.at + 1, C, W);
-    long long before = 0;  // units of the sequences before this round's
+    long long before = 0;  // units of the sequences before these
     for (int b0 = 0; b0 < l.batch; b0 += 32) {
         const kv::Seq s = b0 + lane < l.batch ? p.seq(b0 + lane, nullptr) : kv::Seq{0, 0, 0};
         const int per = units(s);
