@@ -61,7 +61,7 @@ def _ints(t: torch.Tensor, name: str, dims: int, dev: Optional[int] = None) -> t
         raise ValueError(f"{name}: needs an int32 device tensor of {dims} dimension(s)")
     if dev is not None and t.get_device() != dev:
         raise ValueError(f"{name}: on device {t.get_device()}, the call's is {dev}")
-    if t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
+    if not t.is_contiguous() and t.numel() and t.stride(-1) != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name}: needs consecutive elements")
     return t
 

@@ -54,9 +54,10 @@ def _flat(t: torch.Tensor, name: str, dtype, dev: int, dim: int, rows: Optional[
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or len(shape := t.shape) != 2:
         raise ValueError(f"{name}: needs a {dtype} tensor [rows, {dim}] on device {dev}")
     n, d = shape
-    if d != dim or t.stride(1) != 1 or (rows is not None and n != rows):
+    row, one = t.stride()
+    if d != dim or one != 1 or (rows is not None and n != rows):
         raise ValueError(f"{name}: shape {list(shape)}, needs [{rows if rows is not None else 'rows'}, {dim}] with contiguous rows")
-    return t.data_ptr(), t.stride(0) if n > 1 else dim, n
+    return t.data_ptr(), row if n > 1 else dim, n
 
 
 def _lse(t: Optional[torch.Tensor], n: int, heads: int, dev: int):
@@ -199,6 +200,14 @@ class ExpandedBatch(Workspaces, Status):
         self.max_q, self.max_kv = int(max_q), int(max_kv)
         Workspaces.__init__(self, cu_q.device)
         Status.__init__(self, cu_q.device)
+        self._refs = {}
+
+    def _ref(self, n: int, m: int):
+        ref = self._refs.get((n, m))
+        if ref is None:
+            ref = self._refs[n, m] = ctypes.byref(F.RowBatchView(self.cu_q.data_ptr(), self.cu_kv.data_ptr(), self.batch, n, m, self.max_q,
+                                                                 self.max_kv, self._status.data_ptr()))
+        return ref
 
     def attend(self, q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
                causal: bool = True, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -208,9 +217,10 @@ class ExpandedBatch(Workspaces, Status):
         ``lse`` fp32 [tokens, heads] receives the log-sum-exp. Returns out [tokens, heads, v_dim]."""
         if q.dtype not in _DTYPES:
             raise ValueError(f"q: {q.dtype}, bfloat16 or float16")
-        if k.dim() != 3 or v.dim() != 3 or k_rope.dim() != 2:
+        k_shape, v_shape, r_shape = k.shape, v.shape, k_rope.shape
+        if len(k_shape) != 3 or len(v_shape) != 3 or len(r_shape) != 2:
             raise ValueError("k and v need three dimensions, k_rope two")
-        dt, dev, nope, rope, vd = q.dtype, self._dev, k.shape[2], k_rope.shape[1], v.shape[2]
+        dt, dev, nope, rope, vd = q.dtype, self._dev, k_shape[2], r_shape[1], v_shape[2]
         qr, n, heads = _rows(q, "q", dt, dev, nope + rope)
         kr, m, _ = _rows(k, "k", dt, dev, nope, heads)
         vr, _, _ = _rows(v, "v", dt, dev, vd, heads, m)
@@ -221,8 +231,7 @@ class ExpandedBatch(Workspaces, Status):
         la = _lse(lse, n, heads, dev)
         if n == 0 or heads == 0:
             return out
-        ref = ctypes.byref(F.RowBatchView(self.cu_q.data_ptr(), self.cu_kv.data_ptr(), self.batch, n, m, self.max_q, self.max_kv,
-                                          self._status.data_ptr()))
+        ref = self._ref(n, m)
         key = (n, m, heads, nope, rope, vd, causal)
         need = self._bytes.get(key)
         if need is None:
