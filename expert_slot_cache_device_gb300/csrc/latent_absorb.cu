@@ -761,11 +761,13 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 // first FIRST parts may have is loaded before it is known how many there are, one trip instead of four: eight where the grid is
 // small and has nothing else to wait for, else the two that an item that is joined has, in few registers (seven parts of one
 // sequence, 16 heads: 13.5 us with the kernel before, two first 15.5; 48 sequences of 128 heads: 97 us, 100 with four first).
-constexpr int kJoinThreads = 256, kJoinRows = 8;
+// Rows of a CTA: two of a small grid, over more SMs (one sequence of 777, 16 heads: 11.9 us, with eight 12.4, with sixteen 15.1).
+template <int FIRST>
+constexpr int kJoinRows = FIRST == 2 ? 8 : 2;
 
 template <bool BF, int FIRST>
-__global__ void __launch_bounds__(kJoinThreads, FIRST == 2 ? 4 : 1) absorb_combine(const AttendParams p, int rows) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x, row = blockIdx.y * kJoinRows + warp;
+__global__ void __launch_bounds__(32 * kJoinRows<FIRST>, FIRST == 2 ? 4 : 1) absorb_combine(const AttendParams p, int rows) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x, row = blockIdx.y * kJoinRows<FIRST> + warp;
     const int of = gridDim.x >> p.line.pair, rank = p.line.pair && c >= of ? 1 : 0, end = (rank + 1) * of;  // (Where)
     const int t = row / p.heads;
     if (t >= p.line.item_tokens) return;
@@ -864,7 +866,8 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     if (rc != cudaSuccess) return rc;
     absorb_kernel<BF, Q8, NR><<<C, S::kThreads, S::kSmem, st>>>(p, m);
     if ((rc = cudaGetLastError()) != cudaSuccess || !p.line.join) return rc;
-    return kv::launch_after(C * (NR / kJoinRows) <= 304 ? absorb_combine<BF, 8> : absorb_combine<BF, 2>, dim3(C, NR / kJoinRows), kJoinThreads, 0, st, p, NR);
+    auto join = [&](auto kern, int per) { return kv::launch_after(kern, dim3(C, NR / per), 32 * per, 0, st, p, NR); };
+    return C * NR <= 2432 ? join(absorb_combine<BF, 8>, kJoinRows<8>) : join(absorb_combine<BF, 2>, kJoinRows<2>);
 }
 
 template <bool BF>
