@@ -844,7 +844,7 @@ bool cut(const AttendParams &p, int num_sms) {
 int ctas(const AttendParams &p, int num_sms) {
     const int64_t items = most_items(p);
     if (!cut(p, num_sms)) return (int)items << p.line.pair;
-    const int64_t most = items * (p.bt.max_kv / kStep + 1 + kItemCost), have = num_sms >> p.line.pair;
+    const int64_t have = num_sms >> p.line.pair, most = items < have ? items * (p.bt.max_kv / kStep + 1 + kItemCost) : have;
     return (int)(most < have ? (most > 0 ? most : 1) : have) << p.line.pair;
 }
 

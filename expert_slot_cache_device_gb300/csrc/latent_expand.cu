@@ -529,7 +529,7 @@ bool cut(const ExpandParams &p, int num_sms) { return cut_pays(most_items(p), ((
 int ctas(const ExpandParams &p, int num_sms) {
     const int64_t items = most_items(p);
     if (!cut(p, num_sms)) return (int)items;
-    const int64_t most = items * (p.max_kv / kStep + 1 + kItemCost);
+    const int64_t most = items < num_sms ? items * (p.max_kv / kStep + 1 + kItemCost) : num_sms;
     return (int)(most < num_sms ? (most > 0 ? most : 1) : num_sms);
 }
 

@@ -42,6 +42,24 @@ def test_attend_plans(q_lens, kv_lens, heads, latent, page, dt, bits):
     check_attend(World(q_lens, kv_lens, latent, 32, page, dt, bits, seed=heads), heads)
 
 
+def test_loose_bounds():
+    """Bounds far above the lengths (2^31 - 1 new tokens, 2^30 slots where the table allows them) only cost time."""
+    from expert_slot_cache_device_gb300.kv_cache import KVBatch
+    from expert_slot_cache_device_gb300.latent_cache import ExpandedBatch
+
+    w = World([3, 1], [300, 64], 256, 32, 16, BF, 16, seed=7)
+    w.batch = KVBatch(w.table.cuda(), ints(w.kv_lens), ints(w.cu), max_q=2 ** 31 - 1, max_kv=w.table.shape[1] * 16)
+    check_attend(w, 20)
+    b, q, k, key, v, cu_q, cu_kv = expand_world([30, 200], [500, 200], 2, 64, 32, BF)
+    b = ExpandedBatch(ints(cu_q), ints(cu_kv), 2 ** 31 - 1, 2 ** 30)
+    out = b.attend(q, k, key, v)
+    assert b.status() == 0
+    for i in range(2):
+        t, r = slice(cu_q[i], cu_q[i + 1]), slice(cu_kv[i], cu_kv[i + 1])
+        o, _, ot, _ = lref.expanded(q[t].cpu(), k[r].cpu(), key[r].cpu(), v[r].cpu(), 96 ** -0.5, True)
+        check_rows(i, out[t], o, ot, None, None, None)
+
+
 @pytest.mark.parametrize("bits", [16, 8])
 def test_nothing_cached(bits):
     w = World([1, 2, 0], [0, 0, 0], 256, 32, 16, BF, bits)
