@@ -184,7 +184,7 @@ class ExpandedBatch(Workspaces, Status):
 
     cu_q    int32 [batch + 1]: first row of each sequence's new tokens in the token arrays
     cu_kv   int32 [batch + 1]: first row of its keys and values, the new tokens' the last of them
-    max_q   upper bound of the new tokens of one sequence, max_kv of its key rows
+    max_q   upper bound of the new tokens of one sequence, max_kv of its key rows (either may be above what a call has)
     The tensors are read when the kernels run."""
 
     def __init__(self, cu_q: torch.Tensor, cu_kv: torch.Tensor, max_q: int, max_kv: int):
@@ -206,7 +206,7 @@ class ExpandedBatch(Workspaces, Status):
         ref = self._refs.get((n, m))
         if ref is None:
             ref = self._refs[n, m] = ctypes.byref(F.RowBatchView(self.cu_q.data_ptr(), self.cu_kv.data_ptr(), self.batch, n, m, self.max_q,
-                                                                 self.max_kv, self._status.data_ptr()))
+                                                                 min(self.max_kv, m), self._status.data_ptr()))
         return ref
 
     def attend(self, q: torch.Tensor, k: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,

@@ -641,7 +641,8 @@ int ftmoe_latent_attention(const ftmoe_latent_cache *kv, const ftmoe_kv_batch *b
 /* The sequences of an expanded call: sequence b has new tokens cu_q[b] .. cu_q[b + 1] - 1 of the token
  * arrays and keys and values in rows cu_kv[b] .. cu_kv[b + 1] - 1, the new tokens' the last of them.
  * Entries below their predecessor or out of range, and sequences longer than max_q or max_kv, give
- * FTMOE_ERR_STATE in d_status (nullable, sticky) and are cut to their range. */
+ * FTMOE_ERR_STATE in d_status (nullable, sticky) and are cut to their range. max_q and max_kv are host-side
+ * upper bounds, as in ftmoe_kv_batch; max_kv is at most 2^30. */
 typedef struct {
     const int32_t *d_cu_q, *d_cu_kv; /* [batch + 1] */
     int32_t batch, tokens, rows, max_q, max_kv;
