@@ -39,7 +39,6 @@ int attend_params(const ftmoe_latent_cache *kvc, const ftmoe_kv_batch *batch, in
     if (q_heads <= 0 || q_heads > 65535) return fail(FTMOE_ERR_INVALID_ARG, "q_heads=%d", q_heads);
     if ((int64_t)p.bt.tokens * q_heads > INT32_MAX)
         return fail(FTMOE_ERR_INVALID_ARG, "%d tokens of %d heads: more than 2^31 - 1 rows", p.bt.tokens, q_heads);
-    if (p.bt.max_q > p.bt.tokens) p.bt.max_q = p.bt.tokens;  // (no sequence is longer: a loose bound would cost rows and overflow items)
     p.q_heads = q_heads, p.causal = causal != 0;
     return FTMOE_OK;
 }
