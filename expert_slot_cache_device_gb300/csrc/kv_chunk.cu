@@ -757,17 +757,15 @@ bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool box_map(CUtensorMap &m, Elem type, const void *x, const int64_t (&dims)[3], int64_t stride1, int64_t stride2, const int (&box)[3],
+bool box_map(CUtensorMap &m, bool bf16, const void *x, const int64_t (&dims)[3], int64_t stride1, int64_t stride2, const int (&box)[3],
              bool swizzle) {
     const EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t d[3] = {(cuuint64_t)dims[0], (cuuint64_t)dims[1], (cuuint64_t)dims[2]}, st[2] = {(cuuint64_t)stride1, (cuuint64_t)stride2};
     const cuuint32_t b[3] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]}, es[3] = {1, 1, 1};
-    const CUtensorMapDataType t = type == Elem::U8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type == Elem::BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const CUtensorMapSwizzle sw = swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-    return fn(&m, t, 3, const_cast<void *>(x), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(&m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(x), d, st, b, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Whether the call's items are cut. Not if there is an SM for each, and the longest has few steps and hardly more than an

@@ -74,8 +74,8 @@ constexpr uint32_t kInstrM = (kInstr<BF, N, B_MN> & ~(31u << 24)) | ((A_MN ? 1u 
 // Operand of 128-byte rows with the 128-byte swizzle, groups of eight rows 1024 bytes apart
 // (stride offset), as the low word of its descriptor; the high word is kDescHi. K-major: rows are M
 // or N, a K = 16 step 32 bytes further in the row. MN-major: rows are K, the next 64 elements of
-// N `lead` bytes further (leading offset). Shared addresses fit the field (in a cluster, bits above them name the
-// CTA), so a step of n bytes adds n / 16.
+// N `lead` bytes further (leading offset). Shared addresses fit the field (in a cluster, as the 4-bit products'
+// kernel runs, bits above them name the CTA), so a step of n bytes adds n / 16.
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) { return ((addr & 0x3ffffu) >> 4) | ((lead >> 4) << 16); }
 
@@ -268,10 +268,9 @@ bool page_map(CUtensorMap &m, const View &c, bool keys, bool bf16, int box_slots
 bool query_map(CUtensorMap &m, const AttendParams &p, bool bf16);
 // Tensor map of rows: [row][column], boxes of 64 columns x box_rows rows; zeros past the ends.
 bool row_map(CUtensorMap &m, const void *x, int cols, int rows, int64_t stride, int box_rows, bool bf16);
-// Tensor map of three axes, the first consecutive: elements of 8 bits or of a 16-bit type, strides in bytes, with the 128-byte
-// swizzle or none; zeros past the ends.
-enum class Elem { U8, BF16, F16 };
-bool box_map(CUtensorMap &m, Elem type, const void *x, const int64_t (&dims)[3], int64_t stride1, int64_t stride2, const int (&box)[3],
+// Tensor map of three axes, the first consecutive: elements of 16 bits, strides in bytes, with the 128-byte swizzle or none; zeros
+// past the ends.
+bool box_map(CUtensorMap &m, bool bf16, const void *x, const int64_t (&dims)[3], int64_t stride1, int64_t stride2, const int (&box)[3],
              bool swizzle);
 
 }  // namespace kv

@@ -851,16 +851,15 @@ int ctas(const AttendParams &p, int num_sms) {
 template <bool BF, bool Q8, int NR>
 cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     using S = Shape<Q8, NR>;
-    const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
     const int box = 1 << p.c.page_shift < S::kTile ? 1 << p.c.page_shift : S::kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
     Maps m;
-    bool ok = kv::box_map(m.q, e, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, true) &&
-              kv::box_map(m.q_rope, e, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, true) &&
-              kv::box_map(m.rope, e, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+    bool ok = kv::box_map(m.q, BF, p.q.d, {p.c.latent, p.q_heads, p.bt.tokens}, 2 * p.q.head, 2 * p.q.token, {64, p.heads, per}, true) &&
+              kv::box_map(m.q_rope, BF, p.q_rope.d, {p.c.rope, p.q_heads, p.bt.tokens}, 2 * p.q_rope.head, 2 * p.q_rope.token, {64, p.heads, per}, true) &&
+              kv::box_map(m.rope, BF, p.c.pages + rope_at(p.c.latent, p.c.bits), {p.c.rope, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     const int row = rope_at(p.c.latent, p.c.bits) / 2 + p.c.rope;
-    ok = ok && kv::box_map(m.all, e, p.c.pages, {row, slots, p.c.num_pages}, p.c.slot, p.c.page, {kWide, box, 1}, false);
+    ok = ok && kv::box_map(m.all, BF, p.c.pages, {row, slots, p.c.num_pages}, p.c.slot, p.c.page, {kWide, box, 1}, false);
     if (!Q8)
-        ok = ok && kv::box_map(m.lat, e, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
+        ok = ok && kv::box_map(m.lat, BF, p.c.pages, {p.c.latent, slots, p.c.num_pages}, p.c.slot, p.c.page, {64, box, 1}, true);
     if (!ok) return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<absorb_kernel<BF, Q8, NR>>(S::kSmem);
     if (rc != cudaSuccess) return rc;

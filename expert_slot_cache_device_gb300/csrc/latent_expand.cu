@@ -506,14 +506,13 @@ __global__ void __launch_bounds__(kJoinThreads) expand_combine(const ExpandParam
 template <bool BF, int D>
 cudaError_t launch(const ExpandParams &p, int C, cudaStream_t st) {
     using S = Shape<D>;
-    const kv::Elem e = BF ? kv::Elem::BF16 : kv::Elem::F16;
     Maps m;
     const bool keys = p.rows > 0;  // (without one, no chunk's rows are ever seen)
     const void *some = p.q.d;
-    if (!kv::box_map(m.q, e, p.q.d, {p.nope + p.rope, p.heads, p.tokens}, 2 * p.q.head, 2 * p.q.token, {64, 1, 128}, true) ||
-        !kv::box_map(m.k, e, keys ? p.k.d : some, {p.nope, p.heads, keys ? p.rows : 1}, keys ? 2 * p.k.head : 16, keys ? 2 * p.k.token : 16, {64, 1, 128}, true) ||
-        !kv::box_map(m.v, e, keys ? p.v.d : some, {p.vdim, p.heads, keys ? p.rows : 1}, keys ? 2 * p.v.head : 16, keys ? 2 * p.v.token : 16, {64, 1, 128}, true) ||
-        !kv::box_map(m.key, e, keys ? p.key : some, {p.rope, keys ? p.rows : 1, 1}, keys ? 2 * p.key_stride : 16, keys ? 2 * p.key_stride : 16, {64, 128, 1}, true))
+    if (!kv::box_map(m.q, BF, p.q.d, {p.nope + p.rope, p.heads, p.tokens}, 2 * p.q.head, 2 * p.q.token, {64, 1, 128}, true) ||
+        !kv::box_map(m.k, BF, keys ? p.k.d : some, {p.nope, p.heads, keys ? p.rows : 1}, keys ? 2 * p.k.head : 16, keys ? 2 * p.k.token : 16, {64, 1, 128}, true) ||
+        !kv::box_map(m.v, BF, keys ? p.v.d : some, {p.vdim, p.heads, keys ? p.rows : 1}, keys ? 2 * p.v.head : 16, keys ? 2 * p.v.token : 16, {64, 1, 128}, true) ||
+        !kv::box_map(m.key, BF, keys ? p.key : some, {p.rope, keys ? p.rows : 1, 1}, keys ? 2 * p.key_stride : 16, keys ? 2 * p.key_stride : 16, {64, 128, 1}, true))
         return cudaErrorInvalidValue;
     cudaError_t rc = kv::allow_smem<expand_kernel<BF, D>>(S::kSmem);
     if (rc != cudaSuccess) return rc;
