@@ -759,7 +759,7 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 
 // Joins the parts of the item that CTA c of the kernel before started: a warp a row, a lane four latents at a time. What the
 // first FIRST parts may have is loaded before it is known how many there are, one trip instead of four: eight where the grid is
-// small and has nothing else to wait for, else the two that an item that is joined has, in few registers (seven parts of one
+// small (16 rows an SM at most, whose CTAs all run at once) and has nothing else to wait for, else the two that an item that is joined has, in few registers (seven parts of one
 // sequence, 16 heads: 13.5 us with the kernel before, two first 15.5; 48 sequences of 128 heads: 97 us, 100 with four first).
 // Rows of a CTA: two of a small grid, over more SMs (one sequence of 777, 16 heads: 11.9 us, with eight 12.4, with sixteen 15.1).
 template <int FIRST>
@@ -849,7 +849,7 @@ int ctas(const AttendParams &p, int num_sms) {
 }
 
 template <bool BF, bool Q8, int NR>
-cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
+cudaError_t launch(const AttendParams &p, int C, int num_sms, cudaStream_t st) {
     using S = Shape<Q8, NR>;
     const int box = 1 << p.c.page_shift < S::kTile ? 1 << p.c.page_shift : S::kTile, slots = 1 << p.c.page_shift, per = p.line.item_tokens;
     Maps m;
@@ -866,14 +866,15 @@ cudaError_t launch(const AttendParams &p, int C, cudaStream_t st) {
     absorb_kernel<BF, Q8, NR><<<C, S::kThreads, S::kSmem, st>>>(p, m);
     if ((rc = cudaGetLastError()) != cudaSuccess || !p.line.join) return rc;
     auto join = [&](auto kern, int per) { return kv::launch_after(kern, dim3(C, NR / per), 32 * per, 0, st, p, NR); };
-    return C * NR <= 2432 ? join(absorb_combine<BF, 8>, kJoinRows<8>) : join(absorb_combine<BF, 2>, kJoinRows<2>);
+    return C * NR <= 16 * num_sms ? join(absorb_combine<BF, 8>, kJoinRows<8>) : join(absorb_combine<BF, 2>, kJoinRows<2>);
 }
 
 template <bool BF>
-cudaError_t launch_rows(const AttendParams &p, int C, cudaStream_t st) {
+cudaError_t launch_rows(const AttendParams &p, int C, int num_sms, cudaStream_t st) {
     const int n = rows_of(p);
-    if (p.c.bits == 8) return n == 16 ? launch<BF, true, 16>(p, C, st) : launch<BF, true, 32>(p, C, st);
-    return n == 16 ? launch<BF, false, 16>(p, C, st) : n == 32 ? launch<BF, false, 32>(p, C, st) : launch<BF, false, 64>(p, C, st);
+    if (p.c.bits == 8) return n == 16 ? launch<BF, true, 16>(p, C, num_sms, st) : launch<BF, true, 32>(p, C, num_sms, st);
+    if (n == 16) return launch<BF, false, 16>(p, C, num_sms, st);
+    return n == 32 ? launch<BF, false, 32>(p, C, num_sms, st) : launch<BF, false, 64>(p, C, num_sms, st);
 }
 
 }  // namespace
@@ -904,7 +905,7 @@ size_t attend_workspace(AttendParams &p, int num_sms, unsigned char *base) {
 
 cudaError_t launch_attend(const AttendParams &p, bool bf16, int num_sms, cudaStream_t st) {
     const int C = ctas(p, num_sms);
-    return bf16 ? launch_rows<true>(p, C, st) : launch_rows<false>(p, C, st);
+    return bf16 ? launch_rows<true>(p, C, num_sms, st) : launch_rows<false>(p, C, num_sms, st);
 }
 
 }  // namespace latent
