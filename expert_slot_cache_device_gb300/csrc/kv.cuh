@@ -62,6 +62,9 @@ __device__ __forceinline__ Seq seq_info(const Batch &bt, int b, int32_t *status)
     return seq_cut(bt, bt.cu_q[b], bt.cu_q[b + 1], bt.kv_lens[b], status);
 }
 
+// A sequence and a slot of it (below 0: none) in one word.
+__device__ __forceinline__ long long seq_slot(int b, int slot) { return (long long)b << 32 | (uint32_t)slot; }
+
 // Page of a slot of sequence b, or -1 (recorded) where the table names none.
 __device__ __forceinline__ int page_of(const View &c, const Batch &bt, int b, int slot) {
     const int page = bt.table[(int64_t)b * bt.table_stride + (slot >> c.page_shift)];

@@ -23,17 +23,14 @@ constexpr int kThreads = 128;
 template <bool BF>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
     __shared__ float2 s_cs[128];  // (cos, sin) * factor of each pair
-    __shared__ int s_seq[2];      // sequence of this token, its slot
+    __shared__ long long s_seq;   // of this token: (sequence, slot), -1 without one; one store, so that of two sequences that claim it one does
     const int t = blockIdx.x, tid = threadIdx.x;
-    if (tid == 0) s_seq[0] = -1;
+    if (tid == 0) s_seq = -1;
     __syncthreads();
     const float pos = (float)p.pos[t];
     for (int b = tid; b < p.bt.batch; b += kThreads) {
         const Seq s = seq_info(p.bt, b, p.c.status);
-        if (t >= s.q0 && t < s.q0 + s.q_len) {
-            s_seq[0] = b;
-            s_seq[1] = s.kv_len - s.q_len + (t - s.q0);
-        }
+        if (t >= s.q0 && t < s.q0 + s.q_len) s_seq = seq_slot(b, s.kv_len - s.q_len + (t - s.q0));
     }
     for (int i = tid; i < p.rot / 2; i += kThreads) {
         const float2 f = p.freq[i];
@@ -44,7 +41,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         s_cs[i] = make_float2(cs * p.factor, sn * p.factor);
     }
     __syncthreads();
-    const int b = s_seq[0], slot = s_seq[1];
+    const int b = (int)(s_seq >> 32), slot = (int)s_seq;
     if (b < 0) return;  // a row that no sequence covers
     const int page = slot < 0 ? -1 : page_of(p.c, p.bt, b, slot);
     const int row = slot & ((1 << p.c.page_shift) - 1);

@@ -28,9 +28,9 @@ template <bool BF, bool Q8>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
     __shared__ float2 s_cs[32];
     __shared__ float s_sum[kThreads / 32];
-    __shared__ int s_seq[2];
+    __shared__ long long s_seq;  // of this token: (sequence, slot), -1 without one; one store, so that of two sequences that claim it one does
     const int t = blockIdx.x, tid = threadIdx.x, rope = p.c.rope, latent = p.c.latent;
-    if (tid == 0) s_seq[0] = -1;
+    if (tid == 0) s_seq = -1;
     uint4 x = make_uint4(0, 0, 0, 0), w = x;
     if (tid < latent >> 3) {
         x = *reinterpret_cast<const uint4 *>(p.lat + t * p.lat_stride + 8 * tid);
@@ -39,10 +39,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     __syncthreads();
     for (int b = tid; b < p.bt.batch; b += kThreads) {
         const kv::Seq s = kv::seq_info(p.bt, b, p.c.status);
-        if (t >= s.q0 && t < s.q0 + s.q_len) {
-            s_seq[0] = b;
-            s_seq[1] = s.kv_len - s.q_len + (t - s.q0);
-        }
+        if (t >= s.q0 && t < s.q0 + s.q_len) s_seq = kv::seq_slot(b, s.kv_len - s.q_len + (t - s.q0));
     }
     if (tid < rope >> 1) {
         const float2 f = p.freq[tid];
@@ -64,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
     __syncthreads();
-    const int b = s_seq[0], slot = s_seq[1];
+    const int b = (int)(s_seq >> 32), slot = (int)s_seq;
     if (b < 0) return;  // a row that no sequence covers
     const int page = slot < 0 ? -1 : page_of(p.c, p.bt, b, slot);
     unsigned char *dst = page < 0 ? nullptr : cell(p.c, page, slot);
