@@ -6,7 +6,7 @@ import torch
 
 import attention_reference as ref
 import latent_reference as lref
-from test_gpu_latent import BF, HF, World, check_rows, expand_world, ints, starts
+from test_gpu_latent import BF, HF, World, check_attend, check_rows, expand_world, ints, starts
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU")]
 
@@ -208,3 +208,23 @@ def test_sequences_that_share_their_first_pages_write_their_own():
         for i in range(2):
             o, _, ot, _ = lref.absorbed(q[i:i + 1], qr[i:i + 1], *values[i], 0.08, True)
             check_rows(i, out[i:i + 1], o, ot, None, None, None)
+
+
+@pytest.mark.parametrize("bits,page", [(16, 16), (16, 256), (8, 64)])
+def test_pages_whose_slots_are_apart(bits, page):
+    """Slot r of every page before slot r + 1 of the first: the strides of pages and slots the other way round."""
+    from expert_slot_cache_device_gb300.kv_cache import Rotary
+    from expert_slot_cache_device_gb300.latent_cache import LatentCache
+
+    w = World([3, 1, 70], [300, 64, 500], 256, 48, page, BF, bits, seed=5)
+    turned = w.cache.pages.transpose(0, 1).contiguous().transpose(0, 1)
+    w.cache = LatentCache(turned.shape[0], page, 256, 48, BF, bits, pages=turned)
+    check_attend(w, 20)
+    rows = w.cache.read(w.batch, ints(starts(w.kv_lens)), rows=864).cpu()
+    assert torch.equal(rows, torch.cat([torch.cat([c, k], 1) for c, k in zip(w.c, w.key)]))
+    c, key = torch.randn((74, 256), generator=w.gen).to(BF), torch.randn((74, 48), generator=w.gen).to(BF)
+    w.cache.append(w.batch, Rotary(48), c.cuda(), key.cuda(), torch.zeros(74, dtype=torch.int32, device="cuda"))
+    new = torch.cat([c if bits == 16 else lref.decode(*lref.encode(c)[:2], BF).to(BF), key], 1)  # position 0: nothing turns
+    for at, t in ((297, slice(0, 3)), (363, slice(3, 4)), (794, slice(4, 74))):
+        rows[at:at + t.stop - t.start] = new[t]
+    assert torch.equal(w.cache.read(w.batch, ints(starts(w.kv_lens)), rows=864).cpu(), rows) and w.cache.status() == 0
