@@ -22,11 +22,12 @@
 //               their way: shared memory has no place for more than a quarter of a tile's, which let too few be under way.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 //
-// Measured: 48 sequences of 9000 tokens, 128 heads: 94 us (85, and 9 for the join), 3.2 TB/s of the 6.8 of a plain copy, DRAM read
-// once (307 MB), the tensor pipe 29 % busy. Shared memory holds one tile (128 KB) beside 72 KB of queries, so an SM's time is the chain of a
+// Measured: 48 sequences of 9000 tokens, 128 heads: 94 us with the join, 3.2 TB/s of the 6.8 of a plain copy (this kernel alone: 3.4, DRAM
+// read once, 307 MB, the tensor pipe 34 % busy). Shared memory holds one tile (128 KB) beside 72 KB of queries, so an SM's time is the chain of a
 // tile: its scores (36 products of 50 cycles: M128 N64 runs no faster), softmax, outputs (32), and the refill behind them. 8 bits, 96
 // of 7000, 32 heads: 98 us, 2.3 TB/s; there the chain is conversion (about 1500 cycles of 64 slots), scores, softmax, outputs over two places,
-// and shared memory passes 4 KB a slot, half its bandwidth over the call. One sequence of 777: 12 us, latency (launch, plan, two tiles, join).
+// and shared memory passes 4 KB a slot, half its bandwidth over the call. More than 32 rows are blocks of 32 in 8 bits, each of which converts the
+// cache for itself: 48 of 9000, 64 heads 126 us, 128 heads 229. One sequence of 777: 12 us, latency (launch, plan, one tile, join).
 #include "latent_line.cuh"
 
 namespace ftmoe {
@@ -759,8 +760,9 @@ __global__ void __launch_bounds__((Shape<Q8, NR>::kThreads), 1) absorb_kernel(co
 
 // Joins the parts of the item that CTA c of the kernel before started: a warp a row, a lane four latents at a time. What the
 // first FIRST parts may have is loaded before it is known how many there are, one trip instead of four: eight where the grid is
-// small (16 rows an SM at most, whose CTAs all run at once) and has nothing else to wait for, else the two that an item that is joined has, in few registers (seven parts of one
-// sequence, 16 heads: 13.5 us with the kernel before, two first 15.5; 48 sequences of 128 heads: 97 us, 100 with four first).
+// small (16 rows an SM at most) and has nothing else to wait for, else the two that an item that is joined has, in few registers
+// (seven parts of one sequence, 16 heads: 13.5 us with the kernel before, two first 15.5; 48 sequences of 128 heads: 97 us, 100 with four
+// first).
 // Rows of a CTA: two of a small grid, over more SMs (one sequence of 777, 16 heads: 11.9 us, with eight 12.4, with sixteen 15.1).
 template <int FIRST>
 constexpr int kJoinRows = FIRST == 2 ? 8 : 2;
@@ -826,7 +828,7 @@ __global__ void __launch_bounds__(32 * kJoinRows<FIRST>, FIRST == 2 ? 4 : 1) abs
 
 // Rows of an item: as few as hold the tokens of the longest sequence, since they cost products and queries' place (64 x 2000 tokens: 16
 // heads 39 us, 43 as 32 rows, 53 as 64; 32 heads 42, 54 as 64). With 8 bits 32 at most: two tiles of elements and more queries do not fit
-// shared memory.
+// shared memory (64 rows are two blocks there, 48 x 9000 tokens of 64 heads 126 us, 16 bits 73).
 int rows_of(const AttendParams &p) {
     const int64_t n = (int64_t)p.q_heads * p.bt.max_q;
     return n <= 16 ? 16 : n <= 32 || p.c.bits == 8 ? 32 : 64;

@@ -12,8 +12,8 @@
 //   warp 11         walks the work and hands the parts out.
 // Every wait is bounded; one that runs out is recorded and ends the role.
 //
-// Measured: a prompt of 4096, 32 heads: 132 us, 1.30 PFLOP/s of the 1.94 of a large library product (tensor pipe 60 % busy: 32 heads x 16
-// items of unequal length, their starts and ends, and 6 us of join); 2048 tokens over 25000 rows, 16 heads: 336 us, 1.50 PFLOP/s; five
+// Measured: a prompt of 4096, 32 heads: 133 us, 1.29 PFLOP/s of the 1.94 of a large library product (tensor pipe 66 % busy: 32 heads x 16
+// items of unequal length, their starts and ends, and 6 us of join); 2048 tokens over 25000 rows, 16 heads: 338 us, 1.49 PFLOP/s; five
 // chunks of at most 301: 26 us, cold starts of two kernels and a few steps' latency.
 #include "latent_line.cuh"
 
