@@ -228,3 +228,23 @@ def test_pages_whose_slots_are_apart(bits, page):
     for at, t in ((297, slice(0, 3)), (363, slice(3, 4)), (794, slice(4, 74))):
         rows[at:at + t.stop - t.start] = new[t]
     assert torch.equal(w.cache.read(w.batch, ints(starts(w.kv_lens)), rows=864).cpu(), rows) and w.cache.status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+def test_read_under_a_loose_bound(bits):
+    """A bound of cached tokens far above the rows of `out`: the same rows; a sequence with more tokens than rows is recorded and cut."""
+    from expert_slot_cache_device_gb300 import ftmoe as F
+    from expert_slot_cache_device_gb300.kv_cache import KVBatch
+
+    w = World([1, 1, 1], [33, 1, 200], 128, 32, 16, HF, bits, seed=4)
+    table = torch.full((3, 1 << 13), -1, dtype=torch.int32)
+    table[:, :w.table.shape[1]] = w.table
+    batch = KVBatch(table.cuda(), ints(w.kv_lens), ints(w.cu), 1, 1 << 17)
+    want = torch.cat([torch.cat([c, k], 1) for c, k in zip(w.c, w.key)])
+    for rows in (234, 300):
+        out = torch.full((rows, 160), 7.0, dtype=HF, device="cuda")
+        w.cache.read(batch, ints([0, 33, 34, 234]), out=out)
+        assert w.cache.status() == 0 and torch.equal(out[:234].cpu(), want) and (out[234:] == 7).all()
+    out = torch.full((40, 160), 7.0, dtype=HF, device="cuda")
+    w.cache.read(batch, ints([0, 33, 34, 234]), out=out)  # six rows for the last sequence
+    assert w.cache.status() == F.ERR_STATE and torch.equal(out.cpu(), want[:40])
