@@ -462,7 +462,8 @@ typedef struct {
  * that no sequence covers are left alone.
  *   max_pages  readable entries of a block_table row;
  *   tokens     rows of the token arrays; max_q and max_kv: host-side upper bounds of q_len
- *              and kv_lens (they size grids and workspaces; max_kv <= max_pages * page_size). */
+ *              and kv_lens (they size grids and workspaces; max_kv <= max_pages * page_size, at
+ *              most 2^30). */
 typedef struct {
     const int32_t *d_block_table;
     int64_t table_stride;
